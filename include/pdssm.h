@@ -64,7 +64,11 @@ typedef struct pdssm_dims {
     int64_t B, H, L, N, K, D_in;   /* D_in is used by pdssm_select only */
 } pdssm_dims;
 
-typedef enum pdssm_dtype { PDSSM_F32 = 0, PDSSM_BF16 = 1 } pdssm_dtype;
+typedef enum pdssm_dtype {
+    PDSSM_F32 = 0,
+    PDSSM_BF16 = 1,
+    PDSSM_E4M3 = 2   /* output of pdssm_add_rmsnorm_fwd only */
+} pdssm_dtype;
 
 typedef enum pdssm_status {
     PDSSM_OK = 0,
@@ -460,6 +464,183 @@ pdssm_status pdssm_validate(const pdssm_dims *dims, const int32_t *pi_dict,
  * recorded.
  */
 pdssm_status pdssm_ws_status(void *ws, size_t ws_bytes, void *stream);
+
+/* ------------------------------------------------------------------------
+ * The operators around the PD-SSM scan in a pre-norm block
+ * ------------------------------------------------------------------------ */
+
+/* Sizes of the decay scan: B sequences, H heads, G groups of heads that share
+ * one c and one b (G divides H; G = H: none shared), L steps, a state of
+ * N x P per head. */
+typedef struct pdssm_decay_dims {
+    int64_t B, H, G, L, N, P;
+} pdssm_decay_dims;
+
+/* Order of the leading dimensions of c, b, x, y, a per-step log_a and their
+ * gradients: [B][heads][L][...] or, as a projection leaves them,
+ * [B][L][heads][...]. */
+typedef enum pdssm_layout { PDSSM_BHL = 0, PDSSM_BLH = 1 } pdssm_layout;
+
+/*
+ * Decay scan: the matrix-state sibling of the PD-SSM scan (linear attention
+ * with a decay for each head).  Per (batch, head), with a_t = exp(log_a_t):
+ *     S_t = a_t S_{t-1} + b_t x_t^T        (N x P)
+ *     y_t = S_t^T c_t                      (P)
+ * c, b: [B][G][L][N], x, y: [B][H][L][P] (layout PDSSM_BHL; with PDSSM_BLH
+ * [B][L][G][N] and [B][L][H][P]), all of `dtype`; head h reads c and b of
+ * group h / (H / G).  log_a fp32: one per step, [B][H][L] or [B][L][H]
+ * (log_a_per_step = 1), or one per head, [H] (0).  h0, h_last [B][H][N][P]
+ * fp32 (S_{-1}, S_{L-1}); h0 may be NULL (zero), h_last may be NULL.
+ * lengths: device int32 [B] or NULL: sequence b ends after lengths[b] steps
+ * (clamped to [0, L]); nothing behind its end is read, its y rows there are
+ * zero, and h_last is the state at its end.
+ *  * log_a below -200 counts as -200 (whose exp is 0 in fp32), so -inf resets
+ *    the state: sequences packed one behind another are separated by it (the
+ *    gradient of a log_a at or below -200 is zero).
+ *    log_a > 0 grows the state, as the formula says.
+ *  * The sums run over chunks of steps: a non-finite value in x reaches the
+ *    y of earlier steps of its chunk too, not only later ones.
+ *  * States, sums and decays are fp32 (cumulated decays fp64).  bf16 inputs
+ *    run on the tensor cores: the decayed products (c . b) and the state read
+ *    by c are rounded to bf16 there; the state itself is not.
+ *  * Limits: 1 <= N, P <= 128; B, H, G >= 1, H a multiple of G, L >= 0.
+ *  * for_bwd = 1 also leaves in ws the state at every chunk's start, which
+ *    pdssm_decay_scan_bwd needs.  ws: pdssm_decay_workspace_bytes(dims,
+ *    dtype, for_bwd) bytes, 256-byte aligned, overwritten.
+ * Deterministic: every sum in a fixed order.
+ */
+size_t pdssm_decay_workspace_bytes(const pdssm_decay_dims *dims,
+                                   pdssm_dtype dtype, int for_bwd);
+pdssm_status pdssm_decay_scan_fwd(const pdssm_decay_dims *dims, const void *c,
+                                  const void *b, const void *x,
+                                  pdssm_dtype dtype, pdssm_layout layout,
+                                  const float *log_a, int log_a_per_step,
+                                  const float *h0, const int32_t *lengths,
+                                  void *y, float *h_last, int for_bwd,
+                                  void *ws, size_t ws_bytes, void *stream);
+
+/*
+ * Exact adjoint of pdssm_decay_scan_fwd for the loss
+ *     sum_t <g_y[t], y_t> + <g_hlast, h_last>:
+ * with R_t = dl/dS_t = c_t g_y[t]^T + a_{t+1} R_{t+1},
+ *     g_c_t = S_t g_y[t],  g_b_t = R_t x_t,  g_x_t = R_t^T b_t,
+ *     g_log_a_t = a_t <R_t, S_{t-1}>,  g_h0 = a_0 R_0;
+ * g_c and g_b of shared keys are summed over the heads of their group and a
+ * per-head g_log_a over (b, t), each in a fixed order.  Must follow
+ * pdssm_decay_scan_fwd(for_bwd = 1) with the same arguments and the same ws,
+ * untouched in between; it may be called again on the same ws (the forward's
+ * states stay).  g_c, g_b, g_x and g_y are of `dtype` in `layout`; g_log_a
+ * (like log_a) and g_h0 fp32.  g_hlast may be NULL (zero), g_h0 may be NULL
+ * (not written).  Rows behind a sequence's length get zero gradients.
+ */
+pdssm_status pdssm_decay_scan_bwd(const pdssm_decay_dims *dims, const void *c,
+                                  const void *b, const void *x,
+                                  pdssm_dtype dtype, pdssm_layout layout,
+                                  const float *log_a, int log_a_per_step,
+                                  const float *h0, const int32_t *lengths,
+                                  const void *g_y, const float *g_hlast,
+                                  void *g_c, void *g_b, void *g_x,
+                                  float *g_log_a, float *g_h0, void *ws,
+                                  size_t ws_bytes, void *stream);
+
+/*
+ * One step of the decay scan for single tokens: dims->L is ignored; c, b
+ * [B][G][N], x, y [B][H][P] of `dtype`; log_a fp32 [B][H] (log_a_per_step =
+ * 1) or [H] (0).  state fp32 [n_slots][H][N][P] is updated in place; row r of
+ * the batch uses slot slots[r] (device int32 [B]), or slot r when slots is
+ * NULL (then n_slots >= B).  A row whose slot lies outside [0, n_slots) is
+ * empty: its y is zero and no state is touched.  So is a row whose slot an
+ * earlier row of the batch already uses.  y_t reads the updated state, in
+ * fp32.  Needs no workspace.
+ */
+pdssm_status pdssm_decay_step(const pdssm_decay_dims *dims, const void *c,
+                              const void *b, const void *x, pdssm_dtype dtype,
+                              const float *log_a, int log_a_per_step,
+                              float *state, int64_t n_slots,
+                              const int32_t *slots, void *y, void *stream);
+
+/*
+ * Residual addition and root-mean-square norm of `rows` rows of D values:
+ *     s = x + residual                    (rounded to res_dtype: res_out)
+ *     rstd = 1 / sqrt(mean(s^2) + eps)
+ *     out = s * rstd * weight
+ * x of x_dtype; residual and res_out of res_dtype; residual may be NULL (then
+ * s = x and res_out is still written, unless it is NULL); out of out_dtype.
+ * weight [D] of w_dtype (fp32 or bf16), rstd fp32 [rows] (may be NULL).
+ * The norm is of the rounded sum, so that it and its backward see the values
+ * that the residual stream carries on.  res_out may be residual, and out may
+ * be x when their types agree (rows are read before they are written).
+ *  * out_dtype PDSSM_E4M3: out holds round(v / scale) of v = s rstd weight
+ *    with one scale per row, scale = max|v| / 448 (1 for a row of zeros),
+ *    written to scale fp32 [rows]; a row with a non-finite value gets a
+ *    non-finite scale.  scale is NULL otherwise.
+ *  * Limits: 1 <= D <= 16384, 0 <= rows < 2^31, eps >= 0.
+ */
+pdssm_status pdssm_add_rmsnorm_fwd(int64_t rows, int64_t D, const void *x,
+                                   pdssm_dtype x_dtype, const void *residual,
+                                   pdssm_dtype res_dtype, const void *weight,
+                                   pdssm_dtype w_dtype, float eps, void *out,
+                                   pdssm_dtype out_dtype, void *res_out,
+                                   float *rstd, float *scale, void *stream);
+
+/*
+ * Its backward: with hat = s * rstd (s = res_out and rstd of the forward),
+ *     g_x = rstd (g_out weight - hat mean(g_out weight hat)) + g_res
+ *     g_weight = sum over the rows of g_out hat
+ * g_x (of res_dtype) is the gradient of x and of residual alike; g_res (of
+ * res_dtype, may be NULL) is the gradient that reaches res_out from later in
+ * the residual stream; g_out is of g_dtype (fp32 or bf16).  g_weight fp32 [D].
+ * g_x may be g_res.  scratch: pdssm_add_rmsnorm_scratch_bytes(rows, D) bytes,
+ * 256-byte aligned.  Deterministic.
+ */
+size_t pdssm_add_rmsnorm_scratch_bytes(int64_t rows, int64_t D);
+pdssm_status pdssm_add_rmsnorm_bwd(int64_t rows, int64_t D, const void *g_out,
+                                   pdssm_dtype g_dtype, const void *res_out,
+                                   pdssm_dtype res_dtype, const void *weight,
+                                   pdssm_dtype w_dtype, const float *rstd,
+                                   const void *g_res, void *g_x,
+                                   float *g_weight, void *scratch,
+                                   size_t scratch_bytes, void *stream);
+
+/*
+ * Balance loss of the hard selection and the use of every dictionary entry.
+ * Over the T = B*L steps (or those in front of lengths[b], device int32 [B],
+ * clamped to [0, L]), per head h:
+ *     counts[h][k] = number of steps with k[b][h][t] = k
+ *     probs[h][k]  = (1/T) sum_{b,t} p_t[k],  p_t = softmax(l_t inv_tau),
+ *                    l_t[k] = sum_q W_sel[h][k][q] u[b][t][q]
+ *     loss[h]      = K sum_k (counts[h][k] / T) probs[h][k]
+ * (1 when both are even, K when all steps fall on one entry).  counts int32
+ * [H][K]; an index of k outside [0, K) is counted nowhere.  T = 0 gives zeros.
+ * u [B][L][D_in] (fp32 or bf16), W_sel [H][K][D_in] fp32, as in pdssm_select;
+ * probs, loss fp32.  dims->N is ignored; limits as pdssm_select, B*L < 2^31.
+ * scratch: pdssm_select_balance_scratch_bytes(dims) bytes, 256-byte aligned.
+ */
+size_t pdssm_select_balance_scratch_bytes(const pdssm_dims *dims);
+pdssm_status pdssm_select_balance_fwd(const pdssm_dims *dims, const void *u,
+                                      pdssm_dtype u_dtype, const float *W_sel,
+                                      const int32_t *k, float inv_tau,
+                                      const int32_t *lengths, float *loss,
+                                      int32_t *counts, float *probs,
+                                      void *scratch, size_t scratch_bytes,
+                                      void *stream);
+
+/*
+ * Gradients of sum_h g_loss[h] loss[h], the counts held fixed:
+ *     g_l_t[k] = g_loss[h] K inv_tau / T p_t[k] (f_k - sum_k' p_t[k'] f_k'),
+ *     f_k = counts[h][k] / T,
+ *     g_W[h][k] = sum_{b,t} g_l_t[k] u[b][t],  g_u[b][t] = sum_{h,k} g_l_t[k] W_sel[h][k].
+ * g_loss fp32 [H]; g_u [B][L][D_in] of u's dtype (zero behind a length), g_W
+ * [H][K][D_in] fp32.  Either may be NULL (not computed).  Same scratch.
+ * Deterministic.
+ */
+pdssm_status pdssm_select_balance_bwd(const pdssm_dims *dims, const void *u,
+                                      pdssm_dtype u_dtype, const float *W_sel,
+                                      const int32_t *counts, float inv_tau,
+                                      const int32_t *lengths,
+                                      const float *g_loss, void *g_u,
+                                      float *g_W, void *scratch,
+                                      size_t scratch_bytes, void *stream);
 
 #ifdef __cplusplus
 }

@@ -25,7 +25,7 @@ import torch
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libpdssm.so")
 
-PDSSM_F32, PDSSM_BF16 = 0, 1
+PDSSM_F32, PDSSM_BF16, PDSSM_E4M3 = 0, 1, 2
 STATUS = {0: "PDSSM_OK", 1: "PDSSM_ERR_INVALID_ARG", 2: "PDSSM_ERR_UNSUPPORTED",
           3: "PDSSM_ERR_BAD_INDEX", 4: "PDSSM_ERR_CUDA", 5: "PDSSM_ERR_TIMEOUT",
           6: "PDSSM_ERR_WORKSPACE"}
@@ -39,7 +39,11 @@ EXPORTS = ("pdssm_status_str", "pdssm_last_error", "pdssm_version",
            "pdssm_scan_fwd_traced", "pdssm_scan_bwd_traced", "pdssm_ws_transfers",
            "pdssm_wait_selftest", "pdssm_wait_selftest_ws_bytes", "pdssm_dict_hardmax",
            "pdssm_soft_maps", "pdssm_scan_fwd_maps", "pdssm_surrogate_scratch_bytes",
-           "pdssm_surrogate_bwd", "pdssm_select_scan_fwd", "pdssm_scan_fwd_single_pass")
+           "pdssm_surrogate_bwd", "pdssm_select_scan_fwd", "pdssm_scan_fwd_single_pass",
+           "pdssm_decay_workspace_bytes", "pdssm_decay_scan_fwd", "pdssm_decay_scan_bwd",
+           "pdssm_decay_step", "pdssm_add_rmsnorm_fwd", "pdssm_add_rmsnorm_scratch_bytes",
+           "pdssm_add_rmsnorm_bwd", "pdssm_select_balance_scratch_bytes",
+           "pdssm_select_balance_fwd", "pdssm_select_balance_bwd")
 
 TRACE_MAX_KERNELS = 8
 
@@ -49,6 +53,11 @@ SELECT_METHODS = {"auto": 0, "fma": 1, "tensor_core": 2}
 class Dims(ctypes.Structure):
     _fields_ = [("B", ctypes.c_int64), ("H", ctypes.c_int64), ("L", ctypes.c_int64),
                 ("N", ctypes.c_int64), ("K", ctypes.c_int64), ("D_in", ctypes.c_int64)]
+
+
+class DecayDims(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int64), ("H", ctypes.c_int64), ("G", ctypes.c_int64),
+                ("L", ctypes.c_int64), ("N", ctypes.c_int64), ("P", ctypes.c_int64)]
 
 
 class Trace(ctypes.Structure):
@@ -69,7 +78,7 @@ def _load() -> ctypes.CDLL:
             "`python -m structured_sparse_state_b200.build` (there is no CPU fallback)")
     lib = ctypes.CDLL(LIB_PATH)
     P, I64, I32, SZ = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_size_t
-    D = ctypes.POINTER(Dims)
+    D, DD = ctypes.POINTER(Dims), ctypes.POINTER(DecayDims)
     sig = {
         "pdssm_status_str": (ctypes.c_char_p, [I32]),
         "pdssm_last_error": (ctypes.c_char_p, []),
@@ -104,6 +113,18 @@ def _load() -> ctypes.CDLL:
                                         ctypes.POINTER(Trace)]),
         "pdssm_scan_bwd_traced": (I32, [D, P, I64, P, P, P, P, I32, P, P, P, P, P, P, P, I64,
                                         P, SZ, P, ctypes.POINTER(Trace)]),
+        "pdssm_decay_workspace_bytes": (SZ, [DD, I32, I32]),
+        "pdssm_decay_scan_fwd": (I32, [DD, P, P, P, I32, I32, P, I32, P, P, P, P, I32, P, SZ, P]),
+        "pdssm_decay_scan_bwd": (I32, [DD, P, P, P, I32, I32, P, I32, P, P, P, P, P, P, P, P, P,
+                                       P, SZ, P]),
+        "pdssm_decay_step": (I32, [DD, P, P, P, I32, P, I32, P, I64, P, P, P]),
+        "pdssm_add_rmsnorm_fwd": (I32, [I64, I64, P, I32, P, I32, P, I32, ctypes.c_float, P, I32,
+                                        P, P, P, P]),
+        "pdssm_add_rmsnorm_scratch_bytes": (SZ, [I64, I64]),
+        "pdssm_add_rmsnorm_bwd": (I32, [I64, I64, P, I32, P, I32, P, I32, P, P, P, P, P, SZ, P]),
+        "pdssm_select_balance_scratch_bytes": (SZ, [D]),
+        "pdssm_select_balance_fwd": (I32, [D, P, I32, P, P, ctypes.c_float, P, P, P, P, P, SZ, P]),
+        "pdssm_select_balance_bwd": (I32, [D, P, I32, P, P, ctypes.c_float, P, P, P, P, P, SZ, P]),
     }
     for name, (res, args) in sig.items():
         f = getattr(lib, name)
@@ -628,3 +649,10 @@ def pdssm_surrogate_bwd(u, W_sel, A, pi_dict, k, d, b, h0, lam, ws, chunk, inv_t
                                     _ptr(scratch), nbytes, _ptr(g_l), _ptr(g_W), _ptr(g_A),
                                     _stream(stream)), "pdssm_surrogate_bwd")
     return g_l, g_W, g_A
+
+
+# the operators around the scan in a pre-norm block (same names as the C ABI)
+from .blocks import (pdssm_add_rmsnorm_bwd, pdssm_add_rmsnorm_fwd,  # noqa: E402,F401
+                     pdssm_decay_scan_bwd, pdssm_decay_scan_fwd, pdssm_decay_step,
+                     pdssm_decay_workspace_bytes, pdssm_select_balance_bwd,
+                     pdssm_select_balance_fwd)

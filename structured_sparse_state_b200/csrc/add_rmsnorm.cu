@@ -1,0 +1,419 @@
+// Residual addition and root-mean-square norm, forward (16-, 32- or 8-bit
+// output) and backward.
+//
+//     s = x + residual,  rstd = (mean(s^2) + eps)^(-1/2),  out = s rstd w
+//     g_s = rstd (g w - hat mean(g w hat)) + g_res,  hat = s rstd
+//     g_w = sum over rows of g hat
+//
+// Bound: HBM, every operand once.  A row stays in the registers of TPR
+// threads (at most 32 values each), so nothing is read twice; sums of squares
+// and products go through warp shuffles and, above one warp, shared memory.
+// The backward's CTAs are persistent: each thread owns the same columns of
+// every row it sees and sums its share of g_w in registers; a CTA's sums go to
+// scratch and a second kernel adds the CTAs in order, so the result does not
+// depend on timing.
+#include <cuda_fp8.h>
+
+#include "common.cuh"
+
+namespace pdssm {
+namespace {
+
+// The types are uniform over a launch: one branch per 16-byte access keeps the
+// kernels few, and these kernels wait for memory, not for issue slots.
+template <int V>
+__device__ __forceinline__ void load_vec(float (&v)[V], const void *p, int64_t at, int dt) {
+    if constexpr (V == 8) {
+        if (dt == PDSSM_F32) {
+            const float4 *q = reinterpret_cast<const float4 *>((const float *)p + at);
+            const float4 a = q[0], b = q[1];
+            v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+            v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+        } else {
+            const uint4 a = *reinterpret_cast<const uint4 *>((const __nv_bfloat16 *)p + at);
+            const unsigned w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                v[2 * i] = __uint_as_float(w[i] << 16);
+                v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+            }
+        }
+    } else {
+        v[0] = dt == PDSSM_F32 ? ((const float *)p)[at]
+                               : __bfloat162float(((const __nv_bfloat16 *)p)[at]);
+    }
+}
+
+__device__ __forceinline__ unsigned pack_bf16(float a, float b) {
+    const __nv_bfloat162 t = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const unsigned *>(&t);
+}
+
+template <int V>
+__device__ __forceinline__ void store_vec(const float (&v)[V], void *p, int64_t at, int dt) {
+    if constexpr (V == 8) {
+        if (dt == PDSSM_F32) {
+            float4 *q = reinterpret_cast<float4 *>((float *)p + at);
+            q[0] = make_float4(v[0], v[1], v[2], v[3]);
+            q[1] = make_float4(v[4], v[5], v[6], v[7]);
+        } else if (dt == PDSSM_BF16) {
+            *reinterpret_cast<uint4 *>((__nv_bfloat16 *)p + at) =
+                make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]),
+                           pack_bf16(v[6], v[7]));
+        } else {
+            // round to nearest, saturating; the row's scale keeps values within 448
+            unsigned w[2] = {0, 0};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const unsigned t = __nv_cvt_float2_to_fp8x2(make_float2(v[2 * i], v[2 * i + 1]),
+                                                            __NV_SATFINITE, __NV_E4M3);
+                w[i / 2] |= t << (16 * (i % 2));
+            }
+            *reinterpret_cast<uint2 *>((unsigned char *)p + at) = make_uint2(w[0], w[1]);
+        }
+    } else {
+        if (dt == PDSSM_F32)
+            ((float *)p)[at] = v[0];
+        else if (dt == PDSSM_BF16)
+            ((__nv_bfloat16 *)p)[at] = __float2bfloat16_rn(v[0]);
+        else
+            ((unsigned char *)p)[at] = __nv_cvt_float_to_fp8(v[0], __NV_SATFINITE, __NV_E4M3);
+    }
+}
+
+// A NaN must reach the row's scale: max that keeps it.
+__device__ __forceinline__ float max_nan(float a, float b) {
+    return (a > b || a != a) ? a : b;
+}
+
+struct AddOp {
+    __device__ __forceinline__ float operator()(float a, float b) const { return a + b; }
+};
+struct MaxOp {
+    __device__ __forceinline__ float operator()(float a, float b) const { return max_nan(a, b); }
+};
+
+// Reduction over the TPR threads of a row (TPR = 32, or the whole CTA); `red`
+// holds one value per warp and is free again after the call's last barrier.
+template <int TPR, class OP>
+__device__ __forceinline__ float row_reduce(float v, float *red, OP op) {
+#pragma unroll
+    for (int d = 16; d; d >>= 1) v = op(v, __shfl_xor_sync(kFull, v, d));
+    if constexpr (TPR > 32) {
+        __syncthreads();
+        if (threadIdx.x % 32 == 0) red[threadIdx.x / 32] = v;
+        __syncthreads();
+        v = red[0];
+#pragma unroll
+        for (int w = 1; w < TPR / 32; ++w) v = op(v, red[w]);
+    }
+    return v;
+}
+
+struct NormParams {
+    int64_t rows;
+    int D;
+    const void *x, *residual, *weight;
+    void *out, *res_out;
+    float *rstd, *scale;
+    int x_dt, res_dt, w_dt, out_dt;
+    float eps;
+};
+
+constexpr int kRowValues = 32;      // most values of a row per thread
+
+// TPR = 32: a warp per row, 4 rows per CTA; else a CTA per row.
+template <int TPR, int V>
+__global__ void __launch_bounds__(TPR == 32 ? 128 : TPR) k_add_rmsnorm(NormParams p) {
+    constexpr int NV = kRowValues / V;
+    __shared__ float red[32];
+    const int lane = TPR == 32 ? threadIdx.x % 32 : threadIdx.x;
+    const int64_t row = TPR == 32 ? (int64_t)blockIdx.x * 4 + threadIdx.x / 32 : blockIdx.x;
+    if (row >= p.rows) return;          // TPR = 32 only, where no barrier follows
+    const int64_t base = row * p.D;
+    float s[NV][V];
+    float sum = 0.f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int col = (i * TPR + lane) * V;
+        if (col < p.D) load_vec<V>(s[i], p.x, base + col, p.x_dt);
+    }
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int col = (i * TPR + lane) * V;
+        if (col >= p.D) continue;
+        if (p.residual) {
+            float r[V];
+            load_vec<V>(r, p.residual, base + col, p.res_dt);
+#pragma unroll
+            for (int j = 0; j < V; ++j) s[i][j] += r[j];
+        }
+        if (p.res_dt == PDSSM_BF16) {   // the norm is of the rounded sum
+#pragma unroll
+            for (int j = 0; j < V; ++j) s[i][j] = __bfloat162float(__float2bfloat16_rn(s[i][j]));
+        }
+#pragma unroll
+        for (int j = 0; j < V; ++j) sum = fmaf(s[i][j], s[i][j], sum);
+    }
+    sum = row_reduce<TPR>(sum, red, AddOp());
+    const float rstd = 1.f / sqrtf(sum / (float)p.D + p.eps);
+    if (p.rstd && lane == 0) p.rstd[row] = rstd;
+    float top = 0.f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int col = (i * TPR + lane) * V;
+        if (col >= p.D) continue;
+        if (p.res_out) store_vec<V>(s[i], p.res_out, base + col, p.res_dt);
+        float w[V];
+        load_vec<V>(w, p.weight, col, p.w_dt);
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            s[i][j] = s[i][j] * rstd * w[j];
+            top = max_nan(top, fabsf(s[i][j]));
+        }
+        if (p.out_dt != PDSSM_E4M3) store_vec<V>(s[i], p.out, base + col, p.out_dt);
+    }
+    if (p.out_dt != PDSSM_E4M3) return;
+    top = row_reduce<TPR>(top, red, MaxOp());
+    float scale = top / 448.f;
+    if (scale == 0.f) scale = 1.f;
+    if (lane == 0) p.scale[row] = scale;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int col = (i * TPR + lane) * V;
+        if (col >= p.D) continue;
+#pragma unroll
+        for (int j = 0; j < V; ++j) s[i][j] = s[i][j] / scale;
+        store_vec<V>(s[i], p.out, base + col, p.out_dt);
+    }
+}
+
+struct NormBwdParams {
+    int64_t rows;
+    int D, ctas;
+    const void *g_out, *s, *weight, *g_res;
+    const float *rstd;
+    void *g_x;
+    float *part;                // [ctas][D]
+    int g_dt, res_dt, w_dt;
+};
+
+constexpr int kBwdValues = 16;      // values of a row per thread
+
+// TPR = 32: 4 warps per CTA, a row per warp at a time; else a row per CTA.
+template <int TPR, int V>
+__global__ void __launch_bounds__(TPR == 32 ? 128 : TPR) k_add_rmsnorm_bwd(NormBwdParams p) {
+    constexpr int NV = kBwdValues / V;
+    constexpr int RPC = TPR == 32 ? 4 : 1;
+    __shared__ float red[32];
+    __shared__ float comb[TPR == 32 ? 4 * 32 * kBwdValues : 1];
+    const int lane = TPR == 32 ? threadIdx.x % 32 : threadIdx.x;
+    const int sub = TPR == 32 ? threadIdx.x / 32 : 0;
+    float w[NV][V], gw[NV][V];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int col = (i * TPR + lane) * V;
+        if (col < p.D) load_vec<V>(w[i], p.weight, col, p.w_dt);
+#pragma unroll
+        for (int j = 0; j < V; ++j) gw[i][j] = 0.f;
+    }
+    for (int64_t row = (int64_t)blockIdx.x * RPC + sub; row < p.rows;
+         row += (int64_t)gridDim.x * RPC) {
+        const int64_t base = row * p.D;
+        const float rstd = p.rstd[row];
+        float g[NV][V], h[NV][V], r[NV][V];
+        float dot = 0.f;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int col = (i * TPR + lane) * V;
+            if (col >= p.D) continue;
+            load_vec<V>(g[i], p.g_out, base + col, p.g_dt);
+            load_vec<V>(h[i], p.s, base + col, p.res_dt);
+            if (p.g_res) load_vec<V>(r[i], p.g_res, base + col, p.res_dt);
+        }
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            if ((i * TPR + lane) * V >= p.D) continue;
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                h[i][j] *= rstd;
+                gw[i][j] = fmaf(g[i][j], h[i][j], gw[i][j]);
+                g[i][j] *= w[i][j];
+                dot = fmaf(g[i][j], h[i][j], dot);
+            }
+        }
+        dot = row_reduce<TPR>(dot, red, AddOp()) / (float)p.D;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int col = (i * TPR + lane) * V;
+            if (col >= p.D) continue;
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                g[i][j] = (g[i][j] - h[i][j] * dot) * rstd;
+                if (p.g_res) g[i][j] += r[i][j];
+            }
+            store_vec<V>(g[i], p.g_x, base + col, p.res_dt);
+        }
+    }
+    if constexpr (TPR == 32) {          // the CTA's four warps hold the same columns
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+#pragma unroll
+            for (int j = 0; j < V; ++j)
+                comb[(sub * 32 + lane) * kBwdValues + i * V + j] = gw[i][j];
+        __syncthreads();
+        if (sub) return;
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+#pragma unroll
+            for (int j = 0; j < V; ++j)
+                for (int q = 1; q < 4; ++q)
+                    gw[i][j] += comb[(q * 32 + lane) * kBwdValues + i * V + j];
+    }
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int col = (i * TPR + lane) * V;
+        if (col >= p.D) continue;
+#pragma unroll
+        for (int j = 0; j < V; ++j) p.part[(int64_t)blockIdx.x * p.D + col + j] = gw[i][j];
+    }
+}
+
+// g_w: the CTAs' sums in order, 32 columns per CTA, 32 partial sums per column
+__global__ void __launch_bounds__(1024) k_rmsnorm_gw(const float *part, int ctas, int D,
+                                                     float *g_w) {
+    __shared__ float sm[32][33];
+    const int col = blockIdx.x * 32 + threadIdx.x % 32, sub = threadIdx.x / 32;
+    float s = 0.f;
+    if (col < D)
+        for (int c = sub; c < ctas; c += 32) s += part[(int64_t)c * D + col];
+    sm[sub][threadIdx.x % 32] = s;
+    __syncthreads();
+    s = sm[threadIdx.x % 32][sub];
+#pragma unroll
+    for (int d = 16; d; d >>= 1) s += __shfl_xor_sync(kFull, s, d);
+    if (threadIdx.x % 32 == 0 && blockIdx.x * 32 + sub < D) g_w[blockIdx.x * 32 + sub] = s;
+}
+
+constexpr int kMaxD = 16384;
+
+// CTAs of the backward: enough to fill the GPU (about 16 warps per SM), no
+// more than rows
+int bwd_tpr(int64_t D) {
+    return D <= 32 * kBwdValues ? 32 : D <= 128 * kBwdValues ? 128 : D <= 256 * kBwdValues ? 256
+           : D <= 512 * kBwdValues ? 512 : 1024;
+}
+int64_t bwd_ctas(int64_t rows, int64_t D) {
+    const int tpr = bwd_tpr(D);
+    const int rpc = tpr == 32 ? 4 : 1;
+    const int per_sm = tpr <= 128 ? 8 : tpr == 256 ? 4 : tpr == 512 ? 2 : 1;
+    const int64_t n = (rows + rpc - 1) / rpc, most = 148 * per_sm;
+    return n < most ? (n > 0 ? n : 1) : most;
+}
+
+bool aligned(const void *p, size_t a) { return ((uintptr_t)p % a) == 0; }
+bool wide(int dt) { return dt == PDSSM_F32 || dt == PDSSM_BF16; }
+
+template <int V>
+cudaError_t run_fwd(const NormParams &p, cudaStream_t st) {
+    const unsigned rows = (unsigned)p.rows;
+    if (p.D <= 32 * kRowValues)
+        k_add_rmsnorm<32, V><<<(rows + 3) / 4, 128, 0, st>>>(p);
+    else if (p.D <= 128 * kRowValues)
+        k_add_rmsnorm<128, V><<<rows, 128, 0, st>>>(p);
+    else if (p.D <= 256 * kRowValues)
+        k_add_rmsnorm<256, V><<<rows, 256, 0, st>>>(p);
+    else
+        k_add_rmsnorm<512, V><<<rows, 512, 0, st>>>(p);
+    return cudaGetLastError();
+}
+
+template <int V>
+cudaError_t run_bwd(const NormBwdParams &p, cudaStream_t st) {
+    switch (bwd_tpr(p.D)) {
+        case 32: k_add_rmsnorm_bwd<32, V><<<p.ctas, 128, 0, st>>>(p); break;
+        case 128: k_add_rmsnorm_bwd<128, V><<<p.ctas, 128, 0, st>>>(p); break;
+        case 256: k_add_rmsnorm_bwd<256, V><<<p.ctas, 256, 0, st>>>(p); break;
+        case 512: k_add_rmsnorm_bwd<512, V><<<p.ctas, 512, 0, st>>>(p); break;
+        default: k_add_rmsnorm_bwd<1024, V><<<p.ctas, 1024, 0, st>>>(p); break;
+    }
+    return cudaGetLastError();
+}
+
+pdssm_status check_sizes(int64_t rows, int64_t D) {
+    if (rows < 0 || D < 1) return arg_fail(PDSSM_ERR_INVALID_ARG, "need rows >= 0 and D >= 1");
+    if (D > kMaxD) return arg_fail(PDSSM_ERR_UNSUPPORTED, "D > 16384");
+    if (rows > 0x7fffffff) return arg_fail(PDSSM_ERR_UNSUPPORTED, "rows >= 2^31");
+    return PDSSM_OK;
+}
+
+}  // namespace
+}  // namespace pdssm
+
+using namespace pdssm;
+
+extern "C" {
+
+pdssm_status pdssm_add_rmsnorm_fwd(int64_t rows, int64_t D, const void *x, pdssm_dtype x_dtype,
+                                   const void *residual, pdssm_dtype res_dtype,
+                                   const void *weight, pdssm_dtype w_dtype, float eps, void *out,
+                                   pdssm_dtype out_dtype, void *res_out, float *rstd, float *scale,
+                                   void *stream) {
+    pdssm_status st = check_sizes(rows, D);
+    if (st != PDSSM_OK) return st;
+    if (!wide(x_dtype) || !wide(res_dtype) || !wide(w_dtype) ||
+        (!wide(out_dtype) && out_dtype != PDSSM_E4M3))
+        return arg_fail(PDSSM_ERR_INVALID_ARG, "unknown dtype");
+    if (!(eps >= 0.f) || eps > 3.0e38f)
+        return arg_fail(PDSSM_ERR_INVALID_ARG, "eps must be finite and >= 0");
+    if ((out_dtype == PDSSM_E4M3) != (scale != nullptr) && rows > 0)
+        return arg_fail(PDSSM_ERR_INVALID_ARG, "scale goes with an 8-bit output, and only with it");
+    if (rows == 0) return PDSSM_OK;
+    if (!x || !weight || !out) return arg_fail(PDSSM_ERR_INVALID_ARG, "NULL tensor pointer");
+    NormParams p{rows, (int)D, x, residual, weight, out, res_out, rstd, scale,
+                 x_dtype, res_dtype, w_dtype, out_dtype, eps};
+    const bool vec = D % 8 == 0 && aligned(x, 16) && aligned(residual, 16) &&
+                     aligned(weight, 16) && aligned(res_out, 16) && aligned(out, 16);
+    cudaError_t e = vec ? run_fwd<8>(p, (cudaStream_t)stream) : run_fwd<1>(p, (cudaStream_t)stream);
+    return e == cudaSuccess ? PDSSM_OK : cuda_fail(e, "add + norm");
+}
+
+size_t pdssm_add_rmsnorm_scratch_bytes(int64_t rows, int64_t D) {
+    if (check_sizes(rows, D) != PDSSM_OK) return 0;
+    return align256((size_t)bwd_ctas(rows, D) * (size_t)D * 4);
+}
+
+pdssm_status pdssm_add_rmsnorm_bwd(int64_t rows, int64_t D, const void *g_out, pdssm_dtype g_dtype,
+                                   const void *res_out, pdssm_dtype res_dtype, const void *weight,
+                                   pdssm_dtype w_dtype, const float *rstd, const void *g_res,
+                                   void *g_x, float *g_weight, void *scratch, size_t scratch_bytes,
+                                   void *stream) {
+    pdssm_status st = check_sizes(rows, D);
+    if (st != PDSSM_OK) return st;
+    if (!wide(g_dtype) || !wide(res_dtype) || !wide(w_dtype))
+        return arg_fail(PDSSM_ERR_INVALID_ARG, "unknown dtype");
+    if (!g_weight) return arg_fail(PDSSM_ERR_INVALID_ARG, "NULL g_weight");
+    cudaStream_t s = (cudaStream_t)stream;
+    cudaError_t e;
+    if (rows == 0) {
+        e = cudaMemsetAsync(g_weight, 0, (size_t)D * 4, s);
+        return e == cudaSuccess ? PDSSM_OK : cuda_fail(e, "g_weight of no rows");
+    }
+    if (!g_out || !res_out || !weight || !rstd || !g_x)
+        return arg_fail(PDSSM_ERR_INVALID_ARG, "NULL tensor pointer");
+    if (!scratch || !aligned(scratch, 256))
+        return arg_fail(PDSSM_ERR_INVALID_ARG, "scratch NULL or not 256-byte aligned");
+    if (scratch_bytes < pdssm_add_rmsnorm_scratch_bytes(rows, D))
+        return arg_fail(PDSSM_ERR_WORKSPACE, "scratch too small");
+    NormBwdParams p{rows, (int)D, (int)bwd_ctas(rows, D), g_out, res_out, weight, g_res, rstd, g_x,
+                    (float *)scratch, g_dtype, res_dtype, w_dtype};
+    const bool vec = D % 8 == 0 && aligned(g_out, 16) && aligned(res_out, 16) &&
+                     aligned(weight, 16) && aligned(g_res, 16) && aligned(g_x, 16);
+    e = vec ? run_bwd<8>(p, s) : run_bwd<1>(p, s);
+    if (e != cudaSuccess) return cuda_fail(e, "add + norm backward");
+    k_rmsnorm_gw<<<(unsigned)((D + 31) / 32), 1024, 0, s>>>(p.part, p.ctas, (int)D, g_weight);
+    e = cudaGetLastError();
+    return e == cudaSuccess ? PDSSM_OK : cuda_fail(e, "weight gradient");
+}
+
+}  // extern "C"

@@ -1,0 +1,684 @@
+// Decay scan on the CUDA cores: every type and width, the path of fp32
+// inputs.  One CTA of 256 threads (16 x 16) per segment of a (batch, head);
+// a chunk's operands sit in shared memory as fp32 rows of odd length, so both
+// orientations of a product read them without bank conflicts, and each thread
+// owns a strided TM x TN tile of a product's result.
+//
+// Bound: shared-memory loads, (TM + TN) per TM * TN multiply-adds.
+#include "decay.cuh"
+
+namespace pdssm {
+namespace {
+
+constexpr int kThreads = 256;
+
+// acc[i][j] += sum_k a(ty + 16 i, k) b(tx + 16 j, k)
+template <int TM, int TN, class FA, class FB>
+__device__ __forceinline__ void tile_mm(float (&acc)[TM][TN], int K, FA a, FB b) {
+#pragma unroll 4
+    for (int k = 0; k < K; ++k) {
+        float av[TM], bv[TN];
+#pragma unroll
+        for (int i = 0; i < TM; ++i) av[i] = a(i, k);
+#pragma unroll
+        for (int j = 0; j < TN; ++j) bv[j] = b(j, k);
+#pragma unroll
+        for (int i = 0; i < TM; ++i)
+#pragma unroll
+            for (int j = 0; j < TN; ++j) acc[i][j] = fmaf(av[i], bv[j], acc[i][j]);
+    }
+}
+
+template <int TM, int TN>
+__device__ __forceinline__ void zero(float (&acc)[TM][TN]) {
+#pragma unroll
+    for (int i = 0; i < TM; ++i)
+#pragma unroll
+        for (int j = 0; j < TN; ++j) acc[i][j] = 0.f;
+}
+
+// rows t0..t0+C-1 of a [step][width] tensor into shared rows of WT + 1
+// floats; zero behind `len` and behind the width
+template <typename T, int C, int WT>
+__device__ __forceinline__ void load_rows(float *dst, const T *src, int64_t stride, int width,
+                                          int64_t t0, int64_t len) {
+    for (int e = threadIdx.x; e < C * WT; e += kThreads) {
+        const int t = e / WT, n = e % WT;
+        float v = 0.f;
+        if (n < width && t0 + t < len) v = to_f<T>(src[(t0 + t) * stride + n]);
+        dst[t * (WT + 1) + n] = v;
+    }
+}
+
+struct Head {
+    int bh, b, h;
+    int64_t len;
+    const float *la;
+    __device__ __forceinline__ float log_a(const DecayParams &p, int64_t t) const {
+        return t < len ? la[t * p.la_t] : 0.f;
+    }
+};
+
+__device__ __forceinline__ Head head_of(const DecayParams &p, int64_t bh) {
+    Head hd;
+    hd.bh = (int)bh;
+    hd.b = (int)(bh / p.H);
+    hd.h = (int)(bh % p.H);
+    hd.len = decay_len(p, hd.b);
+    hd.la = p.log_a + hd.b * p.la_b + hd.h * p.la_h;
+    return hd;
+}
+
+// The state alone over one segment from zero.  Forward (REV = false): rows u
+// = b, v = x, weights e^{G_C - G_t}, chunks in order.  Reverse: u = c, v =
+// g_y, weights e^{G_t}, chunks in reverse.
+template <typename T, int C, int WT, bool REV>
+__global__ void __launch_bounds__(kThreads) k_decay_seg_gen(DecayParams p) {
+    extern __shared__ float sm[];
+    constexpr int LD = WT + 1;
+    float *su = sm, *sv = su + C * LD;
+    float2 *sG = reinterpret_cast<float2 *>(sv + C * LD + ((2 * C * LD) & 1));
+    const int seg = blockIdx.x % p.nseg;
+    const Head hd = head_of(p, blockIdx.x / p.nseg);
+    const int ty = threadIdx.x / 16, tx = threadIdx.x % 16;
+    const T *u = (const T *)(REV ? p.c : p.b) + hd.b * p.key_b + (hd.h / p.rep) * p.key_h;
+    const T *v = (const T *)(REV ? p.g_y : p.x) + hd.b * p.val_b + hd.h * p.val_h;
+    constexpr int TN = WT / 16;
+    float S[TN][TN];
+    zero(S);
+    double total = 0.0;
+    const int c0 = seg * p.seg_chunks, c1 = min(c0 + p.seg_chunks, p.nchunks);
+    for (int i = c0; i < c1; ++i) {
+        const int64_t t0 = (int64_t)(REV ? c1 - 1 - (i - c0) : i) * C;
+        if (t0 >= hd.len) continue;     // behind the end: nothing is added, nothing decays
+        load_rows<T, C, WT>(su, u, p.key_t, p.N, t0, hd.len);
+        load_rows<T, C, WT>(sv, v, p.val_t, p.P, t0, hd.len);
+        if (threadIdx.x < 32)
+            decay_sums<C>([&](int t) { return hd.log_a(p, t0 + t); }, sG, threadIdx.x);
+        __syncthreads();
+        const float2 end = sG[C - 1];
+        total += (double)end.x + (double)end.y;
+        for (int e = threadIdx.x; e < C * WT; e += kThreads) {
+            const int t = e / WT;
+            const float w = REV ? decay_from_start(sG[t]) : decay_between(end, sG[t]);
+            su[t * LD + e % WT] *= w;
+        }
+        __syncthreads();
+        const float a = decay_from_start(end);
+#pragma unroll
+        for (int m = 0; m < TN; ++m)
+#pragma unroll
+            for (int n = 0; n < TN; ++n) S[m][n] *= a;
+        tile_mm(S, C, [&](int m, int k) { return su[k * LD + ty + 16 * m]; },
+                [&](int n, int k) { return sv[k * LD + tx + 16 * n]; });
+        __syncthreads();
+    }
+    float *out = p.seg_state + ((int64_t)hd.bh * p.nseg + seg) * p.N * p.P;
+#pragma unroll
+    for (int m = 0; m < TN; ++m)
+#pragma unroll
+        for (int n = 0; n < TN; ++n) {
+            const int r = ty + 16 * m, q = tx + 16 * n;
+            if (r < p.N && q < p.P) out[r * p.P + q] = S[m][n];
+        }
+    if (threadIdx.x == 0) p.seg_decay[(int64_t)hd.bh * p.nseg + seg] = exp2f((float)total);
+}
+
+template <typename T, int C, int WT>
+__global__ void __launch_bounds__(kThreads) k_decay_fwd_gen(DecayParams p) {
+    constexpr int PS = WT < 64 ? WT : 64;
+    constexpr int LD = WT + 1, LP = PS + 1, LC = C + 1;
+    constexpr int TM = C / 16, TN = WT / 16, TP = PS / 16;
+    extern __shared__ float sm[];
+    float *sc = sm, *sb = sc + C * LD, *sx = sb + C * LD, *sS = sx + C * LP, *sP = sS + WT * LP;
+    float2 *sG = reinterpret_cast<float2 *>(sP + C * LC + ((WT * LP + C * LP + C * LC) & 1));
+    const int seg = blockIdx.x % p.nseg;
+    const int ps = (blockIdx.x / p.nseg) % p.pslices;
+    const Head hd = head_of(p, blockIdx.x / p.nseg / p.pslices);
+    const int p0 = ps * PS, pw = min(PS, p.P - p0);
+    const int ty = threadIdx.x / 16, tx = threadIdx.x % 16;
+    const int64_t koff = hd.b * p.key_b + (hd.h / p.rep) * p.key_h;
+    const int64_t voff = hd.b * p.val_b + hd.h * p.val_h + p0;
+    const T *c = (const T *)p.c + koff, *b = (const T *)p.b + koff, *x = (const T *)p.x + voff;
+    T *y = (T *)p.y + voff;
+    const int64_t np = (int64_t)p.N * p.P;
+
+    // the segment's incoming state
+    const float *in = p.nseg > 1 ? p.seg_state + ((int64_t)hd.bh * p.nseg + seg) * np
+                                 : (p.h0 ? p.h0 + (int64_t)hd.bh * np : nullptr);
+    for (int e = threadIdx.x; e < WT * PS; e += kThreads) {
+        const int n = e / PS, q = e % PS;
+        sS[n * LP + q] = (in && n < p.N && q < pw) ? in[(int64_t)n * p.P + p0 + q] : 0.f;
+    }
+    const int c0 = seg * p.seg_chunks, c1 = min(c0 + p.seg_chunks, p.nchunks);
+    for (int i = c0; i < c1; ++i) {
+        const int64_t t0 = (int64_t)i * C;
+        __syncthreads();
+        if (t0 < hd.len) {
+            load_rows<T, C, WT>(sc, c, p.key_t, p.N, t0, hd.len);
+            load_rows<T, C, WT>(sb, b, p.key_t, p.N, t0, hd.len);
+            load_rows<T, C, PS>(sx, x, p.val_t, pw, t0, hd.len);
+            if (threadIdx.x < 32)
+                decay_sums<C>([&](int t) { return hd.log_a(p, t0 + t); }, sG, threadIdx.x);
+        }
+        if (p.carry && i > 0) {
+            float *out = p.carry + ((int64_t)hd.bh * p.nchunks + i) * np + p0;
+            for (int e = threadIdx.x; e < WT * PS; e += kThreads) {
+                const int n = e / PS, q = e % PS;
+                if (n < p.N && q < pw) out[(int64_t)n * p.P + q] = sS[n * LP + q];
+            }
+        }
+        if (t0 >= hd.len) {             // behind the end: y is zero, the state stays
+            for (int e = threadIdx.x; e < C * PS; e += kThreads) {
+                const int64_t t = t0 + e / PS;
+                if (t < p.L && e % PS < pw) y[t * p.val_t + e % PS] = from_f<T>(0.f);
+            }
+            continue;
+        }
+        __syncthreads();
+        const float2 end = sG[C - 1];
+        {
+            float acc[TM][TM];
+            zero(acc);
+            tile_mm(acc, WT, [&](int m, int k) { return sc[(ty + 16 * m) * LD + k]; },
+                    [&](int n, int k) { return sb[(tx + 16 * n) * LD + k]; });
+#pragma unroll
+            for (int m = 0; m < TM; ++m)
+#pragma unroll
+                for (int n = 0; n < TM; ++n) {
+                    const int r = ty + 16 * m, q = tx + 16 * n;
+                    sP[r * LC + q] = q <= r ? acc[m][n] * decay_between(sG[r], sG[q]) : 0.f;
+                }
+        }
+        __syncthreads();
+        {
+            float acc[TM][TP];
+            zero(acc);
+            tile_mm(acc, WT, [&](int m, int k) { return sc[(ty + 16 * m) * LD + k]; },
+                    [&](int n, int k) { return sS[k * LP + tx + 16 * n]; });
+#pragma unroll
+            for (int m = 0; m < TM; ++m) {
+                const float e = decay_from_start(sG[ty + 16 * m]);
+#pragma unroll
+                for (int n = 0; n < TP; ++n) acc[m][n] *= e;
+            }
+            tile_mm(acc, C, [&](int m, int k) { return sP[(ty + 16 * m) * LC + k]; },
+                    [&](int n, int k) { return sx[k * LP + tx + 16 * n]; });
+#pragma unroll
+            for (int m = 0; m < TM; ++m) {
+                const int64_t t = t0 + ty + 16 * m;
+#pragma unroll
+                for (int n = 0; n < TP; ++n)
+                    if (t < p.L && tx + 16 * n < pw)
+                        y[t * p.val_t + tx + 16 * n] = from_f<T>(t < hd.len ? acc[m][n] : 0.f);
+            }
+        }
+        for (int e = threadIdx.x; e < C * WT; e += kThreads)
+            sb[(e / WT) * LD + e % WT] *= decay_between(end, sG[e / WT]);
+        __syncthreads();
+        {
+            float acc[TN][TP];
+            zero(acc);
+            tile_mm(acc, C, [&](int m, int k) { return sb[k * LD + ty + 16 * m]; },
+                    [&](int n, int k) { return sx[k * LP + tx + 16 * n]; });
+            const float a = decay_from_start(end);
+#pragma unroll
+            for (int m = 0; m < TN; ++m)
+#pragma unroll
+                for (int n = 0; n < TP; ++n) {
+                    float *s = &sS[(ty + 16 * m) * LP + tx + 16 * n];
+                    *s = fmaf(a, *s, acc[m][n]);
+                }
+        }
+    }
+    __syncthreads();
+    if (p.h_last && seg == p.nseg - 1) {
+        float *out = p.h_last + (int64_t)hd.bh * np + p0;
+        for (int e = threadIdx.x; e < WT * PS; e += kThreads) {
+            const int n = e / PS, q = e % PS;
+            if (n < p.N && q < pw) out[(int64_t)n * p.P + q] = sS[n * LP + q];
+        }
+    }
+}
+
+// Adjoint of one segment's chunks in reverse; sR is dl/dS at the chunk's end.
+template <typename T, int C, int WT>
+__global__ void __launch_bounds__(kThreads) k_decay_bwd_gen(DecayParams p) {
+    constexpr int LD = WT + 1, LC = C + 1, TM = C / 16, TN = WT / 16;
+    extern __shared__ float sm[];
+    float *sc = sm, *sb = sc + C * LD, *sx = sb + C * LD, *sg = sx + C * LD, *sR = sg + C * LD;
+    float *sP = sR + WT * LD, *sQ = sP + C * LC;
+    float *sfrom = sQ + C * LC, *sto = sfrom + C;       // per step: pairs' and states' sums
+    float *sred = sto + C;                              // 16 x C + 32
+    float2 *sG = reinterpret_cast<float2 *>(sred + 16 * C + 32 + ((WT * LD) & 1));
+    const int seg = blockIdx.x % p.nseg;
+    const Head hd = head_of(p, blockIdx.x / p.nseg);
+    const int ty = threadIdx.x / 16, tx = threadIdx.x % 16;
+    const int64_t koff = hd.b * p.key_b + (hd.h / p.rep) * p.key_h;
+    const int64_t voff = hd.b * p.val_b + hd.h * p.val_h;
+    const T *c = (const T *)p.c + koff, *b = (const T *)p.b + koff;
+    const T *x = (const T *)p.x + voff, *gy = (const T *)p.g_y + voff;
+    T *gx = (T *)p.g_x + voff;
+    const int64_t np = (int64_t)p.N * p.P;
+    float *gla = p.g_la + hd.b * p.gla_b + hd.h * p.gla_h;
+    // gradients of shared keys go to fp32 [B][H][L][N] partials
+    const bool part = p.rep > 1;
+    const int64_t poff = (int64_t)hd.bh * p.L * p.N;
+
+    const float *in = p.nseg > 1 ? p.seg_state + ((int64_t)hd.bh * p.nseg + seg) * np
+                                 : (p.g_hlast ? p.g_hlast + (int64_t)hd.bh * np : nullptr);
+    for (int e = threadIdx.x; e < WT * WT; e += kThreads) {
+        const int n = e / WT, q = e % WT;
+        sR[n * LD + q] = (in && n < p.N && q < p.P) ? in[(int64_t)n * p.P + q] : 0.f;
+    }
+    const int c0 = seg * p.seg_chunks, c1 = min(c0 + p.seg_chunks, p.nchunks);
+    for (int i = c1 - 1; i >= c0; --i) {
+        const int64_t t0 = (int64_t)i * C;
+        __syncthreads();
+        const bool live = t0 < hd.len;
+        if (live) {
+            load_rows<T, C, WT>(sc, c, p.key_t, p.N, t0, hd.len);
+            load_rows<T, C, WT>(sb, b, p.key_t, p.N, t0, hd.len);
+            load_rows<T, C, WT>(sx, x, p.val_t, p.P, t0, hd.len);
+            load_rows<T, C, WT>(sg, gy, p.val_t, p.P, t0, hd.len);
+            if (threadIdx.x < 32)
+                decay_sums<C>([&](int t) { return hd.log_a(p, t0 + t); }, sG, threadIdx.x);
+        } else {                        // behind the end: zero gradients, the state's stays
+            for (int e = threadIdx.x; e < C * WT; e += kThreads) {
+                const int64_t t = t0 + e / WT;
+                const int q = e % WT;
+                if (t >= p.L) continue;
+                if (q < p.P) gx[t * p.val_t + q] = from_f<T>(0.f);
+                if (q < p.N) {
+                    if (part) {
+                        ((float *)p.g_c)[poff + t * p.N + q] = 0.f;
+                        ((float *)p.g_b)[poff + t * p.N + q] = 0.f;
+                    } else {
+                        ((T *)p.g_c)[koff + t * p.key_t + q] = from_f<T>(0.f);
+                        ((T *)p.g_b)[koff + t * p.key_t + q] = from_f<T>(0.f);
+                    }
+                }
+                if (q == 0) gla[t * p.gla_t] = 0.f;
+            }
+            continue;
+        }
+        __syncthreads();
+        const float2 end = sG[C - 1];
+        const float aend = decay_from_start(end);
+        const float *S0 = i > 0 ? p.carry + ((int64_t)hd.bh * p.nchunks + i) * np
+                                : (p.h0 ? p.h0 + (int64_t)hd.bh * np : nullptr);
+        // decayed scores P and Q, and the pair products' row and column sums
+        {
+            float s[TM][TM], v[TM][TM];
+            zero(s);
+            zero(v);
+            tile_mm(s, WT, [&](int m, int k) { return sc[(ty + 16 * m) * LD + k]; },
+                    [&](int n, int k) { return sb[(tx + 16 * n) * LD + k]; });
+            tile_mm(v, WT, [&](int m, int k) { return sg[(ty + 16 * m) * LD + k]; },
+                    [&](int n, int k) { return sx[(tx + 16 * n) * LD + k]; });
+            float col[TM];
+#pragma unroll
+            for (int n = 0; n < TM; ++n) col[n] = 0.f;
+#pragma unroll
+            for (int m = 0; m < TM; ++m) {
+                float row = 0.f;
+#pragma unroll
+                for (int n = 0; n < TM; ++n) {
+                    const int r = ty + 16 * m, q = tx + 16 * n;
+                    const float d = q <= r ? decay_between(sG[r], sG[q]) : 0.f;
+                    const float pv = q <= r ? s[m][n] * d : 0.f, qv = q <= r ? v[m][n] * d : 0.f;
+                    sP[r * LC + q] = pv;
+                    sQ[r * LC + q] = qv;
+                    const float e = q < r ? pv * v[m][n] : 0.f;
+                    row += e;
+                    col[n] += e;
+                }
+                // the 16 threads of a row are half a warp
+#pragma unroll
+                for (int d = 8; d; d >>= 1) row += __shfl_xor_sync(kFull, row, d);
+                if (tx == 0) sfrom[ty + 16 * m] = row;
+            }
+#pragma unroll
+            for (int n = 0; n < TM; ++n) sred[ty * C + tx + 16 * n] = col[n];
+        }
+        __syncthreads();
+        for (int t = threadIdx.x; t < C; t += kThreads) {
+            float s = 0.f;
+            for (int r = 0; r < 16; ++r) s += sred[r * C + t];
+            sto[t] = s;                 // sum over i > t of the pairs (i, t)
+        }
+        __syncthreads();
+        // g_c: state part (kept for g_log_a), then the pairs
+        float uc[TM], vb[TM];
+        {
+            float acc[TM][TN];
+            zero(acc);
+            if (S0)
+                tile_mm(acc, p.P, [&](int m, int k) { return sg[(ty + 16 * m) * LD + k]; },
+                        [&](int n, int k) {
+                            const int r = tx + 16 * n;
+                            return r < p.N ? __ldg(S0 + (int64_t)r * p.P + k) : 0.f;
+                        });
+#pragma unroll
+            for (int m = 0; m < TM; ++m) {
+                const float e = decay_from_start(sG[ty + 16 * m]);
+                uc[m] = 0.f;
+#pragma unroll
+                for (int n = 0; n < TN; ++n) {
+                    acc[m][n] *= e;
+                    uc[m] = fmaf(acc[m][n], sc[(ty + 16 * m) * LD + tx + 16 * n], uc[m]);
+                }
+            }
+            tile_mm(acc, C, [&](int m, int k) { return sQ[(ty + 16 * m) * LC + k]; },
+                    [&](int n, int k) { return sb[k * LD + tx + 16 * n]; });
+#pragma unroll
+            for (int m = 0; m < TM; ++m) {
+                const int64_t t = t0 + ty + 16 * m;
+#pragma unroll
+                for (int n = 0; n < TN; ++n) {
+                    const int q = tx + 16 * n;
+                    if (t >= p.L || q >= p.N) continue;
+                    const float v = t < hd.len ? acc[m][n] : 0.f;
+                    if (part)
+                        ((float *)p.g_c)[poff + t * p.N + q] = v;
+                    else
+                        ((T *)p.g_c)[koff + t * p.key_t + q] = from_f<T>(v);
+                }
+            }
+        }
+        // g_b
+        {
+            float acc[TM][TN];
+            zero(acc);
+            tile_mm(acc, WT, [&](int m, int k) { return sx[(ty + 16 * m) * LD + k]; },
+                    [&](int n, int k) { return sR[(tx + 16 * n) * LD + k]; });
+#pragma unroll
+            for (int m = 0; m < TM; ++m) {
+                const float w = decay_between(end, sG[ty + 16 * m]);
+                vb[m] = 0.f;
+#pragma unroll
+                for (int n = 0; n < TN; ++n) {
+                    acc[m][n] *= w;
+                    vb[m] = fmaf(acc[m][n], sb[(ty + 16 * m) * LD + tx + 16 * n], vb[m]);
+                }
+            }
+            tile_mm(acc, C, [&](int m, int k) { return sQ[k * LC + ty + 16 * m]; },
+                    [&](int n, int k) { return sc[k * LD + tx + 16 * n]; });
+#pragma unroll
+            for (int m = 0; m < TM; ++m) {
+                const int64_t t = t0 + ty + 16 * m;
+#pragma unroll
+                for (int n = 0; n < TN; ++n) {
+                    const int q = tx + 16 * n;
+                    if (t >= p.L || q >= p.N) continue;
+                    const float v = t < hd.len ? acc[m][n] : 0.f;
+                    if (part)
+                        ((float *)p.g_b)[poff + t * p.N + q] = v;
+                    else
+                        ((T *)p.g_b)[koff + t * p.key_t + q] = from_f<T>(v);
+                }
+            }
+        }
+        // g_x
+        {
+            float acc[TM][TN];
+            zero(acc);
+            tile_mm(acc, WT, [&](int m, int k) { return sb[(ty + 16 * m) * LD + k]; },
+                    [&](int n, int k) { return sR[k * LD + tx + 16 * n]; });
+#pragma unroll
+            for (int m = 0; m < TM; ++m) {
+                const float w = decay_between(end, sG[ty + 16 * m]);
+#pragma unroll
+                for (int n = 0; n < TN; ++n) acc[m][n] *= w;
+            }
+            tile_mm(acc, C, [&](int m, int k) { return sP[k * LC + ty + 16 * m]; },
+                    [&](int n, int k) { return sg[k * LD + tx + 16 * n]; });
+#pragma unroll
+            for (int m = 0; m < TM; ++m) {
+                const int64_t t = t0 + ty + 16 * m;
+#pragma unroll
+                for (int n = 0; n < TN; ++n)
+                    if (t < p.L && tx + 16 * n < p.P)
+                        gx[t * p.val_t + tx + 16 * n] = from_f<T>(t < hd.len ? acc[m][n] : 0.f);
+            }
+        }
+        // e^{G_C} <S0, R>, the row sums u_i + R_i and v_j
+        float dot = 0.f;
+        if (S0)
+            for (int e = threadIdx.x; e < p.N * p.P; e += kThreads)
+                dot = fmaf(__ldg(S0 + e), sR[(e / p.P) * LD + e % p.P], dot);
+#pragma unroll
+        for (int d = 16; d; d >>= 1) dot += __shfl_xor_sync(kFull, dot, d);
+#pragma unroll
+        for (int m = 0; m < TM; ++m)
+#pragma unroll
+            for (int d = 8; d; d >>= 1) {
+                uc[m] += __shfl_xor_sync(kFull, uc[m], d);
+                vb[m] += __shfl_xor_sync(kFull, vb[m], d);
+            }
+        __syncthreads();                // sR and the column sums have been read
+        if (threadIdx.x % 32 == 0) sred[16 * C + threadIdx.x / 32] = dot;
+        if (tx == 0)
+#pragma unroll
+            for (int m = 0; m < TM; ++m) {
+                sred[ty + 16 * m] = uc[m];
+                sred[C + ty + 16 * m] = vb[m];
+            }
+        for (int e = threadIdx.x; e < C * WT; e += kThreads)
+            sc[(e / WT) * LD + e % WT] *= decay_from_start(sG[e / WT]);
+        __syncthreads();
+        if (threadIdx.x < 32) {
+            // g_log_a[t] = sum_{i>=t} (row_i + u_i - col_i) + sum_{j<t} v_j + e^{G_C} <S0, R>
+            const int lane = threadIdx.x;
+            double through = 0.0;
+            for (int w = 0; w < kThreads / 32; ++w) through += (double)sred[16 * C + w];
+            through *= (double)aend;
+            double before = 0.0, total = 0.0;
+            double inc[C / 32], pre[C / 32];
+#pragma unroll
+            for (int q = 0; q < C / 32; ++q) {
+                const int t = q * 32 + lane;
+                double a = (double)sfrom[t] + (double)sred[t] - (double)sto[t];
+                double v = (double)sred[C + t];
+                const double a0 = a, v0 = v;
+#pragma unroll
+                for (int d = 1; d < 32; d *= 2) {
+                    const double oa = shfl_up_d(a, d), ov = shfl_up_d(v, d);
+                    if (lane >= d) {
+                        a += oa;
+                        v += ov;
+                    }
+                }
+                inc[q] = total + a - a0;        // sum over i < t
+                pre[q] = before + v - v0;
+                total += __shfl_sync(kFull, a, 31);
+                before += __shfl_sync(kFull, v, 31);
+            }
+#pragma unroll
+            for (int q = 0; q < C / 32; ++q) {
+                const int64_t t = t0 + q * 32 + lane;
+                if (t < p.L)
+                    // a floored decay is a constant: its gradient is zero, and
+                    // not what rounding leaves of the cancelled pairs
+                    gla[t * p.gla_t] = t < hd.len && !(hd.log_a(p, t) <= (float)kDecayFloor)
+                                           ? (float)(total - inc[q] + pre[q] + through)
+                                           : 0.f;
+            }
+        }
+        {
+            float acc[TN][TN];
+            zero(acc);
+            tile_mm(acc, C, [&](int m, int k) { return sc[k * LD + ty + 16 * m]; },
+                    [&](int n, int k) { return sg[k * LD + tx + 16 * n]; });
+#pragma unroll
+            for (int m = 0; m < TN; ++m)
+#pragma unroll
+                for (int n = 0; n < TN; ++n) {
+                    float *s = &sR[(ty + 16 * m) * LD + tx + 16 * n];
+                    *s = fmaf(aend, *s, acc[m][n]);
+                }
+        }
+    }
+    __syncthreads();
+    if (p.g_h0 && seg == 0) {
+        float *out = p.g_h0 + (int64_t)hd.bh * np;
+        for (int e = threadIdx.x; e < WT * WT; e += kThreads) {
+            const int n = e / WT, q = e % WT;
+            if (n < p.N && q < p.P) out[(int64_t)n * p.P + q] = sR[n * LD + q];
+        }
+    }
+}
+
+// Joins the segments: seg_state[s] becomes the state that enters segment s
+// (from its left, or, reversed, its right), starting from `first`.
+__global__ void k_decay_join(DecayParams p, const float *first, int reverse, float *last) {
+    const int64_t np = (int64_t)p.N * p.P;
+    const int64_t e = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
+    if (e >= (int64_t)p.B * p.H * np) return;
+    const int64_t bh = e / np, i = e % np;
+    float s = first ? first[e] : 0.f;
+    for (int q = 0; q < p.nseg; ++q) {
+        const int seg = reverse ? p.nseg - 1 - q : q;
+        float *at = p.seg_state + (bh * p.nseg + seg) * np + i;
+        const float loc = *at;
+        *at = s;
+        s = fmaf(p.seg_decay[bh * p.nseg + seg], s, loc);
+    }
+    if (last) last[e] = s;
+}
+
+// g_c, g_b of shared keys: the sum over their heads, in head order.
+template <typename T>
+__global__ void k_decay_sum_heads(DecayParams p, const float *part_c, const float *part_b, T *g_c,
+                                  T *g_b) {
+    const int64_t n = (int64_t)p.B * p.G * p.L * p.N;
+    for (int64_t e = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; e < n;
+         e += (int64_t)gridDim.x * blockDim.x) {
+        const int64_t j = e % p.N, t = e / p.N % p.L, g = e / p.N / p.L % p.G,
+                      b = e / p.N / p.L / p.G;
+        const int64_t from = ((b * p.H + g * p.rep) * p.L + t) * p.N + j;
+        float sc = 0.f, sb = 0.f;
+        for (int r = 0; r < p.rep; ++r) {
+            sc += part_c[from + (int64_t)r * p.L * p.N];
+            sb += part_b[from + (int64_t)r * p.L * p.N];
+        }
+        const int64_t to = b * p.key_b + g * p.key_h + t * p.key_t + j;
+        g_c[to] = from_f<T>(sc);
+        g_b[to] = from_f<T>(sb);
+    }
+}
+
+// g_log_a of a per-head decay: the sum over (b, t), one CTA per head, in fp64
+// (steps of opposite sign cancel over a long sequence).
+__global__ void __launch_bounds__(1024) k_decay_sum_steps(DecayParams p, const float *part,
+                                                          float *g_log_a) {
+    __shared__ double red[32];
+    const int h = blockIdx.x;
+    double s = 0.0;
+    for (int64_t e = threadIdx.x; e < (int64_t)p.B * p.L; e += blockDim.x)
+        s += (double)part[((e / p.L) * p.H + h) * p.L + e % p.L];
+#pragma unroll
+    for (int d = 16; d; d >>= 1) s += __shfl_xor_sync(kFull, s, d);
+    if (threadIdx.x % 32 == 0) red[threadIdx.x / 32] = s;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        double t = 0.0;
+        for (int w = 0; w < (int)blockDim.x / 32; ++w) t += red[w];
+        g_log_a[h] = (float)t;
+    }
+}
+
+template <typename K>
+cudaError_t launch(K kern, int64_t grid, size_t smem, cudaStream_t st, const DecayParams &p) {
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         (int)smem);
+    if (e != cudaSuccess) return e;
+    kern<<<dim3((unsigned)grid), kThreads, smem, st>>>(p);
+    return cudaGetLastError();
+}
+
+template <typename T, int C, int WT, bool REV>
+cudaError_t seg_gen(const DecayParams &p, cudaStream_t st) {
+    const size_t smem = (size_t)(2 * C * (WT + 1) + 1 + 2 * C) * 4;
+    return launch(k_decay_seg_gen<T, C, WT, REV>, (int64_t)p.B * p.H * p.nseg, smem, st, p);
+}
+
+template <typename T, int C, int WT>
+cudaError_t fwd_gen(const DecayParams &p, cudaStream_t st) {
+    constexpr int PS = WT < 64 ? WT : 64;
+    if (p.nseg > 1) {
+        cudaError_t e = seg_gen<T, C, WT, false>(p, st);
+        if (e != cudaSuccess) return e;
+        e = launch_decay_join(p, p.h0, false, nullptr, st);
+        if (e != cudaSuccess) return e;
+    }
+    const size_t smem = (size_t)(2 * C * (WT + 1) + (C + WT) * (PS + 1) + C * (C + 1) + 1 + 2 * C) * 4;
+    return launch(k_decay_fwd_gen<T, C, WT>, (int64_t)p.B * p.H * p.nseg * p.pslices, smem, st, p);
+}
+
+template <typename T, int C, int WT>
+cudaError_t bwd_gen(const DecayParams &p, cudaStream_t st) {
+    if (p.nseg > 1) {
+        cudaError_t e = seg_gen<T, C, WT, true>(p, st);
+        if (e != cudaSuccess) return e;
+        e = launch_decay_join(p, p.g_hlast, true, nullptr, st);
+        if (e != cudaSuccess) return e;
+    }
+    const size_t smem = (size_t)((4 * C + WT) * (WT + 1) + 2 * C * (C + 1) + 2 * C + 16 * C + 32 +
+                                 1 + 2 * C) * 4;
+    return launch(k_decay_bwd_gen<T, C, WT>, (int64_t)p.B * p.H * p.nseg, smem, st, p);
+}
+
+}  // namespace
+
+cudaError_t launch_decay_join(const DecayParams &p, const float *first, bool reverse, float *last,
+                              cudaStream_t st) {
+    const int64_t n = (int64_t)p.B * p.H * p.N * p.P;
+    k_decay_join<<<dim3((unsigned)((n + 127) / 128)), 128, 0, st>>>(p, first, reverse ? 1 : 0, last);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_decay_sum_heads(const DecayParams &p, pdssm_dtype dt, const float *part_c,
+                                   const float *part_b, void *g_c, void *g_b, cudaStream_t st) {
+    const int64_t n = (int64_t)p.B * p.G * p.L * p.N;
+    const unsigned grid = (unsigned)imin64((n + 255) / 256, (int64_t)kDecaySMs * 16);
+    if (dt == PDSSM_BF16)
+        k_decay_sum_heads<__nv_bfloat16><<<grid, 256, 0, st>>>(
+            p, part_c, part_b, (__nv_bfloat16 *)g_c, (__nv_bfloat16 *)g_b);
+    else
+        k_decay_sum_heads<float><<<grid, 256, 0, st>>>(p, part_c, part_b, (float *)g_c,
+                                                       (float *)g_b);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_decay_sum_steps(const DecayParams &p, const float *part, float *g_log_a,
+                                   cudaStream_t st) {
+    k_decay_sum_steps<<<p.H, 1024, 0, st>>>(p, part, g_log_a);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_decay_fwd_gen(const DecayParams &p, pdssm_dtype dt, cudaStream_t st) {
+    const int w = p.N > p.P ? p.N : p.P;
+    if (dt == PDSSM_BF16) {
+        if (w <= 32) return fwd_gen<__nv_bfloat16, 64, 32>(p, st);
+        if (w <= 64) return fwd_gen<__nv_bfloat16, 64, 64>(p, st);
+        return fwd_gen<__nv_bfloat16, 32, 128>(p, st);
+    }
+    if (w <= 32) return fwd_gen<float, 32, 32>(p, st);
+    if (w <= 64) return fwd_gen<float, 32, 64>(p, st);
+    return fwd_gen<float, 32, 128>(p, st);
+}
+
+cudaError_t launch_decay_bwd_gen(const DecayParams &p, pdssm_dtype dt, cudaStream_t st) {
+    const int w = p.N > p.P ? p.N : p.P;
+    if (dt == PDSSM_BF16) {
+        if (w <= 32) return bwd_gen<__nv_bfloat16, 64, 32>(p, st);
+        if (w <= 64) return bwd_gen<__nv_bfloat16, 64, 64>(p, st);
+        return bwd_gen<__nv_bfloat16, 32, 128>(p, st);
+    }
+    if (w <= 32) return bwd_gen<float, 32, 32>(p, st);
+    if (w <= 64) return bwd_gen<float, 32, 64>(p, st);
+    return bwd_gen<float, 32, 128>(p, st);
+}
+
+}  // namespace pdssm

@@ -1,0 +1,371 @@
+"""GPU checks of the decay scan (linear attention with a decay for each head):
+forward, adjoint and single step against a step-by-step 64-bit implementation,
+with counted error bounds (tests/block_ref.py)."""
+import math
+
+import pytest
+import torch
+
+import block_ref as ref
+import structured_sparse_state_b200 as pd
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(autouse=True, scope="module")
+def _need_gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("needs a CUDA device")
+
+
+BF, F32 = torch.bfloat16, torch.float32
+
+# dtype, B, H, G, L, N, P, layout, decay, h0, ragged
+CASES = [
+    (F32, 1, 1, 1, 1, 1, 1, "bhl", "step", True, False),
+    (F32, 2, 3, 3, 31, 12, 20, "bhl", "head", False, False),
+    (F32, 2, 2, 1, 32, 32, 32, "blh", "step", True, False),
+    (F32, 3, 4, 2, 33, 33, 17, "blh", "step", True, True),
+    (F32, 1, 2, 2, 700, 64, 48, "bhl", "step", True, False),
+    (F32, 2, 2, 2, 130, 128, 100, "bhl", "head", True, True),
+    (F32, 1, 1, 1, 1500, 16, 128, "blh", "step", False, False),
+    (BF, 1, 1, 1, 1, 64, 64, "bhl", "step", True, False),
+    (BF, 2, 3, 3, 63, 64, 64, "bhl", "step", True, False),
+    (BF, 2, 2, 2, 64, 32, 64, "blh", "head", False, False),
+    (BF, 2, 4, 1, 65, 64, 32, "blh", "step", True, True),
+    (BF, 1, 2, 2, 1100, 64, 64, "bhl", "step", True, False),
+    (BF, 3, 2, 2, 257, 31, 63, "bhl", "step", True, True),
+    (BF, 1, 4, 2, 300, 128, 64, "blh", "step", True, False),
+    (BF, 2, 2, 2, 200, 64, 128, "bhl", "head", True, True),
+    (BF, 1, 2, 1, 513, 128, 128, "bhl", "step", False, False),
+    (BF, 1, 1, 1, 3000, 48, 40, "bhl", "step", True, False),
+]
+
+
+def make(dtype, B, H, G, L, N, P, layout, decay, h0, ragged, seed=0):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+
+    def normal(*s, dtype=F32, by=1.0):
+        return (torch.randn(*s, generator=g, device="cuda") * by).to(dtype)
+
+    keys, vals, gate = ((B, G, L, N), (B, H, L, P), (B, H, L)) if layout == "bhl" else \
+        ((B, L, G, N), (B, L, H, P), (B, L, H))
+    t = dict(c=normal(*keys, dtype=dtype), b=normal(*keys, dtype=dtype, by=N ** -0.5),
+             x=normal(*vals, dtype=dtype))
+    if decay == "head":
+        t["log_a"] = -torch.rand(H, generator=g, device="cuda") * 0.3
+    else:
+        t["log_a"] = -torch.nn.functional.softplus(normal(*gate) - 3.0)
+    t["h0"] = normal(B, H, N, P) if h0 else None
+    t["lengths"] = None
+    if ragged:
+        n = torch.randint(0, L + 1, (B,), generator=g, device="cuda", dtype=torch.int32)
+        n[-1] = 0
+        t["lengths"] = n
+    t["g_y"] = normal(*vals, dtype=dtype)
+    t["g_hlast"] = normal(B, H, N, P) if h0 else None
+    return t
+
+
+def within(name, got, want, bound):
+    err = (got.double() - want).abs()
+    assert torch.isfinite(got).all(), name
+    worst = (err - bound).max().item() if err.numel() else 0.0
+    assert worst <= 0, f"{name}: off by {err.max().item():.3g}, {worst:.3g} more than counted"
+
+
+def check_all(t, got, layout, names):
+    args = (t["c"], t["b"], t["x"], t["log_a"], t["h0"], t["lengths"], layout)
+    grads = "g_c" in names
+    extra = (t["g_y"], t["g_hlast"]) if grads else (None, None)
+    want = ref.decay_scan(*args, *extra)
+    mag = ref.decay_scan(*args, *extra, magnitudes=True)
+    N, P = t["c"].shape[-1], t["x"].shape[-1]
+    L = t["x"].shape[2 if layout == "bhl" else 1]
+    # bf16: a score or a state is rounded on the way to an output, and the
+    # decayed weights of a score at most once more
+    bound = ref.decay_bounds(t["x"].dtype, N, P, L, mag, 2)
+    for name in names:
+        b = bound[name]
+        if isinstance(b, tuple):
+            m, whole, tol = b
+            w = whole[:, :, None] if layout == "bhl" else whole[:, None, :]
+            b = tol * m + w + 1e-37
+        within(name, got[name], want[name], b)
+
+
+def fwd_bwd(t, layout):
+    y, h_last, ws = pd.pdssm_decay_scan_fwd(t["c"], t["b"], t["x"], t["log_a"], t["h0"],
+                                            lengths=t["lengths"], layout=layout, for_bwd=True)
+    g = pd.pdssm_decay_scan_bwd(t["c"], t["b"], t["x"], t["log_a"], t["h0"], t["g_y"], ws,
+                                g_hlast=t["g_hlast"], lengths=t["lengths"], layout=layout)
+    return dict(y=y, h_last=h_last, g_c=g[0], g_b=g[1], g_x=g[2], g_log_a=g[3], g_h0=g[4])
+
+
+@pytest.mark.parametrize("case", CASES, ids=lambda c: "-".join(str(v).replace("torch.", "") for v in c))
+def test_forward(case):
+    t = make(*case)
+    y, h_last, _ = pd.pdssm_decay_scan_fwd(t["c"], t["b"], t["x"], t["log_a"], t["h0"],
+                                           lengths=t["lengths"], layout=case[7])
+    check_all(t, dict(y=y, h_last=h_last), case[7], ("y", "h_last"))
+
+
+@pytest.mark.parametrize("case", CASES, ids=lambda c: "-".join(str(v).replace("torch.", "") for v in c))
+def test_forward_and_adjoint(case):
+    t = make(*case, seed=1)
+    check_all(t, fwd_bwd(t, case[7]), case[7],
+              ("y", "h_last", "g_c", "g_b", "g_x", "g_log_a", "g_h0"))
+
+
+@pytest.mark.parametrize("dtype", [F32, BF])
+def test_adjoint_against_differences(dtype):
+    """<g, dx> against (f(x + dx) - f(x - dx)) / 2 in 64 bits on a direction of
+    the inputs: the adjoint is that of the definition, not only of the
+    reference's formulas."""
+    case = (dtype, 1, 2, 1, 97, 24, 40, "bhl", "step", True, False)
+    t = make(*case, seed=2)
+    got = fwd_bwd(t, "bhl")
+    g = torch.Generator(device="cuda").manual_seed(5)
+    names = ("c", "b", "x", "log_a", "h0")
+    d = {n: torch.randn(t[n].shape, generator=g, device="cuda", dtype=torch.float64) for n in names}
+
+    def loss(h):
+        v = {n: t[n].double() + h * d[n] for n in names}
+        o = ref.decay_scan(v["c"], v["b"], v["x"], v["log_a"], v["h0"], None, "bhl")
+        return ((o["y"] * t["g_y"].double()).sum() + (o["h_last"] * t["g_hlast"].double()).sum()).item()
+
+    h = 1e-5
+    numeric = (loss(h) - loss(-h)) / (2 * h)
+    mags = {n: (got["g_" + n].double().abs() * d[n].abs()).sum().item() for n in names}
+    analytic = sum((got["g_" + n].double() * d[n]).sum().item() for n in names)
+    # each gradient element within its counted bound; here their sum
+    tol = (3 * ref.UBF if dtype == BF else 0) + 400 * ref.U32
+    assert abs(analytic - numeric) <= tol * sum(mags.values()) + 1e-6 * abs(numeric)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF])
+def test_minus_infinity_separates_packed_sequences(dtype):
+    """Sequences packed one behind another with log_a = -inf at each first
+    step give what they give alone, forward and backward."""
+    cuts = [0, 1, 40, 104, 168, 230]
+    t = make(dtype, 1, 2, 2, cuts[-1], 32, 32, "bhl", "step", False, False, seed=3)
+    t["log_a"][:, :, cuts[:-1]] = -math.inf
+    got = fwd_bwd(t, "bhl")
+    for lo, hi in zip(cuts, cuts[1:]):
+        part = {n: (v[:, :, lo:hi].contiguous() if v is not None and n != "h0" and v.dim() >= 3 else None)
+                for n, v in t.items()}
+        part["h0"] = part["g_hlast"] = part["lengths"] = None
+        want = ref.decay_scan(part["c"], part["b"], part["x"], part["log_a"], None, None, "bhl", part["g_y"])
+        mag = ref.decay_scan(part["c"], part["b"], part["x"], part["log_a"], None, None, "bhl", part["g_y"],
+                             magnitudes=True)
+        bound = ref.decay_bounds(dtype, 32, 32, cuts[-1], mag, 2)
+        for n in ("y", "g_c", "g_b", "g_x"):
+            within(n, got[n][:, :, lo:hi], want[n], bound[n])
+    assert (got["g_log_a"][:, :, cuts[:-1]] == 0).all()
+
+
+@pytest.mark.parametrize("dtype", [F32, BF])
+def test_strong_and_absent_decay(dtype):
+    t = make(dtype, 1, 3, 3, 200, 16, 16, "bhl", "step", True, False, seed=4)
+    t["log_a"][:, 0] = 0.0                  # a = 1: plain linear attention
+    t["log_a"][:, 1] = -150.0               # each step forgets what went before
+    t["log_a"][:, 2] = -9.0
+    check_all(t, fwd_bwd(t, "bhl"), "bhl", ("y", "h_last", "g_c", "g_b", "g_x", "g_log_a", "g_h0"))
+
+
+@pytest.mark.parametrize("dtype", [F32, BF])
+@pytest.mark.parametrize("layout", ["bhl", "blh"])
+def test_nothing_behind_a_length_is_read(dtype, layout):
+    t = make(dtype, 3, 2, 2, 150, 64, 64, layout, "step", True, False, seed=5)
+    t["lengths"] = torch.tensor([0, 64, 101], dtype=torch.int32, device="cuda")
+    clean = fwd_bwd(t, layout)
+    axis = 2 if layout == "bhl" else 1
+    behind = torch.arange(150, device="cuda") >= t["lengths"][:, None]
+    for n in ("c", "b", "x", "g_y", "log_a"):
+        v = t[n]
+        m = behind[:, None] if axis == 2 else behind[:, :, None]
+        m = m[..., None] if v.dim() == 4 else m
+        t[n] = torch.where(m, torch.full((), math.nan, dtype=v.dtype, device="cuda"), v).contiguous()
+    got = fwd_bwd(t, layout)
+    for n in clean:
+        assert torch.equal(got[n], clean[n]), n
+    y = got["y"] if layout == "bhl" else got["y"].transpose(1, 2)
+    assert (y[0] == 0).all() and (y[1, :, 64:] == 0).all() and (y[2, :, 101:] == 0).all()
+    assert torch.equal(got["h_last"][0], t["h0"][0])
+    # lengths beyond L count as L, negative ones as 0
+    t2 = make(dtype, 2, 2, 2, 70, 32, 32, layout, "step", True, False, seed=6)
+    t2["lengths"] = torch.tensor([1000, -5], dtype=torch.int32, device="cuda")
+    a = fwd_bwd(t2, layout)
+    t2["lengths"] = torch.tensor([70, 0], dtype=torch.int32, device="cuda")
+    b = fwd_bwd(t2, layout)
+    for n in a:
+        assert torch.equal(a[n], b[n]), n
+
+
+def test_no_steps():
+    for layout in ("bhl", "blh"):
+        t = make(F32, 2, 2, 1, 0, 8, 8, layout, "head", True, False)
+        got = fwd_bwd(t, layout)
+        assert torch.equal(got["h_last"], t["h0"]) and torch.equal(got["g_h0"], t["g_hlast"])
+        assert (got["g_log_a"] == 0).all() and got["y"].numel() == 0
+    y, h_last, _ = pd.pdssm_decay_scan_fwd(t["c"], t["b"], t["x"], t["log_a"], layout=layout)
+    assert (h_last == 0).all()
+
+
+@pytest.mark.parametrize("dtype", [F32, BF])
+def test_same_bits_again_and_on_other_streams_and_graphs(dtype):
+    t = make(dtype, 2, 4, 2, 700, 64, 64, "blh", "head", True, False, seed=7)
+    first = fwd_bwd(t, "blh")
+    again = fwd_bwd(t, "blh")
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        other = fwd_bwd(t, "blh")
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        held = fwd_bwd(t, "blh")
+    for v in held.values():
+        v.fill_(0)
+    graph.replay()
+    graph.replay()
+    torch.cuda.synchronize()
+    for n in first:
+        assert torch.equal(first[n], again[n]), n
+        assert torch.equal(first[n], other[n]), n
+        assert torch.equal(first[n], held[n]), n
+
+
+def test_the_adjoint_may_run_twice_on_one_workspace():
+    t = make(BF, 1, 2, 2, 900, 64, 64, "bhl", "step", True, False, seed=8)
+    y, h_last, ws = pd.pdssm_decay_scan_fwd(t["c"], t["b"], t["x"], t["log_a"], t["h0"], for_bwd=True)
+    a = pd.pdssm_decay_scan_bwd(t["c"], t["b"], t["x"], t["log_a"], t["h0"], t["g_y"], ws)
+    b = pd.pdssm_decay_scan_bwd(t["c"], t["b"], t["x"], t["log_a"], t["h0"], t["g_y"], ws)
+    for u, v in zip(a, b):
+        assert torch.equal(u, v)
+
+
+def test_a_given_stream_owns_the_call():
+    t = make(BF, 1, 2, 2, 300, 64, 64, "bhl", "step", True, False, seed=9)
+    want = fwd_bwd(t, "bhl")["y"]
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    y, _, _ = pd.pdssm_decay_scan_fwd(t["c"], t["b"], t["x"], t["log_a"], t["h0"], stream=side)
+    side.synchronize()
+    assert torch.equal(y, want)
+
+
+@pytest.mark.parametrize("offset", [1, 2, 3])
+def test_pointers_off_the_16_byte_grid(offset):
+    """Contiguous tensors that start inside a storage."""
+    t = make(BF, 1, 2, 2, 130, 64, 64, "bhl", "step", True, False, seed=10)
+    want = fwd_bwd(t, "bhl")
+    for n in ("c", "b", "x", "g_y"):
+        room = torch.empty(t[n].numel() + 8, dtype=BF, device="cuda")
+        v = room[offset:offset + t[n].numel()].view(t[n].shape)
+        v.copy_(t[n])
+        t[n] = v
+    got = fwd_bwd(t, "bhl")
+    for n in want:
+        assert torch.equal(got[n], want[n]), n
+
+
+# ----------------------------------------------------------------------------
+# single tokens
+# ----------------------------------------------------------------------------
+STEPS = [
+    # dtype, B, S, H, G, N, P, decay
+    (F32, 1, 1, 1, 1, 1, 1, "step"),
+    (F32, 3, 5, 4, 2, 12, 20, "head"),
+    (BF, 7, 9, 3, 1, 64, 64, "step"),
+    (BF, 130, 140, 2, 2, 32, 63, "step"),
+    (BF, 2, 2, 2, 2, 128, 128, "head"),
+    (F32, 4, 4, 2, 2, 100, 7, "step"),
+]
+
+
+def make_step(dtype, B, S, H, G, N, P, decay, seed=0):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    r = lambda *s: torch.randn(*s, generator=g, device="cuda")  # noqa: E731
+    la = -torch.rand(*((B, H) if decay == "step" else (H,)), generator=g, device="cuda")
+    slots = torch.randperm(S, generator=g, device="cuda")[:B].to(torch.int32)
+    return dict(c=r(B, G, N).to(dtype), b=r(B, G, N).to(dtype), x=r(B, H, P).to(dtype), log_a=la,
+                state=r(S, H, N, P), slots=slots)
+
+
+def step_ref(t, magnitudes=False):
+    f = torch.abs if magnitudes else (lambda v: v)
+    B, H, P = t["x"].shape
+    rep = H // t["c"].shape[1]
+    state = f(t["state"].double()).clone()
+    y = torch.zeros(B, H, P, dtype=torch.float64, device="cuda")
+    a = t["log_a"].double().exp().expand(B, H)
+    seen = set()
+    for r, s in enumerate(t["slots"].tolist()):
+        if not 0 <= s < state.shape[0] or s in seen:
+            continue
+        seen.add(s)
+        b, c = (f(t[n][r].double()).repeat_interleave(rep, 0) for n in ("b", "c"))
+        state[s] = a[r, :, None, None] * state[s] + b[..., None] * f(t["x"][r].double())[:, None, :]
+        y[r] = (c[..., None] * state[s]).sum(1)
+    return y, state
+
+
+@pytest.mark.parametrize("case", STEPS, ids=lambda c: "-".join(str(v).replace("torch.", "") for v in c))
+@pytest.mark.parametrize("empty", [False, True])
+def test_step(case, empty):
+    t = make_step(*case)
+    if empty:
+        t["slots"][0] = -1
+        t["slots"][-1] = t["state"].shape[0]
+        if len(t["slots"]) > 3:
+            t["slots"][2] = t["slots"][1]           # the earlier row has it
+    want_y, want_s = step_ref(t)
+    mag_y, mag_s = step_ref(t, True)
+    y = pd.pdssm_decay_step(t["c"], t["b"], t["x"], t["log_a"], t["state"], t["slots"])
+    # a state element: two products, an addition, the decay; y: N additions
+    within("state", t["state"], want_s, 8 * ref.U32 * mag_s)
+    within("y", y, want_y, ((case[5] + 16) * ref.U32 + ref.unit(case[0])) * mag_y)
+
+
+def test_step_without_slots_and_in_a_graph():
+    t = make_step(BF, 6, 8, 4, 2, 64, 64, "step")
+    t["slots"] = torch.arange(6, dtype=torch.int32, device="cuda")
+    start = t["state"].clone()
+    y0 = pd.pdssm_decay_step(t["c"], t["b"], t["x"], t["log_a"], t["state"], t["slots"])
+    after = t["state"].clone()
+    t["state"].copy_(start)
+    y1 = pd.pdssm_decay_step(t["c"], t["b"], t["x"], t["log_a"], t["state"])
+    assert torch.equal(y0, y1) and torch.equal(after, t["state"])
+    assert torch.equal(after[6:], start[6:])
+    t["state"].copy_(start)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        y2 = pd.pdssm_decay_step(t["c"], t["b"], t["x"], t["log_a"], t["state"])
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(y0, y2) and torch.equal(after, t["state"])
+
+
+def test_step_resets_on_minus_infinity():
+    t = make_step(F32, 2, 2, 2, 2, 16, 16, "step")
+    t["log_a"][:] = -math.inf
+    t["slots"] = torch.arange(2, dtype=torch.int32, device="cuda")
+    pd.pdssm_decay_step(t["c"], t["b"], t["x"], t["log_a"], t["state"])
+    assert torch.equal(t["state"], t["b"][..., None] * t["x"][:, :, None, :])
+
+
+@pytest.mark.parametrize("dtype", [F32, BF])
+def test_steps_continue_a_prompt(dtype):
+    """A prompt by the scan, then tokens by the step: what the scan gives for
+    the whole."""
+    L, cut = 90, 77
+    t = make(dtype, 2, 4, 2, L, 64, 48, "blh", "step", True, False, seed=11)
+    head = lambda v: v[:, :cut].contiguous()  # noqa: E731
+    y, state, _ = pd.pdssm_decay_scan_fwd(head(t["c"]), head(t["b"]), head(t["x"]), head(t["log_a"]),
+                                          t["h0"], layout="blh")
+    ys = [y]
+    for i in range(cut, L):
+        at = lambda v: v[:, i].contiguous()  # noqa: E731
+        ys.append(pd.pdssm_decay_step(at(t["c"]), at(t["b"]), at(t["x"]), at(t["log_a"]), state)[:, None])
+    check_all(t, dict(y=torch.cat(ys, 1), h_last=state), "blh", ("y", "h_last"))
