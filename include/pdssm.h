@@ -506,7 +506,8 @@ typedef enum pdssm_layout { PDSSM_BHL = 0, PDSSM_BLH = 1 } pdssm_layout;
  *  * Limits: 1 <= N, P <= 128; B, H, G >= 1, H a multiple of G, L >= 0.
  *  * for_bwd = 1 also leaves in ws the state at every chunk's start, which
  *    pdssm_decay_scan_bwd needs.  ws: pdssm_decay_workspace_bytes(dims,
- *    dtype, for_bwd) bytes, 256-byte aligned, overwritten.
+ *    dtype, for_bwd) bytes, 256-byte aligned, overwritten; pdssm_ws_status
+ *    reads its status word.
  * Deterministic: every sum in a fixed order.
  */
 size_t pdssm_decay_workspace_bytes(const pdssm_decay_dims *dims,

@@ -47,7 +47,7 @@ struct DecayParams {
     float *seg_decay;                   // [B*H][nseg]
     float *carry;                       // [B*H][nchunks][N][P]: state at every chunk's start
     int nseg, seg_chunks, nchunks, pslices;
-    int vec;                            // rows and pointers allow 16-byte copies
+    int vec;                            // rows and pointers allow 16-byte (2: 32-byte) accesses
 };
 
 // One step's log decay in base 2, floored (a NaN passes).
@@ -114,13 +114,20 @@ cudaError_t launch_decay_sum_steps(const DecayParams &p, const float *part, floa
                                    cudaStream_t st);
 cudaError_t launch_decay_fwd_gen(const DecayParams &p, pdssm_dtype dt, cudaStream_t st);
 cudaError_t launch_decay_bwd_gen(const DecayParams &p, pdssm_dtype dt, cudaStream_t st);
+cudaError_t launch_decay_fwd_tc(const DecayParams &p, int *status, cudaStream_t st);
+cudaError_t launch_decay_seg_rev_tc(const DecayParams &p, int *status, cudaStream_t st);
+cudaError_t launch_decay_bwd_mma(const DecayParams &p, int *status, cudaStream_t st);
+bool decay_tc_copies();                 // the driver's tensor maps are at hand
 cudaError_t launch_decay_step(const DecayParams &p, pdssm_dtype dt, float *state, int64_t n_slots,
                               const int32_t *slots, cudaStream_t st);
+
+// Kernels of a call: the CUDA cores (any size), or the tensor cores.
+enum DecayPath { kDecayGen, kDecayTc };
 
 // Chunk and segments of one direction, from the sizes alone.
 struct DecayPlan {
     int chunk, nchunks, nseg, seg_chunks, pslices;
 };
-DecayPlan decay_plan(const pdssm_decay_dims &d, pdssm_dtype dt, bool bwd);
+DecayPlan decay_plan(const pdssm_decay_dims &d, DecayPath path, bool bf16, bool adjoint);
 
 }  // namespace pdssm

@@ -1,26 +1,32 @@
 // C ABI of the decay scan: argument checks, workspace, launch sequence.
 #include <string.h>
 
+#include <initializer_list>
+
 #include "decay.cuh"
 
 using namespace pdssm;
 
 namespace pdssm {
 
-DecayPlan decay_plan(const pdssm_decay_dims &d, pdssm_dtype dt, bool bwd) {
+// Chunks and segments from the sizes alone, so that workspace sizes follow.
+// Segments fill the GPU when the (batch, head, 64 columns) units do not: one
+// CTA of the tensor-core forward fits an SM, two of its adjoint, about three
+// of the others.  Each segment costs a second read of b and x (the adjoint: of
+// c and g_y), so it has at least four chunks.
+DecayPlan decay_plan(const pdssm_decay_dims &d, DecayPath path, bool bf16, bool adjoint) {
     DecayPlan pl{};
+    const bool tc = path == kDecayTc;
     const int w = (int)(d.N > d.P ? d.N : d.P);
-    pl.chunk = dt == PDSSM_BF16 && w <= 64 ? 64 : 32;
+    pl.chunk = tc ? (adjoint ? 64 : 128) : (bf16 && w <= 64 ? 64 : 32);
     pl.nchunks = (int)((d.L + pl.chunk - 1) / pl.chunk);
-    pl.pslices = bwd ? 1 : (int)((d.P + 63) / 64);
-    // About three CTAs fit an SM.  Segments fill the GPU when the heads alone
-    // do not; each costs the forward a second read of b and x (the adjoint
-    // one of c and g_y), so a segment has at least four chunks.
+    pl.pslices = adjoint ? 1 : (int)((d.P + 63) / 64);
     const int64_t units = d.B * d.H * pl.pslices;
-    int64_t nseg = (int64_t)kDecaySMs * 3 / units;
+    int64_t nseg = (int64_t)kDecaySMs * (tc ? (adjoint ? 2 : 1) : 3) / units;
     if (nseg > pl.nchunks / 4) nseg = pl.nchunks / 4;
     if (nseg < 1) nseg = 1;
     pl.seg_chunks = (int)((pl.nchunks + nseg - 1) / nseg);
+    if (tc && adjoint) pl.seg_chunks = (pl.seg_chunks + 1) / 2 * 2;     // whole chunks of 128
     if (pl.seg_chunks < 1) pl.seg_chunks = 1;
     pl.nseg = pl.nchunks > 0 ? (pl.nchunks + pl.seg_chunks - 1) / pl.seg_chunks : 1;
     return pl;
@@ -49,20 +55,29 @@ pdssm_status check_dims(const pdssm_decay_dims *d, pdssm_dtype dt, bool step) {
     return PDSSM_OK;
 }
 
+// bf16 runs on the tensor cores; with an adjoint, up to 64 x 64 states.
+DecayPath path_of(const pdssm_decay_dims &d, pdssm_dtype dt, bool for_bwd) {
+    return dt == PDSSM_BF16 && (!for_bwd || (d.N <= 64 && d.P <= 64)) ? kDecayTc : kDecayGen;
+}
+
+DecayPlan plan_of(const pdssm_decay_dims &d, pdssm_dtype dt, bool for_bwd, bool adjoint) {
+    return decay_plan(d, path_of(d, dt, for_bwd), dt == PDSSM_BF16, adjoint);
+}
+
 struct DecayWs {
     size_t seg_state, seg_decay, carry, part_c, part_b, part_la, total;
 };
 
 DecayWs ws_of(const pdssm_decay_dims &d, pdssm_dtype dt, bool for_bwd) {
     DecayWs w{};
-    const DecayPlan f = decay_plan(d, dt, false), r = decay_plan(d, dt, true);
+    const DecayPlan f = plan_of(d, dt, for_bwd, false), r = plan_of(d, dt, for_bwd, true);
     const size_t np = (size_t)(d.N * d.P) * 4, bh = (size_t)(d.B * d.H);
     const size_t nseg = (size_t)(for_bwd && r.nseg > f.nseg ? r.nseg : f.nseg);
-    size_t o = 256;     // never 0, so that 0 means bad arguments
+    size_t o = 256;     // the status word's block
     w.seg_state = o; o = align256(o + bh * nseg * np);
     w.seg_decay = o; o = align256(o + bh * nseg * 4);
     if (for_bwd) {
-        w.carry = o; o = align256(o + bh * (size_t)f.nchunks * np);
+        w.carry = o; o = align256(o + bh * (size_t)r.nchunks * np);
         if (d.G < d.H) {
             const size_t keys = bh * (size_t)(d.L * d.N) * 4;
             w.part_c = o; o = align256(o + keys);
@@ -94,6 +109,17 @@ void set_strides(DecayParams &p, const pdssm_decay_dims &d, pdssm_layout lay, bo
         p.la_t = 0; p.la_h = 1; p.la_b = 0;
         p.gla_t = 1; p.gla_h = d.L; p.gla_b = d.H * d.L;     // partials [B][H][L]
     }
+}
+
+// 2: 32-byte stores of x-like rows, 1: 16-byte accesses, 0: neither
+int vec_of(const pdssm_decay_dims &d, std::initializer_list<const void *> ptrs) {
+    if (!decay_tc_copies() || d.N % 8 || d.P % 8) return 0;
+    size_t grid = 32;
+    for (const void *q : ptrs) {
+        if (!aligned(q, 16)) return 0;
+        if (!aligned(q, 32)) grid = 16;
+    }
+    return d.P % 16 == 0 && grid == 32 ? 2 : 1;
 }
 
 void set_plan(DecayParams &p, const DecayPlan &pl, const DecayWs &w, unsigned char *base) {
@@ -151,11 +177,17 @@ pdssm_status pdssm_decay_scan_fwd(const pdssm_decay_dims *dims, const void *c, c
     memset(&p, 0, sizeof(p));
     unsigned char *base = reinterpret_cast<unsigned char *>(ws);
     set_strides(p, *dims, layout, log_a_per_step != 0);
-    set_plan(p, decay_plan(*dims, dtype, false), w, base);
+    set_plan(p, plan_of(*dims, dtype, for_bwd != 0, false), w, base);
     p.c = c; p.b = b; p.x = x; p.log_a = log_a; p.h0 = h0; p.lengths = lengths;
     p.y = y; p.h_last = h_last;
     if (for_bwd) p.carry = reinterpret_cast<float *>(base + w.carry);
-    e = launch_decay_fwd_gen(p, dtype, s);
+    if (path_of(*dims, dtype, for_bwd != 0) == kDecayTc) {
+        p.vec = vec_of(*dims, {c, b, x, y});
+        e = launch_decay_fwd_tc(p, reinterpret_cast<int *>(base), s);
+    } else {
+        e = cudaMemsetAsync(base, 0, 4, s);     // the status word
+        if (e == cudaSuccess) e = launch_decay_fwd_gen(p, dtype, s);
+    }
     return e == cudaSuccess ? PDSSM_OK : cuda_fail(e, "decay scan");
 }
 
@@ -191,7 +223,7 @@ pdssm_status pdssm_decay_scan_bwd(const pdssm_decay_dims *dims, const void *c, c
     memset(&p, 0, sizeof(p));
     unsigned char *base = reinterpret_cast<unsigned char *>(ws);
     set_strides(p, *dims, layout, log_a_per_step != 0);
-    set_plan(p, decay_plan(*dims, dtype, true), w, base);
+    set_plan(p, plan_of(*dims, dtype, true, true), w, base);
     p.c = c; p.b = b; p.x = x; p.log_a = log_a; p.h0 = h0; p.lengths = lengths;
     p.g_y = g_y; p.g_hlast = g_hlast; p.g_h0 = g_h0;
     p.carry = reinterpret_cast<float *>(base + w.carry);
@@ -203,7 +235,12 @@ pdssm_status pdssm_decay_scan_bwd(const pdssm_decay_dims *dims, const void *c, c
     p.g_b = shared ? (void *)part_b : g_b;
     p.g_x = g_x;
     p.g_la = log_a_per_step ? g_log_a : part_la;
-    e = launch_decay_bwd_gen(p, dtype, s);
+    if (path_of(*dims, dtype, true) == kDecayTc) {
+        p.vec = vec_of(*dims, {c, b, x, g_y, g_x, shared ? g_x : g_c, shared ? g_x : g_b});
+        e = launch_decay_bwd_mma(p, reinterpret_cast<int *>(base), s);
+    } else {
+        e = launch_decay_bwd_gen(p, dtype, s);
+    }
     if (e != cudaSuccess) return cuda_fail(e, "decay scan adjoint");
     if (shared) {
         e = launch_decay_sum_heads(p, dtype, part_c, part_b, g_c, g_b, s);

@@ -1,0 +1,571 @@
+// Adjoint of the decay scan for bf16 inputs with N, P <= 64: chunks of 64
+// steps in reverse, warp-level bf16 products (m16n8k16, fp32 accumulation).
+//
+// With S0 the state at the chunk's start (the forward left it), R = dl/dS at
+// its end, e_i = e^{G_i}, w_j = e^{G_C - G_j}, D_ij = e^{G_i - G_j} (j <= i):
+//     P = D (c b^T),  Q = D (g_y x^T)
+//     g_c = e (g_y S0^T) + Q b          g_b = w (x R^T) + Q^T c
+//     g_x = w (b R) + P^T g_y           R' = e^{G_C} R + (e c)^T g_y
+//     g_log_a[t] = sum_{j<t<=i} P_ij (g_y_i . x_j) + sum_{i>=t} c_i . e_i (S0 g_y_i)
+//                  + sum_{j<t} b_j . w_j (R x_j) + e^{G_C} <S0, R>
+// R stays in fp32 registers.  Where a result is fp32 (R', and g_log_a through
+// the state parts of g_c and g_b) the operand that is not bf16 by itself is
+// split into three bf16 parts (24 bits); P, Q and the R that g_x reads are
+// rounded to bf16 once (g_x, g_c, g_b are bf16 themselves).
+//
+// tcgen05 is not used here: a chunk has nine 64-wide products whose results
+// are all rescaled, masked or summed by rows and columns before the next one,
+// and accumulators in registers take that without a round trip.  Bound: the
+// warp-level tensor pipe, 107 kflop per step of a 64 x 64 head.
+#include "decay.cuh"
+
+namespace pdssm {
+namespace {
+
+constexpr int kC = 64, kTh = 256;
+constexpr uint32_t kTile = 64 * 128;        // 64 rows of 64 bf16, 128-byte swizzle
+
+struct Smem {
+    static constexpr uint32_t kc = 0, kb = kTile, kx = 2 * kTile, kg = 3 * kTile;
+    static constexpr uint32_t kS = 4 * kTile, kR = 7 * kTile;       // three parts each
+    static constexpr uint32_t kP = 10 * kTile, kQ = 11 * kTile;
+    static constexpr uint32_t kF = 12 * kTile;                      // floats below
+    static constexpr uint32_t kTotal = kF + (2 * kC + 2 * kC + 2 * kC + 4 * kC + 2 * kC + 2 * kC + 8) * 4;
+};
+
+__device__ __forceinline__ uint32_t piece(int r, int q) {
+    return (uint32_t)(r * 128 + ((q ^ (r & 7)) << 4));
+}
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+__device__ __forceinline__ float lo_of(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float hi_of(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
+
+__device__ __forceinline__ void ldm4(uint32_t (&r)[4], uint32_t a) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(a));
+}
+__device__ __forceinline__ void ldm4t(uint32_t (&r)[4], uint32_t a) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(a));
+}
+__device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+        "{%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// Fragment addresses in a tile; `l` is the lane.
+// A (16 x 16 at row m0, k-step ks) of rows stored [m][k]
+__device__ __forceinline__ uint32_t at_a(uint32_t t, int m0, int ks, int l) {
+    return t + piece(m0 + (l & 15), 2 * ks + (l >> 4));
+}
+// A of columns stored [k][m]
+__device__ __forceinline__ uint32_t at_at(uint32_t t, int m0, int ks, int l) {
+    return t + piece(16 * ks + (l & 7) + ((l >> 4) << 3), m0 / 8 + ((l >> 3) & 1));
+}
+// B (k-step ks, columns n0..n0+15) stored [n][k]
+__device__ __forceinline__ uint32_t at_b(uint32_t t, int n0, int ks, int l) {
+    return t + piece(n0 + (l & 7) + ((l >> 4) << 3), 2 * ks + ((l >> 3) & 1));
+}
+// B stored [k][n]
+__device__ __forceinline__ uint32_t at_bt(uint32_t t, int n0, int ks, int l) {
+    return t + piece(16 * ks + (l & 15), n0 / 8 + (l >> 4));
+}
+
+// three bf16 parts of a pair
+__device__ __forceinline__ void split3(float a, float b, uint32_t (&o)[3]) {
+    o[0] = pack2(a, b);
+    a -= lo_of(o[0]);
+    b -= hi_of(o[0]);
+    o[1] = pack2(a, b);
+    a -= lo_of(o[1]);
+    b -= hi_of(o[1]);
+    o[2] = pack2(a, b);
+}
+
+__device__ __forceinline__ void sts32(uint32_t a, uint32_t v) {
+    asm volatile("st.shared.u32 [%0], %1;" ::"r"(a), "r"(v) : "memory");
+}
+__device__ __forceinline__ float quad_sum(float v) {
+    v += __shfl_xor_sync(kFull, v, 1);
+    return v + __shfl_xor_sync(kFull, v, 2);
+}
+
+__global__ void __launch_bounds__(kTh, 2) k_decay_bwd_mma(DecayParams p) {
+    extern __shared__ __align__(128) unsigned char sm_raw[];
+    const uint32_t sm = smem_u32(sm_raw);
+    float2 *sG = reinterpret_cast<float2 *>(sm_raw + Smem::kF);
+    float *s_e = reinterpret_cast<float *>(sG + kC), *s_w = s_e + kC;   // e_i, w_j
+    float *s_row = s_w + kC;            // [2][64] pair sums by row, per column half
+    float *s_col = s_row + 2 * kC;      // [4][64] by column, per row block
+    float *s_u = s_col + 4 * kC, *s_v = s_u + 2 * kC;   // [2][64]
+    float *s_dot = s_v + 2 * kC;        // [8]
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int wr = warp & 3, wc = warp >> 2;    // 16 rows and 32 columns of each product
+    const int g = lane >> 2, q2 = (lane & 3) * 2;
+    const int m0 = 16 * wr, n0 = 32 * wc;
+
+    const int seg = blockIdx.x % p.nseg;
+    const int64_t bh = blockIdx.x / p.nseg;
+    const int b = (int)(bh / p.H), h = (int)(bh % p.H);
+    const int64_t len = decay_len(p, b);
+    const int64_t koff = b * p.key_b + (h / p.rep) * p.key_h, voff = b * p.val_b + h * p.val_h;
+    typedef __nv_bfloat16 T;
+    const T *c = (const T *)p.c + koff, *bb = (const T *)p.b + koff;
+    const T *x = (const T *)p.x + voff, *gy = (const T *)p.g_y + voff;
+    T *gx = (T *)p.g_x + voff;
+    const float *la = p.log_a + b * p.la_b + h * p.la_h;
+    float *gla = p.g_la + b * p.gla_b + h * p.gla_h;
+    const bool part = p.rep > 1;        // gradients of shared keys: fp32 [B][H][L][N] partials
+    const int64_t poff = bh * p.L * p.N, np = (int64_t)p.N * p.P;
+
+    // R: rows m0 + g (+ 8), columns n0 + 8 f + q2 (+ 1)
+    float R[4][4];
+    {
+        const float *in = p.nseg > 1 ? p.seg_state + (bh * p.nseg + seg) * np
+                                     : (p.g_hlast ? p.g_hlast + bh * np : nullptr);
+#pragma unroll
+        for (int f = 0; f < 4; ++f)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int n = m0 + g + 8 * (e >> 1), q = n0 + 8 * f + q2 + (e & 1);
+                R[f][e] = in && n < p.N && q < p.P ? in[(int64_t)n * p.P + q] : 0.f;
+            }
+    }
+    // blocks above the diagonal of P and Q stay zero
+    for (int e = tid; e < 2 * 512; e += kTh)
+        *reinterpret_cast<uint4 *>(sm_raw + Smem::kP + 16 * e) = make_uint4(0, 0, 0, 0);
+
+    const int c0 = seg * p.seg_chunks, c1 = min(c0 + p.seg_chunks, p.nchunks);
+    auto store_key = [&](void *out, int64_t t, int q, float v0, float v1) {     // columns q, q + 1
+        if (t >= p.L) return;
+        if (t >= len) v0 = v1 = 0.f;
+        if (part) {
+            float *o = (float *)out + poff + t * p.N + q;
+            if (q < p.N) o[0] = v0;
+            if (q + 1 < p.N) o[1] = v1;
+        } else {
+            T *o = (T *)out + koff + t * p.key_t + q;
+            if (p.vec) {
+                if (q < p.N) *reinterpret_cast<uint32_t *>(o) = pack2(v0, v1);
+            } else {
+                if (q < p.N) o[0] = __float2bfloat16_rn(v0);
+                if (q + 1 < p.N) o[1] = __float2bfloat16_rn(v1);
+            }
+        }
+    };
+
+    for (int ch = c1 - 1; ch >= c0; --ch) {
+        const int64_t t0 = (int64_t)ch * kC;
+        __syncthreads();                // the last chunk's tiles have been read
+        if (t0 >= len) {                // behind the end: zero gradients, R stays
+            for (int e = tid; e < kC * 64; e += kTh) {
+                const int64_t t = t0 + e / 64;
+                const int q = e % 64;
+                if (t >= p.L) continue;
+                if (q < p.P) gx[t * p.val_t + q] = __float2bfloat16_rn(0.f);
+                if (q < p.N) {
+                    if (part) {
+                        ((float *)p.g_c)[poff + t * p.N + q] = 0.f;
+                        ((float *)p.g_b)[poff + t * p.N + q] = 0.f;
+                    } else {
+                        ((T *)p.g_c)[koff + t * p.key_t + q] = __float2bfloat16_rn(0.f);
+                        ((T *)p.g_b)[koff + t * p.key_t + q] = __float2bfloat16_rn(0.f);
+                    }
+                }
+                if (q == 0) gla[t * p.gla_t] = 0.f;
+            }
+            continue;
+        }
+        // ---- tiles: zero behind the end and behind the widths
+        if (p.vec) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int e = tid + i * kTh, r = e >> 3, q = e & 7;
+                const bool on = t0 + r < len;
+                const int64_t t = on ? t0 + r : t0;
+                auto cp = [&](uint32_t tile, const T *src, bool in) {
+                    const int n = on && in ? 16 : 0;
+                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(sm + tile + piece(r, q)),
+                                 "l"(src), "r"(n)
+                                 : "memory");
+                };
+                const int qk = 8 * q < p.N ? 8 * q : 0, qv = 8 * q < p.P ? 8 * q : 0;
+                cp(Smem::kc, c + t * p.key_t + qk, 8 * q < p.N);
+                cp(Smem::kb, bb + t * p.key_t + qk, 8 * q < p.N);
+                cp(Smem::kx, x + t * p.val_t + qv, 8 * q < p.P);
+                cp(Smem::kg, gy + t * p.val_t + qv, 8 * q < p.P);
+            }
+            asm volatile("cp.async.commit_group;" ::: "memory");
+        } else {
+            for (int e = tid; e < kC * 32; e += kTh) {
+                const int r = e >> 5, q = (e & 31) * 2;
+                const int64_t t = t0 + r;
+                auto cp = [&](uint32_t tile, const T *src, int64_t stride, int width) {
+                    uint32_t w = 0;
+                    if (t < len) {
+                        const unsigned short *s = reinterpret_cast<const unsigned short *>(src + t * stride) + q;
+                        if (q < width) w = s[0];
+                        if (q + 1 < width) w |= (uint32_t)s[1] << 16;
+                    }
+                    sts32(sm + tile + piece(r, q / 8) + (q & 7) * 2, w);
+                };
+                cp(Smem::kc, c, p.key_t, p.N);
+                cp(Smem::kb, bb, p.key_t, p.N);
+                cp(Smem::kx, x, p.val_t, p.P);
+                cp(Smem::kg, gy, p.val_t, p.P);
+            }
+        }
+        if (warp == 0) {
+            decay_sums<kC>([&](int t) { return t0 + t < len ? la[(t0 + t) * p.la_t] : 0.f; }, sG, lane);
+            __syncwarp();
+            const float2 end = sG[kC - 1];
+#pragma unroll
+            for (int i = 0; i < kC; i += 32) {
+                s_e[i + lane] = decay_from_start(sG[i + lane]);
+                s_w[i + lane] = decay_between(end, sG[i + lane]);
+            }
+        }
+        // ---- parts of S0 and R, and <S0, R>
+        {
+            const float *S0 = ch > 0 ? p.carry + (bh * p.nchunks + ch) * np
+                                     : (p.h0 ? p.h0 + bh * np : nullptr);
+            float S[4][4], dot = 0.f;
+#pragma unroll
+            for (int f = 0; f < 4; ++f)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int n = m0 + g + 8 * (e >> 1), q = n0 + 8 * f + q2 + (e & 1);
+                    S[f][e] = S0 && n < p.N && q < p.P ? S0[(int64_t)n * p.P + q] : 0.f;
+                }
+#pragma unroll
+            for (int f = 0; f < 4; ++f)
+#pragma unroll
+                for (int e = 0; e < 4; e += 2) {
+                    const int n = m0 + g + 4 * e;
+                    const uint32_t at = sm + piece(n, n0 / 8 + f) + q2 * 2;
+                    uint32_t o[3];
+                    dot = fmaf(S[f][e], R[f][e], dot);
+                    dot = fmaf(S[f][e + 1], R[f][e + 1], dot);
+                    split3(S[f][e], S[f][e + 1], o);
+#pragma unroll
+                    for (int k = 0; k < 3; ++k) sts32(at + Smem::kS + k * kTile, o[k]);
+                    split3(R[f][e], R[f][e + 1], o);
+#pragma unroll
+                    for (int k = 0; k < 3; ++k) sts32(at + Smem::kR + k * kTile, o[k]);
+                }
+#pragma unroll
+            for (int d = 16; d; d >>= 1) dot += __shfl_xor_sync(kFull, dot, d);
+            if (lane == 0) s_dot[warp] = dot;
+        }
+        asm volatile("cp.async.wait_group 0;" ::: "memory");
+        __syncthreads();
+        const float aend = s_e[kC - 1];
+
+        // ---- P and Q of rows m0.., the 16-column blocks k = wc, wc + 2, .. <= wr
+        {
+            uint32_t ca[4][4], ga[4][4];
+#pragma unroll
+            for (int ks = 0; ks < 4; ++ks) {
+                ldm4(ca[ks], at_a(sm + Smem::kc, m0, ks, lane));
+                ldm4(ga[ks], at_a(sm + Smem::kg, m0, ks, lane));
+            }
+            const float2 gr0 = sG[m0 + g], gr1 = sG[m0 + g + 8];
+            float row0 = 0.f, row1 = 0.f;
+#pragma unroll 1
+            for (int k = wc; k < 4; k += 2) {
+                float *col = s_col + wr * kC + 16 * k;
+                if (k > wr) {
+                    if (lane < 16) col[lane] = 0.f;
+                    continue;
+                }
+                float s[2][4], v[2][4];
+#pragma unroll
+                for (int f = 0; f < 2; ++f)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) s[f][e] = v[f][e] = 0.f;
+#pragma unroll
+                for (int ks = 0; ks < 4; ++ks) {
+                    uint32_t fb[4], fx[4];
+                    ldm4(fb, at_b(sm + Smem::kb, 16 * k, ks, lane));
+                    ldm4(fx, at_b(sm + Smem::kx, 16 * k, ks, lane));
+                    mma(s[0], ca[ks], fb[0], fb[1]);
+                    mma(s[1], ca[ks], fb[2], fb[3]);
+                    mma(v[0], ga[ks], fx[0], fx[1]);
+                    mma(v[1], ga[ks], fx[2], fx[3]);
+                }
+#pragma unroll
+                for (int f = 0; f < 2; ++f) {
+                    const int j = 16 * k + 8 * f + q2;
+                    const float2 gj0 = sG[j], gj1 = sG[j + 1];
+                    float pv[4], qv[4], ev[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const int i = m0 + g + 8 * (e >> 1), jj = j + (e & 1);
+                        const float d = decay_between(e < 2 ? gr0 : gr1, e & 1 ? gj1 : gj0);
+                        pv[e] = jj <= i ? s[f][e] * d : 0.f;
+                        qv[e] = jj <= i ? v[f][e] * d : 0.f;
+                        ev[e] = jj < i ? pv[e] * v[f][e] : 0.f;
+                    }
+                    row0 += ev[0] + ev[1];
+                    row1 += ev[2] + ev[3];
+                    float c0s = ev[0] + ev[2], c1s = ev[1] + ev[3];
+#pragma unroll
+                    for (int d = 4; d < 32; d *= 2) {
+                        c0s += __shfl_xor_sync(kFull, c0s, d);
+                        c1s += __shfl_xor_sync(kFull, c1s, d);
+                    }
+                    if (g == 0) {
+                        col[8 * f + q2] = c0s;
+                        col[8 * f + q2 + 1] = c1s;
+                    }
+                    const uint32_t a0 = sm + piece(m0 + g, 2 * k + f) + q2 * 2,
+                                   a1 = sm + piece(m0 + g + 8, 2 * k + f) + q2 * 2;
+                    sts32(a0 + Smem::kP, pack2(pv[0], pv[1]));
+                    sts32(a1 + Smem::kP, pack2(pv[2], pv[3]));
+                    sts32(a0 + Smem::kQ, pack2(qv[0], qv[1]));
+                    sts32(a1 + Smem::kQ, pack2(qv[2], qv[3]));
+                }
+            }
+            row0 = quad_sum(row0);
+            row1 = quad_sum(row1);
+            if ((lane & 3) == 0) {
+                s_row[wc * kC + m0 + g] = row0;
+                s_row[wc * kC + m0 + g + 8] = row1;
+            }
+        }
+        __syncthreads();
+
+        float acc[4][4];
+        auto zero = [&]() {
+#pragma unroll
+            for (int f = 0; f < 4; ++f)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) acc[f][e] = 0.f;
+        };
+        // rows times the transpose of a [n][k] operand in three parts
+        auto by_parts = [&](uint32_t rows, uint32_t parts) {
+#pragma unroll
+            for (int ks = 0; ks < 4; ++ks) {
+                uint32_t a[4];
+                ldm4(a, at_a(rows, m0, ks, lane));
+#pragma unroll
+                for (int k = 0; k < 3; ++k) {
+                    uint32_t f0[4], f1[4];
+                    ldm4(f0, at_b(parts + k * kTile, n0, ks, lane));
+                    ldm4(f1, at_b(parts + k * kTile, n0 + 16, ks, lane));
+                    mma(acc[0], a, f0[0], f0[1]);
+                    mma(acc[1], a, f0[2], f0[3]);
+                    mma(acc[2], a, f1[0], f1[1]);
+                    mma(acc[3], a, f1[2], f1[3]);
+                }
+            }
+        };
+        // acc *= by row factors; the rows' products with a tile's rows
+        auto scale_rows = [&](float f0, float f1) {
+#pragma unroll
+            for (int f = 0; f < 4; ++f) {
+                acc[f][0] *= f0;
+                acc[f][1] *= f0;
+                acc[f][2] *= f1;
+                acc[f][3] *= f1;
+            }
+        };
+        auto row_dots = [&](uint32_t tile, float *out) {
+            float d0 = 0.f, d1 = 0.f;
+#pragma unroll
+            for (int f = 0; f < 4; ++f) {
+                const uint32_t w0 = lds_u32(sm + tile + piece(m0 + g, n0 / 8 + f) + q2 * 2),
+                               w1 = lds_u32(sm + tile + piece(m0 + g + 8, n0 / 8 + f) + q2 * 2);
+                d0 = fmaf(acc[f][0], lo_of(w0), fmaf(acc[f][1], hi_of(w0), d0));
+                d1 = fmaf(acc[f][2], lo_of(w1), fmaf(acc[f][3], hi_of(w1), d1));
+            }
+            d0 = quad_sum(d0);
+            d1 = quad_sum(d1);
+            if ((lane & 3) == 0) {
+                out[wc * kC + m0 + g] = d0;
+                out[wc * kC + m0 + g + 8] = d1;
+            }
+        };
+        auto add_pairs = [&](const uint32_t (&a)[4], uint32_t tile, int ks) {
+            uint32_t f0[4], f1[4];
+            ldm4t(f0, at_bt(tile, n0, ks, lane));
+            ldm4t(f1, at_bt(tile, n0 + 16, ks, lane));
+            mma(acc[0], a, f0[0], f0[1]);
+            mma(acc[1], a, f0[2], f0[3]);
+            mma(acc[2], a, f1[0], f1[1]);
+            mma(acc[3], a, f1[2], f1[3]);
+        };
+        const int64_t tr0 = t0 + m0 + g, tr1 = tr0 + 8;
+
+        // ---- g_c
+        zero();
+        by_parts(sm + Smem::kg, sm + Smem::kS);
+        scale_rows(s_e[m0 + g], s_e[m0 + g + 8]);
+        row_dots(Smem::kc, s_u);
+#pragma unroll 1
+        for (int ks = 0; ks <= wr; ++ks) {
+            uint32_t a[4];
+            ldm4(a, at_a(sm + Smem::kQ, m0, ks, lane));
+            add_pairs(a, sm + Smem::kb, ks);
+        }
+#pragma unroll
+        for (int f = 0; f < 4; ++f) {
+            store_key(p.g_c, tr0, n0 + 8 * f + q2, acc[f][0], acc[f][1]);
+            store_key(p.g_c, tr1, n0 + 8 * f + q2, acc[f][2], acc[f][3]);
+        }
+        // ---- g_b
+        zero();
+        by_parts(sm + Smem::kx, sm + Smem::kR);
+        const float w0 = s_w[m0 + g], w1 = s_w[m0 + g + 8];
+        scale_rows(w0, w1);
+        row_dots(Smem::kb, s_v);
+#pragma unroll 1
+        for (int ks = wr; ks < 4; ++ks) {
+            uint32_t a[4];
+            ldm4t(a, at_at(sm + Smem::kQ, m0, ks, lane));
+            add_pairs(a, sm + Smem::kc, ks);
+        }
+#pragma unroll
+        for (int f = 0; f < 4; ++f) {
+            store_key(p.g_b, tr0, n0 + 8 * f + q2, acc[f][0], acc[f][1]);
+            store_key(p.g_b, tr1, n0 + 8 * f + q2, acc[f][2], acc[f][3]);
+        }
+        // ---- g_x
+        zero();
+#pragma unroll
+        for (int ks = 0; ks < 4; ++ks) {
+            uint32_t a[4];
+            ldm4(a, at_a(sm + Smem::kb, m0, ks, lane));
+            add_pairs(a, sm + Smem::kR, ks);
+        }
+        scale_rows(w0, w1);
+#pragma unroll 1
+        for (int ks = wr; ks < 4; ++ks) {
+            uint32_t a[4];
+            ldm4t(a, at_at(sm + Smem::kP, m0, ks, lane));
+            add_pairs(a, sm + Smem::kg, ks);
+        }
+#pragma unroll
+        for (int f = 0; f < 4; ++f) {
+            const int q = n0 + 8 * f + q2;
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int64_t t = e ? tr1 : tr0;
+                if (t >= p.L) continue;
+                const float v0 = t < len ? acc[f][2 * e] : 0.f, v1 = t < len ? acc[f][2 * e + 1] : 0.f;
+                T *o = gx + t * p.val_t + q;
+                if (p.vec) {
+                    if (q < p.P) *reinterpret_cast<uint32_t *>(o) = pack2(v0, v1);
+                } else {
+                    if (q < p.P) o[0] = __float2bfloat16_rn(v0);
+                    if (q + 1 < p.P) o[1] = __float2bfloat16_rn(v1);
+                }
+            }
+        }
+        // ---- R
+#pragma unroll
+        for (int f = 0; f < 4; ++f)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) R[f][e] *= aend;
+#pragma unroll
+        for (int ks = 0; ks < 4; ++ks) {
+            uint32_t a[4], parts[3][4], f0[4], f1[4];
+            ldm4t(a, at_at(sm + Smem::kc, m0, ks, lane));
+            ldm4t(f0, at_bt(sm + Smem::kg, n0, ks, lane));
+            ldm4t(f1, at_bt(sm + Smem::kg, n0 + 16, ks, lane));
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const float2 w = *reinterpret_cast<const float2 *>(s_e + 16 * ks + 8 * (e >> 1) + q2);
+                uint32_t o[3];
+                split3(lo_of(a[e]) * w.x, hi_of(a[e]) * w.y, o);
+#pragma unroll
+                for (int k = 0; k < 3; ++k) parts[k][e] = o[k];
+            }
+#pragma unroll
+            for (int k = 0; k < 3; ++k) {
+                mma(R[0], parts[k], f0[0], f0[1]);
+                mma(R[1], parts[k], f0[2], f0[3]);
+                mma(R[2], parts[k], f1[0], f1[1]);
+                mma(R[3], parts[k], f1[2], f1[3]);
+            }
+        }
+        __syncthreads();                // s_u, s_v are in
+        if (warp == 0) {
+            double through = 0.0;
+            for (int w = 0; w < kTh / 32; ++w) through += (double)s_dot[w];
+            through *= (double)aend;
+            double before = 0.0, total = 0.0, inc[2], pre[2];
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+                const int t = q * 32 + lane;
+                double a = (double)s_row[t] + (double)s_row[kC + t] + (double)s_u[t] + (double)s_u[kC + t] -
+                           ((double)s_col[t] + (double)s_col[kC + t] + (double)s_col[2 * kC + t] +
+                            (double)s_col[3 * kC + t]);
+                double v = (double)s_v[t] + (double)s_v[kC + t];
+                const double a0 = a, v0 = v;
+#pragma unroll
+                for (int d = 1; d < 32; d *= 2) {
+                    const double oa = shfl_up_d(a, d), ov = shfl_up_d(v, d);
+                    if (lane >= d) {
+                        a += oa;
+                        v += ov;
+                    }
+                }
+                inc[q] = total + a - a0;
+                pre[q] = before + v - v0;
+                total += __shfl_sync(kFull, a, 31);
+                before += __shfl_sync(kFull, v, 31);
+            }
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+                const int64_t t = t0 + q * 32 + lane;
+                if (t < p.L)    // a floored decay is a constant
+                    gla[t * p.gla_t] = t < len && !(la[t * p.la_t] <= (float)kDecayFloor)
+                                           ? (float)(total - inc[q] + pre[q] + through)
+                                           : 0.f;
+            }
+        }
+    }
+    if (p.g_h0 && seg == 0) {
+        float *out = p.g_h0 + bh * np;
+#pragma unroll
+        for (int f = 0; f < 4; ++f)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int n = m0 + g + 8 * (e >> 1), q = n0 + 8 * f + q2 + (e & 1);
+                if (n < p.N && q < p.P) out[(int64_t)n * p.P + q] = R[f][e];
+            }
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_decay_bwd_mma(const DecayParams &p, int *status, cudaStream_t st) {
+    if (p.nseg > 1) {
+        // the segments in the tensor-core kernel's chunks of 128 steps
+        DecayParams s = p;
+        s.nchunks = (int)((p.L + 127) / 128);
+        s.seg_chunks = p.seg_chunks / 2;
+        s.pslices = 1;
+        cudaError_t e = launch_decay_seg_rev_tc(s, status, st);
+        if (e != cudaSuccess) return e;
+        e = launch_decay_join(p, p.g_hlast, true, nullptr, st);
+        if (e != cudaSuccess) return e;
+    }
+    cudaError_t e = cudaFuncSetAttribute(k_decay_bwd_mma, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         (int)Smem::kTotal);
+    if (e != cudaSuccess) return e;
+    k_decay_bwd_mma<<<dim3((unsigned)((int64_t)p.B * p.H * p.nseg)), kTh, Smem::kTotal, st>>>(p);
+    return cudaGetLastError();
+}
+
+}  // namespace pdssm

@@ -1,0 +1,798 @@
+// Decay scan of bf16 inputs on the tensor cores (tcgen05): the forward, and
+// the state alone over a segment (forward and reverse) for the join.
+//
+// A CTA runs one segment of one (batch, head) and 64 columns of the state, in
+// chunks of 128 steps (M = 128).  Per chunk, with G_i the cumulated log
+// decays and S0 the state at the chunk's start:
+//     1. Sc = c b^T                            128 x 128, K = N
+//     2. P  = Sc * e^{G_i - G_j}, j <= i, as bf16 back into Sc's columns
+//     3. Y  = P x                              128 x 64, K = 128, P from TMEM
+//     4. Yi = c S0                             128 x 64, K = N
+//     5. y  = Y + e^{G_i} Yi
+//     6. S  = e^{G_C} S0 + sum_j (e^{G_C - G_j} b_j) x_j^T, in halves of 64 steps
+//        (so that the adjoint, which has chunks of 64, finds each one's state)
+// The state is an fp32 register of one of 128 threads per row and is decayed
+// there; only product 6 adds to it.  Its decayed operand is split into three
+// bf16 parts (8 + 8 + 8 bits), so that the state keeps fp32 accuracy (two
+// parts were measured at 2.4e-6 of the state's norm, three at 2e-7); the other
+// operand is exact.  P and the copy of S0 that product 4 reads are rounded to
+// bf16 once each: y is bf16 itself, so they add a rounding of its own size.
+//
+// N <= 64 (STK): the split operand is b; parts 0 and 1 are stacked along M (64
+// rows each), part 2 (halved, which is exact) is added to both halves, and
+// the two half-states are decayed and used side by side (product 4 reads
+// [c, c] against both).  N <= 128: the split operand is x, and M = N = 128.
+//
+// Decays: within a 32 x 32 diagonal block each pair's exponential; a block to
+// its left as e^{G_i - G_e} e^{G_e - G_j}, e the last step of j's block: both
+// factors are at most 1 for a decaying state, so neither over- nor underflows
+// where the product does not.
+//
+// Warps: 0-3 and 4-7 take chunks in turn (steps 2 and 5), 8-15 hold the state
+// (32 columns each), 16-19 build the split operand, 20 and 21 issue the
+// products (scores, state), 22 the copies, 23 and 24 compute the decays in
+// turn.  Accumulators, decays and (N <= 64) split parts are double-buffered,
+// c and b tiles three deep (N <= 64; the scores of chunk i + 1 run ahead of
+// the rest of chunk i, so two stages would expose each copy's latency), all
+// handed over by mbarriers.
+#include <string.h>
+
+#include "decay.cuh"
+#include "umma.cuh"
+
+namespace pdssm {
+namespace {
+
+constexpr int kC = 128;                 // steps per chunk
+// warps by role
+constexpr int kState = 8, kBuild = 16, kControl = 20, kControl2 = 21, kProducer = 22, kDecay = 23;
+constexpr int kTcTh = 25 * 32;
+constexpr int kLoaders = 32;            // threads of plain loads (the producer's warp)
+constexpr uint32_t kTile = kC * 128;    // 128 rows of 64 bf16
+
+// forward; the state alone; the state alone in reverse; forward that leaves
+// the state at every 64 steps for the adjoint
+enum { kFwd = 0, kSegFwd = 1, kSegRev = 2, kFwdCarry = 3 };
+
+// Decays of one chunk in shared memory.
+struct __align__(16) Decays {
+    float2 G[kC];           // cumulated, base 2, hi + lo
+    float start[kC];        // e^{G_t}
+    float weight[kC];       // of the state's update: to the end of t's half of the chunk (in
+                            // reverse: from its start)
+    float col[kC];          // e^{G_e - G_t}, e = last step of t's block of 32
+    float row[3][kC];       // e^{G_t - G_e}, e = last step of block 0..2 (t behind it)
+    float half[2], pad[2];  // decay over the first and the second half
+};
+
+// Barriers: four slots of each kind (chunk i: slot i & 3, phase i >> 2, so
+// that no role can be a whole round of a slot behind), and the rings' own.
+enum {
+    kFullCB, kFullX, kScFull, kPReady, kPlReady, kDFull, kS0Ready, kYFull, kYFree,
+    kDecReady, kDecFree, kSumIn, kSumOut, kNumBars
+};
+
+template <bool STK, int MODE>
+struct Smem {
+    static constexpr int kNCB = STK && MODE != kFwdCarry ? 3 : 2;       // stages of c and b
+    static constexpr int kNX = STK ? 2 : 1;             // stages of x
+    static constexpr int kNPL = STK ? 2 : 1;            // sets of split parts
+    static constexpr int kParts = STK ? 2 : 3;          // of a set (STK: part 2 takes b's place)
+    static constexpr uint32_t kKey = STK ? kTile : 2 * kTile;   // one c or b tile
+    static constexpr uint32_t kC0 = 0;                  // [kNCB][c, b]
+    static constexpr uint32_t kX = kC0 + kNCB * 2 * kKey;       // [kNX]
+    static constexpr uint32_t kPl = kX + kNX * kTile;   // [kNPL][kParts]
+    static constexpr uint32_t kS0 = kPl + kNPL * kParts * kTile;
+    // the sum of the half-states on its way to memory
+    static constexpr uint32_t kSum = kS0 + kTile;
+    static constexpr uint32_t kDec = kSum + (STK && MODE == kFwdCarry ? 64 * 256 : 0);
+    static constexpr uint32_t kBar = kDec + 2 * sizeof(Decays);
+    static constexpr uint32_t kTotal = kBar + 32 * kNumBars + 1024;       // + alignment
+};
+
+struct TcParams {
+    DecayParams d;
+    int *status;
+    int first;              // this launch clears the status word
+};
+
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+__device__ __forceinline__ float lo_of(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float hi_of(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
+
+// Byte offset of 16-byte piece q of row r in a 128-byte-swizzled tile of
+// 128-byte rows.
+__device__ __forceinline__ uint32_t piece(int r, int q) {
+    return (uint32_t)(r * 128 + ((q ^ (r & 7)) << 4));
+}
+
+__device__ __forceinline__ uint4 lds128(uint32_t a) {
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "r"(a));
+    return v;
+}
+__device__ __forceinline__ void sts128(uint32_t a, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
+    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(x), "r"(y), "r"(z), "r"(w)
+                 : "memory");
+}
+
+template <bool STK, int MODE>
+__global__ void __launch_bounds__(kTcTh, 1)
+    k_decay_tc(const __grid_constant__ CUtensorMap cmap, const __grid_constant__ CUtensorMap bmap,
+               const __grid_constant__ CUtensorMap xmap, const TcParams tp) {
+    using SM = Smem<STK, MODE>;
+    constexpr bool FWD = MODE == kFwd || MODE == kFwdCarry;
+    const DecayParams &p = tp.d;
+    extern __shared__ unsigned char sm_raw[];
+    const uint32_t sm = (smem_u32(sm_raw) + 1023u) & ~1023u;
+    unsigned char *smg = sm_raw + (sm - smem_u32(sm_raw));
+    Decays *dec = reinterpret_cast<Decays *>(smg + SM::kDec);
+    __shared__ uint32_t tmem_slot;
+    __shared__ double totals[2];
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    auto bar = [&](int which, int i) { return sm + SM::kBar + 8u * (uint32_t)(4 * which + (i & 3)); };
+    auto bar_cb = [&](int i) { return sm + SM::kBar + 8u * (uint32_t)(4 * kFullCB + i % SM::kNCB); };
+    auto bar_x = [&](int i) { return sm + SM::kBar + 8u * (uint32_t)(4 * kFullX + i % SM::kNX); };
+
+    const int seg = blockIdx.x % p.nseg;
+    const int ps = (blockIdx.x / p.nseg) % p.pslices;
+    const int64_t bh = blockIdx.x / p.nseg / p.pslices;
+    const int b = (int)(bh / p.H), h = (int)(bh % p.H), g = h / p.rep;
+    const int p0 = ps * 64, pw = min(64, p.P - p0);
+    const int64_t len = decay_len(p, b);
+    const int c0 = seg * p.seg_chunks, c1 = min(c0 + p.seg_chunks, p.nchunks);
+    // chunks with a live step: n of them, first .. first + n - 1 (reverse: from
+    // the last one down)
+    const int live_end = (int)((len + kC - 1) / kC);
+    const int n = max(0, min(c1, live_end) - c0);
+    auto chunk_t0 = [&](int i) {
+        return (int64_t)(MODE == kSegRev ? c0 + n - 1 - i : c0 + i) * kC;
+    };
+
+    if (tid == 0) {
+        if (tp.first && blockIdx.x == 0) *tp.status = 0;
+        // a tile lands by one copy's bytes, or by the loader threads
+        const uint32_t loaders = p.vec ? 1 : kLoaders;
+        for (int s = 0; s < 4; ++s) {
+            mbar_init(bar(kFullCB, s), loaders);
+            mbar_init(bar(kFullX, s), loaders);
+            mbar_init(bar(kScFull, s), 1);
+            mbar_init(bar(kPReady, s), 128);
+            mbar_init(bar(kPlReady, s), 128);
+            mbar_init(bar(kDFull, s), 1);
+            mbar_init(bar(kS0Ready, s), 256);
+            mbar_init(bar(kSumIn, s), 256);
+            mbar_init(bar(kSumOut, s), 256);
+            mbar_init(bar(kYFull, s), 1);
+            mbar_init(bar(kYFree, s), 128);
+            mbar_init(bar(kDecReady, s), 32);
+            mbar_init(bar(kDecFree, s), FWD ? 512 : 384);
+        }
+        fence_mbar_init();
+    }
+    if (warp == kControl) tmem_alloc(smem_u32(&tmem_slot), 512);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = tmem_slot;
+    // TMEM columns of buffer i & 1: Sc 128 (P in its first 64, Y in its last 64,
+    // Yi 64), and what the chunk's first and second half add to the state, 64 each
+    auto tcol = [&](int i, int col) { return tmem + (uint32_t)((i & 1) * 256 + col); };
+
+    // Bounded waits of one thread, or of a whole warp (which then agrees on the
+    // outcome, as the warp-wide TMEM accesses need).  After the first that
+    // gives up, a role waits for nothing more and leaves its loop.
+    bool ok = true;
+    auto wait_at = [&](uint32_t at, int phase) {
+        if (ok && !mbar_wait_hot(at, (uint32_t)(phase & 1))) {
+            ok = false;
+            flag_status(tp.status, kStTimeout);
+        }
+        return ok;
+    };
+    auto wait = [&](int which, int i) { return wait_at(bar(which, i), i >> 2); };
+    auto wait_cb = [&](int i) { return wait_at(bar_cb(i), i / SM::kNCB); };
+    auto wait_x = [&](int i) { return wait_at(bar_x(i), i / SM::kNX); };
+    auto wait_warp = [&](int which, int i) { return ok = __all_sync(kFull, wait(which, i)); };
+    auto wait_cb_warp = [&](int i) { return ok = __all_sync(kFull, wait_cb(i)); };
+    auto wait_x_warp = [&](int i) { return ok = __all_sync(kFull, wait_x(i)); };
+
+    if (warp < 8) {
+        if (FWD) {
+            // ---- decayed scores and y: row r of chunks i = warp / 4, + 2, ...
+            const int r = tid & 127, quad = warp & 3;
+            const uint32_t tlane = (uint32_t)(quad * 32) << 16;
+            __nv_bfloat16 *y = (__nv_bfloat16 *)p.y + b * p.val_b + h * p.val_h + p0;
+            for (int i = warp >> 2; i < n; i += 2) {
+                const Decays &dc = dec[i & 1];
+                if (!wait_warp(kDecReady, i) || !wait_warp(kScFull, i)) break;
+                tc_fence_after();
+                const float es = dc.start[r];
+                // 16 columns at a time; the loops stay rolled: six roles share each
+                // scheduler's instruction cache
+#pragma unroll 1
+                for (int c = 0; c < 8; ++c) {
+                    uint32_t o[8];
+                    const int J = c >> 1;
+                    if (J <= quad) {
+                        uint32_t v[16];
+                        tmem_ld16_raw(tcol(i, 16 * c) + tlane, v);
+                        tmem_wait_ld();
+                        if (J < quad) {
+                            const float rf = dc.row[J][r];
+                            const float4 *cf = reinterpret_cast<const float4 *>(dc.col + 16 * c);
+#pragma unroll
+                            for (int q = 0; q < 4; ++q) {
+                                const float4 f = cf[q];
+                                o[2 * q] = pack2(__uint_as_float(v[4 * q]) * (f.x * rf),
+                                                 __uint_as_float(v[4 * q + 1]) * (f.y * rf));
+                                o[2 * q + 1] = pack2(__uint_as_float(v[4 * q + 2]) * (f.z * rf),
+                                                     __uint_as_float(v[4 * q + 3]) * (f.w * rf));
+                            }
+                        } else {
+                            const float2 gr = dc.G[r];
+                            const float4 *gc = reinterpret_cast<const float4 *>(dc.G + 16 * c);
+                            const int past = r - 16 * c;        // columns up to here count
+#pragma unroll
+                            for (int q = 0; q < 8; ++q) {
+                                const float4 g = gc[q];
+                                const float e0 = ex2((gr.x - g.x) + (gr.y - g.y));
+                                const float e1 = ex2((gr.x - g.z) + (gr.y - g.w));
+                                o[q] = pack2(2 * q <= past ? __uint_as_float(v[2 * q]) * e0 : 0.f,
+                                             2 * q < past ? __uint_as_float(v[2 * q + 1]) * e1 : 0.f);
+                            }
+                        }
+                    } else {
+#pragma unroll
+                        for (int q = 0; q < 8; ++q) o[q] = 0;
+                    }
+                    tmem_st8(tcol(i, 8 * c) + tlane, o);
+                }
+                tmem_wait_st();
+                tc_fence_before();
+                mbar_arrive(bar(kPReady, i));
+                mbar_arrive(bar(kDecFree, i));
+
+                // Yi was done before what its chunk adds to the state
+                if (!wait_warp(kYFull, i) || !wait_warp(kDFull, i)) break;
+                tc_fence_after();
+                const int64_t t = chunk_t0(i) + r;
+#pragma unroll 1
+                for (int q = 0; q < 4; ++q) {
+                    uint32_t u[16], w[16], o[8];
+                    tmem_ld16_raw(tcol(i, 64 + 16 * q) + tlane, u);
+                    tmem_ld16_raw(tcol(i, 128 + 16 * q) + tlane, w);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        const float y0 = fmaf(es, __uint_as_float(w[2 * e]), __uint_as_float(u[2 * e]));
+                        const float y1 =
+                            fmaf(es, __uint_as_float(w[2 * e + 1]), __uint_as_float(u[2 * e + 1]));
+                        o[e] = t < len ? pack2(y0, y1) : 0u;
+                    }
+                    if (q == 3) {
+                        tc_fence_before();
+                        mbar_arrive(bar(kYFree, i));
+                    }
+                    const int left = pw - 16 * q;               // columns left
+                    if (t >= p.L || left <= 0) continue;
+                    __nv_bfloat16 *row = y + t * p.val_t + 16 * q;
+                    if (p.vec == 2 && left >= 16) {
+                        asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(row),
+                                     "r"(o[0]), "r"(o[1]), "r"(o[2]), "r"(o[3]), "r"(o[4]), "r"(o[5]),
+                                     "r"(o[6]), "r"(o[7])
+                                     : "memory");
+                    } else if (p.vec) {                         // widths in eights
+                        *reinterpret_cast<uint4 *>(row) = make_uint4(o[0], o[1], o[2], o[3]);
+                        if (left >= 16)
+                            *reinterpret_cast<uint4 *>(row + 8) = make_uint4(o[4], o[5], o[6], o[7]);
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 16; ++e)
+                            if (e < left)
+                                reinterpret_cast<unsigned short *>(row)[e] =
+                                    (unsigned short)(o[e / 2] >> (16 * (e % 2)));
+                    }
+                }
+            }
+        }
+    } else if (warp < kBuild) {
+        // ---- the state: row r of 128 (STK: half-states of 64 rows), 32 columns
+        const int r = tid & 127, q0 = ((warp - kState) >> 2) * 32;
+        const int nrow = STK ? (r & 63) : r;                // row of N
+        const uint32_t tlane = (uint32_t)((warp & 3) * 32) << 16;
+        const int64_t np = (int64_t)p.N * p.P;
+        const int left = pw - q0;                           // columns of the 32
+        float S[32];
+        {
+            const float *in = nullptr;
+            if (FWD)
+                in = p.nseg > 1 ? p.seg_state + (bh * p.nseg + seg) * np
+                                : (p.h0 ? p.h0 + bh * np : nullptr);
+            const bool mine = in && nrow < p.N && (!STK || r < 64);
+            if (mine) in += (int64_t)nrow * p.P + p0 + q0;
+#pragma unroll
+            for (int q = 0; q < 32; ++q) S[q] = mine && q < left ? in[q] : 0.f;
+        }
+        // piece q of this thread's 32 columns in a buffer of 64 fp32 rows
+        auto half_at = [&](uint32_t buf, int row, int q) {
+            return sm + buf + (uint32_t)(row * 256 + (((q0 / 4 + q) ^ (row & 15)) << 4));
+        };
+        auto put_S0 = [&](int i) {
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+                sts128(sm + SM::kS0 + piece(r, q0 / 8 + q), pack2(S[8 * q], S[8 * q + 1]),
+                       pack2(S[8 * q + 2], S[8 * q + 3]), pack2(S[8 * q + 4], S[8 * q + 5]),
+                       pack2(S[8 * q + 6], S[8 * q + 7]));
+            fence_proxy_async_smem();
+            tc_fence_before();
+            mbar_arrive(bar(kS0Ready, i));
+        };
+        // kFwdCarry: the state at the start of the sequence's 64-step chunk ch
+        int sums = 0;       // exchanges so far; these warps meet on bounded barriers too
+        auto meet = [&](int which) {
+            mbar_arrive(bar(which, sums));
+            return wait_warp(which, sums);
+        };
+        auto leave = [&](int ch) {
+            if (ch == 0 || (int64_t)ch * 64 >= p.L) return;
+            float *out = p.carry + (bh * ((p.L + 63) / 64) + ch) * np;
+            float4 v[8];
+#pragma unroll
+            for (int q = 0; q < 8; ++q) v[q] = make_float4(S[4 * q], S[4 * q + 1], S[4 * q + 2], S[4 * q + 3]);
+            if (STK) {
+                if (r >= 64) {
+#pragma unroll
+                    for (int q = 0; q < 8; ++q)
+                        sts128(half_at(SM::kSum, r - 64, q), __float_as_uint(v[q].x), __float_as_uint(v[q].y),
+                               __float_as_uint(v[q].z), __float_as_uint(v[q].w));
+                }
+                if (!meet(kSumIn)) return;
+                if (r < 64) {
+#pragma unroll
+                    for (int q = 0; q < 8; ++q) {
+                        const uint4 u = lds128(half_at(SM::kSum, r, q));
+                        v[q].x += __uint_as_float(u.x);
+                        v[q].y += __uint_as_float(u.y);
+                        v[q].z += __uint_as_float(u.z);
+                        v[q].w += __uint_as_float(u.w);
+                    }
+                }
+                if (!meet(kSumOut)) return;
+                ++sums;
+            }
+            if (nrow >= p.N || (STK && r >= 64)) return;
+            out += (int64_t)nrow * p.P + p0 + q0;
+#pragma unroll
+            for (int q = 0; q < 8; ++q) {
+                if (p.P % 4 == 0) {
+                    if (4 * q < left) *reinterpret_cast<float4 *>(out + 4 * q) = v[q];
+                } else {
+                    if (4 * q < left) out[4 * q] = v[q].x;
+                    if (4 * q + 1 < left) out[4 * q + 1] = v[q].y;
+                    if (4 * q + 2 < left) out[4 * q + 2] = v[q].z;
+                    if (4 * q + 3 < left) out[4 * q + 3] = v[q].w;
+                }
+            }
+        };
+        if (FWD && n > 0) put_S0(0);
+        for (int i = 0; i < n; ++i) {
+            if (!wait_warp(kDecReady, i)) break;
+            const float a[2] = {dec[i & 1].half[0], dec[i & 1].half[1]};
+            mbar_arrive(bar(kDecFree, i));
+            if (MODE == kFwdCarry) leave(2 * (c0 + i));
+            if (!wait_warp(kDFull, i)) break;
+            tc_fence_after();
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                const int half = MODE == kSegRev ? 1 - k : k;
+                if (MODE == kFwdCarry && k == 1) leave(2 * (c0 + i) + 1);
+#pragma unroll
+                for (int q = 0; q < 2; ++q) {
+                    uint32_t v[16];
+                    tmem_ld16_raw(tcol(half, 192 + q0 + 16 * q) + tlane, v);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int e = 0; e < 16; ++e)
+                        S[16 * q + e] = fmaf(a[half], S[16 * q + e], __uint_as_float(v[e]));
+                }
+            }
+            if (FWD) {
+                if (i + 1 < n) put_S0(i + 1);
+            } else {
+                tc_fence_before();
+                mbar_arrive(bar(kS0Ready, i));              // the accumulator is free
+            }
+        }
+        // the last state (STK: the two halves' sum, through product 4's buffer)
+        float *out = !FWD ? p.seg_state + (bh * p.nseg + seg) * np
+                                  : (p.h_last && seg == p.nseg - 1 ? p.h_last + bh * np : nullptr);
+        if (out) {
+            if (STK) {
+                if (r >= 64) {
+#pragma unroll
+                    for (int q = 0; q < 8; ++q)
+                        sts128(half_at(SM::kS0, r - 64, q), __float_as_uint(S[4 * q]), __float_as_uint(S[4 * q + 1]),
+                               __float_as_uint(S[4 * q + 2]), __float_as_uint(S[4 * q + 3]));
+                }
+                if (meet(kSumIn) && r < 64) {
+#pragma unroll
+                    for (int q = 0; q < 8; ++q) {
+                        const uint4 u = lds128(half_at(SM::kS0, r, q));
+                        S[4 * q] += __uint_as_float(u.x);
+                        S[4 * q + 1] += __uint_as_float(u.y);
+                        S[4 * q + 2] += __uint_as_float(u.z);
+                        S[4 * q + 3] += __uint_as_float(u.w);
+                    }
+                }
+            }
+            if (nrow < p.N && (!STK || r < 64)) {
+                out += (int64_t)nrow * p.P + p0 + q0;
+#pragma unroll
+                for (int q = 0; q < 32; ++q)
+                    if (q < left) out[q] = S[q];
+            }
+        }
+    } else if (warp < kControl) {
+        // ---- the three parts of each chunk's decayed operand, row r = step t0 + r
+        const int r = tid & 127;
+        for (int i = 0; i < n; ++i) {
+            if (!wait_warp(kDecReady, i)) break;
+            const float w = dec[i & 1].weight[r];
+            mbar_arrive(bar(kDecFree, i));
+            const bool on = chunk_t0(i) + r < len;
+            if (!wait_cb_warp(i)) break;
+            if ((!STK || chunk_t0(i) + kC > len) && !wait_x_warp(i)) break;
+            // the tiles change (part 2, rows behind the end) and are given back only
+            // once the scores have read them
+            if (FWD && !wait_warp(kScFull, i)) break;
+            if (i >= SM::kNPL && !wait_warp(kDFull, i - SM::kNPL)) break;
+            const uint32_t keys = sm + SM::kC0 + (uint32_t)(i % SM::kNCB) * 2 * SM::kKey;
+            const uint32_t bt = keys + SM::kKey, xt = sm + SM::kX + (uint32_t)(i % SM::kNX) * kTile;
+            if (!on) {      // behind the end: whatever lies there must not meet a zero weight
+#pragma unroll
+                for (int q = 0; q < 8; ++q) {
+                    sts128(xt + piece(r, q), 0, 0, 0, 0);
+                    sts128(bt + piece(r, q), 0, 0, 0, 0);
+                    if (!STK) sts128(bt + kTile + piece(r, q), 0, 0, 0, 0);
+                }
+            }
+            const uint32_t src = STK ? bt : xt;
+            const uint32_t dst = sm + SM::kPl + (uint32_t)(i % SM::kNPL) * SM::kParts * kTile;
+            const uint32_t dst2 = STK ? bt : dst + 2 * kTile;
+#pragma unroll 2
+            for (int q = 0; q < 8; ++q) {
+                const uint4 u = lds128(src + piece(r, q));
+                const uint32_t in[4] = {u.x, u.y, u.z, u.w};
+                uint32_t p1[4], p2[4], p3[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    float v0 = lo_of(in[e]) * w, v1 = hi_of(in[e]) * w;
+                    p1[e] = pack2(v0, v1);
+                    v0 -= lo_of(p1[e]);
+                    v1 -= hi_of(p1[e]);
+                    p2[e] = pack2(v0, v1);
+                    v0 -= lo_of(p2[e]);
+                    v1 -= hi_of(p2[e]);
+                    p3[e] = STK ? pack2(0.5f * v0, 0.5f * v1) : pack2(v0, v1);
+                }
+                const uint32_t at = dst + piece(r, q);
+                sts128(at, p1[0], p1[1], p1[2], p1[3]);
+                sts128(at + kTile, p2[0], p2[1], p2[2], p2[3]);
+                sts128(dst2 + piece(r, q), p3[0], p3[1], p3[2], p3[3]);
+            }
+            fence_proxy_async_smem();
+            mbar_arrive(bar(kPlReady, i));
+        }
+    } else if (warp == kControl) {
+        // ---- the scores' products: Sc of chunk i + 1, then Y of chunk i
+        if (lane == 0 && FWD) {
+            constexpr uint32_t kIdSc = umma_idesc_bf16(128);
+            constexpr uint32_t kIdY = umma_idesc_bf16(64, false, true);
+            const uint32_t key0 = umma_lo(sm + SM::kC0, kTile), x0 = umma_lo(sm + SM::kX, 0);
+            for (int i = 0; i <= n && n > 0; ++i) {
+                if (i < n) {
+                    if (!wait_cb(i) || (i >= 2 && !wait(kYFree, i - 2))) break;
+                    tc_fence_after();
+                    const uint32_t ct = key0 + (uint32_t)(i % SM::kNCB) * umma_step(2 * SM::kKey);
+                    const uint32_t bt = ct + umma_step(SM::kKey), dS = tcol(i, 0);
+#pragma unroll
+                    for (int k = 0; k < (STK ? 4 : 8); ++k) {
+                        const uint32_t off = (k >> 2) * umma_step(kTile) + (k & 3) * umma_step(32);
+                        umma_ss(dS, ct + off, bt + off, kIdSc, k > 0);
+                    }
+                    umma_commit(bar(kScFull, i));
+                }
+                if (i > 0) {
+                    const int j = i - 1;
+                    if (!wait(kPReady, j) || !wait_x(j) || !wait(kPlReady, j)) break;
+                    tc_fence_after();
+                    const uint32_t dY = tcol(j, 64), pa = tcol(j, 0);
+                    const uint32_t xr = x0 + (uint32_t)(j % SM::kNX) * umma_step(kTile);
+#pragma unroll
+                    for (int k = 0; k < 8; ++k)
+                        umma_ts(dY, pa + 8 * k, xr + k * umma_step(2048), kIdY, k > 0);
+                    umma_commit(bar(kYFull, j));
+                }
+            }
+            if (n > 0 && ok) wait(kYFull, n - 1);   // nothing is in flight when the CTA ends
+        }
+        __syncwarp();
+    } else if (warp == kControl2) {
+        // ---- the state's products: Yi, then what the chunk adds to the state
+        if (lane == 0) {
+            constexpr uint32_t kIdY = umma_idesc_bf16(64, false, true);
+            constexpr uint32_t kIdD = umma_idesc_bf16(64, true, true);
+            constexpr uint32_t kRow16 = umma_step(2048);    // 16 rows of a tile
+            const uint32_t key0 = umma_lo(sm + SM::kC0, kTile), x0 = umma_lo(sm + SM::kX, 0),
+                           pl0 = umma_lo(sm + SM::kPl, kTile), s0 = umma_lo(sm + SM::kS0, 0);
+            for (int i = 0; i < n; ++i) {
+                const uint32_t ct = key0 + (uint32_t)(i % SM::kNCB) * umma_step(2 * SM::kKey);
+                const uint32_t bt = ct + umma_step(SM::kKey);
+                const uint32_t xr = x0 + (uint32_t)(i % SM::kNX) * umma_step(kTile);
+                if (!wait_cb(i)) break;
+                if (FWD) {
+                    if (!wait(kS0Ready, i) || (i >= 2 && !wait(kYFree, i - 2))) break;
+                    tc_fence_after();
+                    const uint32_t dYi = tcol(i, 128);
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) {
+                        const int kc = STK ? k & 3 : k;
+                        umma_ss(dYi, ct + (kc >> 2) * umma_step(kTile) + (kc & 3) * umma_step(32),
+                                s0 + k * kRow16, kIdY, k > 0);
+                    }
+                } else if (i >= 1 && !wait(kS0Ready, i - 1)) {
+                    break;
+                }
+                if (!wait(kPlReady, i) || !wait_x(i)) break;
+                tc_fence_after();
+                const uint32_t pl = pl0 + (uint32_t)(i % SM::kNPL) * umma_step(SM::kParts * kTile);
+                // the accumulators of the chunk's halves are free: the state took the
+                // last chunk's before it gave this one's S0
+                // STK: [part 0; part 1] x, then part 2 / 2 (in b's place, the same
+                // rows for both halves: leading offset 0)
+#pragma unroll 1
+                for (int part = 0; part < (STK ? 2 : 3); ++part) {
+                    const uint32_t ar = STK ? (part ? bt - umma_lo(0, kTile) : pl) : bt;
+                    const uint32_t br = STK ? xr : pl + part * umma_step(kTile);
+#pragma unroll
+                    for (int k = 0; k < 8; ++k)
+                        umma_ss(tcol(k >> 2, 192), ar + k * kRow16, br + k * kRow16, kIdD,
+                                (k & 3) > 0 || part > 0);
+                }
+                umma_commit(bar(kDFull, i));
+            }
+            if (n > 0 && ok) wait(kDFull, n - 1);
+        }
+        __syncwarp();
+    } else if (warp >= kDecay) {
+        // ---- decays: the two warps take chunks in turn, four consecutive steps per
+        // lane
+        const float *la = p.log_a + b * p.la_b + h * p.la_h;
+        double total = 0.0;
+        float nx[4];
+        auto fetch = [&](int i) {
+            const int64_t t0 = chunk_t0(i) + 4 * lane;
+#pragma unroll
+            for (int q = 0; q < 4; ++q) nx[q] = i < n && t0 + q < len ? la[(t0 + q) * p.la_t] : 0.f;
+        };
+        fetch(warp - kDecay);
+        for (int i = warp - kDecay; i < n; i += 2) {
+            double v[4];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) v[q] = decay_log2(nx[q]) + (q ? v[q ? q - 1 : 0] : 0.0);
+            fetch(i + 2);
+            double s = v[3];
+#pragma unroll
+            for (int d = 1; d < 32; d *= 2) {
+                const double o = shfl_up_d(s, d);
+                if (lane >= d) s += o;
+            }
+            total += __shfl_sync(kFull, s, 31);
+            s -= v[3];
+            float2 G[4];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const double c = s + v[q];
+                const float hi = (float)c;
+                G[q] = make_float2(hi, (float)(c - (double)hi));
+            }
+            if (i >= 2 && !wait_warp(kDecFree, i - 2)) break;
+            Decays &dc = dec[i & 1];
+            float4 *gs = reinterpret_cast<float4 *>(dc.G + 4 * lane);
+            gs[0] = make_float4(G[0].x, G[0].y, G[1].x, G[1].y);
+            gs[1] = make_float4(G[2].x, G[2].y, G[3].x, G[3].y);
+            __syncwarp();
+            const float2 mid = dc.G[kC / 2 - 1], end = dc.G[kC - 1];
+#pragma unroll 1
+            for (int q = 0; q < 4; ++q) {
+                const int t = 32 * q + lane;
+                const float2 g = dc.G[t];
+                const float es = ex2(g.x + g.y);
+                dc.start[t] = es;
+                const float2 to = q < 2 ? mid : end;
+                dc.weight[t] = MODE != kSegRev ? ex2((to.x - g.x) + (to.y - g.y))
+                               : q < 2         ? es
+                                               : ex2((g.x - mid.x) + (g.y - mid.y));
+                if (FWD) {
+                    const float2 own = dc.G[32 * q + 31];
+                    dc.col[t] = ex2((own.x - g.x) + (own.y - g.y));
+#pragma unroll 1
+                    for (int e = 0; e < q; ++e) {
+                        const float2 b = dc.G[32 * e + 31];
+                        dc.row[e][t] = ex2((g.x - b.x) + (g.y - b.y));
+                    }
+                }
+            }
+            if (lane == 0) {
+                dc.half[0] = ex2(mid.x + mid.y);
+                dc.half[1] = ex2((end.x - mid.x) + (end.y - mid.y));
+            }
+            mbar_arrive(bar(kDecReady, i));
+        }
+        if (!FWD && lane == 0) totals[warp - kDecay] = total;
+    } else if (p.vec) {
+        // ---- copies
+        if (warp == kProducer && lane == 0) {
+            int i = 0;
+            for (; i < n && ok; ++i) {
+                const int t0 = (int)chunk_t0(i);
+                if (i >= SM::kNCB && !wait(kDFull, i - SM::kNCB)) break;
+                const uint32_t keys = sm + SM::kC0 + (uint32_t)(i % SM::kNCB) * 2 * SM::kKey;
+                const uint32_t cb = bar_cb(i);
+                const int subs = STK ? 1 : 2;
+                mbar_expect_tx(cb, (uint32_t)(FWD ? 2 : 1) * SM::kKey);
+                for (int q = 0; q < subs; ++q) {
+                    // the state alone needs one key tensor: b, or c in reverse
+                    if (FWD) tma_load_4d(keys + q * kTile, &cmap, 64 * q, t0, g, b, cb);
+                    tma_load_4d(keys + SM::kKey + q * kTile, MODE == kSegRev ? &cmap : &bmap, 64 * q, t0,
+                                g, b, cb);
+                }
+                if (i >= SM::kNX && (!wait(kDFull, i - SM::kNX) || (FWD && !wait(kYFull, i - SM::kNX)))) break;
+                const uint32_t xb = bar_x(i);
+                mbar_expect_tx(xb, kTile);
+                tma_load_4d(sm + SM::kX + (uint32_t)(i % SM::kNX) * kTile, &xmap, p0, t0, h, b, xb);
+            }
+        }
+        __syncwarp();
+    } else {
+        // ---- the same tiles by plain loads of one warp: odd widths, odd
+        // addresses
+        const int l = lane;
+        const __nv_bfloat16 *kc = (const __nv_bfloat16 *)p.c + b * p.key_b + g * p.key_h;
+        const __nv_bfloat16 *kb = (const __nv_bfloat16 *)(MODE == kSegRev ? p.c : p.b) + b * p.key_b +
+                                  g * p.key_h;
+        const __nv_bfloat16 *vx = (const __nv_bfloat16 *)(MODE == kSegRev ? p.g_y : p.x) + b * p.val_b +
+                                  h * p.val_h + p0;
+        auto copy = [&](uint32_t dst, const __nv_bfloat16 *src, int64_t stride, int width, int64_t t0) {
+            for (int e = l; e < kC * 8; e += kLoaders) {
+                const int r = e / 8, q = e % 8;
+                uint32_t w[4] = {0, 0, 0, 0};
+                if (t0 + r < len) {
+                    const unsigned short *s =
+                        reinterpret_cast<const unsigned short *>(src + (t0 + r) * stride) + 8 * q;
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        if (8 * q + j < width) w[j / 2] |= (uint32_t)s[j] << (16 * (j % 2));
+                }
+                sts128(dst + piece(r, q), w[0], w[1], w[2], w[3]);
+            }
+        };
+        for (int i = 0; i < n && ok; ++i) {
+            const int64_t t0 = chunk_t0(i);
+            if (i >= SM::kNCB && !wait_warp(kDFull, i - SM::kNCB)) break;
+            const uint32_t keys = sm + SM::kC0 + (uint32_t)(i % SM::kNCB) * 2 * SM::kKey;
+            for (int q = 0; q < (STK ? 1 : 2); ++q) {
+                if (FWD)
+                    copy(keys + q * kTile, kc + 64 * q, p.key_t, p.N - 64 * q, t0);
+                copy(keys + SM::kKey + q * kTile, kb + 64 * q, p.key_t, p.N - 64 * q, t0);
+            }
+            fence_proxy_async_smem();
+            mbar_arrive(bar_cb(i));
+            if (i >= SM::kNX && (!wait_warp(kDFull, i - SM::kNX) ||
+                                  (FWD && !wait_warp(kYFull, i - SM::kNX))))
+                break;
+            copy(sm + SM::kX + (uint32_t)(i % SM::kNX) * kTile, vx, p.val_t, pw, t0);
+            fence_proxy_async_smem();
+            mbar_arrive(bar_x(i));
+        }
+    }
+    tc_fence_before();
+    if (__syncthreads_or(!ok)) {
+        // a wait gave up (the status word says so): let copies and products in
+        // flight land, for a millisecond at most, before the CTA ends
+        const uint64_t t = global_ns();
+        for (int it = 0; it < (1 << 20) && global_ns() - t < 1000000u; ++it) __nanosleep(1000);
+        __syncthreads();
+    }
+    tc_fence_after();
+    if (warp == kControl) tmem_dealloc(tmem, 512);
+    if (!FWD && ps == 0 && tid == 0)
+        p.seg_decay[bh * p.nseg + seg] = exp2f((float)(totals[0] + totals[1]));
+    if (FWD) {
+        // rows of the segment's chunks behind the sequence's end
+        __nv_bfloat16 *y = (__nv_bfloat16 *)p.y + b * p.val_b + h * p.val_h + p0;
+        const int64_t t_end = imin64((int64_t)c1 * kC, p.L);
+        for (int64_t t = (int64_t)(c0 + n) * kC + warp; t < t_end; t += kTcTh / 32)
+            for (int q = lane; q < pw; q += 32) y[t * p.val_t + q] = __float2bfloat16_rn(0.f);
+    }
+}
+
+bool encode_map(CUtensorMap *m, const void *ptr, int width, int heads, const DecayParams &p,
+                int64_t st, int64_t sh, int64_t sb) {
+    const cuuint64_t dim[4] = {(cuuint64_t)width, (cuuint64_t)p.L, (cuuint64_t)heads, (cuuint64_t)p.B};
+    const cuuint64_t stride[3] = {(cuuint64_t)st * 2, (cuuint64_t)sh * 2, (cuuint64_t)sb * 2};
+    const cuuint32_t box[4] = {64, kC, 1, 1};
+    const cuuint32_t es[4] = {1, 1, 1, 1};
+    return tensor_map_encoder()(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(ptr), dim,
+                                stride, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                                CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+                                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <bool STK, int MODE>
+cudaError_t go(const DecayParams &p, int *status, bool first, cudaStream_t st) {
+    CUtensorMap cm, bm, xm;
+    memset(&cm, 0, sizeof(cm));
+    memset(&bm, 0, sizeof(bm));
+    memset(&xm, 0, sizeof(xm));
+    const void *x = MODE == kSegRev ? p.g_y : p.x;
+    if (p.vec) {
+        if (!encode_map(&cm, p.c, p.N, p.G, p, p.key_t, p.key_h, p.key_b) ||
+            !encode_map(&bm, p.b, p.N, p.G, p, p.key_t, p.key_h, p.key_b) ||
+            !encode_map(&xm, x, p.P, p.H, p, p.val_t, p.val_h, p.val_b))
+            return cudaErrorInvalidValue;
+    }
+    auto kern = k_decay_tc<STK, MODE>;
+    const int smem = (int)Smem<STK, MODE>::kTotal;
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    const int64_t grid = (int64_t)p.B * p.H * p.nseg * p.pslices;
+    kern<<<dim3((unsigned)grid), kTcTh, smem, st>>>(cm, bm, xm, TcParams{p, status, first ? 1 : 0});
+    return cudaGetLastError();
+}
+
+template <bool STK>
+cudaError_t fwd_tc(const DecayParams &p, int *status, cudaStream_t st) {
+    if (p.nseg > 1) {
+        cudaError_t e = go<STK, kSegFwd>(p, status, true, st);
+        if (e != cudaSuccess) return e;
+        e = launch_decay_join(p, p.h0, false, nullptr, st);
+        if (e != cudaSuccess) return e;
+    }
+    return go<STK, kFwd>(p, status, p.nseg <= 1, st);
+}
+
+}  // namespace
+
+bool decay_tc_copies() { return tensor_map_encoder() != nullptr; }
+
+cudaError_t launch_decay_fwd_tc(const DecayParams &p, int *status, cudaStream_t st) {
+    if (!p.carry) return p.N <= 64 ? fwd_tc<true>(p, status, st) : fwd_tc<false>(p, status, st);
+    // with the adjoint's states: N, P <= 64
+    if (p.nseg > 1) {
+        cudaError_t e = go<true, kSegFwd>(p, status, true, st);
+        if (e != cudaSuccess) return e;
+        e = launch_decay_join(p, p.h0, false, nullptr, st);
+        if (e != cudaSuccess) return e;
+    }
+    return go<true, kFwdCarry>(p, status, p.nseg <= 1, st);
+}
+
+cudaError_t launch_decay_seg_rev_tc(const DecayParams &p, int *status, cudaStream_t st) {
+    return go<true, kSegRev>(p, status, false, st);
+}
+
+}  // namespace pdssm
