@@ -9,52 +9,15 @@
 // The logits are recomputed where they are needed: they are H K values per
 // step against D_in inputs, so writing them would move more bytes than u.
 // Sums over steps go per CTA to scratch and are added in order by a second
-// kernel.
-#include "common.cuh"
+// kernel.  bf16 u runs on the tensor cores (balance_tc.cu); fp32 u here, on
+// the CUDA cores.
+#include "balance.cuh"
 
 namespace pdssm {
 namespace {
 
 constexpr int kBalThreads = 256;
 constexpr int kBalRows = 64;            // steps per tile
-constexpr int kBalMaxK = 32, kBalMaxD = 256;
-
-struct BalParams {
-    int B, H, K, D;
-    int64_t L, rows;                    // rows = B L
-    const void *u;
-    const float *W;
-    const int32_t *k;
-    const int32_t *lengths;
-    float inv_tau;
-    const int32_t *counts;
-    const float *g_loss;
-    void *g_u;
-    int slices;
-    float *part;                        // per slice: sums of p [H][K], or of g_W [H][K][D]
-    int32_t *part_n;                    // per slice: counts [H][K]
-};
-
-__device__ __forceinline__ int64_t bal_len(const BalParams &p, int b) {
-    if (!p.lengths) return p.L;
-    const int64_t n = p.lengths[b];
-    return n < 0 ? 0 : (n > p.L ? p.L : n);
-}
-
-// steps in front of the lengths, by one warp or more; every thread gets it
-__device__ __forceinline__ int64_t bal_steps(const BalParams &p) {
-    if (!p.lengths) return p.rows;
-    int64_t n = 0;
-    for (int b = 0; b < p.B; ++b) n += bal_len(p, b);
-    return n;
-}
-
-__device__ __forceinline__ bool bal_live(const BalParams &p, int64_t row) {
-    if (row >= p.rows) return false;
-    if (!p.lengths) return true;
-    const int b = (int)(row / p.L);
-    return row - (int64_t)b * p.L < bal_len(p, b);
-}
 
 // CTA work over one tile of kBalRows steps: u tile in shared memory (odd row
 // length), one head's weights, logits and softmax weights.
@@ -360,9 +323,16 @@ pdssm_status check_bal(const pdssm_dims *d) {
     return PDSSM_OK;
 }
 
+// partial sums of g_W, or of p with the counts
+size_t bal_partials(const pdssm_dims &d, int slices) {
+    return align256((size_t)slices * (size_t)(d.H * d.K) * (size_t)(d.D_in > 2 ? d.D_in : 2) * 4);
+}
+
 size_t bal_scratch(const pdssm_dims &d) {
-    const size_t n = (size_t)bal_slices(d.B * d.L, d.H) * (size_t)(d.H * d.K);
-    return align256(n * (size_t)(d.D_in > 2 ? d.D_in : 2) * 4);
+    const BalTcPlan pl = bal_tc_plan(d);
+    const size_t a = bal_partials(d, bal_slices(d.B * d.L, d.H));
+    const size_t b = bal_partials(d, pl.slices) + bal_tc_extra(pl);
+    return a > b ? a : b;
 }
 
 pdssm_status bal_common(const pdssm_dims *d, const void *u, pdssm_dtype dt, const float *W,
@@ -382,15 +352,25 @@ pdssm_status bal_common(const pdssm_dims *d, const void *u, pdssm_dtype dt, cons
     q.B = (int)d->B; q.H = (int)d->H; q.K = (int)d->K; q.D = (int)d->D_in;
     q.L = d->L; q.rows = d->B * d->L;
     q.u = u; q.W = W; q.lengths = lengths; q.inv_tau = inv_tau;
-    q.slices = bal_slices(q.rows, d->H);
+    q.slices = dt == PDSSM_BF16 ? bal_tc_plan(*d).slices : bal_slices(q.rows, d->H);
     q.part = (float *)scratch;
     q.part_n = (int32_t *)(q.part + (int64_t)q.slices * q.H * q.K);
     *p = q;
     return PDSSM_OK;
 }
 
-cudaError_t run_any(const BalParams &p, pdssm_dtype dt, int what, cudaStream_t st) {
-    return dt == PDSSM_BF16 ? run_k<__nv_bfloat16>(p, what, st) : run_k<float>(p, what, st);
+// fp32 on the CUDA cores, bf16 on the tensor cores (which keep W's parts
+// behind the partial sums in scratch)
+cudaError_t run_any(const pdssm_dims &d, const BalParams &p, pdssm_dtype dt, int what,
+                    cudaStream_t st) {
+    if (dt != PDSSM_BF16) return run_k<float>(p, what, st);
+    const BalTcPlan pl = bal_tc_plan(d);
+    unsigned char *parts = reinterpret_cast<unsigned char *>(p.part) + bal_partials(d, pl.slices);
+    if (what == 0 || what == 1 || !p.g_u) {
+        const cudaError_t e = launch_bal_tc_prep(p, pl, parts, st);
+        if (e != cudaSuccess) return e;
+    }
+    return launch_bal_tc(p, pl, what, parts, st);
 }
 
 }  // namespace
@@ -417,7 +397,7 @@ pdssm_status pdssm_select_balance_fwd(const pdssm_dims *dims, const void *u, pds
         return arg_fail(PDSSM_ERR_INVALID_ARG, "NULL k, loss, counts or probs");
     p.k = k;
     cudaStream_t s = (cudaStream_t)stream;
-    cudaError_t e = run_any(p, u_dtype, 0, s);
+    cudaError_t e = run_any(*dims, p, u_dtype, 0, s);
     if (e != cudaSuccess) return cuda_fail(e, "balance sums");
     k_bal_loss<<<p.H, 32, 0, s>>>(p, loss, counts, probs);
     e = cudaGetLastError();
@@ -439,11 +419,11 @@ pdssm_status pdssm_select_balance_bwd(const pdssm_dims *dims, const void *u, pds
     cudaStream_t s = (cudaStream_t)stream;
     cudaError_t e;
     if (g_u && p.rows > 0) {
-        e = run_any(p, u_dtype, 1, s);
+        e = run_any(*dims, p, u_dtype, 1, s);
         if (e != cudaSuccess) return cuda_fail(e, "balance g_u");
     }
     if (g_W) {
-        e = run_any(p, u_dtype, 2, s);
+        e = run_any(*dims, p, u_dtype, 2, s);
         if (e != cudaSuccess) return cuda_fail(e, "balance g_W");
         const int64_t n = (int64_t)p.H * p.K * p.D;
         k_bal_gw_sum<<<(unsigned)((n + 255) / 256), 256, 0, s>>>(p, g_W);

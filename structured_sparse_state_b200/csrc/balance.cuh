@@ -1,0 +1,64 @@
+// Balance loss of the hard selection: what its kernels share.
+#pragma once
+
+#include "common.cuh"
+
+namespace pdssm {
+
+constexpr int kBalMaxK = 32, kBalMaxD = 256;
+
+struct BalParams {
+    int B, H, K, D;
+    int64_t L, rows;                    // rows = B L
+    const void *u;
+    const float *W;
+    const int32_t *k;
+    const int32_t *lengths;
+    float inv_tau;
+    const int32_t *counts;
+    const float *g_loss;
+    void *g_u;
+    int slices;
+    float *part;                        // per slice: sums of p [H][K], or of g_W [H][K][D]
+    int32_t *part_n;                    // per slice: counts [H][K]
+};
+
+__device__ __forceinline__ int64_t bal_len(const BalParams &p, int b) {
+    if (!p.lengths) return p.L;
+    const int64_t n = p.lengths[b];
+    return n < 0 ? 0 : (n > p.L ? p.L : n);
+}
+
+// steps in front of the lengths, by one warp or more; every thread gets it
+__device__ __forceinline__ int64_t bal_steps(const BalParams &p) {
+    if (!p.lengths) return p.rows;
+    int64_t n = 0;
+    for (int b = 0; b < p.B; ++b) n += bal_len(p, b);
+    return n;
+}
+
+__device__ __forceinline__ bool bal_live(const BalParams &p, int64_t row) {
+    if (row >= p.rows) return false;
+    if (!p.lengths) return true;
+    const int b = (int)(row / p.L);
+    return row - (int64_t)b * p.L < bal_len(p, b);
+}
+
+// Plan of the tensor-core kernels (bf16 u): groups of heads whose weights, as
+// three bf16 parts, lie in shared memory.
+struct BalTcPlan {
+    int KT;                             // entries of a head, rounded up to a power of two
+    int N;                              // entries of a group (heads per group * KT): 64 or 128
+    int Dp;                             // D rounded up to 64
+    int groups, slices, tiles;          // slices of the 128-row tiles per group
+    size_t w_bytes;                     // bytes of one group's parts
+};
+BalTcPlan bal_tc_plan(const pdssm_dims &d);
+size_t bal_tc_extra(const BalTcPlan &pl);   // scratch behind the partial sums
+// what: 0 sums and counts, 1 g_u, 2 g_W partials (slices of [H][K][D])
+cudaError_t launch_bal_tc(const BalParams &p, const BalTcPlan &pl, int what, void *w_parts,
+                          cudaStream_t st);
+cudaError_t launch_bal_tc_prep(const BalParams &p, const BalTcPlan &pl, void *w_parts,
+                               cudaStream_t st);
+
+}  // namespace pdssm

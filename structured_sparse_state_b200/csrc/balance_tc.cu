@@ -1,0 +1,624 @@
+// Balance loss of the hard selection for bf16 u on the tensor cores (tcgen05).
+//
+// A group is as many heads as fill N = 128 entries (64 above D = 128; a head
+// takes K entries rounded up to a power of two).  Its weights lie in shared
+// memory as three bf16 parts (8 + 8 + 8 bits of fp32), so that the logits
+//     L = u W^T            128 rows x N, K = D, three products
+// have fp32 accuracy (u is bf16 by itself).  Eight warps take a finished L
+// from TMEM, a row and half of its columns per thread: softmax per head, then
+//   sums    column sums of p over the rows, in registers over the CTA's tiles;
+//           counts by shared-memory atomics (integers)
+//   g_u     G, the logits' gradients, back to TMEM as bf16, and
+//           g_u += G W  (K = N; W's first two parts: G's rounding to bf16 is
+//           then the only one besides g_u's own), over the groups
+//   g_W     G as three bf16 parts to shared memory (two, then the third), and
+//           g_W += G^T u  (K = 128 rows), kept in TMEM over the CTA's tiles
+// L is double-buffered: the next tile's products run under this one's softmax.
+//
+// Bound: tensor pipe and the softmax's issue slots, about equal; u is read
+// once per group (from L2 after the first).
+#include <string.h>
+
+#include "balance.cuh"
+#include "umma.cuh"
+
+namespace pdssm {
+namespace {
+
+enum { kSums = 0, kGu = 1, kGw = 2 };
+constexpr int kEpi = 8;                         // softmax warps
+constexpr int kTh = (kEpi + 2) * 32;            // + products, + copies
+constexpr int kRows = 128;
+
+enum { kUFull, kWFull, kLFull, kGReady, kGHalf, kGThird, kDone, kGuFull, kGuFree, kBars };
+
+struct TcP {
+    BalParams p;
+    BalTcPlan pl;
+    const unsigned char *parts;                 // [groups][3][Dp/64][N][128 bytes], swizzled
+    const float *freq;                          // counts / T [groups * N], then per head the
+                                                // factor g_loss K inv_tau / T
+    int vec;
+    int nslot, ustages;
+    uint32_t o_u, o_g, o_tab, o_bar;            // shared-memory offsets (weights at 0)
+};
+
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+__device__ __forceinline__ float lo_of(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float hi_of(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
+__device__ __forceinline__ uint32_t piece(int r, int q) {
+    return (uint32_t)(r * 128 + ((q ^ (r & 7)) << 4));
+}
+__device__ __forceinline__ void sts128(uint32_t a, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
+    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(x), "r"(y), "r"(z), "r"(w)
+                 : "memory");
+}
+
+// Softmax of the heads in 32 columns, logits in units of log2 e / tau applied
+// here; columns of absent entries (k >= K) get 0.
+template <int KT>
+__device__ __forceinline__ void softmax32(float (&v)[32], int K, float scale, bool live) {
+#pragma unroll
+    for (int h = 0; h < 32 / KT; ++h) {
+        float *x = v + h * KT;
+        float m = x[0];
+#pragma unroll
+        for (int k = 1; k < KT; ++k)
+            if (k < K) m = fmaxf(m, x[k]);
+        float z = 0.f;
+#pragma unroll
+        for (int k = 0; k < KT; ++k) {
+            x[k] = k < K ? exp2f((x[k] - m) * scale) : 0.f;
+            z += x[k];
+        }
+        const float inv = live ? 1.f / z : 0.f;
+#pragma unroll
+        for (int k = 0; k < KT; ++k) x[k] = live ? x[k] * inv : 0.f;
+    }
+}
+
+template <int KT, int MODE>
+__global__ void __launch_bounds__(kTh, 1)
+    k_bal_tc(const __grid_constant__ CUtensorMap umap, const TcP t) {
+    const BalParams &p = t.p;
+    const BalTcPlan &pl = t.pl;
+    extern __shared__ unsigned char sm_raw[];
+    const uint32_t sm = (smem_u32(sm_raw) + 1023u) & ~1023u;
+    unsigned char *smg = sm_raw + (sm - smem_u32(sm_raw));
+    __shared__ uint32_t tmem_slot;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int N = pl.N, Dp = pl.Dp, atoms = Dp / 64;
+    const uint32_t ubytes = (uint32_t)kRows * Dp * 2, wpart = (uint32_t)N * Dp * 2;
+    auto bar = [&](int which, int i) { return sm + t.o_bar + 8u * (uint32_t)(4 * which + (i & 3)); };
+    bool ok = true;
+    auto wait = [&](int which, int i) {
+        return ok = ok && mbar_wait_hot(bar(which, i), (uint32_t)((i >> 2) & 1));
+    };
+    auto wait_warp = [&](int which, int i) { return ok = __all_sync(kFull, wait(which, i)); };
+
+    // an item is a tile and a group: the CTA's group and every slices-th tile,
+    // or (g_u) every group of every gridDim-th tile
+    const int group0 = MODE == kGu ? 0 : blockIdx.x % pl.groups;
+    const int ng = MODE == kGu ? pl.groups : 1;
+    const int tile0 = MODE == kGu ? blockIdx.x : blockIdx.x / pl.groups;
+    const int tstep = MODE == kGu ? gridDim.x : pl.slices;
+    const int ntiles = tile0 < pl.tiles ? (pl.tiles - tile0 + tstep - 1) / tstep : 0;
+    const int items = ntiles * ng;
+    auto row0 = [&](int tile) { return (int64_t)(tile0 + tile * tstep) * kRows; };
+    // W's slot of an item: resident when the groups fit, else a ring
+    const bool resident = ng <= t.nslot;
+    auto wslot = [&](int i) { return resident ? i % ng : i % t.nslot; };
+    auto wait_w = [&](int i) {
+        const int use = resident ? 0 : i / t.nslot;
+        return ok = ok && mbar_wait_hot(bar(kWFull, wslot(i)), (uint32_t)(use & 1));
+    };
+    auto wait_u = [&](int tile) {
+        return ok = ok && mbar_wait_hot(bar(kUFull, tile % t.ustages), (uint32_t)((tile / t.ustages) & 1));
+    };
+
+    if (tid == 0) {
+        for (int s = 0; s < 4; ++s) {
+            mbar_init(bar(kUFull, s), t.vec ? 1 : 32);
+            mbar_init(bar(kWFull, s), 1);
+            mbar_init(bar(kLFull, s), 1);
+            mbar_init(bar(kGReady, s), 32 * kEpi);
+            mbar_init(bar(kGHalf, s), 1);
+            mbar_init(bar(kGThird, s), 32 * kEpi);
+            mbar_init(bar(kDone, s), 1);
+            mbar_init(bar(kGuFull, s), 1);
+            mbar_init(bar(kGuFree, s), 32 * kEpi);
+        }
+        fence_mbar_init();
+    }
+    if (warp == kEpi) tmem_alloc(smem_u32(&tmem_slot), 512);
+    int *cnt = reinterpret_cast<int *>(smg + t.o_tab);          // sums: [N]
+    if (MODE == kSums)
+        for (int e = tid; e < N; e += kTh) cnt[e] = 0;
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = tmem_slot;
+    // TMEM: L 2 x 128 columns (g_u: G as bf16 in the first half of each half),
+    // then g_u or g_W, Dp columns
+    auto tL = [&](int i) { return tmem + (uint32_t)(i & 1) * 128; };
+    const uint32_t tAcc = tmem + 256;
+
+    const float scale = p.inv_tau * 1.4426950408889634f;
+    const int quad = warp & 3, half = (warp >> 2) & 1, r = quad * 32 + lane;
+    const int cols = N / 2;                                     // of this thread
+    const uint32_t tlane = (uint32_t)(quad * 32) << 16;
+
+    if (warp < kEpi) {
+        float acc[MODE == kSums ? 64 : 1];
+#pragma unroll
+        for (int q = 0; q < (MODE == kSums ? 64 : 1); ++q) acc[q] = 0.f;
+        for (int i = 0; i < items; ++i) {
+            const int tile = i / ng, gi = i % ng;
+            const int c0 = (group0 + gi) * N + half * cols;     // first entry of this thread
+            const int64_t row = row0(tile) + r;
+            const bool live = bal_live(p, row);
+            if (MODE == kSums) {                                // while the products run
+                const int64_t b = row / p.L, s = row - b * p.L;
+                if (live)
+                    for (int h = c0 / KT; h < (c0 + cols) / KT && h < p.H; ++h) {
+                        const int kk = p.k[(b * p.H + h) * p.L + s];
+                        if (kk >= 0 && kk < p.K) atomicAdd(&cnt[h * KT + kk - group0 * N], 1);
+                    }
+            }
+            if (!wait_warp(kLFull, i)) break;
+            tc_fence_after();
+            if (MODE == kGw) {
+                // the parts of the last tile's G have been read
+                if (i > 0 && !wait_warp(kDone, i - 1)) break;
+                if (!live) {        // behind an end: u must not meet a zero gradient as a NaN
+                    const uint32_t ut = sm + t.o_u + (uint32_t)(tile % t.ustages) * ubytes;
+                    for (int a = half; a < atoms; a += 2)
+                        for (int q = 0; q < 8; ++q) sts128(ut + a * (kRows * 128) + piece(r, q), 0, 0, 0, 0);
+                }
+            }
+            uint32_t third[MODE == kGw ? 32 : 1];
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+                if (32 * q >= cols) break;
+                uint32_t raw[32];
+                float v[32];
+                tmem_ld32(tL(i) + half * cols + 32 * q + tlane, raw);
+                tmem_wait_ld();
+#pragma unroll
+                for (int e = 0; e < 32; ++e) v[e] = __uint_as_float(raw[e]);
+                softmax32<KT>(v, p.K, scale, live);
+                if constexpr (MODE == kSums) {
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) acc[32 * q + e] += v[e];
+                } else {
+                    const float4 *tf = reinterpret_cast<const float4 *>(t.freq + c0 + 32 * q);
+                    const int heads = pl.groups * N / KT;
+                    float fq[32];
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        const float4 a = __ldg(tf + e);
+                        fq[4 * e] = a.x;
+                        fq[4 * e + 1] = a.y;
+                        fq[4 * e + 2] = a.z;
+                        fq[4 * e + 3] = a.w;
+                    }
+#pragma unroll
+                    for (int h = 0; h < 32 / KT; ++h) {
+                        const float by = __ldg(t.freq + heads * KT + (c0 + 32 * q) / KT + h);
+                        float dot = 0.f;
+#pragma unroll
+                        for (int k = 0; k < KT; ++k) dot = fmaf(v[h * KT + k], fq[h * KT + k], dot);
+#pragma unroll
+                        for (int k = 0; k < KT; ++k)
+                            v[h * KT + k] = by * v[h * KT + k] * (fq[h * KT + k] - dot);
+                    }
+                    if constexpr (MODE == kGu) {
+                        uint32_t o[16];
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) o[e] = pack2(v[2 * e], v[2 * e + 1]);
+                        tmem_st16(tL(i) + half * cols + 16 * q + tlane, o);
+                    } else {
+                        // piece e of this row: entries half * cols + 32 q + 8 e
+                        const uint32_t gt = sm + t.o_g;
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            uint32_t p1[4], p2[4];
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) {
+                                float a = v[8 * e + 2 * k], b = v[8 * e + 2 * k + 1];
+                                p1[k] = pack2(a, b);
+                                a -= lo_of(p1[k]);
+                                b -= hi_of(p1[k]);
+                                p2[k] = pack2(a, b);
+                                third[16 * q + 4 * e + k] = pack2(a - lo_of(p2[k]), b - hi_of(p2[k]));
+                            }
+                            const int col = half * cols + 32 * q + 8 * e;
+                            const uint32_t at = gt + (uint32_t)(col / 64) * (kRows * 128) + piece(r, (col & 63) / 8);
+                            sts128(at, p1[0], p1[1], p1[2], p1[3]);
+                            sts128(at + (uint32_t)kRows * N * 2, p2[0], p2[1], p2[2], p2[3]);
+                        }
+                    }
+                }
+            }
+            if (MODE == kGu) tmem_wait_st();
+            if (MODE == kGw) fence_proxy_async_smem();
+            tc_fence_before();
+            mbar_arrive(bar(kGReady, i));
+            if constexpr (MODE == kGw) {
+                if (!wait_warp(kGHalf, i)) break;       // parts 0 and 1 have been read
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    if (8 * e >= cols) break;
+                    const int col = half * cols + 8 * e;
+                    sts128(sm + t.o_g + (uint32_t)(col / 64) * (kRows * 128) + piece(r, (col & 63) / 8),
+                           third[4 * e], third[4 * e + 1], third[4 * e + 2], third[4 * e + 3]);
+                }
+                fence_proxy_async_smem();
+                mbar_arrive(bar(kGThird, i));
+            }
+            if (MODE == kGu && gi == ng - 1) {
+                if (!wait_warp(kGuFull, tile)) break;
+                tc_fence_after();
+                __nv_bfloat16 *out = (__nv_bfloat16 *)p.g_u + row * p.D;
+                const int dcols = Dp / 2;
+#pragma unroll 1
+                for (int q = 0; q < dcols; q += 16) {
+                    uint32_t raw[16];
+                    float v[16];
+                    tmem_ld16_raw(tAcc + half * dcols + q + tlane, raw);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) v[e] = live ? __uint_as_float(raw[e]) : 0.f;
+                    const int col = half * dcols + q;
+                    if (row >= p.rows) continue;
+                    if (t.vec) {
+#pragma unroll
+                        for (int e = 0; e < 16; e += 8)
+                            if (col + e < p.D)
+                                *reinterpret_cast<uint4 *>(out + col + e) =
+                                    make_uint4(pack2(v[e], v[e + 1]), pack2(v[e + 2], v[e + 3]),
+                                               pack2(v[e + 4], v[e + 5]), pack2(v[e + 6], v[e + 7]));
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 16; ++e)
+                            if (col + e < p.D) out[col + e] = __float2bfloat16_rn(v[e]);
+                    }
+                }
+                tc_fence_before();
+                mbar_arrive(bar(kGuFree, tile));
+            }
+        }
+        if constexpr (MODE == kGw) {
+            // g_W of the group over the CTA's tiles: lane = entry
+            if (items > 0) wait_warp(kDone, items - 1);
+            tc_fence_after();
+            const int c = group0 * N + r, h = c / KT, k = c % KT;
+            const int slice = blockIdx.x / pl.groups;
+            const bool mine = r < N && h < p.H && k < p.K;
+            float *out = p.part + (((int64_t)slice * p.H + h) * p.K + k) * p.D;
+            const int dcols = Dp / 2;
+#pragma unroll 1
+            for (int q = 0; q < dcols; q += 16) {
+                uint32_t raw[16];
+                tmem_ld16_raw(tAcc + half * dcols + q + tlane, raw);
+                tmem_wait_ld();
+#pragma unroll
+                for (int e = 0; e < 16; ++e) {
+                    const int col = half * dcols + q + e;
+                    if (mine && col < p.D) out[col] = items > 0 ? __uint_as_float(raw[e]) : 0.f;
+                }
+            }
+        }
+        if constexpr (MODE == kSums) {
+            // column sums over the warp's rows, one warp's 64 columns at a time
+            float *red = reinterpret_cast<float *>(smg + t.o_g);        // [8][64]
+#pragma unroll
+            for (int q = 0; q < 64; ++q) {
+                float s = acc[q];
+#pragma unroll
+                for (int d = 16; d; d >>= 1) s += __shfl_xor_sync(kFull, s, d);
+                if (lane == 0) red[warp * 64 + q] = s;
+            }
+        }
+    } else if (warp == kEpi) {
+        // ---- products
+        if (lane == 0) {
+            const uint32_t idL = umma_idesc_bf16(N), idU = umma_idesc_bf16(Dp, false, true),
+                           idW = umma_idesc_bf16(Dp, true, true);
+            const uint32_t w0 = umma_lo(sm, 16), wmn0 = umma_lo(sm, (uint32_t)N * 128);
+            const uint32_t u0 = umma_lo(sm + t.o_u, 16), umn0 = umma_lo(sm + t.o_u, kRows * 128);
+            // the two 64-entry blocks of G (one: the same rows twice)
+            const uint32_t g0 = umma_lo(sm + t.o_g, N > 64 ? kRows * 128 : 0);
+            auto second = [&](int j) {          // what an item's G goes into
+                const int tile = j / ng, gi = j % ng;
+                if (!wait(kGReady, j)) return;
+                if (MODE == kGu) {
+                    if (gi == 0 && tile > 0 && !wait(kGuFree, tile - 1)) return;
+                    tc_fence_after();
+                    const uint32_t wb = wmn0 + (uint32_t)wslot(j) * umma_step((uint32_t)pl.w_bytes);
+#pragma unroll 1
+                    for (int part = 0; part < 2; ++part) {
+                        uint32_t br = wb + part * umma_step(wpart);
+#pragma unroll 1
+                        for (int k = 0; k < N / 16; ++k, br += umma_step(2048)) {
+                            // entries 16 k.. lie in half k / (N / 32), packed two to a column
+                            const int kh = k / (N / 32), kr = k % (N / 32);
+                            umma_ts(tAcc, tL(j) + kh * (N / 2) + 8 * kr, br, idU, gi > 0 || part > 0 || k > 0);
+                        }
+                    }
+                    if (gi == ng - 1) umma_commit(bar(kGuFull, tile));
+                } else {
+                    const uint32_t ub = umn0 + (uint32_t)(tile % t.ustages) * umma_step(ubytes);
+#pragma unroll 1
+                    for (int part = 0; part < 3; ++part) {
+                        if (part == 2) {
+                            umma_commit(bar(kGHalf, j));
+                            if (!wait(kGThird, j)) return;
+                        }
+                        tc_fence_after();
+                        uint32_t ar = g0 + (part == 1 ? umma_step((uint32_t)kRows * N * 2) : 0u), br = ub;
+#pragma unroll 1
+                        for (int k = 0; k < 8; ++k, ar += umma_step(2048), br += umma_step(2048))
+                            umma_ss(tAcc, ar, br, idW, j > 0 || part > 0 || k > 0);
+                    }
+                }
+                umma_commit(bar(kDone, j));
+            };
+            // with one slot for several groups' weights, the next item's can only
+            // come once this one is done with them
+            const bool ahead = resident || t.nslot > 1;
+            for (int i = 0; i < items && ok; ++i) {
+                const int tile = i / ng;
+                if (MODE != kSums && i > 0 && !ahead) second(i - 1);
+                if (!wait_u(tile) || !wait_w(i)) break;
+                // L's buffer: its G was taken by the second product (g_u, g_W), or
+                // its columns have been read
+                if (i >= 2 && !wait(kGReady, i - 2)) break;
+                tc_fence_after();
+                const uint32_t ub = u0 + (uint32_t)(tile % t.ustages) * umma_step(ubytes);
+                const uint32_t wb = w0 + (uint32_t)wslot(i) * umma_step((uint32_t)pl.w_bytes);
+#pragma unroll 1
+                for (int part = 0; part < 3; ++part)
+#pragma unroll 1
+                    for (int a = 0; a < atoms; ++a) {
+                        const uint32_t ar = ub + a * umma_step(kRows * 128);
+                        const uint32_t br = wb + part * umma_step(wpart) + a * umma_step((uint32_t)N * 128);
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            umma_ss(tL(i), ar + k * umma_step(32), br + k * umma_step(32), idL,
+                                    part > 0 || a > 0 || k > 0);
+                    }
+                umma_commit(bar(kLFull, i));
+                if (MODE != kSums && i > 0 && ahead) second(i - 1);
+            }
+            if (MODE != kSums && items > 0 && ok) second(items - 1);
+            // nothing is in flight when the CTA ends
+            if (items > 0 && ok) wait(MODE == kSums ? kLFull : kDone, items - 1);
+        }
+        __syncwarp();
+    } else {
+        // ---- copies: W's parts as they lie, u by tensor map or plain loads
+        for (int i = 0; i < items && ok; ++i) {
+            const int tile = i / ng, gi = i % ng;
+            if (lane == 0) {
+                const bool load = resident ? i < ng : true;
+                if (load) {
+                    if (!resident && i >= t.nslot) wait(kDone, i - t.nslot);
+                    if (ok) {
+                        const uint32_t wb = bar(kWFull, wslot(i));
+                        const uint32_t bytes = (uint32_t)pl.w_bytes;
+                        mbar_expect_tx(wb, bytes);
+                        const unsigned char *src = t.parts + (size_t)(group0 + gi) * pl.w_bytes;
+                        for (uint32_t o = 0; o < bytes; o += 16384)
+                            bulk_g2s(sm + (uint32_t)wslot(i) * bytes + o, src + o, min(16384u, bytes - o), wb);
+                    }
+                }
+            }
+            ok = __shfl_sync(kFull, (int)ok, 0) != 0;
+            if (!ok) break;
+            if (gi) continue;
+            // a stage of u is free once its last reader is done
+            if (tile >= t.ustages) {
+                const int last = (tile - t.ustages) * ng + ng - 1;
+                if (!wait_warp(MODE == kGw ? kDone : kLFull, last)) break;
+            }
+            const uint32_t ut = sm + t.o_u + (uint32_t)(tile % t.ustages) * ubytes;
+            const uint32_t ub = bar(kUFull, tile % t.ustages);
+            if (t.vec) {
+                if (lane == 0) {
+                    mbar_expect_tx(ub, ubytes);
+                    for (int a = 0; a < atoms; ++a)
+                        asm volatile(
+                            "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes "
+                            "[%0], [%1, {%2, %3}], [%4];" ::"r"(ut + a * (kRows * 128)),
+                            "l"(reinterpret_cast<uint64_t>(&umap)), "r"(64 * a), "r"((int)row0(tile)), "r"(ub)
+                            : "memory");
+                }
+                __syncwarp();
+            } else {
+                const unsigned short *u = reinterpret_cast<const unsigned short *>(p.u);
+                for (int e = lane; e < kRows * atoms * 8; e += 32) {
+                    const int rr = e / (atoms * 8), q = e % (atoms * 8);
+                    const int64_t row = row0(tile) + rr;
+                    uint32_t w[4] = {0, 0, 0, 0};
+                    if (row < p.rows)
+#pragma unroll
+                        for (int j = 0; j < 8; ++j)
+                            if (8 * q + j < p.D) w[j / 2] |= (uint32_t)u[row * p.D + 8 * q + j] << (16 * (j % 2));
+                    sts128(ut + (q / 8) * (kRows * 128) + piece(rr, q % 8), w[0], w[1], w[2], w[3]);
+                }
+                fence_proxy_async_smem();
+                mbar_arrive(ub);
+            }
+        }
+    }
+    tc_fence_before();
+    const bool failed = __syncthreads_or(!ok);
+    if (failed) {
+        // a wait gave up: let copies and products in flight land, for a
+        // millisecond at most, before the CTA ends
+        const uint64_t s = global_ns();
+        for (int it = 0; it < (1 << 20) && global_ns() - s < 1000000u; ++it) __nanosleep(1000);
+        __syncthreads();
+    }
+    tc_fence_after();
+    if (warp == kEpi) tmem_dealloc(tmem, 512);
+    // a wait that gave up must not pass for a result
+    const float nan = __int_as_float(0x7fffffff);
+    if (MODE == kSums) {
+        const float *red = reinterpret_cast<const float *>(smg + t.o_g);
+        const int slice = blockIdx.x / pl.groups;
+        for (int e = tid; e < N; e += kTh) {
+            const int c = group0 * N + e, h = c / KT, k = c % KT;
+            if (h >= p.H || k >= p.K) continue;
+            const int w = e / (N / 2) * 4, col = e % (N / 2);
+            const float s = (red[w * 64 + col] + red[(w + 1) * 64 + col]) +
+                            (red[(w + 2) * 64 + col] + red[(w + 3) * 64 + col]);
+            const int64_t at = ((int64_t)slice * p.H + h) * p.K + k;
+            p.part[at] = failed ? nan : s;
+            p.part_n[at] = cnt[e];
+        }
+    } else if (failed) {
+        if (MODE == kGw) {
+            for (int e = tid; e < N * p.D; e += kTh) {
+                const int c = group0 * N + e / p.D, h = c / KT, k = c % KT;
+                if (h < p.H && k < p.K)
+                    p.part[(((int64_t)(blockIdx.x / pl.groups) * p.H + h) * p.K + k) * p.D + e % p.D] = nan;
+            }
+        } else {
+            for (int tile = 0; tile < ntiles; ++tile)
+                for (int64_t e = tid; e < (int64_t)kRows * p.D; e += kTh)
+                    if (row0(tile) + e / p.D < p.rows)
+                        ((__nv_bfloat16 *)p.g_u)[row0(tile) * p.D + e] = __float2bfloat16_rn(nan);
+        }
+    }
+}
+
+// W's three bf16 parts, per group in the shared-memory image of a K-major
+// operand: [3][Dp / 64][N rows][128 bytes], 128-byte swizzle.
+// With counts (backward) also the table of counts / T and the heads' factors.
+__global__ void k_bal_parts(BalParams p, BalTcPlan pl, unsigned char *parts, float *freq) {
+    const int64_t n = (int64_t)pl.groups * pl.N * (pl.Dp / 2);
+    const int64_t e = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
+    if (e >= n) return;
+    const int d = (int)(e % (pl.Dp / 2)) * 2;
+    const int64_t c = e / (pl.Dp / 2);
+    const int h = (int)(c / pl.KT), k = (int)(c % pl.KT);
+    const int g = (int)(c / pl.N), row = (int)(c % pl.N);
+    if (p.counts && d == 0) {
+        const int64_t steps = bal_steps(p);
+        const float inv = steps > 0 ? 1.f / (float)steps : 0.f;
+        freq[c] = h < p.H && k < p.K ? (float)p.counts[h * p.K + k] * inv : 0.f;
+        if (k == 0)
+            freq[(int64_t)pl.groups * pl.N + h] =
+                h < p.H ? p.g_loss[h] * ((float)p.K * p.inv_tau) * inv : 0.f;
+    }
+    float a = 0.f, b = 0.f;
+    if (h < p.H && k < p.K) {
+        const float *w = p.W + ((int64_t)h * p.K + k) * p.D;
+        if (d < p.D) a = w[d];
+        if (d + 1 < p.D) b = w[d + 1];
+    }
+    unsigned char *out = parts + (size_t)g * pl.w_bytes + (size_t)(d / 64) * pl.N * 128 +
+                         piece(row, (d & 63) / 8) + (d & 7) * 2;
+#pragma unroll
+    for (int i = 0; i < 3; ++i) {
+        const uint32_t w = pack2(a, b);
+        a -= lo_of(w);
+        b -= hi_of(w);
+        *reinterpret_cast<uint32_t *>(out + (size_t)i * pl.N * pl.Dp * 2) = w;
+    }
+}
+
+template <int KT, int MODE>
+cudaError_t go(const BalParams &p, const BalTcPlan &pl, const void *parts, cudaStream_t st) {
+    TcP t;
+    memset(&t, 0, sizeof(t));
+    t.p = p;
+    t.pl = pl;
+    t.parts = (const unsigned char *)parts;
+    t.freq = reinterpret_cast<const float *>(t.parts + (size_t)pl.groups * pl.w_bytes);
+    t.nslot = MODE == kGu && pl.groups > 1 && pl.Dp <= 128 ? 2 : 1;
+    t.ustages = MODE == kGu || pl.Dp > 128 ? 1 : 2;
+    const uint32_t u = (uint32_t)kRows * pl.Dp * 2;
+    uint32_t o = t.nslot * (uint32_t)pl.w_bytes;
+    t.o_u = o; o += t.ustages * u;
+    t.o_g = o; o += MODE == kGw ? 2u * kRows * pl.N * 2 : MODE == kSums ? 8 * 64 * 4 : 0;
+    t.o_tab = o; o += MODE == kSums ? pl.N * 4 : 0;
+    t.o_bar = o; o += 32 * kBars;
+    const int smem = (int)o + 1024;
+    t.vec = p.D % 8 == 0 && ((uintptr_t)p.u % 16) == 0 && ((uintptr_t)p.g_u % 16) == 0 &&
+            p.rows > 0 && tensor_map_encoder() != nullptr;
+    CUtensorMap map;
+    memset(&map, 0, sizeof(map));
+    if (t.vec) {
+        const cuuint64_t gdim[2] = {(cuuint64_t)p.D, (cuuint64_t)p.rows};
+        const cuuint64_t gstride[1] = {(cuuint64_t)p.D * 2};
+        const cuuint32_t box[2] = {64u, (cuuint32_t)kRows};
+        const cuuint32_t es[2] = {1, 1};
+        if (tensor_map_encoder()(&map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void *>(p.u), gdim,
+                                 gstride, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                                 CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+                                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+            return cudaErrorInvalidValue;
+    }
+    auto kern = k_bal_tc<KT, MODE>;
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    const int grid = MODE == kGu ? (pl.tiles < 148 ? pl.tiles : 148) : pl.groups * pl.slices;
+    kern<<<grid, kTh, smem, st>>>(map, t);
+    return cudaGetLastError();
+}
+
+template <int KT>
+cudaError_t go_k(const BalParams &p, const BalTcPlan &pl, int what, const void *parts, cudaStream_t st) {
+    if (what == kSums) return go<KT, kSums>(p, pl, parts, st);
+    if (what == kGu) return go<KT, kGu>(p, pl, parts, st);
+    return go<KT, kGw>(p, pl, parts, st);
+}
+
+}  // namespace
+
+BalTcPlan bal_tc_plan(const pdssm_dims &d) {
+    BalTcPlan pl{};
+    pl.KT = 2;
+    while (pl.KT < d.K) pl.KT *= 2;
+    pl.Dp = (int)((d.D_in + 63) / 64 * 64);
+    pl.N = pl.Dp <= 128 ? 128 : 64;     // three parts of a group: at most 96 KB
+    pl.groups = (int)((d.H * pl.KT + pl.N - 1) / pl.N);
+    pl.tiles = (int)((d.B * d.L + kRows - 1) / kRows);
+    int s = 148 / pl.groups;
+    if (s > pl.tiles) s = pl.tiles;
+    pl.slices = s < 1 ? 1 : s;
+    pl.w_bytes = (size_t)3 * pl.N * pl.Dp * 2;
+    return pl;
+}
+
+size_t bal_tc_extra(const BalTcPlan &pl) {
+    return (size_t)pl.groups * pl.w_bytes + align256((size_t)pl.groups * pl.N * 8);
+}
+
+cudaError_t launch_bal_tc_prep(const BalParams &p, const BalTcPlan &pl, void *parts, cudaStream_t st) {
+    const int64_t n = (int64_t)pl.groups * pl.N * (pl.Dp / 2);
+    unsigned char *w = (unsigned char *)parts;
+    k_bal_parts<<<dim3((unsigned)((n + 255) / 256)), 256, 0, st>>>(
+        p, pl, w, reinterpret_cast<float *>(w + (size_t)pl.groups * pl.w_bytes));
+    return cudaGetLastError();
+}
+
+cudaError_t launch_bal_tc(const BalParams &p, const BalTcPlan &pl, int what, void *parts,
+                          cudaStream_t st) {
+    switch (pl.KT) {
+        case 2: return go_k<2>(p, pl, what, parts, st);
+        case 4: return go_k<4>(p, pl, what, parts, st);
+        case 8: return go_k<8>(p, pl, what, parts, st);
+        case 16: return go_k<16>(p, pl, what, parts, st);
+        default: return go_k<32>(p, pl, what, parts, st);
+    }
+}
+
+}  // namespace pdssm
