@@ -58,6 +58,12 @@ __device__ __forceinline__ void sts128(uint32_t a, uint32_t x, uint32_t y, uint3
                  : "memory");
 }
 
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
 // Softmax of the heads in 32 columns, logits in units of log2 e / tau applied
 // here; columns of absent entries (k >= K) get 0.
 template <int KT>
@@ -72,7 +78,7 @@ __device__ __forceinline__ void softmax32(float (&v)[32], int K, float scale, bo
         float z = 0.f;
 #pragma unroll
         for (int k = 0; k < KT; ++k) {
-            x[k] = k < K ? exp2f((x[k] - m) * scale) : 0.f;
+            x[k] = k < K ? ex2((x[k] - m) * scale) : 0.f;
             z += x[k];
         }
         const float inv = live ? 1.f / z : 0.f;
@@ -161,13 +167,16 @@ __global__ void __launch_bounds__(kTh, 1)
             const int c0 = (group0 + gi) * N + half * cols;     // first entry of this thread
             const int64_t row = row0(tile) + r;
             const bool live = bal_live(p, row);
-            if (MODE == kSums) {                                // while the products run
-                const int64_t b = row / p.L, s = row - b * p.L;
-                if (live)
-                    for (int h = c0 / KT; h < (c0 + cols) / KT && h < p.H; ++h) {
-                        const int kk = p.k[(b * p.H + h) * p.L + s];
-                        if (kk >= 0 && kk < p.K) atomicAdd(&cnt[h * KT + kk - group0 * N], 1);
-                    }
+            // the selections of this thread's heads: on their way while the
+            // products run
+            constexpr int kHeads = MODE == kSums ? 64 / KT : 1;
+            int sel[kHeads];
+            if (MODE == kSums) {
+                const uint32_t b = (uint32_t)row / (uint32_t)p.L, s = (uint32_t)row - b * (uint32_t)p.L;
+                const int32_t *kr = p.k + ((int64_t)b * p.H + c0 / KT) * p.L + s;
+#pragma unroll
+                for (int h = 0; h < kHeads; ++h)
+                    sel[h] = live && h < cols / KT && c0 / KT + h < p.H ? kr[(int64_t)h * p.L] : -1;
             }
             if (!wait_warp(kLFull, i)) break;
             tc_fence_after();
@@ -243,6 +252,12 @@ __global__ void __launch_bounds__(kTh, 1)
                         }
                     }
                 }
+            }
+            if (MODE == kSums) {
+#pragma unroll
+                for (int h = 0; h < kHeads; ++h)
+                    if (sel[h] >= 0 && sel[h] < p.K)
+                        atomicAdd(&cnt[half * cols + h * KT + sel[h]], 1);
             }
             if (MODE == kGu) tmem_wait_st();
             if (MODE == kGw) fence_proxy_async_smem();
@@ -342,12 +357,18 @@ __global__ void __launch_bounds__(kTh, 1)
                     const uint32_t wb = wmn0 + (uint32_t)wslot(j) * umma_step((uint32_t)pl.w_bytes);
 #pragma unroll 1
                     for (int part = 0; part < 2; ++part) {
-                        uint32_t br = wb + part * umma_step(wpart);
+                        // entries 16 k.. lie in half kh of the columns, packed two to one
 #pragma unroll 1
-                        for (int k = 0; k < N / 16; ++k, br += umma_step(2048)) {
-                            // entries 16 k.. lie in half k / (N / 32), packed two to a column
-                            const int kh = k / (N / 32), kr = k % (N / 32);
-                            umma_ts(tAcc, tL(j) + kh * (N / 2) + 8 * kr, br, idU, gi > 0 || part > 0 || k > 0);
+                        for (int kh = 0; kh < 2; ++kh) {
+                            const uint32_t ar = tL(j) + kh * (N / 2);
+                            const uint32_t br = wb + part * umma_step(wpart) + kh * (N / 32) * umma_step(2048);
+                            const bool more = gi > 0 || part > 0 || kh > 0;
+                            umma_ts(tAcc, ar, br, idU, more);
+                            umma_ts(tAcc, ar + 8, br + umma_step(2048), idU, true);
+                            if (N > 64) {
+                                umma_ts(tAcc, ar + 16, br + 2 * umma_step(2048), idU, true);
+                                umma_ts(tAcc, ar + 24, br + 3 * umma_step(2048), idU, true);
+                            }
                         }
                     }
                     if (gi == ng - 1) umma_commit(bar(kGuFull, tile));
@@ -360,10 +381,11 @@ __global__ void __launch_bounds__(kTh, 1)
                             if (!wait(kGThird, j)) return;
                         }
                         tc_fence_after();
-                        uint32_t ar = g0 + (part == 1 ? umma_step((uint32_t)kRows * N * 2) : 0u), br = ub;
-#pragma unroll 1
-                        for (int k = 0; k < 8; ++k, ar += umma_step(2048), br += umma_step(2048))
-                            umma_ss(tAcc, ar, br, idW, j > 0 || part > 0 || k > 0);
+                        const uint32_t ar = g0 + (part == 1 ? umma_step((uint32_t)kRows * N * 2) : 0u);
+#pragma unroll
+                        for (int k = 0; k < 8; ++k)
+                            umma_ss(tAcc, ar + k * umma_step(2048), ub + k * umma_step(2048), idW,
+                                    j > 0 || part > 0 || k > 0);
                     }
                 }
                 umma_commit(bar(kDone, j));
