@@ -537,12 +537,23 @@ __global__ void k_decay_join(DecayParams p, const float *first, int reverse, flo
     if (e >= (int64_t)p.B * p.H * np) return;
     const int64_t bh = e / np, i = e % np;
     float s = first ? first[e] : 0.f;
-    for (int q = 0; q < p.nseg; ++q) {
-        const int seg = reverse ? p.nseg - 1 - q : q;
-        float *at = p.seg_state + (bh * p.nseg + seg) * np + i;
-        const float loc = *at;
-        *at = s;
-        s = fmaf(p.seg_decay[bh * p.nseg + seg], s, loc);
+    // the loads of several segments on their way at once
+    constexpr int kAhead = 8;
+    for (int q0 = 0; q0 < p.nseg; q0 += kAhead) {
+        float loc[kAhead], a[kAhead];
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) {
+            const int q = q0 + k, seg = reverse ? p.nseg - 1 - q : q;
+            loc[k] = q < p.nseg ? p.seg_state[(bh * p.nseg + seg) * np + i] : 0.f;
+            a[k] = q < p.nseg ? p.seg_decay[bh * p.nseg + seg] : 0.f;
+        }
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) {
+            const int q = q0 + k, seg = reverse ? p.nseg - 1 - q : q;
+            if (q >= p.nseg) break;
+            p.seg_state[(bh * p.nseg + seg) * np + i] = s;
+            s = fmaf(a[k], s, loc[k]);
+        }
     }
     if (last) last[e] = s;
 }

@@ -18,10 +18,8 @@
 // operand is exact.  P and the copy of S0 that product 4 reads are rounded to
 // bf16 once each: y is bf16 itself, so they add a rounding of its own size.
 //
-// N <= 64 (STK): the split operand is b; parts 0 and 1 are stacked along M (64
-// rows each), part 2 (halved, which is exact) is added to both halves, and
-// the two half-states are decayed and used side by side (product 4 reads
-// [c, c] against both).  N <= 128: the split operand is x, and M = N = 128.
+// N <= 64 (STK): the split operand is b, its rows twice to fill M = 128.
+// N <= 128: the split operand is x, and M = N = 128.
 //
 // Decays: within a 32 x 32 diagonal block each pair's exponential; a block to
 // its left as e^{G_i - G_e} e^{G_e - G_j}, e the last step of j's block: both
@@ -69,12 +67,12 @@ struct __align__(16) Decays {
 // that no role can be a whole round of a slot behind), and the rings' own.
 enum {
     kFullCB, kFullX, kScFull, kPReady, kPlReady, kDFull, kS0Ready, kYFull, kYFree,
-    kDecReady, kDecFree, kSumIn, kSumOut, kNumBars
+    kDecReady, kDecFree, kNumBars
 };
 
-template <bool STK, int MODE>
+template <bool STK>
 struct Smem {
-    static constexpr int kNCB = STK && MODE != kFwdCarry ? 3 : 2;       // stages of c and b
+    static constexpr int kNCB = STK ? 3 : 2;            // stages of c and b
     static constexpr int kNX = STK ? 2 : 1;             // stages of x
     static constexpr int kNPL = STK ? 2 : 1;            // sets of split parts
     static constexpr int kParts = STK ? 2 : 3;          // of a set (STK: part 2 takes b's place)
@@ -83,9 +81,7 @@ struct Smem {
     static constexpr uint32_t kX = kC0 + kNCB * 2 * kKey;       // [kNX]
     static constexpr uint32_t kPl = kX + kNX * kTile;   // [kNPL][kParts]
     static constexpr uint32_t kS0 = kPl + kNPL * kParts * kTile;
-    // the sum of the half-states on its way to memory
-    static constexpr uint32_t kSum = kS0 + kTile;
-    static constexpr uint32_t kDec = kSum + (STK && MODE == kFwdCarry ? 64 * 256 : 0);
+    static constexpr uint32_t kDec = kS0 + kTile;
     static constexpr uint32_t kBar = kDec + 2 * sizeof(Decays);
     static constexpr uint32_t kTotal = kBar + 32 * kNumBars + 1024;       // + alignment
 };
@@ -132,7 +128,7 @@ template <bool STK, int MODE>
 __global__ void __launch_bounds__(kTcTh, 1)
     k_decay_tc(const __grid_constant__ CUtensorMap cmap, const __grid_constant__ CUtensorMap bmap,
                const __grid_constant__ CUtensorMap xmap, const TcParams tp) {
-    using SM = Smem<STK, MODE>;
+    using SM = Smem<STK>;
     constexpr bool FWD = MODE == kFwd || MODE == kFwdCarry;
     const DecayParams &p = tp.d;
     extern __shared__ unsigned char sm_raw[];
@@ -173,8 +169,6 @@ __global__ void __launch_bounds__(kTcTh, 1)
             mbar_init(bar(kPlReady, s), 128);
             mbar_init(bar(kDFull, s), 1);
             mbar_init(bar(kS0Ready, s), 256);
-            mbar_init(bar(kSumIn, s), 256);
-            mbar_init(bar(kSumOut, s), 256);
             mbar_init(bar(kYFull, s), 1);
             mbar_init(bar(kYFree, s), 128);
             mbar_init(bar(kDecReady, s), 32);
@@ -309,30 +303,42 @@ __global__ void __launch_bounds__(kTcTh, 1)
             }
         }
     } else if (warp < kBuild) {
-        // ---- the state: row r of 128 (STK: half-states of 64 rows), 32 columns
-        const int r = tid & 127, q0 = ((warp - kState) >> 2) * 32;
-        const int nrow = STK ? (r & 63) : r;                // row of N
-        const uint32_t tlane = (uint32_t)((warp & 3) * 32) << 16;
+        // ---- the state: a row and kCols columns per thread (STK: the accumulators'
+        // rows 64.. repeat 0..63, so their lanes take other columns)
+        constexpr int kCols = STK ? 16 : 32;
+        const int quad = warp & 3, lr = quad * 32 + lane;
+        const int r = STK ? (lr & 63) : lr;                 // row of N
+        const int q0 = ((warp - kState) >> 2) * 32 + (STK ? (quad >> 1) * 16 : 0);
+        const uint32_t tlane = (uint32_t)(quad * 32) << 16;
         const int64_t np = (int64_t)p.N * p.P;
-        const int left = pw - q0;                           // columns of the 32
-        float S[32];
+        const int left = r < p.N ? pw - q0 : 0;             // columns of this thread
+        const int64_t at = (int64_t)r * p.P + p0 + q0;
+        float S[kCols];
         {
             const float *in = nullptr;
             if (FWD)
                 in = p.nseg > 1 ? p.seg_state + (bh * p.nseg + seg) * np
                                 : (p.h0 ? p.h0 + bh * np : nullptr);
-            const bool mine = in && nrow < p.N && (!STK || r < 64);
-            if (mine) in += (int64_t)nrow * p.P + p0 + q0;
 #pragma unroll
-            for (int q = 0; q < 32; ++q) S[q] = mine && q < left ? in[q] : 0.f;
+            for (int q = 0; q < kCols; ++q) S[q] = in && q < left ? in[at + q] : 0.f;
         }
-        // piece q of this thread's 32 columns in a buffer of 64 fp32 rows
-        auto half_at = [&](uint32_t buf, int row, int q) {
-            return sm + buf + (uint32_t)(row * 256 + (((q0 / 4 + q) ^ (row & 15)) << 4));
+        auto leave = [&](float *out) {                      // this thread's part of the state
+            out += at;
+#pragma unroll
+            for (int q = 0; q < kCols; q += 4) {
+                if (p.P % 4 == 0) {
+                    if (q < left)
+                        *reinterpret_cast<float4 *>(out + q) = make_float4(S[q], S[q + 1], S[q + 2], S[q + 3]);
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        if (q + e < left) out[q + e] = S[q + e];
+                }
+            }
         };
         auto put_S0 = [&](int i) {
 #pragma unroll
-            for (int q = 0; q < 4; ++q)
+            for (int q = 0; q < kCols / 8; ++q)
                 sts128(sm + SM::kS0 + piece(r, q0 / 8 + q), pack2(S[8 * q], S[8 * q + 1]),
                        pack2(S[8 * q + 2], S[8 * q + 3]), pack2(S[8 * q + 4], S[8 * q + 5]),
                        pack2(S[8 * q + 6], S[8 * q + 7]));
@@ -341,110 +347,42 @@ __global__ void __launch_bounds__(kTcTh, 1)
             mbar_arrive(bar(kS0Ready, i));
         };
         // kFwdCarry: the state at the start of the sequence's 64-step chunk ch
-        int sums = 0;       // exchanges so far; these warps meet on bounded barriers too
-        auto meet = [&](int which) {
-            mbar_arrive(bar(which, sums));
-            return wait_warp(which, sums);
-        };
-        auto leave = [&](int ch) {
-            if (ch == 0 || (int64_t)ch * 64 >= p.L) return;
-            float *out = p.carry + (bh * ((p.L + 63) / 64) + ch) * np;
-            float4 v[8];
-#pragma unroll
-            for (int q = 0; q < 8; ++q) v[q] = make_float4(S[4 * q], S[4 * q + 1], S[4 * q + 2], S[4 * q + 3]);
-            if (STK) {
-                if (r >= 64) {
-#pragma unroll
-                    for (int q = 0; q < 8; ++q)
-                        sts128(half_at(SM::kSum, r - 64, q), __float_as_uint(v[q].x), __float_as_uint(v[q].y),
-                               __float_as_uint(v[q].z), __float_as_uint(v[q].w));
-                }
-                if (!meet(kSumIn)) return;
-                if (r < 64) {
-#pragma unroll
-                    for (int q = 0; q < 8; ++q) {
-                        const uint4 u = lds128(half_at(SM::kSum, r, q));
-                        v[q].x += __uint_as_float(u.x);
-                        v[q].y += __uint_as_float(u.y);
-                        v[q].z += __uint_as_float(u.z);
-                        v[q].w += __uint_as_float(u.w);
-                    }
-                }
-                if (!meet(kSumOut)) return;
-                ++sums;
-            }
-            if (nrow >= p.N || (STK && r >= 64)) return;
-            out += (int64_t)nrow * p.P + p0 + q0;
-#pragma unroll
-            for (int q = 0; q < 8; ++q) {
-                if (p.P % 4 == 0) {
-                    if (4 * q < left) *reinterpret_cast<float4 *>(out + 4 * q) = v[q];
-                } else {
-                    if (4 * q < left) out[4 * q] = v[q].x;
-                    if (4 * q + 1 < left) out[4 * q + 1] = v[q].y;
-                    if (4 * q + 2 < left) out[4 * q + 2] = v[q].z;
-                    if (4 * q + 3 < left) out[4 * q + 3] = v[q].w;
-                }
-            }
+        const int chunks64 = (int)((p.L + 63) / 64);
+        auto carry = [&](int ch) {
+            if (ch > 0 && ch < chunks64) leave(p.carry + (bh * chunks64 + ch) * np);
         };
         if (FWD && n > 0) put_S0(0);
         for (int i = 0; i < n; ++i) {
             if (!wait_warp(kDecReady, i)) break;
             const float a[2] = {dec[i & 1].half[0], dec[i & 1].half[1]};
             mbar_arrive(bar(kDecFree, i));
-            if (MODE == kFwdCarry) leave(2 * (c0 + i));
+            if (MODE == kFwdCarry) carry(2 * (c0 + i));
             if (!wait_warp(kDFull, i)) break;
             tc_fence_after();
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
                 const int half = MODE == kSegRev ? 1 - k : k;
-                if (MODE == kFwdCarry && k == 1) leave(2 * (c0 + i) + 1);
+                if (MODE == kFwdCarry && k == 1) carry(2 * (c0 + i) + 1);
 #pragma unroll
-                for (int q = 0; q < 2; ++q) {
+                for (int q = 0; q < kCols; q += 16) {
                     uint32_t v[16];
-                    tmem_ld16_raw(tcol(half, 192 + q0 + 16 * q) + tlane, v);
+                    tmem_ld16_raw(tcol(half, 192 + q0 + q) + tlane, v);
                     tmem_wait_ld();
 #pragma unroll
-                    for (int e = 0; e < 16; ++e)
-                        S[16 * q + e] = fmaf(a[half], S[16 * q + e], __uint_as_float(v[e]));
+                    for (int e = 0; e < 16; ++e) S[q + e] = fmaf(a[half], S[q + e], __uint_as_float(v[e]));
                 }
             }
             if (FWD) {
                 if (i + 1 < n) put_S0(i + 1);
             } else {
                 tc_fence_before();
-                mbar_arrive(bar(kS0Ready, i));              // the accumulator is free
+                mbar_arrive(bar(kS0Ready, i));              // the accumulators are free
             }
         }
-        // the last state (STK: the two halves' sum, through product 4's buffer)
-        float *out = !FWD ? p.seg_state + (bh * p.nseg + seg) * np
-                                  : (p.h_last && seg == p.nseg - 1 ? p.h_last + bh * np : nullptr);
-        if (out) {
-            if (STK) {
-                if (r >= 64) {
-#pragma unroll
-                    for (int q = 0; q < 8; ++q)
-                        sts128(half_at(SM::kS0, r - 64, q), __float_as_uint(S[4 * q]), __float_as_uint(S[4 * q + 1]),
-                               __float_as_uint(S[4 * q + 2]), __float_as_uint(S[4 * q + 3]));
-                }
-                if (meet(kSumIn) && r < 64) {
-#pragma unroll
-                    for (int q = 0; q < 8; ++q) {
-                        const uint4 u = lds128(half_at(SM::kS0, r, q));
-                        S[4 * q] += __uint_as_float(u.x);
-                        S[4 * q + 1] += __uint_as_float(u.y);
-                        S[4 * q + 2] += __uint_as_float(u.z);
-                        S[4 * q + 3] += __uint_as_float(u.w);
-                    }
-                }
-            }
-            if (nrow < p.N && (!STK || r < 64)) {
-                out += (int64_t)nrow * p.P + p0 + q0;
-#pragma unroll
-                for (int q = 0; q < 32; ++q)
-                    if (q < left) out[q] = S[q];
-            }
-        }
+        if (!FWD)
+            leave(p.seg_state + (bh * p.nseg + seg) * np);
+        else if (p.h_last && seg == p.nseg - 1)
+            leave(p.h_last + bh * np);
     } else if (warp < kControl) {
         // ---- the three parts of each chunk's decayed operand, row r = step t0 + r
         const int r = tid & 127;
@@ -486,7 +424,7 @@ __global__ void __launch_bounds__(kTcTh, 1)
                     p2[e] = pack2(v0, v1);
                     v0 -= lo_of(p2[e]);
                     v1 -= hi_of(p2[e]);
-                    p3[e] = STK ? pack2(0.5f * v0, 0.5f * v1) : pack2(v0, v1);
+                    p3[e] = pack2(v0, v1);
                 }
                 const uint32_t at = dst + piece(r, q);
                 sts128(at, p1[0], p1[1], p1[2], p1[3]);
@@ -548,11 +486,9 @@ __global__ void __launch_bounds__(kTcTh, 1)
                     tc_fence_after();
                     const uint32_t dYi = tcol(i, 128);
 #pragma unroll
-                    for (int k = 0; k < 8; ++k) {
-                        const int kc = STK ? k & 3 : k;
-                        umma_ss(dYi, ct + (kc >> 2) * umma_step(kTile) + (kc & 3) * umma_step(32),
+                    for (int k = 0; k < (STK ? 4 : 8); ++k)
+                        umma_ss(dYi, ct + (k >> 2) * umma_step(kTile) + (k & 3) * umma_step(32),
                                 s0 + k * kRow16, kIdY, k > 0);
-                    }
                 } else if (i >= 1 && !wait(kS0Ready, i - 1)) {
                     break;
                 }
@@ -561,11 +497,11 @@ __global__ void __launch_bounds__(kTcTh, 1)
                 const uint32_t pl = pl0 + (uint32_t)(i % SM::kNPL) * umma_step(SM::kParts * kTile);
                 // the accumulators of the chunk's halves are free: the state took the
                 // last chunk's before it gave this one's S0
-                // STK: [part 0; part 1] x, then part 2 / 2 (in b's place, the same
-                // rows for both halves: leading offset 0)
+                // STK: the parts' 64 columns twice as the 128 rows (leading offset 0;
+                // part 2 lies in b's place)
 #pragma unroll 1
-                for (int part = 0; part < (STK ? 2 : 3); ++part) {
-                    const uint32_t ar = STK ? (part ? bt - umma_lo(0, kTile) : pl) : bt;
+                for (int part = 0; part < 3; ++part) {
+                    const uint32_t ar = STK ? (part < 2 ? pl + part * umma_step(kTile) : bt) - umma_lo(0, kTile) : bt;
                     const uint32_t br = STK ? xr : pl + part * umma_step(kTile);
 #pragma unroll
                     for (int k = 0; k < 8; ++k)
@@ -756,7 +692,7 @@ cudaError_t go(const DecayParams &p, int *status, bool first, cudaStream_t st) {
             return cudaErrorInvalidValue;
     }
     auto kern = k_decay_tc<STK, MODE>;
-    const int smem = (int)Smem<STK, MODE>::kTotal;
+    const int smem = (int)Smem<STK>::kTotal;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     const int64_t grid = (int64_t)p.B * p.H * p.nseg * p.pslices;
