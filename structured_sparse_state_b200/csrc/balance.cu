@@ -17,7 +17,7 @@ namespace pdssm {
 namespace {
 
 constexpr int kBalThreads = 256;
-constexpr int kBalRows = 64;            // steps per tile
+constexpr int kBalRows = 64;            // steps per tile (four threads per step)
 
 // CTA work over one tile of kBalRows steps: u tile in shared memory (odd row
 // length), one head's weights, logits and softmax weights.
@@ -31,18 +31,23 @@ struct Tile {
         sW = su + kBalRows * ld;
         sp = sW + KT * ld;
     }
+    // a warp per row, its lanes along the row
     __device__ __forceinline__ void load_u(const BalParams &p, int64_t r0) {
         const T *u = (const T *)p.u;
-        for (int e = threadIdx.x; e < kBalRows * p.D; e += kBalThreads) {
-            const int r = e / p.D, q = e % p.D;
-            su[r * ld + q] = bal_live(p, r0 + r) ? to_f<T>(u[(r0 + r) * p.D + q]) : 0.f;
+        const int lane = threadIdx.x % 32;
+#pragma unroll 4
+        for (int r = threadIdx.x / 32; r < kBalRows; r += kBalThreads / 32) {
+            const bool live = bal_live(p, r0 + r);
+            for (int q = lane; q < p.D; q += 32)
+                su[r * ld + q] = live ? to_f<T>(u[(r0 + r) * p.D + q]) : 0.f;
         }
     }
     __device__ __forceinline__ void load_W(const BalParams &p, int h) {
-        for (int e = threadIdx.x; e < KT * p.D; e += kBalThreads) {
-            const int r = e / p.D, q = e % p.D;
-            sW[r * ld + q] = r < p.K ? p.W[((int64_t)h * p.K + r) * p.D + q] : 0.f;
-        }
+        const int lane = threadIdx.x % 32;
+#pragma unroll 4
+        for (int r = threadIdx.x / 32; r < KT; r += kBalThreads / 32)
+            for (int q = lane; q < p.D; q += 32)
+                sW[r * ld + q] = r < p.K ? p.W[((int64_t)h * p.K + r) * p.D + q] : 0.f;
     }
     // sp = softmax weights of the tile's live rows, zero elsewhere; four
     // threads per row
@@ -52,6 +57,7 @@ struct Tile {
         float l[KP];
 #pragma unroll
         for (int i = 0; i < KP; ++i) l[i] = 0.f;
+#pragma unroll 8
         for (int q = 0; q < p.D; ++q) {
             const float uv = su[r * ld + q];
 #pragma unroll

@@ -40,8 +40,8 @@ __device__ __forceinline__ int64_t bal_steps(const BalParams &p) {
 __device__ __forceinline__ bool bal_live(const BalParams &p, int64_t row) {
     if (row >= p.rows) return false;
     if (!p.lengths) return true;
-    const int b = (int)(row / p.L);
-    return row - (int64_t)b * p.L < bal_len(p, b);
+    const uint32_t b = (uint32_t)row / (uint32_t)p.L;       // B L < 2^31
+    return (int64_t)((uint32_t)row - b * (uint32_t)p.L) < bal_len(p, (int)b);
 }
 
 // Plan of the tensor-core kernels (bf16 u): groups of heads whose weights, as

@@ -15,7 +15,7 @@ constexpr int kThreads = 256;
 // acc[i][j] += sum_k a(ty + 16 i, k) b(tx + 16 j, k)
 template <int TM, int TN, class FA, class FB>
 __device__ __forceinline__ void tile_mm(float (&acc)[TM][TN], int K, FA a, FB b) {
-#pragma unroll 4
+#pragma unroll 8
     for (int k = 0; k < K; ++k) {
         float av[TM], bv[TN];
 #pragma unroll
@@ -42,6 +42,7 @@ __device__ __forceinline__ void zero(float (&acc)[TM][TN]) {
 template <typename T, int C, int WT>
 __device__ __forceinline__ void load_rows(float *dst, const T *src, int64_t stride, int width,
                                           int64_t t0, int64_t len) {
+#pragma unroll 8
     for (int e = threadIdx.x; e < C * WT; e += kThreads) {
         const int t = e / WT, n = e % WT;
         float v = 0.f;
@@ -247,10 +248,10 @@ __global__ void __launch_bounds__(kThreads) k_decay_bwd_gen(DecayParams p) {
     constexpr int LD = WT + 1, LC = C + 1, TM = C / 16, TN = WT / 16;
     extern __shared__ float sm[];
     float *sc = sm, *sb = sc + C * LD, *sx = sb + C * LD, *sg = sx + C * LD, *sR = sg + C * LD;
-    float *sP = sR + WT * LD, *sQ = sP + C * LC;
+    float *sS = sR + WT * LD, *sP = sS + WT * LD, *sQ = sP + C * LC;
     float *sfrom = sQ + C * LC, *sto = sfrom + C;       // per step: pairs' and states' sums
     float *sred = sto + C;                              // 16 x C + 32
-    float2 *sG = reinterpret_cast<float2 *>(sred + 16 * C + 32 + ((WT * LD) & 1));
+    float2 *sG = reinterpret_cast<float2 *>(sred + 16 * C + 32);
     const int seg = blockIdx.x % p.nseg;
     const Head hd = head_of(p, blockIdx.x / p.nseg);
     const int ty = threadIdx.x / 16, tx = threadIdx.x % 16;
@@ -281,6 +282,13 @@ __global__ void __launch_bounds__(kThreads) k_decay_bwd_gen(DecayParams p) {
             load_rows<T, C, WT>(sb, b, p.key_t, p.N, t0, hd.len);
             load_rows<T, C, WT>(sx, x, p.val_t, p.P, t0, hd.len);
             load_rows<T, C, WT>(sg, gy, p.val_t, p.P, t0, hd.len);
+            const float *S0 = i > 0 ? p.carry + ((int64_t)hd.bh * p.nchunks + i) * np
+                                    : (p.h0 ? p.h0 + (int64_t)hd.bh * np : nullptr);
+#pragma unroll 4
+            for (int e = threadIdx.x; e < WT * WT; e += kThreads) {
+                const int n = e / WT, q = e % WT;
+                sS[n * LD + q] = S0 && n < p.N && q < p.P ? S0[(int64_t)n * p.P + q] : 0.f;
+            }
             if (threadIdx.x < 32)
                 decay_sums<C>([&](int t) { return hd.log_a(p, t0 + t); }, sG, threadIdx.x);
         } else {                        // behind the end: zero gradients, the state's stays
@@ -305,8 +313,6 @@ __global__ void __launch_bounds__(kThreads) k_decay_bwd_gen(DecayParams p) {
         __syncthreads();
         const float2 end = sG[C - 1];
         const float aend = decay_from_start(end);
-        const float *S0 = i > 0 ? p.carry + ((int64_t)hd.bh * p.nchunks + i) * np
-                                : (p.h0 ? p.h0 + (int64_t)hd.bh * np : nullptr);
         // decayed scores P and Q, and the pair products' row and column sums
         {
             float s[TM][TM], v[TM][TM];
@@ -353,12 +359,8 @@ __global__ void __launch_bounds__(kThreads) k_decay_bwd_gen(DecayParams p) {
         {
             float acc[TM][TN];
             zero(acc);
-            if (S0)
-                tile_mm(acc, p.P, [&](int m, int k) { return sg[(ty + 16 * m) * LD + k]; },
-                        [&](int n, int k) {
-                            const int r = tx + 16 * n;
-                            return r < p.N ? __ldg(S0 + (int64_t)r * p.P + k) : 0.f;
-                        });
+            tile_mm(acc, WT, [&](int m, int k) { return sg[(ty + 16 * m) * LD + k]; },
+                    [&](int n, int k) { return sS[(tx + 16 * n) * LD + k]; });
 #pragma unroll
             for (int m = 0; m < TM; ++m) {
                 const float e = decay_from_start(sG[ty + 16 * m]);
@@ -444,9 +446,8 @@ __global__ void __launch_bounds__(kThreads) k_decay_bwd_gen(DecayParams p) {
         }
         // e^{G_C} <S0, R>, the row sums u_i + R_i and v_j
         float dot = 0.f;
-        if (S0)
-            for (int e = threadIdx.x; e < p.N * p.P; e += kThreads)
-                dot = fmaf(__ldg(S0 + e), sR[(e / p.P) * LD + e % p.P], dot);
+        for (int e = threadIdx.x; e < WT * WT; e += kThreads)
+            dot = fmaf(sS[(e / WT) * LD + e % WT], sR[(e / WT) * LD + e % WT], dot);
 #pragma unroll
         for (int d = 16; d; d >>= 1) dot += __shfl_xor_sync(kFull, dot, d);
 #pragma unroll
@@ -635,8 +636,8 @@ cudaError_t bwd_gen(const DecayParams &p, cudaStream_t st) {
         e = launch_decay_join(p, p.g_hlast, true, nullptr, st);
         if (e != cudaSuccess) return e;
     }
-    const size_t smem = (size_t)((4 * C + WT) * (WT + 1) + 2 * C * (C + 1) + 2 * C + 16 * C + 32 +
-                                 1 + 2 * C) * 4;
+    const size_t smem = (size_t)((4 * C + 2 * WT) * (WT + 1) + 2 * C * (C + 1) + 2 * C + 16 * C + 32 +
+                                 2 * C) * 4;
     return launch(k_decay_bwd_gen<T, C, WT>, (int64_t)p.B * p.H * p.nseg, smem, st, p);
 }
 

@@ -27,9 +27,9 @@
 // where the product does not.
 //
 // Warps: 0-3 and 4-7 take chunks in turn (steps 2 and 5), 8-15 hold the state
-// (32 columns each), 16-19 build the split operand, 20 and 21 issue the
-// products (scores, state), 22 the copies, 23 and 24 compute the decays in
-// turn.  Accumulators, decays and (N <= 64) split parts are double-buffered,
+// (32 columns each), 16-23 build the split operand, 24-26 issue the
+// products (scores, Y, state: one thread would hold each of them back by the
+// others' waits), 27 the copies, 28 and 29 compute the decays in turn.  Accumulators, decays and (N <= 64) split parts are double-buffered,
 // c and b tiles three deep (N <= 64; the scores of chunk i + 1 run ahead of
 // the rest of chunk i, so two stages would expose each copy's latency), all
 // handed over by mbarriers.
@@ -43,8 +43,9 @@ namespace {
 
 constexpr int kC = 128;                 // steps per chunk
 // warps by role
-constexpr int kState = 8, kBuild = 16, kControl = 20, kControl2 = 21, kProducer = 22, kDecay = 23;
-constexpr int kTcTh = 25 * 32;
+constexpr int kState = 8, kBuild = 16, kScores = 24, kOutputs = 25, kStates = 26, kProducer = 27,
+              kDecay = 28;
+constexpr int kTcTh = 30 * 32;
 constexpr int kLoaders = 32;            // threads of plain loads (the producer's warp)
 constexpr uint32_t kTile = kC * 128;    // 128 rows of 64 bf16
 
@@ -166,17 +167,17 @@ __global__ void __launch_bounds__(kTcTh, 1)
             mbar_init(bar(kFullX, s), loaders);
             mbar_init(bar(kScFull, s), 1);
             mbar_init(bar(kPReady, s), 128);
-            mbar_init(bar(kPlReady, s), 128);
+            mbar_init(bar(kPlReady, s), 256);
             mbar_init(bar(kDFull, s), 1);
             mbar_init(bar(kS0Ready, s), 256);
             mbar_init(bar(kYFull, s), 1);
             mbar_init(bar(kYFree, s), 128);
             mbar_init(bar(kDecReady, s), 32);
-            mbar_init(bar(kDecFree, s), FWD ? 512 : 384);
+            mbar_init(bar(kDecFree, s), FWD ? 640 : 512);
         }
         fence_mbar_init();
     }
-    if (warp == kControl) tmem_alloc(smem_u32(&tmem_slot), 512);
+    if (warp == kScores) tmem_alloc(smem_u32(&tmem_slot), 512);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -383,9 +384,10 @@ __global__ void __launch_bounds__(kTcTh, 1)
             leave(p.seg_state + (bh * p.nseg + seg) * np);
         else if (p.h_last && seg == p.nseg - 1)
             leave(p.h_last + bh * np);
-    } else if (warp < kControl) {
-        // ---- the three parts of each chunk's decayed operand, row r = step t0 + r
-        const int r = tid & 127;
+    } else if (warp < kScores) {
+        // ---- the three parts of each chunk's decayed operand: row r = step t0 + r,
+        // four of its eight pieces
+        const int r = tid & 127, h0 = ((warp - kBuild) >> 2) * 4;
         for (int i = 0; i < n; ++i) {
             if (!wait_warp(kDecReady, i)) break;
             const float w = dec[i & 1].weight[r];
@@ -401,7 +403,7 @@ __global__ void __launch_bounds__(kTcTh, 1)
             const uint32_t bt = keys + SM::kKey, xt = sm + SM::kX + (uint32_t)(i % SM::kNX) * kTile;
             if (!on) {      // behind the end: whatever lies there must not meet a zero weight
 #pragma unroll
-                for (int q = 0; q < 8; ++q) {
+                for (int q = h0; q < h0 + 4; ++q) {
                     sts128(xt + piece(r, q), 0, 0, 0, 0);
                     sts128(bt + piece(r, q), 0, 0, 0, 0);
                     if (!STK) sts128(bt + kTile + piece(r, q), 0, 0, 0, 0);
@@ -411,7 +413,7 @@ __global__ void __launch_bounds__(kTcTh, 1)
             const uint32_t dst = sm + SM::kPl + (uint32_t)(i % SM::kNPL) * SM::kParts * kTile;
             const uint32_t dst2 = STK ? bt : dst + 2 * kTile;
 #pragma unroll 2
-            for (int q = 0; q < 8; ++q) {
+            for (int q = h0; q < h0 + 4; ++q) {
                 const uint4 u = lds128(src + piece(r, q));
                 const uint32_t in[4] = {u.x, u.y, u.z, u.w};
                 uint32_t p1[4], p2[4], p3[4];
@@ -434,42 +436,45 @@ __global__ void __launch_bounds__(kTcTh, 1)
             fence_proxy_async_smem();
             mbar_arrive(bar(kPlReady, i));
         }
-    } else if (warp == kControl) {
-        // ---- the scores' products: Sc of chunk i + 1, then Y of chunk i
+    } else if (warp == kScores) {
+        // ---- products: the scores
         if (lane == 0 && FWD) {
             constexpr uint32_t kIdSc = umma_idesc_bf16(128);
-            constexpr uint32_t kIdY = umma_idesc_bf16(64, false, true);
-            const uint32_t key0 = umma_lo(sm + SM::kC0, kTile), x0 = umma_lo(sm + SM::kX, 0);
-            for (int i = 0; i <= n && n > 0; ++i) {
-                if (i < n) {
-                    if (!wait_cb(i) || (i >= 2 && !wait(kYFree, i - 2))) break;
-                    tc_fence_after();
-                    const uint32_t ct = key0 + (uint32_t)(i % SM::kNCB) * umma_step(2 * SM::kKey);
-                    const uint32_t bt = ct + umma_step(SM::kKey), dS = tcol(i, 0);
+            const uint32_t key0 = umma_lo(sm + SM::kC0, kTile);
+            for (int i = 0; i < n; ++i) {
+                if (!wait_cb(i) || (i >= 2 && !wait(kYFree, i - 2))) break;
+                tc_fence_after();
+                const uint32_t ct = key0 + (uint32_t)(i % SM::kNCB) * umma_step(2 * SM::kKey);
+                const uint32_t bt = ct + umma_step(SM::kKey), dS = tcol(i, 0);
 #pragma unroll
-                    for (int k = 0; k < (STK ? 4 : 8); ++k) {
-                        const uint32_t off = (k >> 2) * umma_step(kTile) + (k & 3) * umma_step(32);
-                        umma_ss(dS, ct + off, bt + off, kIdSc, k > 0);
-                    }
-                    umma_commit(bar(kScFull, i));
+                for (int k = 0; k < (STK ? 4 : 8); ++k) {
+                    const uint32_t off = (k >> 2) * umma_step(kTile) + (k & 3) * umma_step(32);
+                    umma_ss(dS, ct + off, bt + off, kIdSc, k > 0);
                 }
-                if (i > 0) {
-                    const int j = i - 1;
-                    if (!wait(kPReady, j) || !wait_x(j) || !wait(kPlReady, j)) break;
-                    tc_fence_after();
-                    const uint32_t dY = tcol(j, 64), pa = tcol(j, 0);
-                    const uint32_t xr = x0 + (uint32_t)(j % SM::kNX) * umma_step(kTile);
-#pragma unroll
-                    for (int k = 0; k < 8; ++k)
-                        umma_ts(dY, pa + 8 * k, xr + k * umma_step(2048), kIdY, k > 0);
-                    umma_commit(bar(kYFull, j));
-                }
+                umma_commit(bar(kScFull, i));
             }
-            if (n > 0 && ok) wait(kYFull, n - 1);   // nothing is in flight when the CTA ends
+            if (n > 0 && ok) wait(kScFull, n - 1);  // nothing is in flight when the CTA ends
         }
         __syncwarp();
-    } else if (warp == kControl2) {
-        // ---- the state's products: Yi, then what the chunk adds to the state
+    } else if (warp == kOutputs) {
+        // ---- products: Y
+        if (lane == 0 && FWD) {
+            constexpr uint32_t kIdY = umma_idesc_bf16(64, false, true);
+            const uint32_t x0 = umma_lo(sm + SM::kX, 0);
+            for (int i = 0; i < n; ++i) {
+                if (!wait(kPReady, i) || !wait_x(i) || !wait(kPlReady, i)) break;
+                tc_fence_after();
+                const uint32_t dY = tcol(i, 64), pa = tcol(i, 0);
+                const uint32_t xr = x0 + (uint32_t)(i % SM::kNX) * umma_step(kTile);
+#pragma unroll
+                for (int k = 0; k < 8; ++k) umma_ts(dY, pa + 8 * k, xr + k * umma_step(2048), kIdY, k > 0);
+                umma_commit(bar(kYFull, i));
+            }
+            if (n > 0 && ok) wait(kYFull, n - 1);
+        }
+        __syncwarp();
+    } else if (warp == kStates) {
+        // ---- products: Yi, then what the chunk adds to the state
         if (lane == 0) {
             constexpr uint32_t kIdY = umma_idesc_bf16(64, false, true);
             constexpr uint32_t kIdD = umma_idesc_bf16(64, true, true);
@@ -654,7 +659,7 @@ __global__ void __launch_bounds__(kTcTh, 1)
         __syncthreads();
     }
     tc_fence_after();
-    if (warp == kControl) tmem_dealloc(tmem, 512);
+    if (warp == kScores) tmem_dealloc(tmem, 512);
     if (!FWD && ps == 0 && tid == 0)
         p.seg_decay[bh * p.nseg + seg] = exp2f((float)(totals[0] + totals[1]));
     if (FWD) {
