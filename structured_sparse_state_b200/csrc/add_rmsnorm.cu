@@ -110,6 +110,22 @@ __device__ __forceinline__ float row_reduce(float v, float *red, OP op) {
     return v;
 }
 
+// The sum alone, with one barrier: the caller alternates between two buffers,
+// so that a buffer is written again only after the next call's barrier.
+template <int TPR>
+__device__ __forceinline__ float row_sum_once(float v, float *red) {
+#pragma unroll
+    for (int d = 16; d; d >>= 1) v += __shfl_xor_sync(kFull, v, d);
+    if constexpr (TPR > 32) {
+        if (threadIdx.x % 32 == 0) red[threadIdx.x / 32] = v;
+        __syncthreads();
+        v = red[0];
+#pragma unroll
+        for (int w = 1; w < TPR / 32; ++w) v += red[w];
+    }
+    return v;
+}
+
 struct NormParams {
     int64_t rows;
     int D;
@@ -138,16 +154,21 @@ __global__ void __launch_bounds__(TPR == 32 ? 128 : TPR) k_add_rmsnorm(NormParam
         const int col = (i * TPR + lane) * V;
         if (col < p.D) load_vec<V>(s[i], p.x, base + col, p.x_dt);
     }
+    if (p.residual) {
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        const int col = (i * TPR + lane) * V;
-        if (col >= p.D) continue;
-        if (p.residual) {
+        for (int i = 0; i < NV; ++i) {
+            const int col = (i * TPR + lane) * V;
+            if (col >= p.D) continue;
             float r[V];
             load_vec<V>(r, p.residual, base + col, p.res_dt);
 #pragma unroll
             for (int j = 0; j < V; ++j) s[i][j] += r[j];
         }
+    }
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int col = (i * TPR + lane) * V;
+        if (col >= p.D) continue;
         if (p.res_dt == PDSSM_BF16) {   // the norm is of the rounded sum
 #pragma unroll
             for (int j = 0; j < V; ++j) s[i][j] = __bfloat162float(__float2bfloat16_rn(s[i][j]));
@@ -201,22 +222,23 @@ struct NormBwdParams {
 constexpr int kBwdValues = 16;      // values of a row per thread
 
 // TPR = 32: 4 warps per CTA, a row per warp at a time; else a row per CTA.
-template <int TPR, int V>
-__global__ void __launch_bounds__(TPR == 32 ? 128 : TPR) k_add_rmsnorm_bwd(NormBwdParams p) {
+// The weights are read again for every row (from L1): held in registers they
+// would cost a CTA per SM.
+template <int TPR, int V, int GD, int RD>
+__global__ void __launch_bounds__(TPR == 32 ? 128 : TPR, TPR <= 128 ? 5 : TPR == 256 ? 2 : 1)
+    k_add_rmsnorm_bwd(NormBwdParams p) {
     constexpr int NV = kBwdValues / V;
     constexpr int RPC = TPR == 32 ? 4 : 1;
-    __shared__ float red[32];
+    __shared__ float red[64];
     __shared__ float comb[TPR == 32 ? 4 * 32 * kBwdValues : 1];
     const int lane = TPR == 32 ? threadIdx.x % 32 : threadIdx.x;
     const int sub = TPR == 32 ? threadIdx.x / 32 : 0;
-    float w[NV][V], gw[NV][V];
+    float gw[NV][V];
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        const int col = (i * TPR + lane) * V;
-        if (col < p.D) load_vec<V>(w[i], p.weight, col, p.w_dt);
+    for (int i = 0; i < NV; ++i)
 #pragma unroll
         for (int j = 0; j < V; ++j) gw[i][j] = 0.f;
-    }
+    int turn = 0;
     for (int64_t row = (int64_t)blockIdx.x * RPC + sub; row < p.rows;
          row += (int64_t)gridDim.x * RPC) {
         const int64_t base = row * p.D;
@@ -227,22 +249,32 @@ __global__ void __launch_bounds__(TPR == 32 ? 128 : TPR) k_add_rmsnorm_bwd(NormB
         for (int i = 0; i < NV; ++i) {
             const int col = (i * TPR + lane) * V;
             if (col >= p.D) continue;
-            load_vec<V>(g[i], p.g_out, base + col, p.g_dt);
-            load_vec<V>(h[i], p.s, base + col, p.res_dt);
-            if (p.g_res) load_vec<V>(r[i], p.g_res, base + col, p.res_dt);
+            load_vec<V>(g[i], p.g_out, base + col, GD);
+            load_vec<V>(h[i], p.s, base + col, RD);
+        }
+        if (p.g_res) {
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                const int col = (i * TPR + lane) * V;
+                if (col < p.D) load_vec<V>(r[i], p.g_res, base + col, RD);
+            }
         }
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            if ((i * TPR + lane) * V >= p.D) continue;
+            const int col = (i * TPR + lane) * V;
+            if (col >= p.D) continue;
+            float w[V];
+            load_vec<V>(w, p.weight, col, p.w_dt);
 #pragma unroll
             for (int j = 0; j < V; ++j) {
                 h[i][j] *= rstd;
                 gw[i][j] = fmaf(g[i][j], h[i][j], gw[i][j]);
-                g[i][j] *= w[i][j];
+                g[i][j] *= w[j];
                 dot = fmaf(g[i][j], h[i][j], dot);
             }
         }
-        dot = row_reduce<TPR>(dot, red, AddOp()) / (float)p.D;
+        // rows take the two halves of `red` in turn: one barrier per row
+        dot = row_sum_once<TPR>(dot, red + 32 * (turn ^= 1)) / (float)p.D;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int col = (i * TPR + lane) * V;
@@ -252,7 +284,7 @@ __global__ void __launch_bounds__(TPR == 32 ? 128 : TPR) k_add_rmsnorm_bwd(NormB
                 g[i][j] = (g[i][j] - h[i][j] * dot) * rstd;
                 if (p.g_res) g[i][j] += r[i][j];
             }
-            store_vec<V>(g[i], p.g_x, base + col, p.res_dt);
+            store_vec<V>(g[i], p.g_x, base + col, RD);
         }
     }
     if constexpr (TPR == 32) {          // the CTA's four warps hold the same columns
@@ -306,7 +338,7 @@ int bwd_tpr(int64_t D) {
 int64_t bwd_ctas(int64_t rows, int64_t D) {
     const int tpr = bwd_tpr(D);
     const int rpc = tpr == 32 ? 4 : 1;
-    const int per_sm = tpr <= 128 ? 8 : tpr == 256 ? 4 : tpr == 512 ? 2 : 1;
+    const int per_sm = tpr <= 128 ? 5 : tpr == 256 ? 2 : 1;     // as many as are resident
     const int64_t n = (rows + rpc - 1) / rpc, most = 148 * per_sm;
     return n < most ? (n > 0 ? n : 1) : most;
 }
@@ -328,16 +360,28 @@ cudaError_t run_fwd(const NormParams &p, cudaStream_t st) {
     return cudaGetLastError();
 }
 
-template <int V>
-cudaError_t run_bwd(const NormBwdParams &p, cudaStream_t st) {
+// Types as template arguments here: with the branch of load_vec the row's
+// registers cost a quarter of the resident CTAs (108 us against 96 at 16384 x
+// 2048, fp32 stream).
+template <int V, int GD, int RD>
+cudaError_t run_bwd_t(const NormBwdParams &p, cudaStream_t st) {
     switch (bwd_tpr(p.D)) {
-        case 32: k_add_rmsnorm_bwd<32, V><<<p.ctas, 128, 0, st>>>(p); break;
-        case 128: k_add_rmsnorm_bwd<128, V><<<p.ctas, 128, 0, st>>>(p); break;
-        case 256: k_add_rmsnorm_bwd<256, V><<<p.ctas, 256, 0, st>>>(p); break;
-        case 512: k_add_rmsnorm_bwd<512, V><<<p.ctas, 512, 0, st>>>(p); break;
-        default: k_add_rmsnorm_bwd<1024, V><<<p.ctas, 1024, 0, st>>>(p); break;
+        case 32: k_add_rmsnorm_bwd<32, V, GD, RD><<<p.ctas, 128, 0, st>>>(p); break;
+        case 128: k_add_rmsnorm_bwd<128, V, GD, RD><<<p.ctas, 128, 0, st>>>(p); break;
+        case 256: k_add_rmsnorm_bwd<256, V, GD, RD><<<p.ctas, 256, 0, st>>>(p); break;
+        case 512: k_add_rmsnorm_bwd<512, V, GD, RD><<<p.ctas, 512, 0, st>>>(p); break;
+        default: k_add_rmsnorm_bwd<1024, V, GD, RD><<<p.ctas, 1024, 0, st>>>(p); break;
     }
     return cudaGetLastError();
+}
+
+template <int V>
+cudaError_t run_bwd(const NormBwdParams &p, cudaStream_t st) {
+    if (p.g_dt == PDSSM_F32)
+        return p.res_dt == PDSSM_F32 ? run_bwd_t<V, PDSSM_F32, PDSSM_F32>(p, st)
+                                     : run_bwd_t<V, PDSSM_F32, PDSSM_BF16>(p, st);
+    return p.res_dt == PDSSM_F32 ? run_bwd_t<V, PDSSM_BF16, PDSSM_F32>(p, st)
+                                 : run_bwd_t<V, PDSSM_BF16, PDSSM_BF16>(p, st);
 }
 
 pdssm_status check_sizes(int64_t rows, int64_t D) {

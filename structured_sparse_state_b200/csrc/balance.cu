@@ -12,6 +12,7 @@
 // kernel.  bf16 u runs on the tensor cores (balance_tc.cu); fp32 u here, on
 // the CUDA cores.
 #include "balance.cuh"
+#include "launch.cuh"
 
 namespace pdssm {
 namespace {
@@ -290,21 +291,21 @@ int bal_slices(int64_t rows, int64_t H) {
     return (int)(n < 1 ? 1 : n);
 }
 
-template <typename K>
-cudaError_t launch(K kern, int64_t grid, size_t smem, cudaStream_t st, const BalParams &p) {
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         (int)smem);
+template <void (*KERN)(BalParams)>
+cudaError_t launch(int64_t grid, size_t smem, cudaStream_t st, const BalParams &p) {
+    static std::atomic<int> set[kLimitDevices];
+    const cudaError_t e = allow_smem((const void *)KERN, (int)smem, set);
     if (e != cudaSuccess) return e;
-    kern<<<dim3((unsigned)grid), kBalThreads, smem, st>>>(p);
+    KERN<<<dim3((unsigned)grid), kBalThreads, smem, st>>>(p);
     return cudaGetLastError();
 }
 
 template <typename T, int KT>
 cudaError_t run(const BalParams &p, int what, cudaStream_t st) {
     const size_t smem = bal_smem<KT>(p.D);
-    if (what == 0) return launch(k_bal_sums<T, KT>, (int64_t)p.H * p.slices, smem, st, p);
-    if (what == 1) return launch(k_bal_gu<T, KT>, (p.rows + kBalRows - 1) / kBalRows, smem, st, p);
-    return launch(k_bal_gw<T, KT>, (int64_t)p.H * p.slices, smem, st, p);
+    if (what == 0) return launch<k_bal_sums<T, KT>>((int64_t)p.H * p.slices, smem, st, p);
+    if (what == 1) return launch<k_bal_gu<T, KT>>((p.rows + kBalRows - 1) / kBalRows, smem, st, p);
+    return launch<k_bal_gw<T, KT>>((int64_t)p.H * p.slices, smem, st, p);
 }
 
 template <typename T>

@@ -20,6 +20,7 @@
 #include <string.h>
 
 #include "balance.cuh"
+#include "launch.cuh"
 #include "umma.cuh"
 
 namespace pdssm {
@@ -589,7 +590,8 @@ cudaError_t go(const BalParams &p, const BalTcPlan &pl, const void *parts, cudaS
             return cudaErrorInvalidValue;
     }
     auto kern = k_bal_tc<KT, MODE>;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    static std::atomic<int> set[kLimitDevices];
+    const cudaError_t e = allow_smem((const void *)kern, smem, set);
     if (e != cudaSuccess) return e;
     const int grid = MODE == kGu ? (pl.tiles < 148 ? pl.tiles : 148) : pl.groups * pl.slices;
     kern<<<grid, kTh, smem, st>>>(map, t);

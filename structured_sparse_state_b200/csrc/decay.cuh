@@ -46,6 +46,7 @@ struct DecayParams {
     float *seg_state;                   // [B*H][nseg][N][P]: per segment, local then incoming
     float *seg_decay;                   // [B*H][nseg]
     float *carry;                       // [B*H][nchunks][N][P]: state at every chunk's start
+    int *status;                        // the workspace's status word
     int nseg, seg_chunks, nchunks, pslices;
     int vec;                            // rows and pointers allow 16-byte (2: 32-byte) accesses
 };
@@ -114,9 +115,9 @@ cudaError_t launch_decay_sum_steps(const DecayParams &p, const float *part, floa
                                    cudaStream_t st);
 cudaError_t launch_decay_fwd_gen(const DecayParams &p, pdssm_dtype dt, cudaStream_t st);
 cudaError_t launch_decay_bwd_gen(const DecayParams &p, pdssm_dtype dt, cudaStream_t st);
-cudaError_t launch_decay_fwd_tc(const DecayParams &p, int *status, cudaStream_t st);
-cudaError_t launch_decay_seg_rev_tc(const DecayParams &p, int *status, cudaStream_t st);
-cudaError_t launch_decay_bwd_mma(const DecayParams &p, int *status, cudaStream_t st);
+cudaError_t launch_decay_fwd_tc(const DecayParams &p, cudaStream_t st);
+cudaError_t launch_decay_seg_rev_tc(const DecayParams &p, cudaStream_t st);
+cudaError_t launch_decay_bwd_mma(const DecayParams &p, cudaStream_t st);
 bool decay_tc_copies();                 // the driver's tensor maps are at hand
 cudaError_t launch_decay_step(const DecayParams &p, pdssm_dtype dt, float *state, int64_t n_slots,
                               const int32_t *slots, cudaStream_t st);

@@ -125,6 +125,7 @@ int vec_of(const pdssm_decay_dims &d, std::initializer_list<const void *> ptrs) 
 }
 
 void set_plan(DecayParams &p, const DecayPlan &pl, const DecayWs &w, unsigned char *base) {
+    p.status = reinterpret_cast<int *>(base);
     p.nseg = pl.nseg; p.seg_chunks = pl.seg_chunks; p.nchunks = pl.nchunks; p.pslices = pl.pslices;
     p.seg_state = reinterpret_cast<float *>(base + w.seg_state);
     p.seg_decay = reinterpret_cast<float *>(base + w.seg_decay);
@@ -185,10 +186,9 @@ pdssm_status pdssm_decay_scan_fwd(const pdssm_decay_dims *dims, const void *c, c
     if (for_bwd) p.carry = reinterpret_cast<float *>(base + w.carry);
     if (path_of(*dims, dtype, for_bwd != 0) == kDecayTc) {
         p.vec = vec_of(*dims, {c, b, x, y});
-        e = launch_decay_fwd_tc(p, reinterpret_cast<int *>(base), s);
+        e = launch_decay_fwd_tc(p, s);
     } else {
-        e = cudaMemsetAsync(base, 0, 4, s);     // the status word
-        if (e == cudaSuccess) e = launch_decay_fwd_gen(p, dtype, s);
+        e = launch_decay_fwd_gen(p, dtype, s);
     }
     return e == cudaSuccess ? PDSSM_OK : cuda_fail(e, "decay scan");
 }
@@ -239,7 +239,7 @@ pdssm_status pdssm_decay_scan_bwd(const pdssm_decay_dims *dims, const void *c, c
     p.g_la = log_a_per_step ? g_log_a : part_la;
     if (path_of(*dims, dtype, true) == kDecayTc) {
         p.vec = vec_of(*dims, {c, b, x, g_y, g_x, shared ? g_x : g_c, shared ? g_x : g_b});
-        e = launch_decay_bwd_mma(p, reinterpret_cast<int *>(base), s);
+        e = launch_decay_bwd_mma(p, s);
     } else {
         e = launch_decay_bwd_gen(p, dtype, s);
     }

@@ -18,6 +18,7 @@
 // and accumulators in registers take that without a round trip.  Bound: the
 // warp-level tensor pipe, 107 kflop per step of a 64 x 64 head.
 #include "decay.cuh"
+#include "launch.cuh"
 
 namespace pdssm {
 namespace {
@@ -549,20 +550,20 @@ __global__ void __launch_bounds__(kTh, 2) k_decay_bwd_mma(DecayParams p) {
 
 }  // namespace
 
-cudaError_t launch_decay_bwd_mma(const DecayParams &p, int *status, cudaStream_t st) {
+cudaError_t launch_decay_bwd_mma(const DecayParams &p, cudaStream_t st) {
     if (p.nseg > 1) {
         // the segments in the tensor-core kernel's chunks of 128 steps
         DecayParams s = p;
         s.nchunks = (int)((p.L + 127) / 128);
         s.seg_chunks = p.seg_chunks / 2;
         s.pslices = 1;
-        cudaError_t e = launch_decay_seg_rev_tc(s, status, st);
+        cudaError_t e = launch_decay_seg_rev_tc(s, st);
         if (e != cudaSuccess) return e;
         e = launch_decay_join(p, p.g_hlast, true, nullptr, st);
         if (e != cudaSuccess) return e;
     }
-    cudaError_t e = cudaFuncSetAttribute(k_decay_bwd_mma, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         (int)Smem::kTotal);
+    static std::atomic<int> set[kLimitDevices];
+    const cudaError_t e = allow_smem((const void *)k_decay_bwd_mma, (int)Smem::kTotal, set);
     if (e != cudaSuccess) return e;
     k_decay_bwd_mma<<<dim3((unsigned)((int64_t)p.B * p.H * p.nseg)), kTh, Smem::kTotal, st>>>(p);
     return cudaGetLastError();

@@ -6,6 +6,7 @@
 //
 // Bound: shared-memory loads, (TM + TN) per TM * TN multiply-adds.
 #include "decay.cuh"
+#include "launch.cuh"
 
 namespace pdssm {
 namespace {
@@ -143,6 +144,8 @@ __global__ void __launch_bounds__(kThreads) k_decay_fwd_gen(DecayParams p) {
     const T *c = (const T *)p.c + koff, *b = (const T *)p.b + koff, *x = (const T *)p.x + voff;
     T *y = (T *)p.y + voff;
     const int64_t np = (int64_t)p.N * p.P;
+    // these kernels have no bounded waits: the workspace's status is good
+    if (blockIdx.x == 0 && threadIdx.x == 0) *p.status = 0;
 
     // the segment's incoming state
     const float *in = p.nseg > 1 ? p.seg_state + ((int64_t)hd.bh * p.nseg + seg) * np
@@ -600,19 +603,19 @@ __global__ void __launch_bounds__(1024) k_decay_sum_steps(DecayParams p, const f
     }
 }
 
-template <typename K>
-cudaError_t launch(K kern, int64_t grid, size_t smem, cudaStream_t st, const DecayParams &p) {
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         (int)smem);
+template <void (*KERN)(DecayParams)>
+cudaError_t launch(int64_t grid, size_t smem, cudaStream_t st, const DecayParams &p) {
+    static std::atomic<int> set[kLimitDevices];
+    const cudaError_t e = allow_smem((const void *)KERN, (int)smem, set);
     if (e != cudaSuccess) return e;
-    kern<<<dim3((unsigned)grid), kThreads, smem, st>>>(p);
+    KERN<<<dim3((unsigned)grid), kThreads, smem, st>>>(p);
     return cudaGetLastError();
 }
 
 template <typename T, int C, int WT, bool REV>
 cudaError_t seg_gen(const DecayParams &p, cudaStream_t st) {
     const size_t smem = (size_t)(2 * C * (WT + 1) + 1 + 2 * C) * 4;
-    return launch(k_decay_seg_gen<T, C, WT, REV>, (int64_t)p.B * p.H * p.nseg, smem, st, p);
+    return launch<k_decay_seg_gen<T, C, WT, REV>>((int64_t)p.B * p.H * p.nseg, smem, st, p);
 }
 
 template <typename T, int C, int WT>
@@ -625,7 +628,7 @@ cudaError_t fwd_gen(const DecayParams &p, cudaStream_t st) {
         if (e != cudaSuccess) return e;
     }
     const size_t smem = (size_t)(2 * C * (WT + 1) + (C + WT) * (PS + 1) + C * (C + 1) + 1 + 2 * C) * 4;
-    return launch(k_decay_fwd_gen<T, C, WT>, (int64_t)p.B * p.H * p.nseg * p.pslices, smem, st, p);
+    return launch<k_decay_fwd_gen<T, C, WT>>((int64_t)p.B * p.H * p.nseg * p.pslices, smem, st, p);
 }
 
 template <typename T, int C, int WT>
@@ -638,7 +641,7 @@ cudaError_t bwd_gen(const DecayParams &p, cudaStream_t st) {
     }
     const size_t smem = (size_t)((4 * C + 2 * WT) * (WT + 1) + 2 * C * (C + 1) + 2 * C + 16 * C + 32 +
                                  2 * C) * 4;
-    return launch(k_decay_bwd_gen<T, C, WT>, (int64_t)p.B * p.H * p.nseg, smem, st, p);
+    return launch<k_decay_bwd_gen<T, C, WT>>((int64_t)p.B * p.H * p.nseg, smem, st, p);
 }
 
 }  // namespace

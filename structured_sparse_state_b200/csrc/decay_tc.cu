@@ -36,6 +36,7 @@
 #include <string.h>
 
 #include "decay.cuh"
+#include "launch.cuh"
 #include "umma.cuh"
 
 namespace pdssm {
@@ -89,7 +90,6 @@ struct Smem {
 
 struct TcParams {
     DecayParams d;
-    int *status;
     int first;              // this launch clears the status word
 };
 
@@ -159,7 +159,7 @@ __global__ void __launch_bounds__(kTcTh, 1)
     };
 
     if (tid == 0) {
-        if (tp.first && blockIdx.x == 0) *tp.status = 0;
+        if (tp.first && blockIdx.x == 0) *p.status = 0;
         // a tile lands by one copy's bytes, or by the loader threads
         const uint32_t loaders = p.vec ? 1 : kLoaders;
         for (int s = 0; s < 4; ++s) {
@@ -193,7 +193,7 @@ __global__ void __launch_bounds__(kTcTh, 1)
     auto wait_at = [&](uint32_t at, int phase) {
         if (ok && !mbar_wait_hot(at, (uint32_t)(phase & 1))) {
             ok = false;
-            flag_status(tp.status, kStTimeout);
+            flag_status(p.status, kStTimeout);
         }
         return ok;
     };
@@ -684,7 +684,7 @@ bool encode_map(CUtensorMap *m, const void *ptr, int width, int heads, const Dec
 }
 
 template <bool STK, int MODE>
-cudaError_t go(const DecayParams &p, int *status, bool first, cudaStream_t st) {
+cudaError_t go(const DecayParams &p, bool first, cudaStream_t st) {
     CUtensorMap cm, bm, xm;
     memset(&cm, 0, sizeof(cm));
     memset(&bm, 0, sizeof(bm));
@@ -698,42 +698,43 @@ cudaError_t go(const DecayParams &p, int *status, bool first, cudaStream_t st) {
     }
     auto kern = k_decay_tc<STK, MODE>;
     const int smem = (int)Smem<STK>::kTotal;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    static std::atomic<int> set[kLimitDevices];
+    const cudaError_t e = allow_smem((const void *)kern, smem, set);
     if (e != cudaSuccess) return e;
     const int64_t grid = (int64_t)p.B * p.H * p.nseg * p.pslices;
-    kern<<<dim3((unsigned)grid), kTcTh, smem, st>>>(cm, bm, xm, TcParams{p, status, first ? 1 : 0});
+    kern<<<dim3((unsigned)grid), kTcTh, smem, st>>>(cm, bm, xm, TcParams{p, first ? 1 : 0});
     return cudaGetLastError();
 }
 
 template <bool STK>
-cudaError_t fwd_tc(const DecayParams &p, int *status, cudaStream_t st) {
+cudaError_t fwd_tc(const DecayParams &p, cudaStream_t st) {
     if (p.nseg > 1) {
-        cudaError_t e = go<STK, kSegFwd>(p, status, true, st);
+        cudaError_t e = go<STK, kSegFwd>(p, true, st);
         if (e != cudaSuccess) return e;
         e = launch_decay_join(p, p.h0, false, nullptr, st);
         if (e != cudaSuccess) return e;
     }
-    return go<STK, kFwd>(p, status, p.nseg <= 1, st);
+    return go<STK, kFwd>(p, p.nseg <= 1, st);
 }
 
 }  // namespace
 
 bool decay_tc_copies() { return tensor_map_encoder() != nullptr; }
 
-cudaError_t launch_decay_fwd_tc(const DecayParams &p, int *status, cudaStream_t st) {
-    if (!p.carry) return p.N <= 64 ? fwd_tc<true>(p, status, st) : fwd_tc<false>(p, status, st);
+cudaError_t launch_decay_fwd_tc(const DecayParams &p, cudaStream_t st) {
+    if (!p.carry) return p.N <= 64 ? fwd_tc<true>(p, st) : fwd_tc<false>(p, st);
     // with the adjoint's states: N, P <= 64
     if (p.nseg > 1) {
-        cudaError_t e = go<true, kSegFwd>(p, status, true, st);
+        cudaError_t e = go<true, kSegFwd>(p, true, st);
         if (e != cudaSuccess) return e;
         e = launch_decay_join(p, p.h0, false, nullptr, st);
         if (e != cudaSuccess) return e;
     }
-    return go<true, kFwdCarry>(p, status, p.nseg <= 1, st);
+    return go<true, kFwdCarry>(p, p.nseg <= 1, st);
 }
 
-cudaError_t launch_decay_seg_rev_tc(const DecayParams &p, int *status, cudaStream_t st) {
-    return go<true, kSegRev>(p, status, false, st);
+cudaError_t launch_decay_seg_rev_tc(const DecayParams &p, cudaStream_t st) {
+    return go<true, kSegRev>(p, false, st);
 }
 
 }  // namespace pdssm
