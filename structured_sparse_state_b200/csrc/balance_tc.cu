@@ -12,7 +12,9 @@
 //           g_u += G W  (K = N; W's first two parts: G's rounding to bf16 is
 //           then the only one besides g_u's own), over the groups
 //   g_W     G as three bf16 parts to shared memory (two, then the third), and
-//           g_W += G^T u  (K = 128 rows), kept in TMEM over the CTA's tiles
+//           g_W += G^T u  (K = 128 rows), a tile's in TMEM, the CTA's tiles'
+//           added up in registers (a product's own additions truncate: over
+//           a CTA's 14 tiles that cost 5.6e-6 of g_W's norm)
 // L is double-buffered: the next tile's products run under this one's softmax.
 //
 // Bound: tensor pipe and the softmax's issue slots, about equal; u is read
@@ -160,9 +162,28 @@ __global__ void __launch_bounds__(kTh, 1)
     const uint32_t tlane = (uint32_t)(quad * 32) << 16;
 
     if (warp < kEpi) {
-        float acc[MODE == kSums ? 64 : 1];
+        // sums: this thread's columns; g_W: entry and 64 columns of d (a group of
+        // 64 entries lies in the lanes twice, so their second half takes others)
+        float acc[MODE == kGu ? 1 : 64];
 #pragma unroll
-        for (int q = 0; q < (MODE == kSums ? 64 : 1); ++q) acc[q] = 0.f;
+        for (int q = 0; q < (MODE == kGu ? 1 : 64); ++q) acc[q] = 0.f;
+        const int we = N > 64 ? r : r & 63;
+        const int wd = N > 64 ? half * (Dp / 2) : (half * 2 + (r >> 6)) * (Dp / 4);
+        const int wn = N > 64 ? Dp / 2 : Dp / 4;
+        auto take = [&]() {         // the finished tile's g_W
+            if constexpr (MODE == kGw) {
+                tc_fence_after();
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    if (16 * q >= wn) break;
+                    uint32_t raw[16];
+                    tmem_ld16_raw(tAcc + wd + 16 * q + tlane, raw);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) acc[16 * q + e] += __uint_as_float(raw[e]);
+                }
+            }
+        };
         for (int i = 0; i < items; ++i) {
             const int tile = i / ng, gi = i % ng;
             const int c0 = (group0 + gi) * N + half * cols;     // first entry of this thread
@@ -182,8 +203,11 @@ __global__ void __launch_bounds__(kTh, 1)
             if (!wait_warp(kLFull, i)) break;
             tc_fence_after();
             if (MODE == kGw) {
-                // the parts of the last tile's G have been read
-                if (i > 0 && !wait_warp(kDone, i - 1)) break;
+                // the last tile's g_W is there, and the parts of its G have been read
+                if (i > 0) {
+                    if (!wait_warp(kDone, i - 1)) break;
+                    take();
+                }
                 if (!live) {        // behind an end: u must not meet a zero gradient as a NaN
                     const uint32_t ut = sm + t.o_u + (uint32_t)(tile % t.ustages) * ubytes;
                     for (int a = half; a < atoms; a += 2)
@@ -309,25 +333,15 @@ __global__ void __launch_bounds__(kTh, 1)
             }
         }
         if constexpr (MODE == kGw) {
-            // g_W of the group over the CTA's tiles: lane = entry
-            if (items > 0) wait_warp(kDone, items - 1);
-            tc_fence_after();
-            const int c = group0 * N + r, h = c / KT, k = c % KT;
+            // g_W of the group over the CTA's tiles
+            if (items > 0 && wait_warp(kDone, items - 1)) take();
+            const int c = group0 * N + we, h = c / KT, k = c % KT;
             const int slice = blockIdx.x / pl.groups;
-            const bool mine = r < N && h < p.H && k < p.K;
-            float *out = p.part + (((int64_t)slice * p.H + h) * p.K + k) * p.D;
-            const int dcols = Dp / 2;
-#pragma unroll 1
-            for (int q = 0; q < dcols; q += 16) {
-                uint32_t raw[16];
-                tmem_ld16_raw(tAcc + half * dcols + q + tlane, raw);
-                tmem_wait_ld();
+            const bool mine = h < p.H && k < p.K;
+            float *out = p.part + (((int64_t)slice * p.H + h) * p.K + k) * p.D + wd;
 #pragma unroll
-                for (int e = 0; e < 16; ++e) {
-                    const int col = half * dcols + q + e;
-                    if (mine && col < p.D) out[col] = items > 0 ? __uint_as_float(raw[e]) : 0.f;
-                }
-            }
+            for (int e = 0; e < 64; ++e)
+                if (mine && e < wn && wd + e < p.D) out[e] = acc[e];
         }
         if constexpr (MODE == kSums) {
             // column sums over the warp's rows, one warp's 64 columns at a time
@@ -386,7 +400,7 @@ __global__ void __launch_bounds__(kTh, 1)
 #pragma unroll
                         for (int k = 0; k < 8; ++k)
                             umma_ss(tAcc, ar + k * umma_step(2048), ub + k * umma_step(2048), idW,
-                                    j > 0 || part > 0 || k > 0);
+                                    part > 0 || k > 0);
                     }
                 }
                 umma_commit(bar(kDone, j));

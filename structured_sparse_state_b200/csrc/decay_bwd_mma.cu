@@ -472,11 +472,9 @@ __global__ void __launch_bounds__(kTh, 2) k_decay_bwd_mma(DecayParams p) {
                 }
             }
         }
-        // ---- R
-#pragma unroll
-        for (int f = 0; f < 4; ++f)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) R[f][e] *= aend;
+        // ---- R: the chunk's part from zero, then one fp32 multiply-add (a product's
+        // own additions truncate, which would pile up over a long memory)
+        zero();
 #pragma unroll
         for (int ks = 0; ks < 4; ++ks) {
             uint32_t a[4], parts[3][4], f0[4], f1[4];
@@ -493,12 +491,16 @@ __global__ void __launch_bounds__(kTh, 2) k_decay_bwd_mma(DecayParams p) {
             }
 #pragma unroll
             for (int k = 0; k < 3; ++k) {
-                mma(R[0], parts[k], f0[0], f0[1]);
-                mma(R[1], parts[k], f0[2], f0[3]);
-                mma(R[2], parts[k], f1[0], f1[1]);
-                mma(R[3], parts[k], f1[2], f1[3]);
+                mma(acc[0], parts[k], f0[0], f0[1]);
+                mma(acc[1], parts[k], f0[2], f0[3]);
+                mma(acc[2], parts[k], f1[0], f1[1]);
+                mma(acc[3], parts[k], f1[2], f1[3]);
             }
         }
+#pragma unroll
+        for (int f = 0; f < 4; ++f)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) R[f][e] = fmaf(aend, R[f][e], acc[f][e]);
         __syncthreads();                // s_u, s_v are in
         if (warp == 0) {
             double through = 0.0;
