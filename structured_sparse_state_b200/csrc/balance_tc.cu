@@ -4,14 +4,15 @@
 // takes K entries rounded up to a power of two).  Its weights lie in shared
 // memory as three bf16 parts (8 + 8 + 8 bits of fp32), so that the logits
 //     L = u W^T            128 rows x N, K = D, three products
-// have fp32 accuracy (u is bf16 by itself).  Eight warps take a finished L
+// have fp32 accuracy (u is bf16 by itself); the small parts are multiplied
+// first, since a product's additions truncate the sum so far.  Eight warps take a finished L
 // from TMEM, a row and half of its columns per thread: softmax per head, then
 //   sums    column sums of p over the rows, in registers over the CTA's tiles;
 //           counts by shared-memory atomics (integers)
 //   g_u     G, the logits' gradients, back to TMEM as bf16, and
 //           g_u += G W  (K = N; W's first two parts: G's rounding to bf16 is
 //           then the only one besides g_u's own), over the groups
-//   g_W     G as three bf16 parts to shared memory (two, then the third), and
+//   g_W     G as three bf16 parts to shared memory (two, then the largest), and
 //           g_W += G^T u  (K = 128 rows), a tile's in TMEM, the CTA's tiles'
 //           added up in registers (a product's own additions truncate: over
 //           a CTA's 14 tiles that cost 5.6e-6 of g_W's norm)
@@ -260,15 +261,16 @@ __global__ void __launch_bounds__(kTh, 1)
                         const uint32_t gt = sm + t.o_g;
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
-                            uint32_t p1[4], p2[4];
+                            uint32_t p1[4], p2[4];      // parts 1 and 2; the first goes last
 #pragma unroll
                             for (int k = 0; k < 4; ++k) {
                                 float a = v[8 * e + 2 * k], b = v[8 * e + 2 * k + 1];
+                                const uint32_t w = pack2(a, b);
+                                third[16 * q + 4 * e + k] = w;
+                                a -= lo_of(w);
+                                b -= hi_of(w);
                                 p1[k] = pack2(a, b);
-                                a -= lo_of(p1[k]);
-                                b -= hi_of(p1[k]);
-                                p2[k] = pack2(a, b);
-                                third[16 * q + 4 * e + k] = pack2(a - lo_of(p2[k]), b - hi_of(p2[k]));
+                                p2[k] = pack2(a - lo_of(p1[k]), b - hi_of(p1[k]));
                             }
                             const int col = half * cols + 32 * q + 8 * e;
                             const uint32_t at = gt + (uint32_t)(col / 64) * (kRows * 128) + piece(r, (col & 63) / 8);
@@ -289,7 +291,7 @@ __global__ void __launch_bounds__(kTh, 1)
             tc_fence_before();
             mbar_arrive(bar(kGReady, i));
             if constexpr (MODE == kGw) {
-                if (!wait_warp(kGHalf, i)) break;       // parts 0 and 1 have been read
+                if (!wait_warp(kGHalf, i)) break;       // part 1's buffer has been read
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
                     if (8 * e >= cols) break;
@@ -390,13 +392,13 @@ __global__ void __launch_bounds__(kTh, 1)
                 } else {
                     const uint32_t ub = umn0 + (uint32_t)(tile % t.ustages) * umma_step(ubytes);
 #pragma unroll 1
-                    for (int part = 0; part < 3; ++part) {
+                    for (int part = 0; part < 3; ++part) {      // parts 2, 1, 0 of G
                         if (part == 2) {
                             umma_commit(bar(kGHalf, j));
                             if (!wait(kGThird, j)) return;
                         }
                         tc_fence_after();
-                        const uint32_t ar = g0 + (part == 1 ? umma_step((uint32_t)kRows * N * 2) : 0u);
+                        const uint32_t ar = g0 + (part == 0 ? umma_step((uint32_t)kRows * N * 2) : 0u);
 #pragma unroll
                         for (int k = 0; k < 8; ++k)
                             umma_ss(tAcc, ar + k * umma_step(2048), ub + k * umma_step(2048), idW,
@@ -419,7 +421,7 @@ __global__ void __launch_bounds__(kTh, 1)
                 const uint32_t ub = u0 + (uint32_t)(tile % t.ustages) * umma_step(ubytes);
                 const uint32_t wb = w0 + (uint32_t)wslot(i) * umma_step((uint32_t)pl.w_bytes);
 #pragma unroll 1
-                for (int part = 0; part < 3; ++part)
+                for (int part = 2; part >= 0; --part)       // the small ones first
 #pragma unroll 1
                     for (int a = 0; a < atoms; ++a) {
                         const uint32_t ar = ub + a * umma_step(kRows * 128);
@@ -427,7 +429,7 @@ __global__ void __launch_bounds__(kTh, 1)
 #pragma unroll
                         for (int k = 0; k < 4; ++k)
                             umma_ss(tL(i), ar + k * umma_step(32), br + k * umma_step(32), idL,
-                                    part > 0 || a > 0 || k > 0);
+                                    part < 2 || a > 0 || k > 0);
                     }
                 umma_commit(bar(kLFull, i));
                 if (MODE != kSums && i > 0 && ahead) second(i - 1);

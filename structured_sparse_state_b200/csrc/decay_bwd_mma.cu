@@ -354,21 +354,21 @@ __global__ void __launch_bounds__(kTh, 2) k_decay_bwd_mma(DecayParams p) {
         };
         // rows times the transpose of a [n][k] operand in three parts
         auto by_parts = [&](uint32_t rows, uint32_t parts) {
+            uint32_t a[4][4];
 #pragma unroll
-            for (int ks = 0; ks < 4; ++ks) {
-                uint32_t a[4];
-                ldm4(a, at_a(rows, m0, ks, lane));
+            for (int ks = 0; ks < 4; ++ks) ldm4(a[ks], at_a(rows, m0, ks, lane));
 #pragma unroll
-                for (int k = 0; k < 3; ++k) {
+            for (int k = 2; k >= 0; --k)        // the small parts first: additions truncate
+#pragma unroll
+                for (int ks = 0; ks < 4; ++ks) {
                     uint32_t f0[4], f1[4];
                     ldm4(f0, at_b(parts + k * kTile, n0, ks, lane));
                     ldm4(f1, at_b(parts + k * kTile, n0 + 16, ks, lane));
-                    mma(acc[0], a, f0[0], f0[1]);
-                    mma(acc[1], a, f0[2], f0[3]);
-                    mma(acc[2], a, f1[0], f1[1]);
-                    mma(acc[3], a, f1[2], f1[3]);
+                    mma(acc[0], a[ks], f0[0], f0[1]);
+                    mma(acc[1], a[ks], f0[2], f0[3]);
+                    mma(acc[2], a[ks], f1[0], f1[1]);
+                    mma(acc[3], a[ks], f1[2], f1[3]);
                 }
-            }
         };
         // acc *= by row factors; the rows' products with a tile's rows
         auto scale_rows = [&](float f0, float f1) {

@@ -505,13 +505,13 @@ __global__ void __launch_bounds__(kTcTh, 1)
                 // STK: the parts' 64 columns twice as the 128 rows (leading offset 0;
                 // part 2 lies in b's place)
 #pragma unroll 1
-                for (int part = 0; part < 3; ++part) {
+                for (int part = 2; part >= 0; --part) {     // the small ones first
                     const uint32_t ar = STK ? (part < 2 ? pl + part * umma_step(kTile) : bt) - umma_lo(0, kTile) : bt;
                     const uint32_t br = STK ? xr : pl + part * umma_step(kTile);
 #pragma unroll
                     for (int k = 0; k < 8; ++k)
                         umma_ss(tcol(k >> 2, 192), ar + k * kRow16, br + k * kRow16, kIdD,
-                                (k & 3) > 0 || part > 0);
+                                (k & 3) > 0 || part < 2);
                 }
                 umma_commit(bar(kDFull, i));
             }
