@@ -13,8 +13,10 @@ namespace pdssm {
 // Segments fill the GPU when the (batch, head, 64 columns) units do not: one
 // CTA of the tensor-core forward fits an SM, two of its adjoint, about three
 // of the others.  Each segment costs a second read of b and x (the adjoint: of
-// c and g_y), so it has at least four chunks of
-// the tensor-core kernels, two of the others, whose chunks take longer.
+// c and g_y).  A segment has at least four chunks of the tensor-core kernels
+// (whose start-up is worth about one), one of the others: a training step of
+// 8 heads x 1501 steps, 64 x 48 fp32, took 222 us with segments of at least
+// four, 127 with two.
 DecayPlan decay_plan(const pdssm_decay_dims &d, DecayPath path, bool bf16, bool adjoint) {
     DecayPlan pl{};
     const bool tc = path == kDecayTc;
@@ -24,8 +26,8 @@ DecayPlan decay_plan(const pdssm_decay_dims &d, DecayPath path, bool bf16, bool 
     pl.pslices = adjoint ? 1 : (int)((d.P + 63) / 64);
     const int64_t units = d.B * d.H * pl.pslices;
     int64_t nseg = (int64_t)kDecaySMs * (tc ? (adjoint ? 2 : 1) : 3) / units;
-    const int least = tc ? 4 : 2;       // chunks of a segment
-    if (nseg > pl.nchunks / least) nseg = pl.nchunks / least;
+    if (tc && nseg > pl.nchunks / 4) nseg = pl.nchunks / 4;
+    if (nseg > pl.nchunks) nseg = pl.nchunks;
     if (nseg < 1) nseg = 1;
     pl.seg_chunks = (int)((pl.nchunks + nseg - 1) / nseg);
     if (tc && adjoint) pl.seg_chunks = (pl.seg_chunks + 1) / 2 * 2;     // whole chunks of 128

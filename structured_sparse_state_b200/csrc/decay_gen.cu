@@ -38,19 +38,29 @@ __device__ __forceinline__ void zero(float (&acc)[TM][TN]) {
         for (int j = 0; j < TN; ++j) acc[i][j] = 0.f;
 }
 
-// rows t0..t0+C-1 of a [step][width] tensor into shared rows of WT + 1
-// floats; zero behind `len` and behind the width
+// Rows t0..t0+C-1 of a [step][width] tensor on their way to shared rows of
+// WT + 1 floats; zero behind `len` and behind the width.  A chunk's rows are
+// fetched while the chunk before it is worked on (their latency, a
+// microsecond, is a third of a short chunk's time).
 template <typename T, int C, int WT>
-__device__ __forceinline__ void load_rows(float *dst, const T *src, int64_t stride, int width,
-                                          int64_t t0, int64_t len) {
-#pragma unroll 8
-    for (int e = threadIdx.x; e < C * WT; e += kThreads) {
-        const int t = e / WT, n = e % WT;
-        float v = 0.f;
-        if (n < width && t0 + t < len) v = to_f<T>(src[(t0 + t) * stride + n]);
-        dst[t * (WT + 1) + n] = v;
+struct Rows {
+    static constexpr int kN = C * WT / kThreads;
+    T v[kN];
+    __device__ __forceinline__ void fetch(const T *src, int64_t stride, int width, int64_t t0,
+                                          int64_t len) {
+        const int n = threadIdx.x % WT;
+#pragma unroll
+        for (int i = 0; i < kN; ++i) {
+            const int64_t t = t0 + (i * kThreads + threadIdx.x) / WT;
+            v[i] = n < width && t < len ? src[t * stride + n] : from_f<T>(0.f);
+        }
     }
-}
+    __device__ __forceinline__ void put(float *dst) const {
+#pragma unroll
+        for (int i = 0; i < kN; ++i)
+            dst[(i * kThreads + threadIdx.x) / WT * (WT + 1) + threadIdx.x % WT] = to_f<T>(v[i]);
+    }
+};
 
 struct Head {
     int bh, b, h;
@@ -71,6 +81,21 @@ __device__ __forceinline__ Head head_of(const DecayParams &p, int64_t bh) {
     return hd;
 }
 
+// A chunk's log decays, fetched likewise, by the first warp.
+template <int C>
+struct Steps {
+    float v[C / 32];
+    __device__ __forceinline__ void fetch(const DecayParams &p, const Head &hd, int64_t t0) {
+        if (threadIdx.x < 32)
+#pragma unroll
+            for (int i = 0; i < C / 32; ++i) v[i] = hd.log_a(p, t0 + 32 * i + threadIdx.x);
+    }
+    __device__ __forceinline__ void sums(float2 *G) const {
+        if (threadIdx.x < 32)
+            decay_sums<C>([&](int t) { return v[t / 32]; }, G, threadIdx.x);
+    }
+};
+
 // The state alone over one segment from zero.  Forward (REV = false): rows u
 // = b, v = x, weights e^{G_C - G_t}, chunks in order.  Reverse: u = c, v =
 // g_y, weights e^{G_t}, chunks in reverse.
@@ -90,13 +115,25 @@ __global__ void __launch_bounds__(kThreads) k_decay_seg_gen(DecayParams p) {
     zero(S);
     double total = 0.0;
     const int c0 = seg * p.seg_chunks, c1 = min(c0 + p.seg_chunks, p.nchunks);
+    Rows<T, C, WT> ru, rv;
+    Steps<C> rl;
+    auto fetch = [&](int i) {
+        const int64_t t0 = i < c1 ? (int64_t)(REV ? c1 - 1 - (i - c0) : i) * C : hd.len;
+        ru.fetch(u, p.key_t, p.N, t0, hd.len);
+        rv.fetch(v, p.val_t, p.P, t0, hd.len);
+        rl.fetch(p, hd, t0);
+    };
+    fetch(c0);
     for (int i = c0; i < c1; ++i) {
         const int64_t t0 = (int64_t)(REV ? c1 - 1 - (i - c0) : i) * C;
-        if (t0 >= hd.len) continue;     // behind the end: nothing is added, nothing decays
-        load_rows<T, C, WT>(su, u, p.key_t, p.N, t0, hd.len);
-        load_rows<T, C, WT>(sv, v, p.val_t, p.P, t0, hd.len);
-        if (threadIdx.x < 32)
-            decay_sums<C>([&](int t) { return hd.log_a(p, t0 + t); }, sG, threadIdx.x);
+        if (t0 >= hd.len) {             // behind the end: nothing is added, nothing decays
+            fetch(i + 1);
+            continue;
+        }
+        ru.put(su);
+        rv.put(sv);
+        rl.sums(sG);
+        fetch(i + 1);
         __syncthreads();
         const float2 end = sG[C - 1];
         total += (double)end.x + (double)end.y;
@@ -155,15 +192,26 @@ __global__ void __launch_bounds__(kThreads) k_decay_fwd_gen(DecayParams p) {
         sS[n * LP + q] = (in && n < p.N && q < pw) ? in[(int64_t)n * p.P + p0 + q] : 0.f;
     }
     const int c0 = seg * p.seg_chunks, c1 = min(c0 + p.seg_chunks, p.nchunks);
+    Rows<T, C, WT> rc, rb;
+    Rows<T, C, PS> rx;
+    Steps<C> rl;
+    auto fetch = [&](int i) {
+        const int64_t t0 = i < c1 ? (int64_t)i * C : hd.len;
+        rc.fetch(c, p.key_t, p.N, t0, hd.len);
+        rb.fetch(b, p.key_t, p.N, t0, hd.len);
+        rx.fetch(x, p.val_t, pw, t0, hd.len);
+        rl.fetch(p, hd, t0);
+    };
+    fetch(c0);
     for (int i = c0; i < c1; ++i) {
         const int64_t t0 = (int64_t)i * C;
         __syncthreads();
         if (t0 < hd.len) {
-            load_rows<T, C, WT>(sc, c, p.key_t, p.N, t0, hd.len);
-            load_rows<T, C, WT>(sb, b, p.key_t, p.N, t0, hd.len);
-            load_rows<T, C, PS>(sx, x, p.val_t, pw, t0, hd.len);
-            if (threadIdx.x < 32)
-                decay_sums<C>([&](int t) { return hd.log_a(p, t0 + t); }, sG, threadIdx.x);
+            rc.put(sc);
+            rb.put(sb);
+            rx.put(sx);
+            rl.sums(sG);
+            fetch(i + 1);
         }
         if (p.carry && i > 0) {
             float *out = p.carry + ((int64_t)hd.bh * p.nchunks + i) * np + p0;
@@ -276,15 +324,28 @@ __global__ void __launch_bounds__(kThreads) k_decay_bwd_gen(DecayParams p) {
         sR[n * LD + q] = (in && n < p.N && q < p.P) ? in[(int64_t)n * p.P + q] : 0.f;
     }
     const int c0 = seg * p.seg_chunks, c1 = min(c0 + p.seg_chunks, p.nchunks);
+    Rows<T, C, WT> rc, rb, rx, rg;
+    Steps<C> rl;
+    auto fetch = [&](int i) {
+        const int64_t t0 = i >= c0 ? (int64_t)i * C : hd.len;
+        rc.fetch(c, p.key_t, p.N, t0, hd.len);
+        rb.fetch(b, p.key_t, p.N, t0, hd.len);
+        rx.fetch(x, p.val_t, p.P, t0, hd.len);
+        rg.fetch(gy, p.val_t, p.P, t0, hd.len);
+        rl.fetch(p, hd, t0);
+    };
+    constexpr bool kAhead = WT <= 64;       // wider rows would not fit the registers
+    if (kAhead) fetch(c1 - 1);
     for (int i = c1 - 1; i >= c0; --i) {
         const int64_t t0 = (int64_t)i * C;
         __syncthreads();
         const bool live = t0 < hd.len;
+        if (!kAhead && live) fetch(i);
         if (live) {
-            load_rows<T, C, WT>(sc, c, p.key_t, p.N, t0, hd.len);
-            load_rows<T, C, WT>(sb, b, p.key_t, p.N, t0, hd.len);
-            load_rows<T, C, WT>(sx, x, p.val_t, p.P, t0, hd.len);
-            load_rows<T, C, WT>(sg, gy, p.val_t, p.P, t0, hd.len);
+            rc.put(sc);
+            rb.put(sb);
+            rx.put(sx);
+            rg.put(sg);
             const float *S0 = i > 0 ? p.carry + ((int64_t)hd.bh * p.nchunks + i) * np
                                     : (p.h0 ? p.h0 + (int64_t)hd.bh * np : nullptr);
 #pragma unroll 4
@@ -292,9 +353,10 @@ __global__ void __launch_bounds__(kThreads) k_decay_bwd_gen(DecayParams p) {
                 const int n = e / WT, q = e % WT;
                 sS[n * LD + q] = S0 && n < p.N && q < p.P ? S0[(int64_t)n * p.P + q] : 0.f;
             }
-            if (threadIdx.x < 32)
-                decay_sums<C>([&](int t) { return hd.log_a(p, t0 + t); }, sG, threadIdx.x);
-        } else {                        // behind the end: zero gradients, the state's stays
+            rl.sums(sG);
+        }
+        if (kAhead) fetch(i - 1);
+        if (!live) {                    // behind the end: zero gradients, the state's stays
             for (int e = threadIdx.x; e < C * WT; e += kThreads) {
                 const int64_t t = t0 + e / WT;
                 const int q = e % WT;
