@@ -1,10 +1,11 @@
 // Decay scan on the CUDA cores: every type and width, the path of fp32
 // inputs.  One CTA of 256 threads (16 x 16) per segment of a (batch, head);
-// a chunk's operands sit in shared memory as fp32 rows of odd length, so both
-// orientations of a product read them without bank conflicts, and each thread
-// owns a strided TM x TN tile of a product's result.
+// a chunk's operands sit in shared memory as fp32 rows of width + 4 floats, and
+// each thread owns a TM x TN tile of a product's result.
 //
-// Bound: shared-memory loads, (TM + TN) per TM * TN multiply-adds.
+// Bound: shared-memory bandwidth.  Both orientations of a product are read by
+// 16- or 8-byte loads (see Along and Across): about half of the wavefronts and
+// a third of the instructions of 4-byte loads.
 #include "decay.cuh"
 #include "launch.cuh"
 
@@ -13,20 +14,59 @@ namespace {
 
 constexpr int kThreads = 256;
 
-// acc[i][j] += sum_k a(ty + 16 i, k) b(tx + 16 j, k)
+// Where a thread's i-th row or column of a tile lies: in pairs, so that an
+// operand whose rows run along the product's k is read by 8-byte loads, or
+// strided, for operands that run across it.
+__device__ __forceinline__ int pairs(int t, int i) { return 2 * t + (i & 1) + 32 * (i >> 1); }
+__device__ __forceinline__ int strided(int t, int i) { return t + 16 * i; }
+
+// Operands of a product, four values of k at a time:
+// Along: element (i, k) at [idx(i)][k], one 16-byte load per row
+template <int T, bool PAIRS>
+struct Along {
+    const float *p;
+    int ld, t;
+    __device__ __forceinline__ void load(float (&v)[T][4], int k) const {
+#pragma unroll
+        for (int i = 0; i < T; ++i) {
+            const float4 x = *reinterpret_cast<const float4 *>(
+                p + (PAIRS ? pairs(t, i) : strided(t, i)) * ld + k);
+            v[i][0] = x.x; v[i][1] = x.y; v[i][2] = x.z; v[i][3] = x.w;
+        }
+    }
+};
+// Across: element (i, k) at [k][idx(i)], one 8-byte load per pair and k
+template <int T>
+struct Across {
+    const float *p;
+    int ld, t;
+    __device__ __forceinline__ void load(float (&v)[T][4], int k) const {
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+#pragma unroll
+            for (int i = 0; i < T; i += 2) {
+                const float2 x =
+                    *reinterpret_cast<const float2 *>(p + (k + q) * ld + pairs(t, i));
+                v[i][q] = x.x;
+                v[i + 1][q] = x.y;
+            }
+    }
+};
+
+// acc[i][j] += sum_k a(i, k) b(j, k), K a multiple of 4
 template <int TM, int TN, class FA, class FB>
-__device__ __forceinline__ void tile_mm(float (&acc)[TM][TN], int K, FA a, FB b) {
-#pragma unroll 8
-    for (int k = 0; k < K; ++k) {
-        float av[TM], bv[TN];
+__device__ __forceinline__ void tile_mm(float (&acc)[TM][TN], int K, const FA &a, const FB &b) {
+#pragma unroll 2
+    for (int k = 0; k < K; k += 4) {
+        float av[TM][4], bv[TN][4];
+        a.load(av, k);
+        b.load(bv, k);
 #pragma unroll
-        for (int i = 0; i < TM; ++i) av[i] = a(i, k);
+        for (int q = 0; q < 4; ++q)
 #pragma unroll
-        for (int j = 0; j < TN; ++j) bv[j] = b(j, k);
+            for (int i = 0; i < TM; ++i)
 #pragma unroll
-        for (int i = 0; i < TM; ++i)
-#pragma unroll
-            for (int j = 0; j < TN; ++j) acc[i][j] = fmaf(av[i], bv[j], acc[i][j]);
+                for (int j = 0; j < TN; ++j) acc[i][j] = fmaf(av[i][q], bv[j][q], acc[i][j]);
     }
 }
 
@@ -39,7 +79,7 @@ __device__ __forceinline__ void zero(float (&acc)[TM][TN]) {
 }
 
 // Rows t0..t0+C-1 of a [step][width] tensor on their way to shared rows of
-// WT + 1 floats; zero behind `len` and behind the width.  A chunk's rows are
+// WT + 4 floats; zero behind `len` and behind the width.  A chunk's rows are
 // fetched while the chunk before it is worked on (their latency, a
 // microsecond, is a third of a short chunk's time).
 template <typename T, int C, int WT>
@@ -58,7 +98,7 @@ struct Rows {
     __device__ __forceinline__ void put(float *dst) const {
 #pragma unroll
         for (int i = 0; i < kN; ++i)
-            dst[(i * kThreads + threadIdx.x) / WT * (WT + 1) + threadIdx.x % WT] = to_f<T>(v[i]);
+            dst[(i * kThreads + threadIdx.x) / WT * (WT + 4) + threadIdx.x % WT] = to_f<T>(v[i]);
     }
 };
 
@@ -102,9 +142,9 @@ struct Steps {
 template <typename T, int C, int WT, bool REV>
 __global__ void __launch_bounds__(kThreads) k_decay_seg_gen(DecayParams p) {
     extern __shared__ float sm[];
-    constexpr int LD = WT + 1;
+    constexpr int LD = WT + 4;
     float *su = sm, *sv = su + C * LD;
-    float2 *sG = reinterpret_cast<float2 *>(sv + C * LD + ((2 * C * LD) & 1));
+    float2 *sG = reinterpret_cast<float2 *>(sv + C * LD);
     const int seg = blockIdx.x % p.nseg;
     const Head hd = head_of(p, blockIdx.x / p.nseg);
     const int ty = threadIdx.x / 16, tx = threadIdx.x % 16;
@@ -148,8 +188,7 @@ __global__ void __launch_bounds__(kThreads) k_decay_seg_gen(DecayParams p) {
         for (int m = 0; m < TN; ++m)
 #pragma unroll
             for (int n = 0; n < TN; ++n) S[m][n] *= a;
-        tile_mm(S, C, [&](int m, int k) { return su[k * LD + ty + 16 * m]; },
-                [&](int n, int k) { return sv[k * LD + tx + 16 * n]; });
+        tile_mm(S, C, Across<TN>{su, LD, ty}, Across<TN>{sv, LD, tx});
         __syncthreads();
     }
     float *out = p.seg_state + ((int64_t)hd.bh * p.nseg + seg) * p.N * p.P;
@@ -157,7 +196,7 @@ __global__ void __launch_bounds__(kThreads) k_decay_seg_gen(DecayParams p) {
     for (int m = 0; m < TN; ++m)
 #pragma unroll
         for (int n = 0; n < TN; ++n) {
-            const int r = ty + 16 * m, q = tx + 16 * n;
+            const int r = pairs(ty, m), q = pairs(tx, n);
             if (r < p.N && q < p.P) out[r * p.P + q] = S[m][n];
         }
     if (threadIdx.x == 0) p.seg_decay[(int64_t)hd.bh * p.nseg + seg] = exp2f((float)total);
@@ -166,11 +205,11 @@ __global__ void __launch_bounds__(kThreads) k_decay_seg_gen(DecayParams p) {
 template <typename T, int C, int WT>
 __global__ void __launch_bounds__(kThreads) k_decay_fwd_gen(DecayParams p) {
     constexpr int PS = WT < 64 ? WT : 64;
-    constexpr int LD = WT + 1, LP = PS + 1, LC = C + 1;
+    constexpr int LD = WT + 4, LP = PS + 4, LC = C + 4;
     constexpr int TM = C / 16, TN = WT / 16, TP = PS / 16;
     extern __shared__ float sm[];
     float *sc = sm, *sb = sc + C * LD, *sx = sb + C * LD, *sS = sx + C * LP, *sP = sS + WT * LP;
-    float2 *sG = reinterpret_cast<float2 *>(sP + C * LC + ((WT * LP + C * LP + C * LC) & 1));
+    float2 *sG = reinterpret_cast<float2 *>(sP + C * LC);
     const int seg = blockIdx.x % p.nseg;
     const int ps = (blockIdx.x / p.nseg) % p.pslices;
     const Head hd = head_of(p, blockIdx.x / p.nseg / p.pslices);
@@ -232,13 +271,12 @@ __global__ void __launch_bounds__(kThreads) k_decay_fwd_gen(DecayParams p) {
         {
             float acc[TM][TM];
             zero(acc);
-            tile_mm(acc, WT, [&](int m, int k) { return sc[(ty + 16 * m) * LD + k]; },
-                    [&](int n, int k) { return sb[(tx + 16 * n) * LD + k]; });
+            tile_mm(acc, WT, Along<TM, true>{sc, LD, ty}, Along<TM, false>{sb, LD, tx});
 #pragma unroll
             for (int m = 0; m < TM; ++m)
 #pragma unroll
                 for (int n = 0; n < TM; ++n) {
-                    const int r = ty + 16 * m, q = tx + 16 * n;
+                    const int r = pairs(ty, m), q = strided(tx, n);
                     sP[r * LC + q] = q <= r ? acc[m][n] * decay_between(sG[r], sG[q]) : 0.f;
                 }
         }
@@ -246,23 +284,21 @@ __global__ void __launch_bounds__(kThreads) k_decay_fwd_gen(DecayParams p) {
         {
             float acc[TM][TP];
             zero(acc);
-            tile_mm(acc, WT, [&](int m, int k) { return sc[(ty + 16 * m) * LD + k]; },
-                    [&](int n, int k) { return sS[k * LP + tx + 16 * n]; });
+            tile_mm(acc, WT, Along<TM, true>{sc, LD, ty}, Across<TP>{sS, LP, tx});
 #pragma unroll
             for (int m = 0; m < TM; ++m) {
-                const float e = decay_from_start(sG[ty + 16 * m]);
+                const float e = decay_from_start(sG[pairs(ty, m)]);
 #pragma unroll
                 for (int n = 0; n < TP; ++n) acc[m][n] *= e;
             }
-            tile_mm(acc, C, [&](int m, int k) { return sP[(ty + 16 * m) * LC + k]; },
-                    [&](int n, int k) { return sx[k * LP + tx + 16 * n]; });
+            tile_mm(acc, C, Along<TM, true>{sP, LC, ty}, Across<TP>{sx, LP, tx});
 #pragma unroll
             for (int m = 0; m < TM; ++m) {
-                const int64_t t = t0 + ty + 16 * m;
+                const int64_t t = t0 + pairs(ty, m);
 #pragma unroll
                 for (int n = 0; n < TP; ++n)
-                    if (t < p.L && tx + 16 * n < pw)
-                        y[t * p.val_t + tx + 16 * n] = from_f<T>(t < hd.len ? acc[m][n] : 0.f);
+                    if (t < p.L && pairs(tx, n) < pw)
+                        y[t * p.val_t + pairs(tx, n)] = from_f<T>(t < hd.len ? acc[m][n] : 0.f);
             }
         }
         for (int e = threadIdx.x; e < C * WT; e += kThreads)
@@ -271,14 +307,13 @@ __global__ void __launch_bounds__(kThreads) k_decay_fwd_gen(DecayParams p) {
         {
             float acc[TN][TP];
             zero(acc);
-            tile_mm(acc, C, [&](int m, int k) { return sb[k * LD + ty + 16 * m]; },
-                    [&](int n, int k) { return sx[k * LP + tx + 16 * n]; });
+            tile_mm(acc, C, Across<TN>{sb, LD, ty}, Across<TP>{sx, LP, tx});
             const float a = decay_from_start(end);
 #pragma unroll
             for (int m = 0; m < TN; ++m)
 #pragma unroll
                 for (int n = 0; n < TP; ++n) {
-                    float *s = &sS[(ty + 16 * m) * LP + tx + 16 * n];
+                    float *s = &sS[pairs(ty, m) * LP + pairs(tx, n)];
                     *s = fmaf(a, *s, acc[m][n]);
                 }
         }
@@ -296,7 +331,7 @@ __global__ void __launch_bounds__(kThreads) k_decay_fwd_gen(DecayParams p) {
 // Adjoint of one segment's chunks in reverse; sR is dl/dS at the chunk's end.
 template <typename T, int C, int WT>
 __global__ void __launch_bounds__(kThreads) k_decay_bwd_gen(DecayParams p) {
-    constexpr int LD = WT + 1, LC = C + 1, TM = C / 16, TN = WT / 16;
+    constexpr int LD = WT + 4, LC = C + 4, TM = C / 16, TN = WT / 16;
     extern __shared__ float sm[];
     float *sc = sm, *sb = sc + C * LD, *sx = sb + C * LD, *sg = sx + C * LD, *sR = sg + C * LD;
     float *sS = sR + WT * LD, *sP = sS + WT * LD, *sQ = sP + C * LC;
@@ -383,10 +418,8 @@ __global__ void __launch_bounds__(kThreads) k_decay_bwd_gen(DecayParams p) {
             float s[TM][TM], v[TM][TM];
             zero(s);
             zero(v);
-            tile_mm(s, WT, [&](int m, int k) { return sc[(ty + 16 * m) * LD + k]; },
-                    [&](int n, int k) { return sb[(tx + 16 * n) * LD + k]; });
-            tile_mm(v, WT, [&](int m, int k) { return sg[(ty + 16 * m) * LD + k]; },
-                    [&](int n, int k) { return sx[(tx + 16 * n) * LD + k]; });
+            tile_mm(s, WT, Along<TM, true>{sc, LD, ty}, Along<TM, false>{sb, LD, tx});
+            tile_mm(v, WT, Along<TM, true>{sg, LD, ty}, Along<TM, false>{sx, LD, tx});
             float col[TM];
 #pragma unroll
             for (int n = 0; n < TM; ++n) col[n] = 0.f;
@@ -395,7 +428,7 @@ __global__ void __launch_bounds__(kThreads) k_decay_bwd_gen(DecayParams p) {
                 float row = 0.f;
 #pragma unroll
                 for (int n = 0; n < TM; ++n) {
-                    const int r = ty + 16 * m, q = tx + 16 * n;
+                    const int r = pairs(ty, m), q = strided(tx, n);
                     const float d = q <= r ? decay_between(sG[r], sG[q]) : 0.f;
                     const float pv = q <= r ? s[m][n] * d : 0.f, qv = q <= r ? v[m][n] * d : 0.f;
                     sP[r * LC + q] = pv;
@@ -407,10 +440,10 @@ __global__ void __launch_bounds__(kThreads) k_decay_bwd_gen(DecayParams p) {
                 // the 16 threads of a row are half a warp
 #pragma unroll
                 for (int d = 8; d; d >>= 1) row += __shfl_xor_sync(kFull, row, d);
-                if (tx == 0) sfrom[ty + 16 * m] = row;
+                if (tx == 0) sfrom[pairs(ty, m)] = row;
             }
 #pragma unroll
-            for (int n = 0; n < TM; ++n) sred[ty * C + tx + 16 * n] = col[n];
+            for (int n = 0; n < TM; ++n) sred[ty * C + strided(tx, n)] = col[n];
         }
         __syncthreads();
         for (int t = threadIdx.x; t < C; t += kThreads) {
@@ -424,26 +457,24 @@ __global__ void __launch_bounds__(kThreads) k_decay_bwd_gen(DecayParams p) {
         {
             float acc[TM][TN];
             zero(acc);
-            tile_mm(acc, WT, [&](int m, int k) { return sg[(ty + 16 * m) * LD + k]; },
-                    [&](int n, int k) { return sS[(tx + 16 * n) * LD + k]; });
+            tile_mm(acc, WT, Along<TM, true>{sg, LD, ty}, Along<TN, true>{sS, LD, tx});
 #pragma unroll
             for (int m = 0; m < TM; ++m) {
-                const float e = decay_from_start(sG[ty + 16 * m]);
+                const float e = decay_from_start(sG[pairs(ty, m)]);
                 uc[m] = 0.f;
 #pragma unroll
                 for (int n = 0; n < TN; ++n) {
                     acc[m][n] *= e;
-                    uc[m] = fmaf(acc[m][n], sc[(ty + 16 * m) * LD + tx + 16 * n], uc[m]);
+                    uc[m] = fmaf(acc[m][n], sc[pairs(ty, m) * LD + pairs(tx, n)], uc[m]);
                 }
             }
-            tile_mm(acc, C, [&](int m, int k) { return sQ[(ty + 16 * m) * LC + k]; },
-                    [&](int n, int k) { return sb[k * LD + tx + 16 * n]; });
+            tile_mm(acc, C, Along<TM, true>{sQ, LC, ty}, Across<TN>{sb, LD, tx});
 #pragma unroll
             for (int m = 0; m < TM; ++m) {
-                const int64_t t = t0 + ty + 16 * m;
+                const int64_t t = t0 + pairs(ty, m);
 #pragma unroll
                 for (int n = 0; n < TN; ++n) {
-                    const int q = tx + 16 * n;
+                    const int q = pairs(tx, n);
                     if (t >= p.L || q >= p.N) continue;
                     const float v = t < hd.len ? acc[m][n] : 0.f;
                     if (part)
@@ -457,26 +488,24 @@ __global__ void __launch_bounds__(kThreads) k_decay_bwd_gen(DecayParams p) {
         {
             float acc[TM][TN];
             zero(acc);
-            tile_mm(acc, WT, [&](int m, int k) { return sx[(ty + 16 * m) * LD + k]; },
-                    [&](int n, int k) { return sR[(tx + 16 * n) * LD + k]; });
+            tile_mm(acc, WT, Along<TM, true>{sx, LD, ty}, Along<TN, true>{sR, LD, tx});
 #pragma unroll
             for (int m = 0; m < TM; ++m) {
-                const float w = decay_between(end, sG[ty + 16 * m]);
+                const float w = decay_between(end, sG[pairs(ty, m)]);
                 vb[m] = 0.f;
 #pragma unroll
                 for (int n = 0; n < TN; ++n) {
                     acc[m][n] *= w;
-                    vb[m] = fmaf(acc[m][n], sb[(ty + 16 * m) * LD + tx + 16 * n], vb[m]);
+                    vb[m] = fmaf(acc[m][n], sb[pairs(ty, m) * LD + pairs(tx, n)], vb[m]);
                 }
             }
-            tile_mm(acc, C, [&](int m, int k) { return sQ[k * LC + ty + 16 * m]; },
-                    [&](int n, int k) { return sc[k * LD + tx + 16 * n]; });
+            tile_mm(acc, C, Across<TM>{sQ, LC, ty}, Across<TN>{sc, LD, tx});
 #pragma unroll
             for (int m = 0; m < TM; ++m) {
-                const int64_t t = t0 + ty + 16 * m;
+                const int64_t t = t0 + pairs(ty, m);
 #pragma unroll
                 for (int n = 0; n < TN; ++n) {
-                    const int q = tx + 16 * n;
+                    const int q = pairs(tx, n);
                     if (t >= p.L || q >= p.N) continue;
                     const float v = t < hd.len ? acc[m][n] : 0.f;
                     if (part)
@@ -490,23 +519,21 @@ __global__ void __launch_bounds__(kThreads) k_decay_bwd_gen(DecayParams p) {
         {
             float acc[TM][TN];
             zero(acc);
-            tile_mm(acc, WT, [&](int m, int k) { return sb[(ty + 16 * m) * LD + k]; },
-                    [&](int n, int k) { return sR[k * LD + tx + 16 * n]; });
+            tile_mm(acc, WT, Along<TM, true>{sb, LD, ty}, Across<TN>{sR, LD, tx});
 #pragma unroll
             for (int m = 0; m < TM; ++m) {
-                const float w = decay_between(end, sG[ty + 16 * m]);
+                const float w = decay_between(end, sG[pairs(ty, m)]);
 #pragma unroll
                 for (int n = 0; n < TN; ++n) acc[m][n] *= w;
             }
-            tile_mm(acc, C, [&](int m, int k) { return sP[k * LC + ty + 16 * m]; },
-                    [&](int n, int k) { return sg[k * LD + tx + 16 * n]; });
+            tile_mm(acc, C, Across<TM>{sP, LC, ty}, Across<TN>{sg, LD, tx});
 #pragma unroll
             for (int m = 0; m < TM; ++m) {
-                const int64_t t = t0 + ty + 16 * m;
+                const int64_t t = t0 + pairs(ty, m);
 #pragma unroll
                 for (int n = 0; n < TN; ++n)
-                    if (t < p.L && tx + 16 * n < p.P)
-                        gx[t * p.val_t + tx + 16 * n] = from_f<T>(t < hd.len ? acc[m][n] : 0.f);
+                    if (t < p.L && pairs(tx, n) < p.P)
+                        gx[t * p.val_t + pairs(tx, n)] = from_f<T>(t < hd.len ? acc[m][n] : 0.f);
             }
         }
         // e^{G_C} <S0, R>, the row sums u_i + R_i and v_j
@@ -527,8 +554,8 @@ __global__ void __launch_bounds__(kThreads) k_decay_bwd_gen(DecayParams p) {
         if (tx == 0)
 #pragma unroll
             for (int m = 0; m < TM; ++m) {
-                sred[ty + 16 * m] = uc[m];
-                sred[C + ty + 16 * m] = vb[m];
+                sred[pairs(ty, m)] = uc[m];
+                sred[C + pairs(ty, m)] = vb[m];
             }
         for (int e = threadIdx.x; e < C * WT; e += kThreads)
             sc[(e / WT) * LD + e % WT] *= decay_from_start(sG[e / WT]);
@@ -574,13 +601,12 @@ __global__ void __launch_bounds__(kThreads) k_decay_bwd_gen(DecayParams p) {
         {
             float acc[TN][TN];
             zero(acc);
-            tile_mm(acc, C, [&](int m, int k) { return sc[k * LD + ty + 16 * m]; },
-                    [&](int n, int k) { return sg[k * LD + tx + 16 * n]; });
+            tile_mm(acc, C, Across<TN>{sc, LD, ty}, Across<TN>{sg, LD, tx});
 #pragma unroll
             for (int m = 0; m < TN; ++m)
 #pragma unroll
                 for (int n = 0; n < TN; ++n) {
-                    float *s = &sR[(ty + 16 * m) * LD + tx + 16 * n];
+                    float *s = &sR[pairs(ty, m) * LD + pairs(tx, n)];
                     *s = fmaf(aend, *s, acc[m][n]);
                 }
         }
@@ -676,7 +702,7 @@ cudaError_t launch(int64_t grid, size_t smem, cudaStream_t st, const DecayParams
 
 template <typename T, int C, int WT, bool REV>
 cudaError_t seg_gen(const DecayParams &p, cudaStream_t st) {
-    const size_t smem = (size_t)(2 * C * (WT + 1) + 1 + 2 * C) * 4;
+    const size_t smem = (size_t)(2 * C * (WT + 4) + 2 * C) * 4;
     return launch<k_decay_seg_gen<T, C, WT, REV>>((int64_t)p.B * p.H * p.nseg, smem, st, p);
 }
 
@@ -689,7 +715,7 @@ cudaError_t fwd_gen(const DecayParams &p, cudaStream_t st) {
         e = launch_decay_join(p, p.h0, false, nullptr, st);
         if (e != cudaSuccess) return e;
     }
-    const size_t smem = (size_t)(2 * C * (WT + 1) + (C + WT) * (PS + 1) + C * (C + 1) + 1 + 2 * C) * 4;
+    const size_t smem = (size_t)(2 * C * (WT + 4) + (C + WT) * (PS + 4) + C * (C + 4) + 2 * C) * 4;
     return launch<k_decay_fwd_gen<T, C, WT>>((int64_t)p.B * p.H * p.nseg * p.pslices, smem, st, p);
 }
 
@@ -701,7 +727,7 @@ cudaError_t bwd_gen(const DecayParams &p, cudaStream_t st) {
         e = launch_decay_join(p, p.g_hlast, true, nullptr, st);
         if (e != cudaSuccess) return e;
     }
-    const size_t smem = (size_t)((4 * C + 2 * WT) * (WT + 1) + 2 * C * (C + 1) + 2 * C + 16 * C + 32 +
+    const size_t smem = (size_t)((4 * C + 2 * WT) * (WT + 4) + 2 * C * (C + 4) + 2 * C + 16 * C + 32 +
                                  2 * C) * 4;
     return launch<k_decay_bwd_gen<T, C, WT>>((int64_t)p.B * p.H * p.nseg, smem, st, p);
 }
