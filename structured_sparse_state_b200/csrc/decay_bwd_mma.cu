@@ -23,15 +23,27 @@
 namespace pdssm {
 namespace {
 
-constexpr int kC = 64, kTh = 256;
+constexpr int kC = 64, kTh = 256;           // steps of a chunk; threads of the products
+constexpr int kAll = kTh + 32;              // and a warp for decays and g_log_a
 constexpr uint32_t kTile = 64 * 128;        // 64 rows of 64 bf16, 128-byte swizzle
+
+// Per chunk, double-buffered: its decays (made a chunk ahead) and what
+// g_log_a adds up (taken a chunk later).
+struct Sums {
+    float2 G[kC];           // cumulated, base 2, hi + lo
+    float e[kC], w[kC];     // e_i, w_j
+    float row[2][kC];       // pair sums by row, per column half
+    float col[4][kC];       // by column, per row block
+    float u[2][kC], v[2][kC];
+    float dot[8];
+};
 
 struct Smem {
     static constexpr uint32_t kc = 0, kb = kTile, kx = 2 * kTile, kg = 3 * kTile;
     static constexpr uint32_t kS = 4 * kTile, kR = 7 * kTile;       // three parts each
     static constexpr uint32_t kP = 10 * kTile, kQ = 11 * kTile;
     static constexpr uint32_t kF = 12 * kTile;                      // floats below
-    static constexpr uint32_t kTotal = kF + (2 * kC + 2 * kC + 2 * kC + 4 * kC + 2 * kC + 2 * kC + 8) * 4;
+    static constexpr uint32_t kTotal = kF + 2 * sizeof(Sums);
 };
 
 __device__ __forceinline__ uint32_t piece(int r, int q) {
@@ -100,15 +112,13 @@ __device__ __forceinline__ float quad_sum(float v) {
     return v + __shfl_xor_sync(kFull, v, 2);
 }
 
-__global__ void __launch_bounds__(kTh, 2) k_decay_bwd_mma(DecayParams p) {
+// Barrier of the product warps.
+__device__ __forceinline__ void sync_products() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
+
+__global__ void __launch_bounds__(kAll, 2) k_decay_bwd_mma(DecayParams p) {
     extern __shared__ __align__(128) unsigned char sm_raw[];
     const uint32_t sm = smem_u32(sm_raw);
-    float2 *sG = reinterpret_cast<float2 *>(sm_raw + Smem::kF);
-    float *s_e = reinterpret_cast<float *>(sG + kC), *s_w = s_e + kC;   // e_i, w_j
-    float *s_row = s_w + kC;            // [2][64] pair sums by row, per column half
-    float *s_col = s_row + 2 * kC;      // [4][64] by column, per row block
-    float *s_u = s_col + 4 * kC, *s_v = s_u + 2 * kC;   // [2][64]
-    float *s_dot = s_v + 2 * kC;        // [8]
+    Sums *sums = reinterpret_cast<Sums *>(sm_raw + Smem::kF);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int wr = warp & 3, wc = warp >> 2;    // 16 rows and 32 columns of each product
     const int g = lane >> 2, q2 = (lane & 3) * 2;
@@ -128,6 +138,74 @@ __global__ void __launch_bounds__(kTh, 2) k_decay_bwd_mma(DecayParams p) {
     const bool part = p.rep > 1;        // gradients of shared keys: fp32 [B][H][L][N] partials
     const int64_t poff = bh * p.L * p.N, np = (int64_t)p.N * p.P;
 
+    const int c0 = seg * p.seg_chunks, c1 = min(c0 + p.seg_chunks, p.nchunks);
+
+    if (warp == 8) {
+        // ---- decays of the next chunk and g_log_a of the last one, while the
+        // product warps work on this one
+        auto decays = [&](int ch) {
+            const int64_t t0 = (int64_t)ch * kC;
+            if (ch < c0 || t0 >= len) return;
+            Sums &s = sums[ch & 1];
+            decay_sums<kC>([&](int t) { return t0 + t < len ? la[(t0 + t) * p.la_t] : 0.f; }, s.G, lane);
+            __syncwarp();
+            const float2 end = s.G[kC - 1];
+#pragma unroll
+            for (int i = 0; i < kC; i += 32) {
+                s.e[i + lane] = decay_from_start(s.G[i + lane]);
+                s.w[i + lane] = decay_between(end, s.G[i + lane]);
+            }
+        };
+        // g_log_a[t] = sum_{i>=t} (row_i + u_i - col_i) + sum_{j<t} v_j + e^{G_C} <S0, R>
+        auto gradient = [&](int ch) {
+            const int64_t t0 = (int64_t)ch * kC;
+            if (ch >= c1 || t0 >= len) return;
+            const Sums &s = sums[ch & 1];
+            double through = 0.0;
+            for (int w = 0; w < 8; ++w) through += (double)s.dot[w];
+            through *= (double)s.e[kC - 1];
+            double before = 0.0, total = 0.0, inc[2], pre[2];
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+                const int t = q * 32 + lane;
+                double a = (double)s.row[0][t] + (double)s.row[1][t] + (double)s.u[0][t] + (double)s.u[1][t] -
+                           ((double)s.col[0][t] + (double)s.col[1][t] + (double)s.col[2][t] + (double)s.col[3][t]);
+                double v = (double)s.v[0][t] + (double)s.v[1][t];
+                const double a0 = a, v0 = v;
+#pragma unroll
+                for (int d = 1; d < 32; d *= 2) {
+                    const double oa = shfl_up_d(a, d), ov = shfl_up_d(v, d);
+                    if (lane >= d) {
+                        a += oa;
+                        v += ov;
+                    }
+                }
+                inc[q] = total + a - a0;
+                pre[q] = before + v - v0;
+                total += __shfl_sync(kFull, a, 31);
+                before += __shfl_sync(kFull, v, 31);
+            }
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+                const int64_t t = t0 + q * 32 + lane;
+                if (t < p.L)    // a floored decay is a constant
+                    gla[t * p.gla_t] = t < len && !(la[t * p.la_t] <= (float)kDecayFloor)
+                                           ? (float)(total - inc[q] + pre[q] + through)
+                                           : 0.f;
+            }
+        };
+        decays(c1 - 1);
+        for (int ch = c1 - 1; ch >= c0; --ch) {
+            __syncthreads();
+            gradient(ch + 1);
+            __syncwarp();
+            decays(ch - 1);
+        }
+        __syncthreads();
+        gradient(c0);
+        return;
+    }
+
     // R: rows m0 + g (+ 8), columns n0 + 8 f + q2 (+ 1)
     float R[4][4];
     {
@@ -145,7 +223,6 @@ __global__ void __launch_bounds__(kTh, 2) k_decay_bwd_mma(DecayParams p) {
     for (int e = tid; e < 2 * 512; e += kTh)
         *reinterpret_cast<uint4 *>(sm_raw + Smem::kP + 16 * e) = make_uint4(0, 0, 0, 0);
 
-    const int c0 = seg * p.seg_chunks, c1 = min(c0 + p.seg_chunks, p.nchunks);
     auto store_key = [&](void *out, int64_t t, int q, float v0, float v1) {     // columns q, q + 1
         if (t >= p.L) return;
         if (t >= len) v0 = v1 = 0.f;
@@ -166,7 +243,8 @@ __global__ void __launch_bounds__(kTh, 2) k_decay_bwd_mma(DecayParams p) {
 
     for (int ch = c1 - 1; ch >= c0; --ch) {
         const int64_t t0 = (int64_t)ch * kC;
-        __syncthreads();                // the last chunk's tiles have been read
+        __syncthreads();                // the last chunk's tiles have been read; decays are in
+        Sums &sw = sums[ch & 1];
         if (t0 >= len) {                // behind the end: zero gradients, R stays
             for (int e = tid; e < kC * 64; e += kTh) {
                 const int64_t t = t0 + e / 64;
@@ -225,27 +303,36 @@ __global__ void __launch_bounds__(kTh, 2) k_decay_bwd_mma(DecayParams p) {
                 cp(Smem::kg, gy, p.val_t, p.P);
             }
         }
-        if (warp == 0) {
-            decay_sums<kC>([&](int t) { return t0 + t < len ? la[(t0 + t) * p.la_t] : 0.f; }, sG, lane);
-            __syncwarp();
-            const float2 end = sG[kC - 1];
-#pragma unroll
-            for (int i = 0; i < kC; i += 32) {
-                s_e[i + lane] = decay_from_start(sG[i + lane]);
-                s_w[i + lane] = decay_between(end, sG[i + lane]);
-            }
+        // the next chunk's rows and state on their way to L2
+        if (ch > c0) {
+            const int64_t tn = t0 - kC + (tid & 63);
+            const void *at = tid < 64 ? (const void *)(c + tn * p.key_t) : tid < 128 ? (const void *)(bb + tn * p.key_t)
+                             : tid < 192 ? (const void *)(x + tn * p.val_t) : (const void *)(gy + tn * p.val_t);
+            asm volatile("prefetch.global.L2 [%0];" ::"l"(at));
+            if (ch > 1 && (int64_t)tid * 32 < np)
+                asm volatile("prefetch.global.L2 [%0];" ::"l"(p.carry + (bh * p.nchunks + ch - 1) * np + tid * 32));
         }
         // ---- parts of S0 and R, and <S0, R>
         {
             const float *S0 = ch > 0 ? p.carry + (bh * p.nchunks + ch) * np
                                      : (p.h0 ? p.h0 + bh * np : nullptr);
             float S[4][4], dot = 0.f;
+            const bool even = p.P % 2 == 0 && ((uintptr_t)S0 & 7) == 0;
 #pragma unroll
             for (int f = 0; f < 4; ++f)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const int n = m0 + g + 8 * (e >> 1), q = n0 + 8 * f + q2 + (e & 1);
-                    S[f][e] = S0 && n < p.N && q < p.P ? S0[(int64_t)n * p.P + q] : 0.f;
+                for (int e = 0; e < 4; e += 2) {
+                    const int n = m0 + g + 4 * e, q = n0 + 8 * f + q2;
+                    const bool in = S0 && n < p.N;
+                    const float *at = S0 + (int64_t)n * p.P + q;
+                    if (even) {
+                        const float2 v = in && q < p.P ? *reinterpret_cast<const float2 *>(at) : make_float2(0.f, 0.f);
+                        S[f][e] = v.x;
+                        S[f][e + 1] = v.y;
+                    } else {
+                        S[f][e] = in && q < p.P ? at[0] : 0.f;
+                        S[f][e + 1] = in && q + 1 < p.P ? at[1] : 0.f;
+                    }
                 }
 #pragma unroll
             for (int f = 0; f < 4; ++f)
@@ -265,11 +352,11 @@ __global__ void __launch_bounds__(kTh, 2) k_decay_bwd_mma(DecayParams p) {
                 }
 #pragma unroll
             for (int d = 16; d; d >>= 1) dot += __shfl_xor_sync(kFull, dot, d);
-            if (lane == 0) s_dot[warp] = dot;
+            if (lane == 0) sw.dot[warp] = dot;
         }
         asm volatile("cp.async.wait_group 0;" ::: "memory");
-        __syncthreads();
-        const float aend = s_e[kC - 1];
+        sync_products();
+        const float aend = sw.e[kC - 1];
 
         // ---- P and Q of rows m0.., the 16-column blocks k = wc, wc + 2, .. <= wr
         {
@@ -279,11 +366,11 @@ __global__ void __launch_bounds__(kTh, 2) k_decay_bwd_mma(DecayParams p) {
                 ldm4(ca[ks], at_a(sm + Smem::kc, m0, ks, lane));
                 ldm4(ga[ks], at_a(sm + Smem::kg, m0, ks, lane));
             }
-            const float2 gr0 = sG[m0 + g], gr1 = sG[m0 + g + 8];
+            const float2 gr0 = sw.G[m0 + g], gr1 = sw.G[m0 + g + 8];
             float row0 = 0.f, row1 = 0.f;
 #pragma unroll 1
             for (int k = wc; k < 4; k += 2) {
-                float *col = s_col + wr * kC + 16 * k;
+                float *col = sw.col[wr] + 16 * k;
                 if (k > wr) {
                     if (lane < 16) col[lane] = 0.f;
                     continue;
@@ -306,7 +393,7 @@ __global__ void __launch_bounds__(kTh, 2) k_decay_bwd_mma(DecayParams p) {
 #pragma unroll
                 for (int f = 0; f < 2; ++f) {
                     const int j = 16 * k + 8 * f + q2;
-                    const float2 gj0 = sG[j], gj1 = sG[j + 1];
+                    const float2 gj0 = sw.G[j], gj1 = sw.G[j + 1];
                     float pv[4], qv[4], ev[4];
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
@@ -339,11 +426,11 @@ __global__ void __launch_bounds__(kTh, 2) k_decay_bwd_mma(DecayParams p) {
             row0 = quad_sum(row0);
             row1 = quad_sum(row1);
             if ((lane & 3) == 0) {
-                s_row[wc * kC + m0 + g] = row0;
-                s_row[wc * kC + m0 + g + 8] = row1;
+                sw.row[wc][m0 + g] = row0;
+                sw.row[wc][m0 + g + 8] = row1;
             }
         }
-        __syncthreads();
+        sync_products();
 
         float acc[4][4];
         auto zero = [&]() {
@@ -380,7 +467,7 @@ __global__ void __launch_bounds__(kTh, 2) k_decay_bwd_mma(DecayParams p) {
                 acc[f][3] *= f1;
             }
         };
-        auto row_dots = [&](uint32_t tile, float *out) {
+        auto row_dots = [&](uint32_t tile, float (&out)[2][kC]) {
             float d0 = 0.f, d1 = 0.f;
 #pragma unroll
             for (int f = 0; f < 4; ++f) {
@@ -392,8 +479,8 @@ __global__ void __launch_bounds__(kTh, 2) k_decay_bwd_mma(DecayParams p) {
             d0 = quad_sum(d0);
             d1 = quad_sum(d1);
             if ((lane & 3) == 0) {
-                out[wc * kC + m0 + g] = d0;
-                out[wc * kC + m0 + g + 8] = d1;
+                out[wc][m0 + g] = d0;
+                out[wc][m0 + g + 8] = d1;
             }
         };
         auto add_pairs = [&](const uint32_t (&a)[4], uint32_t tile, int ks) {
@@ -410,8 +497,8 @@ __global__ void __launch_bounds__(kTh, 2) k_decay_bwd_mma(DecayParams p) {
         // ---- g_c
         zero();
         by_parts(sm + Smem::kg, sm + Smem::kS);
-        scale_rows(s_e[m0 + g], s_e[m0 + g + 8]);
-        row_dots(Smem::kc, s_u);
+        scale_rows(sw.e[m0 + g], sw.e[m0 + g + 8]);
+        row_dots(Smem::kc, sw.u);
 #pragma unroll 1
         for (int ks = 0; ks <= wr; ++ks) {
             uint32_t a[4];
@@ -426,9 +513,9 @@ __global__ void __launch_bounds__(kTh, 2) k_decay_bwd_mma(DecayParams p) {
         // ---- g_b
         zero();
         by_parts(sm + Smem::kx, sm + Smem::kR);
-        const float w0 = s_w[m0 + g], w1 = s_w[m0 + g + 8];
+        const float w0 = sw.w[m0 + g], w1 = sw.w[m0 + g + 8];
         scale_rows(w0, w1);
-        row_dots(Smem::kb, s_v);
+        row_dots(Smem::kb, sw.v);
 #pragma unroll 1
         for (int ks = wr; ks < 4; ++ks) {
             uint32_t a[4];
@@ -483,7 +570,7 @@ __global__ void __launch_bounds__(kTh, 2) k_decay_bwd_mma(DecayParams p) {
             ldm4t(f1, at_bt(sm + Smem::kg, n0 + 16, ks, lane));
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                const float2 w = *reinterpret_cast<const float2 *>(s_e + 16 * ks + 8 * (e >> 1) + q2);
+                const float2 w = *reinterpret_cast<const float2 *>(sw.e + 16 * ks + 8 * (e >> 1) + q2);
                 uint32_t o[3];
                 split3(lo_of(a[e]) * w.x, hi_of(a[e]) * w.y, o);
 #pragma unroll
@@ -501,43 +588,8 @@ __global__ void __launch_bounds__(kTh, 2) k_decay_bwd_mma(DecayParams p) {
         for (int f = 0; f < 4; ++f)
 #pragma unroll
             for (int e = 0; e < 4; ++e) R[f][e] = fmaf(aend, R[f][e], acc[f][e]);
-        __syncthreads();                // s_u, s_v are in
-        if (warp == 0) {
-            double through = 0.0;
-            for (int w = 0; w < kTh / 32; ++w) through += (double)s_dot[w];
-            through *= (double)aend;
-            double before = 0.0, total = 0.0, inc[2], pre[2];
-#pragma unroll
-            for (int q = 0; q < 2; ++q) {
-                const int t = q * 32 + lane;
-                double a = (double)s_row[t] + (double)s_row[kC + t] + (double)s_u[t] + (double)s_u[kC + t] -
-                           ((double)s_col[t] + (double)s_col[kC + t] + (double)s_col[2 * kC + t] +
-                            (double)s_col[3 * kC + t]);
-                double v = (double)s_v[t] + (double)s_v[kC + t];
-                const double a0 = a, v0 = v;
-#pragma unroll
-                for (int d = 1; d < 32; d *= 2) {
-                    const double oa = shfl_up_d(a, d), ov = shfl_up_d(v, d);
-                    if (lane >= d) {
-                        a += oa;
-                        v += ov;
-                    }
-                }
-                inc[q] = total + a - a0;
-                pre[q] = before + v - v0;
-                total += __shfl_sync(kFull, a, 31);
-                before += __shfl_sync(kFull, v, 31);
-            }
-#pragma unroll
-            for (int q = 0; q < 2; ++q) {
-                const int64_t t = t0 + q * 32 + lane;
-                if (t < p.L)    // a floored decay is a constant
-                    gla[t * p.gla_t] = t < len && !(la[t * p.la_t] <= (float)kDecayFloor)
-                                           ? (float)(total - inc[q] + pre[q] + through)
-                                           : 0.f;
-            }
-        }
     }
+    __syncthreads();                    // for the last chunk's g_log_a
     if (p.g_h0 && seg == 0) {
         float *out = p.g_h0 + bh * np;
 #pragma unroll
@@ -567,7 +619,7 @@ cudaError_t launch_decay_bwd_mma(const DecayParams &p, cudaStream_t st) {
     static std::atomic<int> set[kLimitDevices];
     const cudaError_t e = allow_smem((const void *)k_decay_bwd_mma, (int)Smem::kTotal, set);
     if (e != cudaSuccess) return e;
-    k_decay_bwd_mma<<<dim3((unsigned)((int64_t)p.B * p.H * p.nseg)), kTh, Smem::kTotal, st>>>(p);
+    k_decay_bwd_mma<<<dim3((unsigned)((int64_t)p.B * p.H * p.nseg)), kAll, Smem::kTotal, st>>>(p);
     return cudaGetLastError();
 }
 
