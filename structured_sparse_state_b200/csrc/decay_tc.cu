@@ -72,20 +72,24 @@ enum {
     kDecReady, kDecFree, kNumBars
 };
 
-template <bool STK>
+// Shared memory.  The state alone needs no c (in reverse no b) and no S0, so it
+// has deeper rings.
+template <bool STK, bool SEG>
 struct Smem {
-    static constexpr int kNCB = STK ? 3 : 2;            // stages of c and b
-    static constexpr int kNX = STK ? 2 : 1;             // stages of x
-    static constexpr int kNPL = STK ? 2 : 1;            // sets of split parts
+    static constexpr int kNCB = SEG ? (STK ? 4 : 2) : (STK ? 3 : 2);    // stages of c and b
+    static constexpr int kNX = SEG ? 3 : (STK ? 2 : 1);                 // stages of x
+    static constexpr int kNPL = SEG ? (STK ? 3 : 2) : (STK ? 2 : 1);    // sets of split parts
     static constexpr int kParts = STK ? 2 : 3;          // of a set (STK: part 2 takes b's place)
     static constexpr uint32_t kKey = STK ? kTile : 2 * kTile;   // one c or b tile
-    static constexpr uint32_t kC0 = 0;                  // [kNCB][c, b]
-    static constexpr uint32_t kX = kC0 + kNCB * 2 * kKey;       // [kNX]
+    static constexpr uint32_t kB = SEG ? 0 : kKey;      // b (in reverse c) behind the stage's c
+    static constexpr uint32_t kStage = kB + kKey;
+    static constexpr uint32_t kC0 = 0;                  // [kNCB]
+    static constexpr uint32_t kX = kC0 + kNCB * kStage; // [kNX]
     static constexpr uint32_t kPl = kX + kNX * kTile;   // [kNPL][kParts]
     static constexpr uint32_t kS0 = kPl + kNPL * kParts * kTile;
-    static constexpr uint32_t kDec = kS0 + kTile;
+    static constexpr uint32_t kDec = kS0 + (SEG ? 0 : kTile);
     static constexpr uint32_t kBar = kDec + 2 * sizeof(Decays);
-    static constexpr uint32_t kTotal = kBar + 32 * kNumBars + 1024;       // + alignment
+    static constexpr uint32_t kTotal = kBar + 32 * kNumBars + 1024;     // + alignment
 };
 
 struct TcParams {
@@ -129,8 +133,8 @@ template <bool STK, int MODE>
 __global__ void __launch_bounds__(kTcTh, 1)
     k_decay_tc(const __grid_constant__ CUtensorMap cmap, const __grid_constant__ CUtensorMap bmap,
                const __grid_constant__ CUtensorMap xmap, const TcParams tp) {
-    using SM = Smem<STK>;
     constexpr bool FWD = MODE == kFwd || MODE == kFwdCarry;
+    using SM = Smem<STK, !FWD>;
     const DecayParams &p = tp.d;
     extern __shared__ unsigned char sm_raw[];
     const uint32_t sm = (smem_u32(sm_raw) + 1023u) & ~1023u;
@@ -399,8 +403,8 @@ __global__ void __launch_bounds__(kTcTh, 1)
             // once the scores have read them
             if (FWD && !wait_warp(kScFull, i)) break;
             if (i >= SM::kNPL && !wait_warp(kDFull, i - SM::kNPL)) break;
-            const uint32_t keys = sm + SM::kC0 + (uint32_t)(i % SM::kNCB) * 2 * SM::kKey;
-            const uint32_t bt = keys + SM::kKey, xt = sm + SM::kX + (uint32_t)(i % SM::kNX) * kTile;
+            const uint32_t keys = sm + SM::kC0 + (uint32_t)(i % SM::kNCB) * SM::kStage;
+            const uint32_t bt = keys + SM::kB, xt = sm + SM::kX + (uint32_t)(i % SM::kNX) * kTile;
             if (!on) {      // behind the end: whatever lies there must not meet a zero weight
 #pragma unroll
                 for (int q = h0; q < h0 + 4; ++q) {
@@ -444,8 +448,8 @@ __global__ void __launch_bounds__(kTcTh, 1)
             for (int i = 0; i < n; ++i) {
                 if (!wait_cb(i) || (i >= 2 && !wait(kYFree, i - 2))) break;
                 tc_fence_after();
-                const uint32_t ct = key0 + (uint32_t)(i % SM::kNCB) * umma_step(2 * SM::kKey);
-                const uint32_t bt = ct + umma_step(SM::kKey), dS = tcol(i, 0);
+                const uint32_t ct = key0 + (uint32_t)(i % SM::kNCB) * umma_step(SM::kStage);
+                const uint32_t bt = ct + umma_step(SM::kB), dS = tcol(i, 0);
 #pragma unroll
                 for (int k = 0; k < (STK ? 4 : 8); ++k) {
                     const uint32_t off = (k >> 2) * umma_step(kTile) + (k & 3) * umma_step(32);
@@ -482,8 +486,8 @@ __global__ void __launch_bounds__(kTcTh, 1)
             const uint32_t key0 = umma_lo(sm + SM::kC0, kTile), x0 = umma_lo(sm + SM::kX, 0),
                            pl0 = umma_lo(sm + SM::kPl, kTile), s0 = umma_lo(sm + SM::kS0, 0);
             for (int i = 0; i < n; ++i) {
-                const uint32_t ct = key0 + (uint32_t)(i % SM::kNCB) * umma_step(2 * SM::kKey);
-                const uint32_t bt = ct + umma_step(SM::kKey);
+                const uint32_t ct = key0 + (uint32_t)(i % SM::kNCB) * umma_step(SM::kStage);
+                const uint32_t bt = ct + umma_step(SM::kB);
                 const uint32_t xr = x0 + (uint32_t)(i % SM::kNX) * umma_step(kTile);
                 if (!wait_cb(i)) break;
                 if (FWD) {
@@ -591,14 +595,14 @@ __global__ void __launch_bounds__(kTcTh, 1)
             for (; i < n && ok; ++i) {
                 const int t0 = (int)chunk_t0(i);
                 if (i >= SM::kNCB && !wait(kDFull, i - SM::kNCB)) break;
-                const uint32_t keys = sm + SM::kC0 + (uint32_t)(i % SM::kNCB) * 2 * SM::kKey;
+                const uint32_t keys = sm + SM::kC0 + (uint32_t)(i % SM::kNCB) * SM::kStage;
                 const uint32_t cb = bar_cb(i);
                 const int subs = STK ? 1 : 2;
                 mbar_expect_tx(cb, (uint32_t)(FWD ? 2 : 1) * SM::kKey);
                 for (int q = 0; q < subs; ++q) {
                     // the state alone needs one key tensor: b, or c in reverse
                     if (FWD) tma_load_4d(keys + q * kTile, &cmap, 64 * q, t0, g, b, cb);
-                    tma_load_4d(keys + SM::kKey + q * kTile, MODE == kSegRev ? &cmap : &bmap, 64 * q, t0,
+                    tma_load_4d(keys + SM::kB + q * kTile, MODE == kSegRev ? &cmap : &bmap, 64 * q, t0,
                                 g, b, cb);
                 }
                 if (i >= SM::kNX && (!wait(kDFull, i - SM::kNX) || (FWD && !wait(kYFull, i - SM::kNX)))) break;
@@ -634,11 +638,11 @@ __global__ void __launch_bounds__(kTcTh, 1)
         for (int i = 0; i < n && ok; ++i) {
             const int64_t t0 = chunk_t0(i);
             if (i >= SM::kNCB && !wait_warp(kDFull, i - SM::kNCB)) break;
-            const uint32_t keys = sm + SM::kC0 + (uint32_t)(i % SM::kNCB) * 2 * SM::kKey;
+            const uint32_t keys = sm + SM::kC0 + (uint32_t)(i % SM::kNCB) * SM::kStage;
             for (int q = 0; q < (STK ? 1 : 2); ++q) {
                 if (FWD)
                     copy(keys + q * kTile, kc + 64 * q, p.key_t, p.N - 64 * q, t0);
-                copy(keys + SM::kKey + q * kTile, kb + 64 * q, p.key_t, p.N - 64 * q, t0);
+                copy(keys + SM::kB + q * kTile, kb + 64 * q, p.key_t, p.N - 64 * q, t0);
             }
             fence_proxy_async_smem();
             mbar_arrive(bar_cb(i));
@@ -697,7 +701,7 @@ cudaError_t go(const DecayParams &p, bool first, cudaStream_t st) {
             return cudaErrorInvalidValue;
     }
     auto kern = k_decay_tc<STK, MODE>;
-    const int smem = (int)Smem<STK>::kTotal;
+    const int smem = (int)Smem<STK, MODE == kSegFwd || MODE == kSegRev>::kTotal;
     static std::atomic<int> set[kLimitDevices];
     const cudaError_t e = allow_smem((const void *)kern, smem, set);
     if (e != cudaSuccess) return e;
