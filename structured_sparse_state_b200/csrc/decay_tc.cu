@@ -69,7 +69,7 @@ struct __align__(16) Decays {
 // that no role can be a whole round of a slot behind), and the rings' own.
 enum {
     kFullCB, kFullX, kScFull, kPReady, kPlReady, kDFull, kS0Ready, kYFull, kYFree,
-    kDecReady, kDecFree, kNumBars
+    kDecReady, kDecFree, kPlRead, kPlLate, kNumBars
 };
 
 // Shared memory.  The state alone needs no c (in reverse no b) and no S0, so it
@@ -77,9 +77,12 @@ enum {
 template <bool STK, bool SEG>
 struct Smem {
     static constexpr int kNCB = SEG ? (STK ? 4 : 2) : (STK ? 3 : 2);    // stages of c and b
-    static constexpr int kNX = SEG ? 3 : (STK ? 2 : 1);                 // stages of x
+    static constexpr int kNX = SEG ? 3 : 2;             // stages of x
     static constexpr int kNPL = SEG ? (STK ? 3 : 2) : (STK ? 2 : 1);    // sets of split parts
-    static constexpr int kParts = STK ? 2 : 3;          // of a set (STK: part 2 takes b's place)
+    // parts of a set: STK's part 2 takes b's place; the wide forward has room for
+    // two, and its part 0 follows when part 2 has been read
+    static constexpr bool kLate = !STK && !SEG;
+    static constexpr int kParts = STK || kLate ? 2 : 3;
     static constexpr uint32_t kKey = STK ? kTile : 2 * kTile;   // one c or b tile
     static constexpr uint32_t kB = SEG ? 0 : kKey;      // b (in reverse c) behind the stage's c
     static constexpr uint32_t kStage = kB + kKey;
@@ -172,6 +175,8 @@ __global__ void __launch_bounds__(kTcTh, 1)
             mbar_init(bar(kScFull, s), 1);
             mbar_init(bar(kPReady, s), 128);
             mbar_init(bar(kPlReady, s), 256);
+            mbar_init(bar(kPlRead, s), 1);
+            mbar_init(bar(kPlLate, s), 256);
             mbar_init(bar(kDFull, s), 1);
             mbar_init(bar(kS0Ready, s), 256);
             mbar_init(bar(kYFull, s), 1);
@@ -415,9 +420,12 @@ __global__ void __launch_bounds__(kTcTh, 1)
             }
             const uint32_t src = STK ? bt : xt;
             const uint32_t dst = sm + SM::kPl + (uint32_t)(i % SM::kNPL) * SM::kParts * kTile;
-            const uint32_t dst2 = STK ? bt : dst + 2 * kTile;
-#pragma unroll 2
-            for (int q = h0; q < h0 + 4; ++q) {
+            // where parts 0, 1 and 2 go
+            const uint32_t d0 = dst, d1 = dst + kTile, d2 = STK ? bt : SM::kLate ? dst : dst + 2 * kTile;
+            uint32_t late[SM::kLate ? 16 : 1];
+#pragma unroll (SM::kLate ? 4 : 2)
+            for (int k = 0; k < 4; ++k) {
+                const int q = h0 + k;
                 const uint4 u = lds128(src + piece(r, q));
                 const uint32_t in[4] = {u.x, u.y, u.z, u.w};
                 uint32_t p1[4], p2[4], p3[4];
@@ -432,13 +440,27 @@ __global__ void __launch_bounds__(kTcTh, 1)
                     v1 -= hi_of(p2[e]);
                     p3[e] = pack2(v0, v1);
                 }
-                const uint32_t at = dst + piece(r, q);
-                sts128(at, p1[0], p1[1], p1[2], p1[3]);
-                sts128(at + kTile, p2[0], p2[1], p2[2], p2[3]);
-                sts128(dst2 + piece(r, q), p3[0], p3[1], p3[2], p3[3]);
+                const uint32_t at = piece(r, q);
+                if constexpr (SM::kLate) {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) late[4 * k + e] = p1[e];
+                } else {
+                    sts128(d0 + at, p1[0], p1[1], p1[2], p1[3]);
+                }
+                sts128(d1 + at, p2[0], p2[1], p2[2], p2[3]);
+                sts128(d2 + at, p3[0], p3[1], p3[2], p3[3]);
             }
             fence_proxy_async_smem();
             mbar_arrive(bar(kPlReady, i));
+            if constexpr (SM::kLate) {
+                if (!wait_warp(kPlRead, i)) break;
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    sts128(d0 + piece(r, h0 + k), late[4 * k], late[4 * k + 1], late[4 * k + 2],
+                           late[4 * k + 3]);
+                fence_proxy_async_smem();
+                mbar_arrive(bar(kPlLate, i));
+            }
         }
     } else if (warp == kScores) {
         // ---- products: the scores
@@ -510,13 +532,19 @@ __global__ void __launch_bounds__(kTcTh, 1)
                 // part 2 lies in b's place)
 #pragma unroll 1
                 for (int part = 2; part >= 0; --part) {     // the small ones first
+                    if (SM::kLate && part == 0) {       // in part 2's buffer, once that has been read
+                        umma_commit(bar(kPlRead, i));
+                        if (!wait(kPlLate, i)) break;
+                        tc_fence_after();
+                    }
                     const uint32_t ar = STK ? (part < 2 ? pl + part * umma_step(kTile) : bt) - umma_lo(0, kTile) : bt;
-                    const uint32_t br = STK ? xr : pl + part * umma_step(kTile);
+                    const uint32_t br = STK ? xr : pl + (SM::kLate && part == 2 ? 0 : part) * umma_step(kTile);
 #pragma unroll
                     for (int k = 0; k < 8; ++k)
                         umma_ss(tcol(k >> 2, 192), ar + k * kRow16, br + k * kRow16, kIdD,
                                 (k & 3) > 0 || part < 2);
                 }
+                if (!ok) break;
                 umma_commit(bar(kDFull, i));
             }
             if (n > 0 && ok) wait(kDFull, n - 1);
