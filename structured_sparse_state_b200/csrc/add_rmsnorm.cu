@@ -14,6 +14,8 @@
 // depend on timing.
 #include <cuda_fp8.h>
 
+#include <initializer_list>
+
 #include "common.cuh"
 
 namespace pdssm {
@@ -37,6 +39,15 @@ __device__ __forceinline__ void load_vec(float (&v)[V], const void *p, int64_t a
                 v[2 * i] = __uint_as_float(w[i] << 16);
                 v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
             }
+        }
+    } else if constexpr (V == 2) {
+        if (dt == PDSSM_F32) {
+            const float2 a = *reinterpret_cast<const float2 *>((const float *)p + at);
+            v[0] = a.x; v[1] = a.y;
+        } else {
+            const unsigned w = *reinterpret_cast<const unsigned *>((const __nv_bfloat16 *)p + at);
+            v[0] = __uint_as_float(w << 16);
+            v[1] = __uint_as_float(w & 0xffff0000u);
         }
     } else {
         v[0] = dt == PDSSM_F32 ? ((const float *)p)[at]
@@ -71,6 +82,15 @@ __device__ __forceinline__ void store_vec(const float (&v)[V], void *p, int64_t 
             }
             *reinterpret_cast<uint2 *>((unsigned char *)p + at) = make_uint2(w[0], w[1]);
         }
+    } else if constexpr (V == 2) {
+        if (dt == PDSSM_F32)
+            *reinterpret_cast<float2 *>((float *)p + at) = make_float2(v[0], v[1]);
+        else if (dt == PDSSM_BF16)
+            *reinterpret_cast<unsigned *>((__nv_bfloat16 *)p + at) = pack_bf16(v[0], v[1]);
+        else
+            *reinterpret_cast<unsigned short *>((unsigned char *)p + at) =
+                (unsigned short)__nv_cvt_float2_to_fp8x2(make_float2(v[0], v[1]), __NV_SATFINITE,
+                                                         __NV_E4M3);
     } else {
         if (dt == PDSSM_F32)
             ((float *)p)[at] = v[0];
@@ -344,6 +364,15 @@ int64_t bwd_ctas(int64_t rows, int64_t D) {
 }
 
 bool aligned(const void *p, size_t a) { return ((uintptr_t)p % a) == 0; }
+// values per access: eight where rows and pointers lie on 16 bytes, two on 8
+int width_of(int64_t D, std::initializer_list<const void *> ptrs) {
+    int v = D % 8 == 0 ? 8 : D % 2 == 0 ? 2 : 1;
+    for (const void *q : ptrs) {
+        if (!aligned(q, 8)) return 1;
+        if (!aligned(q, 16) && v == 8) v = 2;
+    }
+    return v;
+}
 bool wide(int dt) { return dt == PDSSM_F32 || dt == PDSSM_BF16; }
 
 template <int V>
@@ -416,9 +445,9 @@ pdssm_status pdssm_add_rmsnorm_fwd(int64_t rows, int64_t D, const void *x, pdssm
     if (!x || !weight || !out) return arg_fail(PDSSM_ERR_INVALID_ARG, "NULL tensor pointer");
     NormParams p{rows, (int)D, x, residual, weight, out, res_out, rstd, scale,
                  x_dtype, res_dtype, w_dtype, out_dtype, eps};
-    const bool vec = D % 8 == 0 && aligned(x, 16) && aligned(residual, 16) &&
-                     aligned(weight, 16) && aligned(res_out, 16) && aligned(out, 16);
-    cudaError_t e = vec ? run_fwd<8>(p, (cudaStream_t)stream) : run_fwd<1>(p, (cudaStream_t)stream);
+    const int v = width_of(D, {x, residual, weight, res_out, out});
+    cudaStream_t s = (cudaStream_t)stream;
+    cudaError_t e = v == 8 ? run_fwd<8>(p, s) : v == 2 ? run_fwd<2>(p, s) : run_fwd<1>(p, s);
     return e == cudaSuccess ? PDSSM_OK : cuda_fail(e, "add + norm");
 }
 
@@ -451,9 +480,8 @@ pdssm_status pdssm_add_rmsnorm_bwd(int64_t rows, int64_t D, const void *g_out, p
         return arg_fail(PDSSM_ERR_WORKSPACE, "scratch too small");
     NormBwdParams p{rows, (int)D, (int)bwd_ctas(rows, D), g_out, res_out, weight, g_res, rstd, g_x,
                     (float *)scratch, g_dtype, res_dtype, w_dtype};
-    const bool vec = D % 8 == 0 && aligned(g_out, 16) && aligned(res_out, 16) &&
-                     aligned(weight, 16) && aligned(g_res, 16) && aligned(g_x, 16);
-    e = vec ? run_bwd<8>(p, s) : run_bwd<1>(p, s);
+    const int v = width_of(D, {g_out, res_out, weight, g_res, g_x});
+    e = v == 8 ? run_bwd<8>(p, s) : v == 2 ? run_bwd<2>(p, s) : run_bwd<1>(p, s);
     if (e != cudaSuccess) return cuda_fail(e, "add + norm backward");
     k_rmsnorm_gw<<<(unsigned)((D + 31) / 32), 1024, 0, s>>>(p.part, p.ctas, (int)D, g_weight);
     e = cudaGetLastError();

@@ -407,9 +407,10 @@ __global__ void __launch_bounds__(kTh, 1)
                 }
                 umma_commit(bar(kDone, j));
             };
-            // with one slot for several groups' weights, the next item's can only
-            // come once this one is done with them
-            const bool ahead = resident || t.nslot > 1;
+            // an item's logits run ahead of the last item's second product, unless
+            // what they need comes only when that is done: the weights (one slot
+            // for several groups), or u (one stage, which g_W's product reads)
+            const bool ahead = (resident || t.nslot > 1) && (MODE != kGw || t.ustages > 1);
             for (int i = 0; i < items && ok; ++i) {
                 const int tile = i / ng;
                 if (MODE != kSums && i > 0 && !ahead) second(i - 1);

@@ -30,8 +30,18 @@ __global__ void __launch_bounds__(kStepThreads) k_decay_step(DecayParams p, floa
 
     // a slot outside the pool, or one that an earlier row uses: an empty row
     bool bad = slot < 0 || slot >= n_slots;
-    if (slots)
-        for (int64_t r = tid; r < row; r += kStepThreads) bad |= slots[r] == (int32_t)slot;
+    if (slots) {
+        int64_t r = 0;
+        if (((uintptr_t)slots & 15) == 0) {         // four at a time
+            const int4 *s4 = reinterpret_cast<const int4 *>(slots);
+            for (int64_t q = tid; q < row / 4; q += kStepThreads) {
+                const int4 v = __ldg(s4 + q);
+                bad |= v.x == (int)slot || v.y == (int)slot || v.z == (int)slot || v.w == (int)slot;
+            }
+            r = row / 4 * 4;
+        }
+        for (r += tid; r < row; r += kStepThreads) bad |= slots[r] == (int32_t)slot;
+    }
     if (__syncthreads_or(bad)) {
         for (int q = tid; q < p.P; q += kStepThreads) y[q] = from_f<T>(0.f);
         return;

@@ -29,6 +29,11 @@ CASES = [
     (BF, 3, 130, 2, 5, 31, 0.7, True),
     (BF, 2, 3000, 16, 16, 128, 1.0, False),
     (BF, 2, 500, 3, 4, 200, 1.0, False),
+    # several tiles per CTA at every width of the weights' ring
+    (BF, 3, 14000, 2, 8, 256, 1.0, False),
+    (BF, 2, 13000, 3, 16, 160, 1.0, True),
+    (BF, 1, 25000, 12, 32, 192, 1.0, False),
+    (BF, 2, 20000, 4, 16, 64, 1.0, False),
 ]
 
 
