@@ -22,7 +22,7 @@ constexpr int kBalRows = 64;            // steps per tile (four threads per step
 
 // CTA work over one tile of kBalRows steps: u tile in shared memory (odd row
 // length), one head's weights, logits and softmax weights.
-template <typename T, int KT>
+template <int KT>
 struct Tile {
     float *su, *sW, *sp;                // [64][D|1], [KT][D|1], [64][KT + 1]
     int ld;
@@ -34,13 +34,13 @@ struct Tile {
     }
     // a warp per row, its lanes along the row
     __device__ __forceinline__ void load_u(const BalParams &p, int64_t r0) {
-        const T *u = (const T *)p.u;
+        const float *u = (const float *)p.u;
         const int lane = threadIdx.x % 32;
 #pragma unroll 4
         for (int r = threadIdx.x / 32; r < kBalRows; r += kBalThreads / 32) {
             const bool live = bal_live(p, r0 + r);
             for (int q = lane; q < p.D; q += 32)
-                su[r * ld + q] = live ? to_f<T>(u[(r0 + r) * p.D + q]) : 0.f;
+                su[r * ld + q] = live ? u[(r0 + r) * p.D + q] : 0.f;
         }
     }
     __device__ __forceinline__ void load_W(const BalParams &p, int h) {
@@ -108,12 +108,12 @@ constexpr size_t bal_smem(int D) {
 }
 
 // Sums of p and counts over one slice of the steps of one head.
-template <typename T, int KT>
+template <int KT>
 __global__ void __launch_bounds__(kBalThreads) k_bal_sums(BalParams p) {
     extern __shared__ float sm[];
     __shared__ int scount[KT];
     const int h = blockIdx.x % p.H, slice = blockIdx.x / p.H;
-    Tile<T, KT> t(sm, p.D);
+    Tile<KT> t(sm, p.D);
     t.load_W(p, h);
     if (threadIdx.x < KT) scount[threadIdx.x] = 0;
     float sum = 0.f;                    // column threadIdx.x % KT, rows threadIdx.x / KT ...
@@ -167,14 +167,20 @@ __global__ void k_bal_loss(BalParams p, float *loss, int32_t *counts, float *pro
     if (k == 0) loss[h] = (float)(v * p.K);
 }
 
-// g_u of one tile of steps over all heads: thread (ty, tx) owns rows ty + 16 i
-// and columns tx + 16 j.
-template <typename T, int KT>
+// g_u of one tile of steps over heads h0 .. h1 - 1: thread (ty, tx) owns rows
+// ty + 16 i and columns tx + 16 j.  A head takes about 10 us, most of it the
+// latency of its phases, so where the tiles do not fill the GPU the heads are
+// split over CTAs too, whose sums k_bal_gu_sum adds in order (one step, 16
+// heads of 32 entries: GUSPLIT us for the whole loss and its gradients, by one
+// CTA 190).
+template <int KT>
 __global__ void __launch_bounds__(kBalThreads) k_bal_gu(BalParams p) {
     extern __shared__ float sm[];
     __shared__ float f[KT];
-    Tile<T, KT> t(sm, p.D);
-    const int64_t r0 = (int64_t)blockIdx.x * kBalRows;
+    Tile<KT> t(sm, p.D);
+    const int64_t r0 = (int64_t)(blockIdx.x / p.hslices) * kBalRows;
+    const int hs = blockIdx.x % p.hslices;
+    const int h0 = (int)((int64_t)p.H * hs / p.hslices), h1 = (int)((int64_t)p.H * (hs + 1) / p.hslices);
     const int ty = threadIdx.x / 16, tx = threadIdx.x % 16;
     const int64_t steps = bal_steps(p);
     const float inv = steps > 0 ? 1.f / (float)steps : 0.f;
@@ -184,7 +190,7 @@ __global__ void __launch_bounds__(kBalThreads) k_bal_gu(BalParams p) {
 #pragma unroll
         for (int j = 0; j < kBalMaxD / 16; ++j) acc[i][j] = 0.f;
     t.load_u(p, r0);
-    for (int h = 0; h < p.H; ++h) {
+    for (int h = h0; h < h1; ++h) {
         __syncthreads();
         t.load_W(p, h);
         if (threadIdx.x < KT)
@@ -207,7 +213,7 @@ __global__ void __launch_bounds__(kBalThreads) k_bal_gu(BalParams p) {
             }
         }
     }
-    T *gu = (T *)p.g_u;
+    float *gu = p.hslices > 1 ? p.part + hs * p.rows * p.D : (float *)p.g_u;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const int64_t r = r0 + ty + 16 * i;
@@ -216,20 +222,27 @@ __global__ void __launch_bounds__(kBalThreads) k_bal_gu(BalParams p) {
         for (int j = 0; j < kBalMaxD / 16; ++j) {
             const int q = tx + 16 * j;
             if (q >= p.D) break;
-            if constexpr (sizeof(T) == 4)
-                gu[r * p.D + q] = acc[i][j];
-            else
-                gu[r * p.D + q] = __float2bfloat16_rn(acc[i][j]);
+            gu[r * p.D + q] = acc[i][j];
         }
     }
 }
 
+__global__ void k_bal_gu_sum(BalParams p) {
+    const int64_t n = p.rows * p.D;
+    for (int64_t e = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; e < n;
+         e += (int64_t)gridDim.x * blockDim.x) {
+        float s = 0.f;
+        for (int q = 0; q < p.hslices; ++q) s += p.part[q * n + e];
+        ((float *)p.g_u)[e] = s;
+    }
+}
+
 // g_W of one head over one slice of the steps
-template <typename T, int KT>
+template <int KT>
 __global__ void __launch_bounds__(kBalThreads) k_bal_gw(BalParams p) {
     extern __shared__ float sm[];
     __shared__ float f[KT];
-    Tile<T, KT> t(sm, p.D);
+    Tile<KT> t(sm, p.D);
     const int h = blockIdx.x % p.H, slice = blockIdx.x / p.H;
     const int64_t steps = bal_steps(p);
     const float inv = steps > 0 ? 1.f / (float)steps : 0.f;
@@ -291,6 +304,13 @@ int bal_slices(int64_t rows, int64_t H) {
     return (int)(n < 1 ? 1 : n);
 }
 
+// slices of the heads for fp32 g_u: as many as the GPU takes beside the tiles
+int bal_hslices(int64_t rows, int64_t H) {
+    const int64_t tiles = (rows + kBalRows - 1) / kBalRows;
+    const int64_t n = tiles > 0 ? 148 / tiles : 1;
+    return (int)(n < 1 ? 1 : n > H ? H : n);
+}
+
 template <void (*KERN)(BalParams)>
 cudaError_t launch(int64_t grid, size_t smem, cudaStream_t st, const BalParams &p) {
     static std::atomic<int> set[kLimitDevices];
@@ -300,19 +320,24 @@ cudaError_t launch(int64_t grid, size_t smem, cudaStream_t st, const BalParams &
     return cudaGetLastError();
 }
 
-template <typename T, int KT>
+template <int KT>
 cudaError_t run(const BalParams &p, int what, cudaStream_t st) {
     const size_t smem = bal_smem<KT>(p.D);
-    if (what == 0) return launch<k_bal_sums<T, KT>>((int64_t)p.H * p.slices, smem, st, p);
-    if (what == 1) return launch<k_bal_gu<T, KT>>((p.rows + kBalRows - 1) / kBalRows, smem, st, p);
-    return launch<k_bal_gw<T, KT>>((int64_t)p.H * p.slices, smem, st, p);
+    if (what == 0) return launch<k_bal_sums<KT>>((int64_t)p.H * p.slices, smem, st, p);
+    if (what == 1) {
+        const int64_t tiles = (p.rows + kBalRows - 1) / kBalRows;
+        const cudaError_t e = launch<k_bal_gu<KT>>(tiles * p.hslices, smem, st, p);
+        if (e != cudaSuccess || p.hslices == 1) return e;
+        k_bal_gu_sum<<<(unsigned)((p.rows * p.D + 255) / 256), 256, 0, st>>>(p);
+        return cudaGetLastError();
+    }
+    return launch<k_bal_gw<KT>>((int64_t)p.H * p.slices, smem, st, p);
 }
 
-template <typename T>
 cudaError_t run_k(const BalParams &p, int what, cudaStream_t st) {
-    if (p.K <= 8) return run<T, 8>(p, what, st);
-    if (p.K <= 16) return run<T, 16>(p, what, st);
-    return run<T, 32>(p, what, st);
+    if (p.K <= 8) return run<8>(p, what, st);
+    if (p.K <= 16) return run<16>(p, what, st);
+    return run<32>(p, what, st);
 }
 
 bool aligned(const void *p, size_t a) { return ((uintptr_t)p % a) == 0; }
@@ -339,7 +364,9 @@ size_t bal_scratch(const pdssm_dims &d) {
     const BalTcPlan pl = bal_tc_plan(d);
     const size_t a = bal_partials(d, bal_slices(d.B * d.L, d.H));
     const size_t b = bal_partials(d, pl.slices) + bal_tc_extra(pl);
-    return a > b ? a : b;
+    const int hs = bal_hslices(d.B * d.L, d.H);
+    const size_t c = hs > 1 ? (size_t)hs * (size_t)(d.B * d.L * d.D_in) * 4 : 0;
+    return a > b ? (a > c ? a : c) : (b > c ? b : c);
 }
 
 pdssm_status bal_common(const pdssm_dims *d, const void *u, pdssm_dtype dt, const float *W,
@@ -360,6 +387,7 @@ pdssm_status bal_common(const pdssm_dims *d, const void *u, pdssm_dtype dt, cons
     q.L = d->L; q.rows = d->B * d->L;
     q.u = u; q.W = W; q.lengths = lengths; q.inv_tau = inv_tau;
     q.slices = dt == PDSSM_BF16 ? bal_tc_plan(*d).slices : bal_slices(q.rows, d->H);
+    q.hslices = bal_hslices(q.rows, d->H);
     q.part = (float *)scratch;
     q.part_n = (int32_t *)(q.part + (int64_t)q.slices * q.H * q.K);
     *p = q;
@@ -370,7 +398,7 @@ pdssm_status bal_common(const pdssm_dims *d, const void *u, pdssm_dtype dt, cons
 // behind the partial sums in scratch)
 cudaError_t run_any(const pdssm_dims &d, const BalParams &p, pdssm_dtype dt, int what,
                     cudaStream_t st) {
-    if (dt != PDSSM_BF16) return run_k<float>(p, what, st);
+    if (dt != PDSSM_BF16) return run_k(p, what, st);
     const BalTcPlan pl = bal_tc_plan(d);
     unsigned char *parts = reinterpret_cast<unsigned char *>(p.part) + bal_partials(d, pl.slices);
     if (what == 0 || what == 1 || !p.g_u) {

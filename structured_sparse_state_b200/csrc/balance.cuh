@@ -18,8 +18,9 @@ struct BalParams {
     const int32_t *counts;
     const float *g_loss;
     void *g_u;
-    int slices;
-    float *part;                        // per slice: sums of p [H][K], or of g_W [H][K][D]
+    int slices, hslices;                // of the steps; of the heads (fp32 g_u)
+    float *part;                        // per slice: sums of p [H][K], of g_W [H][K][D], or of
+                                        // g_u [rows][D]
     int32_t *part_n;                    // per slice: counts [H][K]
 };
 

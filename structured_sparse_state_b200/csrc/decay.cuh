@@ -31,6 +31,8 @@ struct DecayParams {
     int64_t L;
     int64_t key_t, key_h, key_b;        // element strides of c, b by step, group, batch
     int64_t val_t, val_h, val_b;        // of x, y
+    int64_t okey_t, okey_h, okey_b;     // of g_c, g_b
+    int64_t oval_t, oval_h, oval_b;     // of y, g_x
     int64_t la_t, la_h, la_b;           // of log_a
     int64_t gla_t, gla_h, gla_b;        // of the per-step g_log_a buffer
     const void *c, *b, *x;
@@ -48,7 +50,8 @@ struct DecayParams {
     float *carry;                       // [B*H][nchunks][N][P]: state at every chunk's start
     int *status;                        // the workspace's status word
     int nseg, seg_chunks, nchunks, pslices;
-    int vec;                            // rows and pointers allow 16-byte (2: 32-byte) accesses
+    int vec, ovec;                      // inputs' rows and pointers allow 16-byte accesses; results'
+                                        // (2: y by 32 bytes)
 };
 
 // One step's log decay in base 2, floored (a NaN passes).
@@ -106,15 +109,25 @@ __device__ __forceinline__ __nv_bfloat16 from_f<__nv_bfloat16>(float x) {
     return __float2bfloat16_rn(x);
 }
 
+// bf16 rows of a width that is not whole 16 bytes, and their padded copy.
+struct DecayPad {
+    const void *src;
+    void *dst;
+    int64_t rows;
+    int width;
+};
+
 // launchers (each returns the launch's error)
 cudaError_t launch_decay_join(const DecayParams &p, const float *first, bool reverse, float *last,
                               cudaStream_t st);
 cudaError_t launch_decay_sum_heads(const DecayParams &p, pdssm_dtype dt, const float *part_c,
                                    const float *part_b, void *g_c, void *g_b, cudaStream_t st);
+cudaError_t launch_decay_pad(const DecayPad *t, int count, cudaStream_t st);
+cudaError_t launch_decay_unpad(const void *padded, void *out, int64_t rows, int width, cudaStream_t st);
 cudaError_t launch_decay_sum_steps(const DecayParams &p, const float *part, float *g_log_a,
                                    cudaStream_t st);
-cudaError_t launch_decay_fwd_gen(const DecayParams &p, pdssm_dtype dt, cudaStream_t st);
-cudaError_t launch_decay_bwd_gen(const DecayParams &p, pdssm_dtype dt, cudaStream_t st);
+cudaError_t launch_decay_fwd_gen(const DecayParams &p, cudaStream_t st);
+cudaError_t launch_decay_bwd_gen(const DecayParams &p, cudaStream_t st);
 cudaError_t launch_decay_fwd_tc(const DecayParams &p, cudaStream_t st);
 cudaError_t launch_decay_seg_rev_tc(const DecayParams &p, cudaStream_t st);
 cudaError_t launch_decay_bwd_mma(const DecayParams &p, cudaStream_t st);
@@ -122,13 +135,10 @@ bool decay_tc_copies();                 // the driver's tensor maps are at hand
 cudaError_t launch_decay_step(const DecayParams &p, pdssm_dtype dt, float *state, int64_t n_slots,
                               const int32_t *slots, cudaStream_t st);
 
-// Kernels of a call: the CUDA cores (any size), or the tensor cores.
-enum DecayPath { kDecayGen, kDecayTc };
-
 // Chunk and segments of one direction, from the sizes alone.
 struct DecayPlan {
     int chunk, nchunks, nseg, seg_chunks, pslices;
 };
-DecayPlan decay_plan(const pdssm_decay_dims &d, DecayPath path, bool bf16, bool adjoint);
+DecayPlan decay_plan(const pdssm_decay_dims &d, bool tc, bool adjoint);
 
 }  // namespace pdssm

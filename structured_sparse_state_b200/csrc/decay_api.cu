@@ -11,21 +11,19 @@ namespace pdssm {
 
 // Chunks and segments from the sizes alone, so that workspace sizes follow.
 // Segments fill the GPU when the (batch, head, 64 columns) units do not: one
-// CTA of the tensor-core forward fits an SM, two of its adjoint, about three
-// of the others.  Each segment costs a second read of b and x (the adjoint: of
+// CTA of the tensor-core forward fits an SM, two of its adjoint (above 64 x 64
+// one), about three of the others.  Each segment costs a second read of b and x (the adjoint: of
 // c and g_y).  A segment has at least four chunks of the tensor-core kernels
 // (whose start-up is worth about one), one of the others: a training step of
 // 8 heads x 1501 steps, 64 x 48 fp32, took 222 us with segments of at least
 // four, 127 with two.
-DecayPlan decay_plan(const pdssm_decay_dims &d, DecayPath path, bool bf16, bool adjoint) {
+DecayPlan decay_plan(const pdssm_decay_dims &d, bool tc, bool adjoint) {
     DecayPlan pl{};
-    const bool tc = path == kDecayTc;
-    const int w = (int)(d.N > d.P ? d.N : d.P);
-    pl.chunk = tc ? (adjoint ? 64 : 128) : (bf16 && w <= 64 ? 64 : 32);
+    pl.chunk = tc ? (adjoint ? 64 : 128) : 32;
     pl.nchunks = (int)((d.L + pl.chunk - 1) / pl.chunk);
     pl.pslices = adjoint ? 1 : (int)((d.P + 63) / 64);
     const int64_t units = d.B * d.H * pl.pslices;
-    int64_t nseg = (int64_t)kDecaySMs * (tc ? (adjoint ? 2 : 1) : 3) / units;
+    int64_t nseg = (int64_t)kDecaySMs * (tc ? (adjoint && d.N <= 64 && d.P <= 64 ? 2 : 1) : 3) / units;
     if (tc && nseg > pl.nchunks / 4) nseg = pl.nchunks / 4;
     if (nseg > pl.nchunks) nseg = pl.nchunks;
     if (nseg < 1) nseg = 1;
@@ -59,22 +57,17 @@ pdssm_status check_dims(const pdssm_decay_dims *d, pdssm_dtype dt, bool step) {
     return PDSSM_OK;
 }
 
-// bf16 runs on the tensor cores; with an adjoint, up to 64 x 64 states.
-DecayPath path_of(const pdssm_decay_dims &d, pdssm_dtype dt, bool for_bwd) {
-    return dt == PDSSM_BF16 && (!for_bwd || (d.N <= 64 && d.P <= 64)) ? kDecayTc : kDecayGen;
-}
-
-DecayPlan plan_of(const pdssm_decay_dims &d, pdssm_dtype dt, bool for_bwd, bool adjoint) {
-    return decay_plan(d, path_of(d, dt, for_bwd), dt == PDSSM_BF16, adjoint);
-}
+// bf16 runs on the tensor cores, fp32 on the CUDA cores.
+bool on_tc(pdssm_dtype dt) { return dt == PDSSM_BF16; }
 
 struct DecayWs {
-    size_t seg_state, seg_decay, carry, part_c, part_b, part_la, total;
+    size_t seg_state, seg_decay, carry, part_c, part_b, part_la;
+    size_t pad_c, pad_b, pad_x, pad_v, total;   // padded rows; pad_v: y, or g_y
 };
 
 DecayWs ws_of(const pdssm_decay_dims &d, pdssm_dtype dt, bool for_bwd) {
     DecayWs w{};
-    const DecayPlan f = plan_of(d, dt, for_bwd, false), r = plan_of(d, dt, for_bwd, true);
+    const DecayPlan f = decay_plan(d, on_tc(dt), false), r = decay_plan(d, on_tc(dt), true);
     const size_t np = (size_t)(d.N * d.P) * 4, bh = (size_t)(d.B * d.H);
     const size_t nseg = (size_t)(for_bwd && r.nseg > f.nseg ? r.nseg : f.nseg);
     size_t o = 256;     // the status word's block
@@ -88,6 +81,16 @@ DecayWs ws_of(const pdssm_decay_dims &d, pdssm_dtype dt, bool for_bwd) {
             w.part_b = o; o = align256(o + keys);
         }
         w.part_la = o; o = align256(o + bh * (size_t)d.L * 4);
+    }
+    if (on_tc(dt) && d.N % 8) {
+        const size_t keys = (size_t)(d.B * d.G * d.L) * (size_t)((d.N + 7) / 8 * 16);
+        w.pad_c = o; o = align256(o + keys);
+        w.pad_b = o; o = align256(o + keys);
+    }
+    if (on_tc(dt) && d.P % 8) {
+        const size_t vals = bh * (size_t)d.L * (size_t)((d.P + 7) / 8 * 16);
+        w.pad_x = o; o = align256(o + vals);
+        w.pad_v = o; o = align256(o + vals);
     }
     w.total = o;
     return w;
@@ -107,6 +110,8 @@ void set_strides(DecayParams &p, const pdssm_decay_dims &d, pdssm_layout lay, bo
     }
     p.key_b = d.G * d.L * d.N;
     p.val_b = d.H * d.L * d.P;
+    p.okey_t = p.key_t; p.okey_h = p.key_h; p.okey_b = p.key_b;
+    p.oval_t = p.val_t; p.oval_h = p.val_h; p.oval_b = p.val_b;
     p.la_b = d.H * d.L;
     p.gla_t = p.la_t; p.gla_h = p.la_h; p.gla_b = p.la_b;
     if (!per_step) {
@@ -115,15 +120,40 @@ void set_strides(DecayParams &p, const pdssm_decay_dims &d, pdssm_layout lay, bo
     }
 }
 
-// 2: 32-byte stores of x-like rows, 1: 16-byte accesses, 0: neither
-int vec_of(const pdssm_decay_dims &d, std::initializer_list<const void *> ptrs) {
-    if (!decay_tc_copies() || d.N % 8 || d.P % 8) return 0;
-    size_t grid = 32;
-    for (const void *q : ptrs) {
-        if (!aligned(q, 16)) return 0;
-        if (!aligned(q, 32)) grid = 16;
+bool all_aligned(std::initializer_list<const void *> ptrs, size_t a) {
+    for (const void *q : ptrs)
+        if (!aligned(q, a)) return false;
+    return true;
+}
+
+// Inputs for the tensor-core kernels: rows whose width is not a multiple of 8
+// are copied to padded ones, and y is made in such rows too: 64 heads x 8192
+// steps of 31 x 31 take PADDED us, by one warp's 2-byte loads and the epilogue's
+// 2-byte stores PLAIN.  The adjoint takes the copies that the forward left, and
+// needs g_y's.  Tensors off the 16-byte grid keep the plain accesses.
+cudaError_t set_inputs(DecayParams &p, const DecayWs &w, unsigned char *base, bool adjoint,
+                       cudaStream_t st) {
+    const bool keys = p.N % 8 != 0, vals = p.P % 8 != 0;
+    const int n8 = (p.N + 7) / 8 * 8, p8 = (p.P + 7) / 8 * 8;
+    const int64_t key_rows = p.B * p.L * p.G, val_rows = p.B * p.L * p.H;
+    DecayPad t[3];
+    int n = 0;
+    auto pad = [&](const void *&src, size_t at, int64_t rows, int width, bool made) {
+        if (!made) t[n++] = DecayPad{src, base + at, rows, width};
+        src = base + at;
+    };
+    if (keys) {
+        pad(p.c, w.pad_c, key_rows, p.N, adjoint);
+        pad(p.b, w.pad_b, key_rows, p.N, adjoint);
+        p.key_t = p.key_t / p.N * n8; p.key_h = p.key_h / p.N * n8; p.key_b = p.key_b / p.N * n8;
     }
-    return d.P % 16 == 0 && grid == 32 ? 2 : 1;
+    if (vals) {
+        pad(p.x, w.pad_x, val_rows, p.P, adjoint);
+        if (adjoint) pad(p.g_y, w.pad_v, val_rows, p.P, false);
+        p.val_t = p.val_t / p.P * p8; p.val_h = p.val_h / p.P * p8; p.val_b = p.val_b / p.P * p8;
+    }
+    p.vec = decay_tc_copies() && all_aligned({p.c, p.b, p.x, adjoint ? p.g_y : p.x}, 16);
+    return launch_decay_pad(t, n, st);
 }
 
 void set_plan(DecayParams &p, const DecayPlan &pl, const DecayWs &w, unsigned char *base) {
@@ -182,15 +212,22 @@ pdssm_status pdssm_decay_scan_fwd(const pdssm_decay_dims *dims, const void *c, c
     memset(&p, 0, sizeof(p));
     unsigned char *base = reinterpret_cast<unsigned char *>(ws);
     set_strides(p, *dims, layout, log_a_per_step != 0);
-    set_plan(p, plan_of(*dims, dtype, for_bwd != 0, false), w, base);
+    set_plan(p, decay_plan(*dims, on_tc(dtype), false), w, base);
     p.c = c; p.b = b; p.x = x; p.log_a = log_a; p.h0 = h0; p.lengths = lengths;
     p.y = y; p.h_last = h_last;
     if (for_bwd) p.carry = reinterpret_cast<float *>(base + w.carry);
-    if (path_of(*dims, dtype, for_bwd != 0) == kDecayTc) {
-        p.vec = vec_of(*dims, {c, b, x, y});
-        e = launch_decay_fwd_tc(p, s);
+    if (on_tc(dtype)) {
+        e = set_inputs(p, w, base, false, s);
+        if (p.P % 8) {                  // y in rows like x's
+            p.y = base + w.pad_v;
+            p.oval_t = p.val_t; p.oval_h = p.val_h; p.oval_b = p.val_b;
+        }
+        p.ovec = (p.P + 7) / 8 % 2 == 0 && aligned(p.y, 32) ? 2 : aligned(p.y, 16);
+        if (e == cudaSuccess) e = launch_decay_fwd_tc(p, s);
+        if (e == cudaSuccess && p.P % 8)
+            e = launch_decay_unpad(p.y, y, p.B * p.L * p.H, p.P, s);
     } else {
-        e = launch_decay_fwd_gen(p, dtype, s);
+        e = launch_decay_fwd_gen(p, s);
     }
     return e == cudaSuccess ? PDSSM_OK : cuda_fail(e, "decay scan");
 }
@@ -227,7 +264,7 @@ pdssm_status pdssm_decay_scan_bwd(const pdssm_decay_dims *dims, const void *c, c
     memset(&p, 0, sizeof(p));
     unsigned char *base = reinterpret_cast<unsigned char *>(ws);
     set_strides(p, *dims, layout, log_a_per_step != 0);
-    set_plan(p, plan_of(*dims, dtype, true, true), w, base);
+    set_plan(p, decay_plan(*dims, on_tc(dtype), true), w, base);
     p.c = c; p.b = b; p.x = x; p.log_a = log_a; p.h0 = h0; p.lengths = lengths;
     p.g_y = g_y; p.g_hlast = g_hlast; p.g_h0 = g_h0;
     p.carry = reinterpret_cast<float *>(base + w.carry);
@@ -239,11 +276,12 @@ pdssm_status pdssm_decay_scan_bwd(const pdssm_decay_dims *dims, const void *c, c
     p.g_b = shared ? (void *)part_b : g_b;
     p.g_x = g_x;
     p.g_la = log_a_per_step ? g_log_a : part_la;
-    if (path_of(*dims, dtype, true) == kDecayTc) {
-        p.vec = vec_of(*dims, {c, b, x, g_y, g_x, shared ? g_x : g_c, shared ? g_x : g_b});
-        e = launch_decay_bwd_mma(p, s);
+    if (on_tc(dtype)) {
+        p.ovec = p.N % 2 == 0 && p.P % 2 == 0 && all_aligned({g_c, g_b, g_x}, 4);
+        e = set_inputs(p, w, base, true, s);
+        if (e == cudaSuccess) e = launch_decay_bwd_mma(p, s);
     } else {
-        e = launch_decay_bwd_gen(p, dtype, s);
+        e = launch_decay_bwd_gen(p, s);
     }
     if (e != cudaSuccess) return cuda_fail(e, "decay scan adjoint");
     if (shared) {

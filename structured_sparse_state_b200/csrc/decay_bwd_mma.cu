@@ -38,11 +38,16 @@ struct Sums {
     float dot[8];
 };
 
+// NT and PT: N and P in units of 64.  Above 64 x 64 R's parts take the place of
+// S0's once those have been read.
+template <int NT, int PT>
 struct Smem {
-    static constexpr uint32_t kc = 0, kb = kTile, kx = 2 * kTile, kg = 3 * kTile;
-    static constexpr uint32_t kS = 4 * kTile, kR = 7 * kTile;       // three parts each
-    static constexpr uint32_t kP = 10 * kTile, kQ = 11 * kTile;
-    static constexpr uint32_t kF = 12 * kTile;                      // floats below
+    static constexpr bool kShare = NT * PT > 1;
+    static constexpr uint32_t kState = NT * PT * kTile;             // one part
+    static constexpr uint32_t kc = 0, kb = NT * kTile, kx = 2 * NT * kTile, kg = kx + PT * kTile;
+    static constexpr uint32_t kS = kg + PT * kTile, kR = kShare ? kS : kS + 3 * kState;
+    static constexpr uint32_t kP = kR + 3 * kState, kQ = kP + kTile;
+    static constexpr uint32_t kF = kQ + kTile;                      // floats below
     static constexpr uint32_t kTotal = kF + 2 * sizeof(Sums);
 };
 
@@ -115,10 +120,12 @@ __device__ __forceinline__ float quad_sum(float v) {
 // Barrier of the product warps.
 __device__ __forceinline__ void sync_products() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
 
-__global__ void __launch_bounds__(kAll, 2) k_decay_bwd_mma(DecayParams p) {
+template <int NT, int PT>
+__global__ void __launch_bounds__(kAll, NT * PT > 1 ? 1 : 2) k_decay_bwd_mma(DecayParams p) {
+    using SM = Smem<NT, PT>;
     extern __shared__ __align__(128) unsigned char sm_raw[];
     const uint32_t sm = smem_u32(sm_raw);
-    Sums *sums = reinterpret_cast<Sums *>(sm_raw + Smem::kF);
+    Sums *sums = reinterpret_cast<Sums *>(sm_raw + SM::kF);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int wr = warp & 3, wc = warp >> 2;    // 16 rows and 32 columns of each product
     const int g = lane >> 2, q2 = (lane & 3) * 2;
@@ -132,9 +139,10 @@ __global__ void __launch_bounds__(kAll, 2) k_decay_bwd_mma(DecayParams p) {
     typedef __nv_bfloat16 T;
     const T *c = (const T *)p.c + koff, *bb = (const T *)p.b + koff;
     const T *x = (const T *)p.x + voff, *gy = (const T *)p.g_y + voff;
-    T *gx = (T *)p.g_x + voff;
+    T *gx = (T *)p.g_x + b * p.oval_b + h * p.oval_h;
     const float *la = p.log_a + b * p.la_b + h * p.la_h;
     float *gla = p.g_la + b * p.gla_b + h * p.gla_h;
+    const int64_t okoff = b * p.okey_b + (h / p.rep) * p.okey_h;
     const bool part = p.rep > 1;        // gradients of shared keys: fp32 [B][H][L][N] partials
     const int64_t poff = bh * p.L * p.N, np = (int64_t)p.N * p.P;
 
@@ -206,22 +214,30 @@ __global__ void __launch_bounds__(kAll, 2) k_decay_bwd_mma(DecayParams p) {
         return;
     }
 
-    // R: rows m0 + g (+ 8), columns n0 + 8 f + q2 (+ 1)
-    float R[4][4];
+    // R: per 64 x 64 rows m0 + g (+ 8), columns n0 + 8 f + q2 (+ 1)
+    float R[NT][PT][4][4];
+    auto each = [&](auto &&f) {         // f(nt, pt)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int pt = 0; pt < PT; ++pt) f(nt, pt);
+    };
     {
         const float *in = p.nseg > 1 ? p.seg_state + (bh * p.nseg + seg) * np
                                      : (p.g_hlast ? p.g_hlast + bh * np : nullptr);
+        each([&](int nt, int pt) {
 #pragma unroll
-        for (int f = 0; f < 4; ++f)
+            for (int f = 0; f < 4; ++f)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const int n = m0 + g + 8 * (e >> 1), q = n0 + 8 * f + q2 + (e & 1);
-                R[f][e] = in && n < p.N && q < p.P ? in[(int64_t)n * p.P + q] : 0.f;
-            }
+                for (int e = 0; e < 4; ++e) {
+                    const int n = 64 * nt + m0 + g + 8 * (e >> 1), q = 64 * pt + n0 + 8 * f + q2 + (e & 1);
+                    R[nt][pt][f][e] = in && n < p.N && q < p.P ? in[(int64_t)n * p.P + q] : 0.f;
+                }
+        });
     }
     // blocks above the diagonal of P and Q stay zero
     for (int e = tid; e < 2 * 512; e += kTh)
-        *reinterpret_cast<uint4 *>(sm_raw + Smem::kP + 16 * e) = make_uint4(0, 0, 0, 0);
+        *reinterpret_cast<uint4 *>(sm_raw + SM::kP + 16 * e) = make_uint4(0, 0, 0, 0);
 
     auto store_key = [&](void *out, int64_t t, int q, float v0, float v1) {     // columns q, q + 1
         if (t >= p.L) return;
@@ -231,8 +247,8 @@ __global__ void __launch_bounds__(kAll, 2) k_decay_bwd_mma(DecayParams p) {
             if (q < p.N) o[0] = v0;
             if (q + 1 < p.N) o[1] = v1;
         } else {
-            T *o = (T *)out + koff + t * p.key_t + q;
-            if (p.vec) {
+            T *o = (T *)out + okoff + t * p.okey_t + q;
+            if (p.ovec) {
                 if (q < p.N) *reinterpret_cast<uint32_t *>(o) = pack2(v0, v1);
             } else {
                 if (q < p.N) o[0] = __float2bfloat16_rn(v0);
@@ -246,18 +262,19 @@ __global__ void __launch_bounds__(kAll, 2) k_decay_bwd_mma(DecayParams p) {
         __syncthreads();                // the last chunk's tiles have been read; decays are in
         Sums &sw = sums[ch & 1];
         if (t0 >= len) {                // behind the end: zero gradients, R stays
-            for (int e = tid; e < kC * 64; e += kTh) {
-                const int64_t t = t0 + e / 64;
-                const int q = e % 64;
+            constexpr int W = 64 * (NT > PT ? NT : PT);
+            for (int e = tid; e < kC * W; e += kTh) {
+                const int64_t t = t0 + e / W;
+                const int q = e % W;
                 if (t >= p.L) continue;
-                if (q < p.P) gx[t * p.val_t + q] = __float2bfloat16_rn(0.f);
+                if (q < p.P) gx[t * p.oval_t + q] = __float2bfloat16_rn(0.f);
                 if (q < p.N) {
                     if (part) {
                         ((float *)p.g_c)[poff + t * p.N + q] = 0.f;
                         ((float *)p.g_b)[poff + t * p.N + q] = 0.f;
                     } else {
-                        ((T *)p.g_c)[koff + t * p.key_t + q] = __float2bfloat16_rn(0.f);
-                        ((T *)p.g_b)[koff + t * p.key_t + q] = __float2bfloat16_rn(0.f);
+                        ((T *)p.g_c)[okoff + t * p.okey_t + q] = __float2bfloat16_rn(0.f);
+                        ((T *)p.g_b)[okoff + t * p.okey_t + q] = __float2bfloat16_rn(0.f);
                     }
                 }
                 if (q == 0) gla[t * p.gla_t] = 0.f;
@@ -277,11 +294,20 @@ __global__ void __launch_bounds__(kAll, 2) k_decay_bwd_mma(DecayParams p) {
                                  "l"(src), "r"(n)
                                  : "memory");
                 };
-                const int qk = 8 * q < p.N ? 8 * q : 0, qv = 8 * q < p.P ? 8 * q : 0;
-                cp(Smem::kc, c + t * p.key_t + qk, 8 * q < p.N);
-                cp(Smem::kb, bb + t * p.key_t + qk, 8 * q < p.N);
-                cp(Smem::kx, x + t * p.val_t + qv, 8 * q < p.P);
-                cp(Smem::kg, gy + t * p.val_t + qv, 8 * q < p.P);
+#pragma unroll
+                for (int j = 0; j < NT; ++j) {
+                    const bool in = 64 * j + 8 * q < p.N;
+                    const int64_t at = t * p.key_t + (in ? 64 * j + 8 * q : 0);
+                    cp(SM::kc + j * kTile, c + at, in);
+                    cp(SM::kb + j * kTile, bb + at, in);
+                }
+#pragma unroll
+                for (int j = 0; j < PT; ++j) {
+                    const bool in = 64 * j + 8 * q < p.P;
+                    const int64_t at = t * p.val_t + (in ? 64 * j + 8 * q : 0);
+                    cp(SM::kx + j * kTile, x + at, in);
+                    cp(SM::kg + j * kTile, gy + at, in);
+                }
             }
             asm volatile("cp.async.commit_group;" ::: "memory");
         } else {
@@ -297,10 +323,16 @@ __global__ void __launch_bounds__(kAll, 2) k_decay_bwd_mma(DecayParams p) {
                     }
                     sts32(sm + tile + piece(r, q / 8) + (q & 7) * 2, w);
                 };
-                cp(Smem::kc, c, p.key_t, p.N);
-                cp(Smem::kb, bb, p.key_t, p.N);
-                cp(Smem::kx, x, p.val_t, p.P);
-                cp(Smem::kg, gy, p.val_t, p.P);
+#pragma unroll
+                for (int j = 0; j < NT; ++j) {
+                    cp(SM::kc + j * kTile, c + 64 * j, p.key_t, p.N - 64 * j);
+                    cp(SM::kb + j * kTile, bb + 64 * j, p.key_t, p.N - 64 * j);
+                }
+#pragma unroll
+                for (int j = 0; j < PT; ++j) {
+                    cp(SM::kx + j * kTile, x + 64 * j, p.val_t, p.P - 64 * j);
+                    cp(SM::kg + j * kTile, gy + 64 * j, p.val_t, p.P - 64 * j);
+                }
             }
         }
         // the next chunk's rows and state on their way to L2
@@ -309,47 +341,54 @@ __global__ void __launch_bounds__(kAll, 2) k_decay_bwd_mma(DecayParams p) {
             const void *at = tid < 64 ? (const void *)(c + tn * p.key_t) : tid < 128 ? (const void *)(bb + tn * p.key_t)
                              : tid < 192 ? (const void *)(x + tn * p.val_t) : (const void *)(gy + tn * p.val_t);
             asm volatile("prefetch.global.L2 [%0];" ::"l"(at));
-            if (ch > 1 && (int64_t)tid * 32 < np)
-                asm volatile("prefetch.global.L2 [%0];" ::"l"(p.carry + (bh * p.nchunks + ch - 1) * np + tid * 32));
+#pragma unroll
+            for (int j = tid; j < NT * PT * 128; j += kTh)
+                if (ch > 1 && j * 32 < np)
+                    asm volatile("prefetch.global.L2 [%0];" ::"l"(p.carry + (bh * p.nchunks + ch - 1) * np + j * 32));
         }
         // ---- parts of S0 and R, and <S0, R>
         {
             const float *S0 = ch > 0 ? p.carry + (bh * p.nchunks + ch) * np
                                      : (p.h0 ? p.h0 + bh * np : nullptr);
-            float S[4][4], dot = 0.f;
+            float dot = 0.f;
             const bool even = p.P % 2 == 0 && ((uintptr_t)S0 & 7) == 0;
+            each([&](int nt, int pt) {
+                float S[4][4];
 #pragma unroll
-            for (int f = 0; f < 4; ++f)
+                for (int f = 0; f < 4; ++f)
 #pragma unroll
-                for (int e = 0; e < 4; e += 2) {
-                    const int n = m0 + g + 4 * e, q = n0 + 8 * f + q2;
-                    const bool in = S0 && n < p.N;
-                    const float *at = S0 + (int64_t)n * p.P + q;
-                    if (even) {
-                        const float2 v = in && q < p.P ? *reinterpret_cast<const float2 *>(at) : make_float2(0.f, 0.f);
-                        S[f][e] = v.x;
-                        S[f][e + 1] = v.y;
-                    } else {
-                        S[f][e] = in && q < p.P ? at[0] : 0.f;
-                        S[f][e + 1] = in && q + 1 < p.P ? at[1] : 0.f;
+                    for (int e = 0; e < 4; e += 2) {
+                        const int n = 64 * nt + m0 + g + 4 * e, q = 64 * pt + n0 + 8 * f + q2;
+                        const bool in = S0 && n < p.N;
+                        const float *at = S0 + (int64_t)n * p.P + q;
+                        if (even) {
+                            const float2 v = in && q < p.P ? *reinterpret_cast<const float2 *>(at) : make_float2(0.f, 0.f);
+                            S[f][e] = v.x;
+                            S[f][e + 1] = v.y;
+                        } else {
+                            S[f][e] = in && q < p.P ? at[0] : 0.f;
+                            S[f][e + 1] = in && q + 1 < p.P ? at[1] : 0.f;
+                        }
                     }
-                }
 #pragma unroll
-            for (int f = 0; f < 4; ++f)
+                for (int f = 0; f < 4; ++f)
 #pragma unroll
-                for (int e = 0; e < 4; e += 2) {
-                    const int n = m0 + g + 4 * e;
-                    const uint32_t at = sm + piece(n, n0 / 8 + f) + q2 * 2;
-                    uint32_t o[3];
-                    dot = fmaf(S[f][e], R[f][e], dot);
-                    dot = fmaf(S[f][e + 1], R[f][e + 1], dot);
-                    split3(S[f][e], S[f][e + 1], o);
+                    for (int e = 0; e < 4; e += 2) {
+                        const float(&r)[4] = R[nt][pt][f];
+                        const uint32_t at = sm + (nt * PT + pt) * kTile + piece(m0 + g + 4 * e, n0 / 8 + f) + q2 * 2;
+                        uint32_t o[3];
+                        dot = fmaf(S[f][e], r[e], dot);
+                        dot = fmaf(S[f][e + 1], r[e + 1], dot);
+                        split3(S[f][e], S[f][e + 1], o);
 #pragma unroll
-                    for (int k = 0; k < 3; ++k) sts32(at + Smem::kS + k * kTile, o[k]);
-                    split3(R[f][e], R[f][e + 1], o);
+                        for (int k = 0; k < 3; ++k) sts32(at + SM::kS + k * SM::kState, o[k]);
+                        if (!SM::kShare) {
+                            split3(r[e], r[e + 1], o);
 #pragma unroll
-                    for (int k = 0; k < 3; ++k) sts32(at + Smem::kR + k * kTile, o[k]);
-                }
+                            for (int k = 0; k < 3; ++k) sts32(at + SM::kR + k * SM::kState, o[k]);
+                        }
+                    }
+            });
 #pragma unroll
             for (int d = 16; d; d >>= 1) dot += __shfl_xor_sync(kFull, dot, d);
             if (lane == 0) sw.dot[warp] = dot;
@@ -360,11 +399,14 @@ __global__ void __launch_bounds__(kAll, 2) k_decay_bwd_mma(DecayParams p) {
 
         // ---- P and Q of rows m0.., the 16-column blocks k = wc, wc + 2, .. <= wr
         {
+            // rows' operands: kept over the blocks, or fetched for each (registers)
             uint32_t ca[4][4], ga[4][4];
+            if (!SM::kShare) {
 #pragma unroll
-            for (int ks = 0; ks < 4; ++ks) {
-                ldm4(ca[ks], at_a(sm + Smem::kc, m0, ks, lane));
-                ldm4(ga[ks], at_a(sm + Smem::kg, m0, ks, lane));
+                for (int ks = 0; ks < 4; ++ks) {
+                    ldm4(ca[ks], at_a(sm + SM::kc, m0, ks, lane));
+                    ldm4(ga[ks], at_a(sm + SM::kg, m0, ks, lane));
+                }
             }
             const float2 gr0 = sw.G[m0 + g], gr1 = sw.G[m0 + g + 8];
             float row0 = 0.f, row1 = 0.f;
@@ -382,13 +424,21 @@ __global__ void __launch_bounds__(kAll, 2) k_decay_bwd_mma(DecayParams p) {
                     for (int e = 0; e < 4; ++e) s[f][e] = v[f][e] = 0.f;
 #pragma unroll
                 for (int ks = 0; ks < 4; ++ks) {
-                    uint32_t fb[4], fx[4];
-                    ldm4(fb, at_b(sm + Smem::kb, 16 * k, ks, lane));
-                    ldm4(fx, at_b(sm + Smem::kx, 16 * k, ks, lane));
-                    mma(s[0], ca[ks], fb[0], fb[1]);
-                    mma(s[1], ca[ks], fb[2], fb[3]);
-                    mma(v[0], ga[ks], fx[0], fx[1]);
-                    mma(v[1], ga[ks], fx[2], fx[3]);
+                    uint32_t f[4];
+#pragma unroll
+                    for (int j = 0; j < NT; ++j) {
+                        if (SM::kShare) ldm4(ca[ks], at_a(sm + SM::kc + j * kTile, m0, ks, lane));
+                        ldm4(f, at_b(sm + SM::kb + j * kTile, 16 * k, ks, lane));
+                        mma(s[0], ca[ks], f[0], f[1]);
+                        mma(s[1], ca[ks], f[2], f[3]);
+                    }
+#pragma unroll
+                    for (int j = 0; j < PT; ++j) {
+                        if (SM::kShare) ldm4(ga[ks], at_a(sm + SM::kg + j * kTile, m0, ks, lane));
+                        ldm4(f, at_b(sm + SM::kx + j * kTile, 16 * k, ks, lane));
+                        mma(v[0], ga[ks], f[0], f[1]);
+                        mma(v[1], ga[ks], f[2], f[3]);
+                    }
                 }
 #pragma unroll
                 for (int f = 0; f < 2; ++f) {
@@ -417,10 +467,10 @@ __global__ void __launch_bounds__(kAll, 2) k_decay_bwd_mma(DecayParams p) {
                     }
                     const uint32_t a0 = sm + piece(m0 + g, 2 * k + f) + q2 * 2,
                                    a1 = sm + piece(m0 + g + 8, 2 * k + f) + q2 * 2;
-                    sts32(a0 + Smem::kP, pack2(pv[0], pv[1]));
-                    sts32(a1 + Smem::kP, pack2(pv[2], pv[3]));
-                    sts32(a0 + Smem::kQ, pack2(qv[0], qv[1]));
-                    sts32(a1 + Smem::kQ, pack2(qv[2], qv[3]));
+                    sts32(a0 + SM::kP, pack2(pv[0], pv[1]));
+                    sts32(a1 + SM::kP, pack2(pv[2], pv[3]));
+                    sts32(a0 + SM::kQ, pack2(qv[0], qv[1]));
+                    sts32(a1 + SM::kQ, pack2(qv[2], qv[3]));
                 }
             }
             row0 = quad_sum(row0);
@@ -449,8 +499,8 @@ __global__ void __launch_bounds__(kAll, 2) k_decay_bwd_mma(DecayParams p) {
 #pragma unroll
                 for (int ks = 0; ks < 4; ++ks) {
                     uint32_t f0[4], f1[4];
-                    ldm4(f0, at_b(parts + k * kTile, n0, ks, lane));
-                    ldm4(f1, at_b(parts + k * kTile, n0 + 16, ks, lane));
+                    ldm4(f0, at_b(parts + k * SM::kState, n0, ks, lane));
+                    ldm4(f1, at_b(parts + k * SM::kState, n0 + 16, ks, lane));
                     mma(acc[0], a[ks], f0[0], f0[1]);
                     mma(acc[1], a[ks], f0[2], f0[3]);
                     mma(acc[2], a[ks], f1[0], f1[1]);
@@ -467,8 +517,8 @@ __global__ void __launch_bounds__(kAll, 2) k_decay_bwd_mma(DecayParams p) {
                 acc[f][3] *= f1;
             }
         };
-        auto row_dots = [&](uint32_t tile, float (&out)[2][kC]) {
-            float d0 = 0.f, d1 = 0.f;
+        float d0, d1;
+        auto row_dots = [&](uint32_t tile) {
 #pragma unroll
             for (int f = 0; f < 4; ++f) {
                 const uint32_t w0 = lds_u32(sm + tile + piece(m0 + g, n0 / 8 + f) + q2 * 2),
@@ -476,6 +526,8 @@ __global__ void __launch_bounds__(kAll, 2) k_decay_bwd_mma(DecayParams p) {
                 d0 = fmaf(acc[f][0], lo_of(w0), fmaf(acc[f][1], hi_of(w0), d0));
                 d1 = fmaf(acc[f][2], lo_of(w1), fmaf(acc[f][3], hi_of(w1), d1));
             }
+        };
+        auto leave_dots = [&](float (&out)[2][kC]) {
             d0 = quad_sum(d0);
             d1 = quad_sum(d1);
             if ((lane & 3) == 0) {
@@ -495,111 +547,162 @@ __global__ void __launch_bounds__(kAll, 2) k_decay_bwd_mma(DecayParams p) {
         const int64_t tr0 = t0 + m0 + g, tr1 = tr0 + 8;
 
         // ---- g_c
-        zero();
-        by_parts(sm + Smem::kg, sm + Smem::kS);
-        scale_rows(sw.e[m0 + g], sw.e[m0 + g + 8]);
-        row_dots(Smem::kc, sw.u);
+        d0 = d1 = 0.f;
 #pragma unroll 1
-        for (int ks = 0; ks <= wr; ++ks) {
-            uint32_t a[4];
-            ldm4(a, at_a(sm + Smem::kQ, m0, ks, lane));
-            add_pairs(a, sm + Smem::kb, ks);
-        }
+        for (int nt = 0; nt < NT; ++nt) {
+            zero();
+#pragma unroll 1
+            for (int pt = 0; pt < PT; ++pt)
+                by_parts(sm + SM::kg + pt * kTile, sm + SM::kS + (nt * PT + pt) * kTile);
+            scale_rows(sw.e[m0 + g], sw.e[m0 + g + 8]);
+            row_dots(SM::kc + nt * kTile);
+#pragma unroll 1
+            for (int ks = 0; ks <= wr; ++ks) {
+                uint32_t a[4];
+                ldm4(a, at_a(sm + SM::kQ, m0, ks, lane));
+                add_pairs(a, sm + SM::kb + nt * kTile, ks);
+            }
 #pragma unroll
-        for (int f = 0; f < 4; ++f) {
-            store_key(p.g_c, tr0, n0 + 8 * f + q2, acc[f][0], acc[f][1]);
-            store_key(p.g_c, tr1, n0 + 8 * f + q2, acc[f][2], acc[f][3]);
+            for (int f = 0; f < 4; ++f) {
+                store_key(p.g_c, tr0, 64 * nt + n0 + 8 * f + q2, acc[f][0], acc[f][1]);
+                store_key(p.g_c, tr1, 64 * nt + n0 + 8 * f + q2, acc[f][2], acc[f][3]);
+            }
+        }
+        leave_dots(sw.u);
+        if (SM::kShare) {
+            sync_products();            // S0's parts have been read
+            each([&](int nt, int pt) {
+#pragma unroll
+                for (int f = 0; f < 4; ++f)
+#pragma unroll
+                    for (int e = 0; e < 4; e += 2) {
+                        const float(&r)[4] = R[nt][pt][f];
+                        const uint32_t at = sm + SM::kR + (nt * PT + pt) * kTile +
+                                            piece(m0 + g + 4 * e, n0 / 8 + f) + q2 * 2;
+                        uint32_t o[3];
+                        split3(r[e], r[e + 1], o);
+#pragma unroll
+                        for (int k = 0; k < 3; ++k) sts32(at + k * SM::kState, o[k]);
+                    }
+            });
+            sync_products();
         }
         // ---- g_b
-        zero();
-        by_parts(sm + Smem::kx, sm + Smem::kR);
         const float w0 = sw.w[m0 + g], w1 = sw.w[m0 + g + 8];
-        scale_rows(w0, w1);
-        row_dots(Smem::kb, sw.v);
+        d0 = d1 = 0.f;
 #pragma unroll 1
-        for (int ks = wr; ks < 4; ++ks) {
-            uint32_t a[4];
-            ldm4t(a, at_at(sm + Smem::kQ, m0, ks, lane));
-            add_pairs(a, sm + Smem::kc, ks);
-        }
+        for (int nt = 0; nt < NT; ++nt) {
+            zero();
+#pragma unroll 1
+            for (int pt = 0; pt < PT; ++pt)
+                by_parts(sm + SM::kx + pt * kTile, sm + SM::kR + (nt * PT + pt) * kTile);
+            scale_rows(w0, w1);
+            row_dots(SM::kb + nt * kTile);
+#pragma unroll 1
+            for (int ks = wr; ks < 4; ++ks) {
+                uint32_t a[4];
+                ldm4t(a, at_at(sm + SM::kQ, m0, ks, lane));
+                add_pairs(a, sm + SM::kc + nt * kTile, ks);
+            }
 #pragma unroll
-        for (int f = 0; f < 4; ++f) {
-            store_key(p.g_b, tr0, n0 + 8 * f + q2, acc[f][0], acc[f][1]);
-            store_key(p.g_b, tr1, n0 + 8 * f + q2, acc[f][2], acc[f][3]);
+            for (int f = 0; f < 4; ++f) {
+                store_key(p.g_b, tr0, 64 * nt + n0 + 8 * f + q2, acc[f][0], acc[f][1]);
+                store_key(p.g_b, tr1, 64 * nt + n0 + 8 * f + q2, acc[f][2], acc[f][3]);
+            }
         }
+        leave_dots(sw.v);
         // ---- g_x
-        zero();
-#pragma unroll
-        for (int ks = 0; ks < 4; ++ks) {
-            uint32_t a[4];
-            ldm4(a, at_a(sm + Smem::kb, m0, ks, lane));
-            add_pairs(a, sm + Smem::kR, ks);
-        }
-        scale_rows(w0, w1);
 #pragma unroll 1
-        for (int ks = wr; ks < 4; ++ks) {
-            uint32_t a[4];
-            ldm4t(a, at_at(sm + Smem::kP, m0, ks, lane));
-            add_pairs(a, sm + Smem::kg, ks);
-        }
+        for (int pt = 0; pt < PT; ++pt) {
+            zero();
+#pragma unroll 1
+            for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int f = 0; f < 4; ++f) {
-            const int q = n0 + 8 * f + q2;
+                for (int ks = 0; ks < 4; ++ks) {
+                    uint32_t a[4];
+                    ldm4(a, at_a(sm + SM::kb + nt * kTile, m0, ks, lane));
+                    add_pairs(a, sm + SM::kR + (nt * PT + pt) * kTile, ks);
+                }
+            scale_rows(w0, w1);
+#pragma unroll 1
+            for (int ks = wr; ks < 4; ++ks) {
+                uint32_t a[4];
+                ldm4t(a, at_at(sm + SM::kP, m0, ks, lane));
+                add_pairs(a, sm + SM::kg + pt * kTile, ks);
+            }
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const int64_t t = e ? tr1 : tr0;
-                if (t >= p.L) continue;
-                const float v0 = t < len ? acc[f][2 * e] : 0.f, v1 = t < len ? acc[f][2 * e + 1] : 0.f;
-                T *o = gx + t * p.val_t + q;
-                if (p.vec) {
-                    if (q < p.P) *reinterpret_cast<uint32_t *>(o) = pack2(v0, v1);
-                } else {
-                    if (q < p.P) o[0] = __float2bfloat16_rn(v0);
-                    if (q + 1 < p.P) o[1] = __float2bfloat16_rn(v1);
+            for (int f = 0; f < 4; ++f) {
+                const int q = 64 * pt + n0 + 8 * f + q2;
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const int64_t t = e ? tr1 : tr0;
+                    if (t >= p.L) continue;
+                    const float v0 = t < len ? acc[f][2 * e] : 0.f, v1 = t < len ? acc[f][2 * e + 1] : 0.f;
+                    T *o = gx + t * p.oval_t + q;
+                    if (p.ovec) {
+                        if (q < p.P) *reinterpret_cast<uint32_t *>(o) = pack2(v0, v1);
+                    } else {
+                        if (q < p.P) o[0] = __float2bfloat16_rn(v0);
+                        if (q + 1 < p.P) o[1] = __float2bfloat16_rn(v1);
+                    }
                 }
             }
         }
         // ---- R: the chunk's part from zero, then one fp32 multiply-add (a product's
         // own additions truncate, which would pile up over a long memory)
-        zero();
+        each([&](int nt, int pt) {
+            zero();
 #pragma unroll
-        for (int ks = 0; ks < 4; ++ks) {
-            uint32_t a[4], parts[3][4], f0[4], f1[4];
-            ldm4t(a, at_at(sm + Smem::kc, m0, ks, lane));
-            ldm4t(f0, at_bt(sm + Smem::kg, n0, ks, lane));
-            ldm4t(f1, at_bt(sm + Smem::kg, n0 + 16, ks, lane));
+            for (int ks = 0; ks < 4; ++ks) {
+                uint32_t a[4], parts[3][4], f0[4], f1[4];
+                ldm4t(a, at_at(sm + SM::kc + nt * kTile, m0, ks, lane));
+                ldm4t(f0, at_bt(sm + SM::kg + pt * kTile, n0, ks, lane));
+                ldm4t(f1, at_bt(sm + SM::kg + pt * kTile, n0 + 16, ks, lane));
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const float2 w = *reinterpret_cast<const float2 *>(sw.e + 16 * ks + 8 * (e >> 1) + q2);
-                uint32_t o[3];
-                split3(lo_of(a[e]) * w.x, hi_of(a[e]) * w.y, o);
+                for (int e = 0; e < 4; ++e) {
+                    const float2 w = *reinterpret_cast<const float2 *>(sw.e + 16 * ks + 8 * (e >> 1) + q2);
+                    uint32_t o[3];
+                    split3(lo_of(a[e]) * w.x, hi_of(a[e]) * w.y, o);
 #pragma unroll
-                for (int k = 0; k < 3; ++k) parts[k][e] = o[k];
+                    for (int k = 0; k < 3; ++k) parts[k][e] = o[k];
+                }
+#pragma unroll
+                for (int k = 0; k < 3; ++k) {
+                    mma(acc[0], parts[k], f0[0], f0[1]);
+                    mma(acc[1], parts[k], f0[2], f0[3]);
+                    mma(acc[2], parts[k], f1[0], f1[1]);
+                    mma(acc[3], parts[k], f1[2], f1[3]);
+                }
             }
 #pragma unroll
-            for (int k = 0; k < 3; ++k) {
-                mma(acc[0], parts[k], f0[0], f0[1]);
-                mma(acc[1], parts[k], f0[2], f0[3]);
-                mma(acc[2], parts[k], f1[0], f1[1]);
-                mma(acc[3], parts[k], f1[2], f1[3]);
-            }
-        }
+            for (int f = 0; f < 4; ++f)
 #pragma unroll
-        for (int f = 0; f < 4; ++f)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) R[f][e] = fmaf(aend, R[f][e], acc[f][e]);
+                for (int e = 0; e < 4; ++e) R[nt][pt][f][e] = fmaf(aend, R[nt][pt][f][e], acc[f][e]);
+        });
     }
     __syncthreads();                    // for the last chunk's g_log_a
     if (p.g_h0 && seg == 0) {
         float *out = p.g_h0 + bh * np;
+        each([&](int nt, int pt) {
 #pragma unroll
-        for (int f = 0; f < 4; ++f)
+            for (int f = 0; f < 4; ++f)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const int n = m0 + g + 8 * (e >> 1), q = n0 + 8 * f + q2 + (e & 1);
-                if (n < p.N && q < p.P) out[(int64_t)n * p.P + q] = R[f][e];
-            }
+                for (int e = 0; e < 4; ++e) {
+                    const int n = 64 * nt + m0 + g + 8 * (e >> 1), q = 64 * pt + n0 + 8 * f + q2 + (e & 1);
+                    if (n < p.N && q < p.P) out[(int64_t)n * p.P + q] = R[nt][pt][f][e];
+                }
+        });
     }
+}
+
+template <int NT, int PT>
+cudaError_t go(const DecayParams &p, cudaStream_t st) {
+    static std::atomic<int> set[kLimitDevices];
+    constexpr int smem = (int)Smem<NT, PT>::kTotal;
+    const cudaError_t e = allow_smem((const void *)k_decay_bwd_mma<NT, PT>, smem, set);
+    if (e != cudaSuccess) return e;
+    k_decay_bwd_mma<NT, PT><<<dim3((unsigned)((int64_t)p.B * p.H * p.nseg)), kAll, smem, st>>>(p);
+    return cudaGetLastError();
 }
 
 }  // namespace
@@ -610,17 +713,14 @@ cudaError_t launch_decay_bwd_mma(const DecayParams &p, cudaStream_t st) {
         DecayParams s = p;
         s.nchunks = (int)((p.L + 127) / 128);
         s.seg_chunks = p.seg_chunks / 2;
-        s.pslices = 1;
+        s.pslices = (p.P + 63) / 64;
         cudaError_t e = launch_decay_seg_rev_tc(s, st);
         if (e != cudaSuccess) return e;
         e = launch_decay_join(p, p.g_hlast, true, nullptr, st);
         if (e != cudaSuccess) return e;
     }
-    static std::atomic<int> set[kLimitDevices];
-    const cudaError_t e = allow_smem((const void *)k_decay_bwd_mma, (int)Smem::kTotal, set);
-    if (e != cudaSuccess) return e;
-    k_decay_bwd_mma<<<dim3((unsigned)((int64_t)p.B * p.H * p.nseg)), kAll, Smem::kTotal, st>>>(p);
-    return cudaGetLastError();
+    if (p.N <= 64) return p.P <= 64 ? go<1, 1>(p, st) : go<1, 2>(p, st);
+    return p.P <= 64 ? go<2, 1>(p, st) : go<2, 2>(p, st);
 }
 
 }  // namespace pdssm

@@ -1,5 +1,5 @@
-// Decay scan on the CUDA cores: every type and width, the path of fp32
-// inputs.  One CTA of 256 threads (16 x 16) per segment of a (batch, head);
+// Decay scan of fp32 inputs on the CUDA cores, any width, and the small kernels
+// of both paths.  One CTA of 256 threads (16 x 16) per segment of a (batch, head);
 // a chunk's operands sit in shared memory as fp32 rows of width + 4 floats, and
 // each thread owns a TM x TN tile of a product's result.
 //
@@ -82,23 +82,23 @@ __device__ __forceinline__ void zero(float (&acc)[TM][TN]) {
 // WT + 4 floats; zero behind `len` and behind the width.  A chunk's rows are
 // fetched while the chunk before it is worked on (their latency, a
 // microsecond, is a third of a short chunk's time).
-template <typename T, int C, int WT>
+template <int C, int WT>
 struct Rows {
     static constexpr int kN = C * WT / kThreads;
-    T v[kN];
-    __device__ __forceinline__ void fetch(const T *src, int64_t stride, int width, int64_t t0,
+    float v[kN];
+    __device__ __forceinline__ void fetch(const float *src, int64_t stride, int width, int64_t t0,
                                           int64_t len) {
         const int n = threadIdx.x % WT;
 #pragma unroll
         for (int i = 0; i < kN; ++i) {
             const int64_t t = t0 + (i * kThreads + threadIdx.x) / WT;
-            v[i] = n < width && t < len ? src[t * stride + n] : from_f<T>(0.f);
+            v[i] = n < width && t < len ? src[t * stride + n] : 0.f;
         }
     }
     __device__ __forceinline__ void put(float *dst) const {
 #pragma unroll
         for (int i = 0; i < kN; ++i)
-            dst[(i * kThreads + threadIdx.x) / WT * (WT + 4) + threadIdx.x % WT] = to_f<T>(v[i]);
+            dst[(i * kThreads + threadIdx.x) / WT * (WT + 4) + threadIdx.x % WT] = v[i];
     }
 };
 
@@ -139,7 +139,7 @@ struct Steps {
 // The state alone over one segment from zero.  Forward (REV = false): rows u
 // = b, v = x, weights e^{G_C - G_t}, chunks in order.  Reverse: u = c, v =
 // g_y, weights e^{G_t}, chunks in reverse.
-template <typename T, int C, int WT, bool REV>
+template <int C, int WT, bool REV>
 __global__ void __launch_bounds__(kThreads) k_decay_seg_gen(DecayParams p) {
     extern __shared__ float sm[];
     constexpr int LD = WT + 4;
@@ -148,14 +148,14 @@ __global__ void __launch_bounds__(kThreads) k_decay_seg_gen(DecayParams p) {
     const int seg = blockIdx.x % p.nseg;
     const Head hd = head_of(p, blockIdx.x / p.nseg);
     const int ty = threadIdx.x / 16, tx = threadIdx.x % 16;
-    const T *u = (const T *)(REV ? p.c : p.b) + hd.b * p.key_b + (hd.h / p.rep) * p.key_h;
-    const T *v = (const T *)(REV ? p.g_y : p.x) + hd.b * p.val_b + hd.h * p.val_h;
+    const float *u = (const float *)(REV ? p.c : p.b) + hd.b * p.key_b + (hd.h / p.rep) * p.key_h;
+    const float *v = (const float *)(REV ? p.g_y : p.x) + hd.b * p.val_b + hd.h * p.val_h;
     constexpr int TN = WT / 16;
     float S[TN][TN];
     zero(S);
     double total = 0.0;
     const int c0 = seg * p.seg_chunks, c1 = min(c0 + p.seg_chunks, p.nchunks);
-    Rows<T, C, WT> ru, rv;
+    Rows<C, WT> ru, rv;
     Steps<C> rl;
     auto fetch = [&](int i) {
         const int64_t t0 = i < c1 ? (int64_t)(REV ? c1 - 1 - (i - c0) : i) * C : hd.len;
@@ -202,7 +202,7 @@ __global__ void __launch_bounds__(kThreads) k_decay_seg_gen(DecayParams p) {
     if (threadIdx.x == 0) p.seg_decay[(int64_t)hd.bh * p.nseg + seg] = exp2f((float)total);
 }
 
-template <typename T, int C, int WT>
+template <int C, int WT>
 __global__ void __launch_bounds__(kThreads) k_decay_fwd_gen(DecayParams p) {
     constexpr int PS = WT < 64 ? WT : 64;
     constexpr int LD = WT + 4, LP = PS + 4, LC = C + 4;
@@ -217,8 +217,8 @@ __global__ void __launch_bounds__(kThreads) k_decay_fwd_gen(DecayParams p) {
     const int ty = threadIdx.x / 16, tx = threadIdx.x % 16;
     const int64_t koff = hd.b * p.key_b + (hd.h / p.rep) * p.key_h;
     const int64_t voff = hd.b * p.val_b + hd.h * p.val_h + p0;
-    const T *c = (const T *)p.c + koff, *b = (const T *)p.b + koff, *x = (const T *)p.x + voff;
-    T *y = (T *)p.y + voff;
+    const float *c = (const float *)p.c + koff, *b = (const float *)p.b + koff, *x = (const float *)p.x + voff;
+    float *y = (float *)p.y + voff;
     const int64_t np = (int64_t)p.N * p.P;
     // these kernels have no bounded waits: the workspace's status is good
     if (blockIdx.x == 0 && threadIdx.x == 0) *p.status = 0;
@@ -231,8 +231,8 @@ __global__ void __launch_bounds__(kThreads) k_decay_fwd_gen(DecayParams p) {
         sS[n * LP + q] = (in && n < p.N && q < pw) ? in[(int64_t)n * p.P + p0 + q] : 0.f;
     }
     const int c0 = seg * p.seg_chunks, c1 = min(c0 + p.seg_chunks, p.nchunks);
-    Rows<T, C, WT> rc, rb;
-    Rows<T, C, PS> rx;
+    Rows<C, WT> rc, rb;
+    Rows<C, PS> rx;
     Steps<C> rl;
     auto fetch = [&](int i) {
         const int64_t t0 = i < c1 ? (int64_t)i * C : hd.len;
@@ -262,7 +262,7 @@ __global__ void __launch_bounds__(kThreads) k_decay_fwd_gen(DecayParams p) {
         if (t0 >= hd.len) {             // behind the end: y is zero, the state stays
             for (int e = threadIdx.x; e < C * PS; e += kThreads) {
                 const int64_t t = t0 + e / PS;
-                if (t < p.L && e % PS < pw) y[t * p.val_t + e % PS] = from_f<T>(0.f);
+                if (t < p.L && e % PS < pw) y[t * p.val_t + e % PS] = 0.f;
             }
             continue;
         }
@@ -298,7 +298,7 @@ __global__ void __launch_bounds__(kThreads) k_decay_fwd_gen(DecayParams p) {
 #pragma unroll
                 for (int n = 0; n < TP; ++n)
                     if (t < p.L && pairs(tx, n) < pw)
-                        y[t * p.val_t + pairs(tx, n)] = from_f<T>(t < hd.len ? acc[m][n] : 0.f);
+                        y[t * p.val_t + pairs(tx, n)] = t < hd.len ? acc[m][n] : 0.f;
             }
         }
         for (int e = threadIdx.x; e < C * WT; e += kThreads)
@@ -329,7 +329,7 @@ __global__ void __launch_bounds__(kThreads) k_decay_fwd_gen(DecayParams p) {
 }
 
 // Adjoint of one segment's chunks in reverse; sR is dl/dS at the chunk's end.
-template <typename T, int C, int WT>
+template <int C, int WT>
 __global__ void __launch_bounds__(kThreads) k_decay_bwd_gen(DecayParams p) {
     constexpr int LD = WT + 4, LC = C + 4, TM = C / 16, TN = WT / 16;
     extern __shared__ float sm[];
@@ -343,9 +343,9 @@ __global__ void __launch_bounds__(kThreads) k_decay_bwd_gen(DecayParams p) {
     const int ty = threadIdx.x / 16, tx = threadIdx.x % 16;
     const int64_t koff = hd.b * p.key_b + (hd.h / p.rep) * p.key_h;
     const int64_t voff = hd.b * p.val_b + hd.h * p.val_h;
-    const T *c = (const T *)p.c + koff, *b = (const T *)p.b + koff;
-    const T *x = (const T *)p.x + voff, *gy = (const T *)p.g_y + voff;
-    T *gx = (T *)p.g_x + voff;
+    const float *c = (const float *)p.c + koff, *b = (const float *)p.b + koff;
+    const float *x = (const float *)p.x + voff, *gy = (const float *)p.g_y + voff;
+    float *gx = (float *)p.g_x + voff;
     const int64_t np = (int64_t)p.N * p.P;
     float *gla = p.g_la + hd.b * p.gla_b + hd.h * p.gla_h;
     // gradients of shared keys go to fp32 [B][H][L][N] partials
@@ -359,7 +359,7 @@ __global__ void __launch_bounds__(kThreads) k_decay_bwd_gen(DecayParams p) {
         sR[n * LD + q] = (in && n < p.N && q < p.P) ? in[(int64_t)n * p.P + q] : 0.f;
     }
     const int c0 = seg * p.seg_chunks, c1 = min(c0 + p.seg_chunks, p.nchunks);
-    Rows<T, C, WT> rc, rb, rx, rg;
+    Rows<C, WT> rc, rb, rx, rg;
     Steps<C> rl;
     auto fetch = [&](int i) {
         const int64_t t0 = i >= c0 ? (int64_t)i * C : hd.len;
@@ -396,14 +396,14 @@ __global__ void __launch_bounds__(kThreads) k_decay_bwd_gen(DecayParams p) {
                 const int64_t t = t0 + e / WT;
                 const int q = e % WT;
                 if (t >= p.L) continue;
-                if (q < p.P) gx[t * p.val_t + q] = from_f<T>(0.f);
+                if (q < p.P) gx[t * p.val_t + q] = 0.f;
                 if (q < p.N) {
                     if (part) {
                         ((float *)p.g_c)[poff + t * p.N + q] = 0.f;
                         ((float *)p.g_b)[poff + t * p.N + q] = 0.f;
                     } else {
-                        ((T *)p.g_c)[koff + t * p.key_t + q] = from_f<T>(0.f);
-                        ((T *)p.g_b)[koff + t * p.key_t + q] = from_f<T>(0.f);
+                        ((float *)p.g_c)[koff + t * p.key_t + q] = 0.f;
+                        ((float *)p.g_b)[koff + t * p.key_t + q] = 0.f;
                     }
                 }
                 if (q == 0) gla[t * p.gla_t] = 0.f;
@@ -480,7 +480,7 @@ __global__ void __launch_bounds__(kThreads) k_decay_bwd_gen(DecayParams p) {
                     if (part)
                         ((float *)p.g_c)[poff + t * p.N + q] = v;
                     else
-                        ((T *)p.g_c)[koff + t * p.key_t + q] = from_f<T>(v);
+                        ((float *)p.g_c)[koff + t * p.key_t + q] = v;
                 }
             }
         }
@@ -511,7 +511,7 @@ __global__ void __launch_bounds__(kThreads) k_decay_bwd_gen(DecayParams p) {
                     if (part)
                         ((float *)p.g_b)[poff + t * p.N + q] = v;
                     else
-                        ((T *)p.g_b)[koff + t * p.key_t + q] = from_f<T>(v);
+                        ((float *)p.g_b)[koff + t * p.key_t + q] = v;
                 }
             }
         }
@@ -533,7 +533,7 @@ __global__ void __launch_bounds__(kThreads) k_decay_bwd_gen(DecayParams p) {
 #pragma unroll
                 for (int n = 0; n < TN; ++n)
                     if (t < p.L && pairs(tx, n) < p.P)
-                        gx[t * p.val_t + pairs(tx, n)] = from_f<T>(t < hd.len ? acc[m][n] : 0.f);
+                        gx[t * p.val_t + pairs(tx, n)] = t < hd.len ? acc[m][n] : 0.f;
             }
         }
         // e^{G_C} <S0, R>, the row sums u_i + R_i and v_j
@@ -665,7 +665,7 @@ __global__ void k_decay_sum_heads(DecayParams p, const float *part_c, const floa
             sc += part_c[from + (int64_t)r * p.L * p.N];
             sb += part_b[from + (int64_t)r * p.L * p.N];
         }
-        const int64_t to = b * p.key_b + g * p.key_h + t * p.key_t + j;
+        const int64_t to = b * p.okey_b + g * p.okey_h + t * p.okey_t + j;
         g_c[to] = from_f<T>(sc);
         g_b[to] = from_f<T>(sb);
     }
@@ -678,8 +678,11 @@ __global__ void __launch_bounds__(1024) k_decay_sum_steps(DecayParams p, const f
     __shared__ double red[32];
     const int h = blockIdx.x;
     double s = 0.0;
-    for (int64_t e = threadIdx.x; e < (int64_t)p.B * p.L; e += blockDim.x)
-        s += (double)part[((e / p.L) * p.H + h) * p.L + e % p.L];
+    for (int b = 0; b < p.B; ++b) {
+        const float *row = part + ((int64_t)b * p.H + h) * p.L;
+#pragma unroll 4
+        for (int64_t t = threadIdx.x; t < p.L; t += blockDim.x) s += (double)row[t];
+    }
 #pragma unroll
     for (int d = 16; d; d >>= 1) s += __shfl_xor_sync(kFull, s, d);
     if (threadIdx.x % 32 == 0) red[threadIdx.x / 32] = s;
@@ -688,6 +691,55 @@ __global__ void __launch_bounds__(1024) k_decay_sum_steps(DecayParams p, const f
         double t = 0.0;
         for (int w = 0; w < (int)blockDim.x / 32; ++w) t += red[w];
         g_log_a[h] = (float)t;
+    }
+}
+
+// Rows to rows of whole 16 bytes, zero behind the width.  A thread makes 16
+// bytes.
+__global__ void k_decay_pad(DecayPad t0, DecayPad t1, DecayPad t2) {
+    const DecayPad &t = blockIdx.y == 0 ? t0 : blockIdx.y == 1 ? t1 : t2;
+    const int q8 = (t.width + 7) / 8;
+    const int64_t n = t.rows * q8;
+    for (int64_t e = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; e < n;
+         e += (int64_t)gridDim.x * blockDim.x) {
+        const int64_t row = e / q8;
+        const int q = 8 * (int)(e - row * q8);
+        const unsigned short *src = (const unsigned short *)t.src + row * t.width + q;
+        uint32_t w[4] = {0, 0, 0, 0};
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            if (q + j < t.width) w[j / 2] |= (uint32_t)__ldg(src + j) << (16 * (j % 2));
+        reinterpret_cast<uint4 *>(t.dst)[e] = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+}
+
+// and back.  A thread makes 8 values, 16 bytes where the result's address and
+// end allow it.
+__global__ void k_decay_unpad(const unsigned short *padded, unsigned short *out, int64_t rows, int width,
+                              int vec) {
+    const int w8 = (width + 7) / 8 * 8;
+    const int64_t n = rows * width;
+    for (int64_t e = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) * 8; e < n;
+         e += (int64_t)gridDim.x * blockDim.x * 8) {
+        const int64_t row = e / width;
+        int col = (int)(e - row * width);
+        const unsigned short *src = padded + row * w8;
+        uint32_t w[4] = {0, 0, 0, 0};
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            if (e + j < n) w[j / 2] |= (uint32_t)__ldg(src + col) << (16 * (j % 2));
+            if (++col == width) {
+                col = 0;
+                src += w8;
+            }
+        }
+        if (vec && e + 8 <= n) {
+            *reinterpret_cast<uint4 *>(out + e) = make_uint4(w[0], w[1], w[2], w[3]);
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                if (e + j < n) out[e + j] = (unsigned short)(w[j / 2] >> (16 * (j % 2)));
+        }
     }
 }
 
@@ -700,36 +752,36 @@ cudaError_t launch(int64_t grid, size_t smem, cudaStream_t st, const DecayParams
     return cudaGetLastError();
 }
 
-template <typename T, int C, int WT, bool REV>
+template <int C, int WT, bool REV>
 cudaError_t seg_gen(const DecayParams &p, cudaStream_t st) {
     const size_t smem = (size_t)(2 * C * (WT + 4) + 2 * C) * 4;
-    return launch<k_decay_seg_gen<T, C, WT, REV>>((int64_t)p.B * p.H * p.nseg, smem, st, p);
+    return launch<k_decay_seg_gen<C, WT, REV>>((int64_t)p.B * p.H * p.nseg, smem, st, p);
 }
 
-template <typename T, int C, int WT>
+template <int C, int WT>
 cudaError_t fwd_gen(const DecayParams &p, cudaStream_t st) {
     constexpr int PS = WT < 64 ? WT : 64;
     if (p.nseg > 1) {
-        cudaError_t e = seg_gen<T, C, WT, false>(p, st);
+        cudaError_t e = seg_gen<C, WT, false>(p, st);
         if (e != cudaSuccess) return e;
         e = launch_decay_join(p, p.h0, false, nullptr, st);
         if (e != cudaSuccess) return e;
     }
     const size_t smem = (size_t)(2 * C * (WT + 4) + (C + WT) * (PS + 4) + C * (C + 4) + 2 * C) * 4;
-    return launch<k_decay_fwd_gen<T, C, WT>>((int64_t)p.B * p.H * p.nseg * p.pslices, smem, st, p);
+    return launch<k_decay_fwd_gen<C, WT>>((int64_t)p.B * p.H * p.nseg * p.pslices, smem, st, p);
 }
 
-template <typename T, int C, int WT>
+template <int C, int WT>
 cudaError_t bwd_gen(const DecayParams &p, cudaStream_t st) {
     if (p.nseg > 1) {
-        cudaError_t e = seg_gen<T, C, WT, true>(p, st);
+        cudaError_t e = seg_gen<C, WT, true>(p, st);
         if (e != cudaSuccess) return e;
         e = launch_decay_join(p, p.g_hlast, true, nullptr, st);
         if (e != cudaSuccess) return e;
     }
     const size_t smem = (size_t)((4 * C + 2 * WT) * (WT + 4) + 2 * C * (C + 4) + 2 * C + 16 * C + 32 +
                                  2 * C) * 4;
-    return launch<k_decay_bwd_gen<T, C, WT>>((int64_t)p.B * p.H * p.nseg, smem, st, p);
+    return launch<k_decay_bwd_gen<C, WT>>((int64_t)p.B * p.H * p.nseg, smem, st, p);
 }
 
 }  // namespace
@@ -754,34 +806,43 @@ cudaError_t launch_decay_sum_heads(const DecayParams &p, pdssm_dtype dt, const f
     return cudaGetLastError();
 }
 
+cudaError_t launch_decay_pad(const DecayPad *t, int count, cudaStream_t st) {
+    if (count < 1) return cudaSuccess;
+    int64_t most = 0;
+    for (int i = 0; i < count; ++i) {
+        const int64_t n = t[i].rows * ((t[i].width + 7) / 8);
+        most = n > most ? n : most;
+    }
+    const dim3 grid((unsigned)imin64((most + 255) / 256, (int64_t)kDecaySMs * 32), (unsigned)count);
+    k_decay_pad<<<grid, 256, 0, st>>>(t[0], t[count > 1 ? 1 : 0], t[count > 2 ? 2 : 0]);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_decay_unpad(const void *padded, void *out, int64_t rows, int width, cudaStream_t st) {
+    const int64_t n = (rows * width + 7) / 8;
+    k_decay_unpad<<<dim3((unsigned)imin64((n + 255) / 256, (int64_t)kDecaySMs * 32)), 256, 0, st>>>(
+        (const unsigned short *)padded, (unsigned short *)out, rows, width, ((uintptr_t)out & 15) == 0);
+    return cudaGetLastError();
+}
+
 cudaError_t launch_decay_sum_steps(const DecayParams &p, const float *part, float *g_log_a,
                                    cudaStream_t st) {
     k_decay_sum_steps<<<p.H, 1024, 0, st>>>(p, part, g_log_a);
     return cudaGetLastError();
 }
 
-cudaError_t launch_decay_fwd_gen(const DecayParams &p, pdssm_dtype dt, cudaStream_t st) {
+cudaError_t launch_decay_fwd_gen(const DecayParams &p, cudaStream_t st) {
     const int w = p.N > p.P ? p.N : p.P;
-    if (dt == PDSSM_BF16) {
-        if (w <= 32) return fwd_gen<__nv_bfloat16, 64, 32>(p, st);
-        if (w <= 64) return fwd_gen<__nv_bfloat16, 64, 64>(p, st);
-        return fwd_gen<__nv_bfloat16, 32, 128>(p, st);
-    }
-    if (w <= 32) return fwd_gen<float, 32, 32>(p, st);
-    if (w <= 64) return fwd_gen<float, 32, 64>(p, st);
-    return fwd_gen<float, 32, 128>(p, st);
+    if (w <= 32) return fwd_gen<32, 32>(p, st);
+    if (w <= 64) return fwd_gen<32, 64>(p, st);
+    return fwd_gen<32, 128>(p, st);
 }
 
-cudaError_t launch_decay_bwd_gen(const DecayParams &p, pdssm_dtype dt, cudaStream_t st) {
+cudaError_t launch_decay_bwd_gen(const DecayParams &p, cudaStream_t st) {
     const int w = p.N > p.P ? p.N : p.P;
-    if (dt == PDSSM_BF16) {
-        if (w <= 32) return bwd_gen<__nv_bfloat16, 64, 32>(p, st);
-        if (w <= 64) return bwd_gen<__nv_bfloat16, 64, 64>(p, st);
-        return bwd_gen<__nv_bfloat16, 32, 128>(p, st);
-    }
-    if (w <= 32) return bwd_gen<float, 32, 32>(p, st);
-    if (w <= 64) return bwd_gen<float, 32, 64>(p, st);
-    return bwd_gen<float, 32, 128>(p, st);
+    if (w <= 32) return bwd_gen<32, 32>(p, st);
+    if (w <= 64) return bwd_gen<32, 64>(p, st);
+    return bwd_gen<32, 128>(p, st);
 }
 
 }  // namespace pdssm

@@ -218,7 +218,7 @@ __global__ void __launch_bounds__(kTcTh, 1)
             // ---- decayed scores and y: row r of chunks i = warp / 4, + 2, ...
             const int r = tid & 127, quad = warp & 3;
             const uint32_t tlane = (uint32_t)(quad * 32) << 16;
-            __nv_bfloat16 *y = (__nv_bfloat16 *)p.y + b * p.val_b + h * p.val_h + p0;
+            __nv_bfloat16 *y = (__nv_bfloat16 *)p.y + b * p.oval_b + h * p.oval_h + p0;
             for (int i = warp >> 2; i < n; i += 2) {
                 const Decays &dc = dec[i & 1];
                 if (!wait_warp(kDecReady, i) || !wait_warp(kScFull, i)) break;
@@ -292,15 +292,15 @@ __global__ void __launch_bounds__(kTcTh, 1)
                     }
                     const int left = pw - 16 * q;               // columns left
                     if (t >= p.L || left <= 0) continue;
-                    __nv_bfloat16 *row = y + t * p.val_t + 16 * q;
-                    if (p.vec == 2 && left >= 16) {
+                    __nv_bfloat16 *row = y + t * p.oval_t + 16 * q;
+                    if (p.ovec == 2 && left > 8) {
                         asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(row),
                                      "r"(o[0]), "r"(o[1]), "r"(o[2]), "r"(o[3]), "r"(o[4]), "r"(o[5]),
                                      "r"(o[6]), "r"(o[7])
                                      : "memory");
-                    } else if (p.vec) {                         // widths in eights
+                    } else if (p.ovec) {                        // rows in eights
                         *reinterpret_cast<uint4 *>(row) = make_uint4(o[0], o[1], o[2], o[3]);
-                        if (left >= 16)
+                        if (left > 8)
                             *reinterpret_cast<uint4 *>(row + 8) = make_uint4(o[4], o[5], o[6], o[7]);
                     } else {
 #pragma unroll
@@ -696,10 +696,10 @@ __global__ void __launch_bounds__(kTcTh, 1)
         p.seg_decay[bh * p.nseg + seg] = exp2f((float)(totals[0] + totals[1]));
     if (FWD) {
         // rows of the segment's chunks behind the sequence's end
-        __nv_bfloat16 *y = (__nv_bfloat16 *)p.y + b * p.val_b + h * p.val_h + p0;
+        __nv_bfloat16 *y = (__nv_bfloat16 *)p.y + b * p.oval_b + h * p.oval_h + p0;
         const int64_t t_end = imin64((int64_t)c1 * kC, p.L);
         for (int64_t t = (int64_t)(c0 + n) * kC + warp; t < t_end; t += kTcTh / 32)
-            for (int q = lane; q < pw; q += 32) y[t * p.val_t + q] = __float2bfloat16_rn(0.f);
+            for (int q = lane; q < pw; q += 32) y[t * p.oval_t + q] = __float2bfloat16_rn(0.f);
     }
 }
 
@@ -746,7 +746,7 @@ cudaError_t fwd_tc(const DecayParams &p, cudaStream_t st) {
         e = launch_decay_join(p, p.h0, false, nullptr, st);
         if (e != cudaSuccess) return e;
     }
-    return go<STK, kFwd>(p, p.nseg <= 1, st);
+    return p.carry ? go<STK, kFwdCarry>(p, p.nseg <= 1, st) : go<STK, kFwd>(p, p.nseg <= 1, st);
 }
 
 }  // namespace
@@ -754,19 +754,11 @@ cudaError_t fwd_tc(const DecayParams &p, cudaStream_t st) {
 bool decay_tc_copies() { return tensor_map_encoder() != nullptr; }
 
 cudaError_t launch_decay_fwd_tc(const DecayParams &p, cudaStream_t st) {
-    if (!p.carry) return p.N <= 64 ? fwd_tc<true>(p, st) : fwd_tc<false>(p, st);
-    // with the adjoint's states: N, P <= 64
-    if (p.nseg > 1) {
-        cudaError_t e = go<true, kSegFwd>(p, true, st);
-        if (e != cudaSuccess) return e;
-        e = launch_decay_join(p, p.h0, false, nullptr, st);
-        if (e != cudaSuccess) return e;
-    }
-    return go<true, kFwdCarry>(p, p.nseg <= 1, st);
+    return p.N <= 64 ? fwd_tc<true>(p, st) : fwd_tc<false>(p, st);
 }
 
 cudaError_t launch_decay_seg_rev_tc(const DecayParams &p, cudaStream_t st) {
-    return go<true, kSegRev>(p, false, st);
+    return p.N <= 64 ? go<true, kSegRev>(p, false, st) : go<false, kSegRev>(p, false, st);
 }
 
 }  // namespace pdssm
