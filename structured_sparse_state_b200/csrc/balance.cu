@@ -13,133 +13,147 @@
 // the CUDA cores.
 #include "balance.cuh"
 #include "launch.cuh"
+#include "tile_mm.cuh"
 
 namespace pdssm {
 namespace {
 
-constexpr int kBalThreads = 256;
-constexpr int kBalRows = 64;            // steps per tile (four threads per step)
+constexpr int kBalThreads = 256;        // 16 x 16
+constexpr int kBalRows = 64;            // steps per tile
+constexpr int kBalCols = 64;            // entries per group: whole heads
+constexpr int kLdP = kBalCols + 2;
 
-// CTA work over one tile of kBalRows steps: u tile in shared memory (odd row
-// length), one head's weights, logits and softmax weights.
-template <int KT>
+int bal_heads(int K) { return kBalCols / K; }
+int bal_groups(int H, int K) { return (H + bal_heads(K) - 1) / bal_heads(K); }
+
+// A CTA's work on one tile of steps and one group of heads in fp32: u and W
+// rows in shared memory, the logits (then softmax weights, then gradients) of
+// 64 steps x 64 entries beside them.  Per 4 of D a thread reads eight 16-byte
+// pieces for 64 multiply-adds, so the logits run at the FFMA units' rate, not
+// at shared memory's.
 struct Tile {
-    float *su, *sW, *sp;                // [64][D|1], [KT][D|1], [64][KT + 1]
-    int ld;
+    float *su, *sW, *sp;                // [64][ld], [64][ld], [64][kLdP]
+    int *live;                          // [64]
+    int ld, Dp;
     __device__ __forceinline__ Tile(float *sm, int D) {
-        ld = D | 1;
+        Dp = (D + 7) / 8 * 8;
+        ld = Dp + 4;                    // an odd number of 16-byte pieces
         su = sm;
         sW = su + kBalRows * ld;
-        sp = sW + KT * ld;
+        sp = sW + kBalCols * ld;
+        live = reinterpret_cast<int *>(sp + kBalRows * kLdP);
     }
-    // a warp per row, its lanes along the row
-    __device__ __forceinline__ void load_u(const BalParams &p, int64_t r0) {
-        const float *u = (const float *)p.u;
-        const int lane = threadIdx.x % 32;
-#pragma unroll 4
-        for (int r = threadIdx.x / 32; r < kBalRows; r += kBalThreads / 32) {
-            const bool live = bal_live(p, r0 + r);
-            for (int q = lane; q < p.D; q += 32)
-                su[r * ld + q] = live ? u[(r0 + r) * p.D + q] : 0.f;
+    // rows of D values, on their way to shared memory; zero where on(r) is false
+    template <class ON>
+    __device__ __forceinline__ void load(float *dst, const float *src, int D, bool vec, ON on) const {
+        const uint32_t to = smem_u32(dst);
+        if (vec) {
+            const int pieces = Dp / 4;
+            for (int i = threadIdx.x; i < 64 * pieces; i += kBalThreads) {
+                const int r = i / pieces, q = 4 * (i - r * pieces);
+                const bool in = q < D && on(r);
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to + 4u * (r * ld + q)),
+                             "l"(in ? src + (int64_t)r * D + q : src), "r"(in ? 16 : 0)
+                             : "memory");
+            }
+        } else {
+            for (int i = threadIdx.x; i < 64 * Dp; i += kBalThreads) {
+                const int r = i / Dp, q = i - r * Dp;
+                const bool in = q < D && on(r);
+                asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(to + 4u * (r * ld + q)),
+                             "l"(in ? src + (int64_t)r * D + q : src), "r"(in ? 4 : 0)
+                             : "memory");
+            }
         }
     }
-    __device__ __forceinline__ void load_W(const BalParams &p, int h) {
-        const int lane = threadIdx.x % 32;
-#pragma unroll 4
-        for (int r = threadIdx.x / 32; r < KT; r += kBalThreads / 32)
-            for (int q = lane; q < p.D; q += 32)
-                sW[r * ld + q] = r < p.K ? p.W[((int64_t)h * p.K + r) * p.D + q] : 0.f;
+    __device__ __forceinline__ void load_u(const BalParams &p, int64_t r0) const {
+        if (threadIdx.x < kBalRows) live[threadIdx.x] = bal_live(p, r0 + threadIdx.x);
+        load(su, (const float *)p.u + r0 * p.D, p.D, p.vec, [&](int r) { return bal_live(p, r0 + r); });
     }
-    // sp = softmax weights of the tile's live rows, zero elsewhere; four
-    // threads per row
-    __device__ __forceinline__ void softmax(const BalParams &p, int64_t r0) {
-        const int r = threadIdx.x / 4, sub = threadIdx.x % 4;
-        constexpr int KP = KT / 4;
-        float l[KP];
-#pragma unroll
-        for (int i = 0; i < KP; ++i) l[i] = 0.f;
-#pragma unroll 8
-        for (int q = 0; q < p.D; ++q) {
-            const float uv = su[r * ld + q];
-#pragma unroll
-            for (int i = 0; i < KP; ++i) l[i] = fmaf(sW[(sub + 4 * i) * ld + q], uv, l[i]);
-        }
-        float m = -INFINITY;
-#pragma unroll
-        for (int i = 0; i < KP; ++i) {
-            l[i] = sub + 4 * i < p.K ? l[i] * p.inv_tau : -INFINITY;
-            m = fmaxf(m, l[i]);
-        }
-        m = fmaxf(m, __shfl_xor_sync(kFull, m, 1));
-        m = fmaxf(m, __shfl_xor_sync(kFull, m, 2));
-        float z = 0.f;
-#pragma unroll
-        for (int i = 0; i < KP; ++i) {
-            l[i] = sub + 4 * i < p.K ? expf(l[i] - m) : 0.f;
-            z += l[i];
-        }
-        z += __shfl_xor_sync(kFull, z, 1);
-        z += __shfl_xor_sync(kFull, z, 2);
-        const bool live = bal_live(p, r0 + r);
-        const float inv = 1.f / z;
-#pragma unroll
-        for (int i = 0; i < KP; ++i) sp[r * (KT + 1) + sub + 4 * i] = live ? l[i] * inv : 0.f;
+    __device__ __forceinline__ void load_W(const BalParams &p, int e0, int ne) const {
+        load(sW, p.W + (int64_t)e0 * p.D, p.D, p.vec, [&](int r) { return r < ne; });
     }
-    // sp = gradients of the logits, from the softmax weights (same threads)
-    __device__ __forceinline__ void grads(const BalParams &p, const float *f, float by) {
-        const int r = threadIdx.x / 4, sub = threadIdx.x % 4;
-        constexpr int KP = KT / 4;
-        float s = 0.f;
+    __device__ __forceinline__ void landed() const {
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        __syncthreads();
+    }
+    // sp = inv_tau u W^T; a barrier follows
+    __device__ __forceinline__ void logits(const BalParams &p) const {
+        const int ty = threadIdx.x / 16, tx = threadIdx.x % 16;
+        float acc[4][4];
+        zero(acc);
+        tile_mm(acc, Dp, Along<4, false>{su, ld, ty}, Along<4, false>{sW, ld, tx});
 #pragma unroll
-        for (int i = 0; i < KP; ++i) s = fmaf(sp[r * (KT + 1) + sub + 4 * i], f[sub + 4 * i], s);
-        s += __shfl_xor_sync(kFull, s, 1);
-        s += __shfl_xor_sync(kFull, s, 2);
+        for (int i = 0; i < 4; ++i)
 #pragma unroll
-        for (int i = 0; i < KP; ++i) {
-            float *v = &sp[r * (KT + 1) + sub + 4 * i];
-            *v = by * *v * (f[sub + 4 * i] - s);
+            for (int j = 0; j < 4; ++j)
+                sp[strided(ty, i) * kLdP + strided(tx, j)] = acc[i][j] * p.inv_tau;
+        __syncthreads();
+    }
+    // per (step, head): sp = softmax weights, zero behind the lengths; with GRAD
+    // the logits' gradients instead.  A barrier follows.
+    template <bool GRAD>
+    __device__ __forceinline__ void softmax(const BalParams &p, int nh, const float *f,
+                                            const float *by) const {
+        for (int i = threadIdx.x; i < kBalRows * nh; i += kBalThreads) {
+            const int r = i % kBalRows, hh = i / kBalRows;
+            float *x = sp + r * kLdP + hh * p.K;
+            const float *fh = f + hh * p.K;
+            float m = x[0];
+            for (int k = 1; k < p.K; ++k) m = fmaxf(m, x[k]);
+            float z = 0.f, s = 0.f;
+            for (int k = 0; k < p.K; ++k) {
+                const float v = expf(x[k] - m);
+                x[k] = v;
+                z += v;
+                if (GRAD) s = fmaf(v, fh[k], s);
+            }
+            const float inv = 1.f / z;
+            for (int k = 0; k < p.K; ++k)
+                x[k] = !live[r] ? 0.f : GRAD ? by[hh] * (x[k] * inv) * (fh[k] - s * inv) : x[k] * inv;
         }
+        __syncthreads();
     }
 };
 
-template <int KT>
-constexpr size_t bal_smem(int D) {
-    return (size_t)((kBalRows + KT) * (D | 1) + kBalRows * (KT + 1)) * 4;
+size_t bal_smem(int D) {
+    return (size_t)((kBalRows + kBalCols) * ((D + 7) / 8 * 8 + 4) + kBalRows * kLdP + kBalRows) * 4;
 }
 
-// Sums of p and counts over one slice of the steps of one head.
-template <int KT>
+// Sums of p and counts over one slice of the steps of one group of heads.
 __global__ void __launch_bounds__(kBalThreads) k_bal_sums(BalParams p) {
     extern __shared__ float sm[];
-    __shared__ int scount[KT];
-    const int h = blockIdx.x % p.H, slice = blockIdx.x / p.H;
-    Tile<KT> t(sm, p.D);
-    t.load_W(p, h);
-    if (threadIdx.x < KT) scount[threadIdx.x] = 0;
-    float sum = 0.f;                    // column threadIdx.x % KT, rows threadIdx.x / KT ...
-    constexpr int RG = kBalThreads / KT;
+    __shared__ int scount[kBalCols];
+    const Tile t(sm, p.D);
+    const int group = blockIdx.x % p.groups, slice = blockIdx.x / p.groups;
+    const int h0 = group * p.heads, nh = min(p.heads, p.H - h0), e0 = h0 * p.K, ne = nh * p.K;
+    const int col = threadIdx.x % kBalCols, rg = threadIdx.x / kBalCols;
+    t.load_W(p, e0, ne);
+    if (threadIdx.x < kBalCols) scount[threadIdx.x] = 0;
+    float sum = 0.f;                    // column col, a quarter of the rows
     for (int64_t r0 = (int64_t)slice * kBalRows; r0 < p.rows; r0 += (int64_t)p.slices * kBalRows) {
         __syncthreads();
         t.load_u(p, r0);
-        __syncthreads();
-        t.softmax(p, r0);
-        if (threadIdx.x < kBalRows && bal_live(p, r0 + threadIdx.x)) {
-            const int64_t r = r0 + threadIdx.x, b = r / p.L;
-            const int kk = p.k[(b * p.H + h) * p.L + r % p.L];
-            if (kk >= 0 && kk < p.K) atomicAdd(&scount[kk], 1);     // integers: any order
+        t.landed();
+        t.logits(p);
+        t.softmax<false>(p, nh, nullptr, nullptr);
+        for (int i = threadIdx.x; i < kBalRows * nh; i += kBalThreads) {
+            const int hh = i / kBalRows;
+            const uint32_t r = (uint32_t)r0 + i % kBalRows;
+            if (!t.live[i % kBalRows]) continue;
+            const uint32_t b = r / (uint32_t)p.L;
+            const int kk = p.k[((int64_t)b * p.H + h0 + hh) * p.L + (r - b * (uint32_t)p.L)];
+            if (kk >= 0 && kk < p.K) atomicAdd(&scount[hh * p.K + kk], 1);      // integers: any order
         }
-        __syncthreads();
-        for (int r = threadIdx.x / KT; r < kBalRows; r += RG)
-            sum += t.sp[r * (KT + 1) + threadIdx.x % KT];
+#pragma unroll
+        for (int r = 0; r < kBalRows / 4; ++r) sum += t.sp[(4 * r + rg) * kLdP + col];
     }
-    __syncthreads();
+    t.landed();                         // also where there was no tile
     t.sp[threadIdx.x] = sum;
     __syncthreads();
-    if (threadIdx.x < p.K) {
-        float s = 0.f;
-        for (int g = 0; g < RG; ++g) s += t.sp[g * KT + threadIdx.x];
-        const int64_t at = ((int64_t)slice * p.H + h) * p.K + threadIdx.x;
-        p.part[at] = s;
+    if (threadIdx.x < ne) {
+        const int64_t at = (int64_t)slice * p.H * p.K + e0 + threadIdx.x;
+        p.part[at] = (t.sp[col] + t.sp[64 + col]) + (t.sp[128 + col] + t.sp[192 + col]);
         p.part_n[at] = scount[threadIdx.x];
     }
 }
@@ -167,62 +181,56 @@ __global__ void k_bal_loss(BalParams p, float *loss, int32_t *counts, float *pro
     if (k == 0) loss[h] = (float)(v * p.K);
 }
 
-// g_u of one tile of steps over heads h0 .. h1 - 1: thread (ty, tx) owns rows
-// ty + 16 i and columns tx + 16 j.  A head takes about 10 us, most of it the
-// latency of its phases, so where the tiles do not fill the GPU the heads are
-// split over CTAs too, whose sums k_bal_gu_sum adds in order (one step, 16
-// heads of 32 entries: GUSPLIT us for the whole loss and its gradients, by one
-// CTA 190).
-template <int KT>
-__global__ void __launch_bounds__(kBalThreads) k_bal_gu(BalParams p) {
-    extern __shared__ float sm[];
-    __shared__ float f[KT];
-    Tile<KT> t(sm, p.D);
-    const int64_t r0 = (int64_t)(blockIdx.x / p.hslices) * kBalRows;
-    const int hs = blockIdx.x % p.hslices;
-    const int h0 = (int)((int64_t)p.H * hs / p.hslices), h1 = (int)((int64_t)p.H * (hs + 1) / p.hslices);
-    const int ty = threadIdx.x / 16, tx = threadIdx.x % 16;
+// what the gradients of a group need: counts / T, and per head the factor
+__device__ __forceinline__ void bal_factors(const BalParams &p, int h0, int nh, float *f, float *by) {
     const int64_t steps = bal_steps(p);
     const float inv = steps > 0 ? 1.f / (float)steps : 0.f;
-    float acc[4][kBalMaxD / 16];
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < kBalMaxD / 16; ++j) acc[i][j] = 0.f;
+    const int i = threadIdx.x;
+    if (i < nh * p.K) f[i] = (float)p.counts[h0 * p.K + i] * inv;
+    if (i < nh) by[i] = p.g_loss[h0 + i] * ((float)p.K * p.inv_tau) * inv;
+}
+
+// g_u of one tile of steps over a slice of the groups: thread (ty, tx) owns rows
+// ty + 16 i and pairs of columns, D <= DT.  A group takes about 10 us, so
+// where the tiles do not fill the GPU the groups are split over CTAs too, and
+// k_bal_gu_sum adds their sums in order.
+template <int DT>
+__global__ void __launch_bounds__(kBalThreads) k_bal_gu(BalParams p) {
+    extern __shared__ float sm[];
+    __shared__ float f[kBalCols], by[kBalCols];
+    const Tile t(sm, p.D);
+    const int gs = blockIdx.x % p.gslices;
+    const int64_t r0 = (int64_t)(blockIdx.x / p.gslices) * kBalRows;
+    const int ty = threadIdx.x / 16, tx = threadIdx.x % 16;
+    float acc[4][DT / 16];
+    zero(acc);
     t.load_u(p, r0);
-    for (int h = h0; h < h1; ++h) {
+    for (int group = gs; group < p.groups; group += p.gslices) {
+        const int h0 = group * p.heads, nh = min(p.heads, p.H - h0);
         __syncthreads();
-        t.load_W(p, h);
-        if (threadIdx.x < KT)
-            f[threadIdx.x] = threadIdx.x < p.K ? (float)p.counts[h * p.K + threadIdx.x] * inv : 0.f;
-        __syncthreads();
-        t.softmax(p, r0);
-        t.grads(p, f, p.g_loss[h] * ((float)p.K * p.inv_tau) * inv);
-        __syncthreads();
-        for (int k = 0; k < KT; ++k) {
-            float g[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) g[i] = t.sp[(ty + 16 * i) * (KT + 1) + k];
-#pragma unroll
-            for (int j = 0; j < kBalMaxD / 16; ++j) {
-                const int q = tx + 16 * j;
-                if (q >= p.D) break;
-                const float w = t.sW[k * t.ld + q];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) acc[i][j] = fmaf(g[i], w, acc[i][j]);
-            }
-        }
+        t.load_W(p, h0 * p.K, nh * p.K);
+        bal_factors(p, h0, nh, f, by);
+        t.landed();
+        t.logits(p);
+        t.softmax<true>(p, nh, f, by);
+        // entries behind the group's have zero weights, and logits that are zero
+        tile_mm(acc, kBalCols, Along2<4>{t.sp, kLdP, ty}, Across<DT / 16>{t.sW, t.ld, tx});
     }
-    float *gu = p.hslices > 1 ? p.part + hs * p.rows * p.D : (float *)p.g_u;
+    float *gu = p.gslices > 1 ? p.part + gs * p.rows * p.D : (float *)p.g_u;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const int64_t r = r0 + ty + 16 * i;
+        const int64_t r = r0 + strided(ty, i);
         if (r >= p.rows) continue;
 #pragma unroll
-        for (int j = 0; j < kBalMaxD / 16; ++j) {
-            const int q = tx + 16 * j;
-            if (q >= p.D) break;
-            gu[r * p.D + q] = acc[i][j];
+        for (int j = 0; j < DT / 16; j += 2) {
+            const int q = pairs(tx, j);
+            float *at = gu + r * p.D + q;
+            if (p.vec) {
+                if (q < p.D) *reinterpret_cast<float2 *>(at) = make_float2(acc[i][j], acc[i][j + 1]);
+            } else {
+                if (q < p.D) at[0] = acc[i][j];
+                if (q + 1 < p.D) at[1] = acc[i][j + 1];
+            }
         }
     }
 }
@@ -232,58 +240,42 @@ __global__ void k_bal_gu_sum(BalParams p) {
     for (int64_t e = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; e < n;
          e += (int64_t)gridDim.x * blockDim.x) {
         float s = 0.f;
-        for (int q = 0; q < p.hslices; ++q) s += p.part[q * n + e];
+        for (int q = 0; q < p.gslices; ++q) s += p.part[q * n + e];
         ((float *)p.g_u)[e] = s;
     }
 }
 
-// g_W of one head over one slice of the steps
-template <int KT>
+// g_W of one group over one slice of the steps
+template <int DT>
 __global__ void __launch_bounds__(kBalThreads) k_bal_gw(BalParams p) {
     extern __shared__ float sm[];
-    __shared__ float f[KT];
-    Tile<KT> t(sm, p.D);
-    const int h = blockIdx.x % p.H, slice = blockIdx.x / p.H;
-    const int64_t steps = bal_steps(p);
-    const float inv = steps > 0 ? 1.f / (float)steps : 0.f;
-    constexpr int KP = KT / 8;          // thread (kr, c): entries kr + 8 i, columns c + 32 j
-    const int kr = threadIdx.x / 32, c = threadIdx.x % 32;
-    float acc[KP][kBalMaxD / 32];
-#pragma unroll
-    for (int i = 0; i < KP; ++i)
-#pragma unroll
-        for (int j = 0; j < kBalMaxD / 32; ++j) acc[i][j] = 0.f;
-    t.load_W(p, h);
-    if (threadIdx.x < KT)
-        f[threadIdx.x] = threadIdx.x < p.K ? (float)p.counts[h * p.K + threadIdx.x] * inv : 0.f;
-    const float by = p.g_loss[h] * ((float)p.K * p.inv_tau) * inv;
+    __shared__ float f[kBalCols], by[kBalCols];
+    const Tile t(sm, p.D);
+    const int group = blockIdx.x % p.groups, slice = blockIdx.x / p.groups;
+    const int h0 = group * p.heads, nh = min(p.heads, p.H - h0), ne = nh * p.K;
+    const int ty = threadIdx.x / 16, tx = threadIdx.x % 16;
+    float acc[4][DT / 16];
+    zero(acc);
+    t.load_W(p, h0 * p.K, ne);
+    bal_factors(p, h0, nh, f, by);
     for (int64_t r0 = (int64_t)slice * kBalRows; r0 < p.rows; r0 += (int64_t)p.slices * kBalRows) {
         __syncthreads();
         t.load_u(p, r0);
-        __syncthreads();
-        t.softmax(p, r0);
-        t.grads(p, f, by);
-        __syncthreads();
-        for (int r = 0; r < kBalRows; ++r) {
-            float g[KP];
-#pragma unroll
-            for (int i = 0; i < KP; ++i) g[i] = t.sp[r * (KT + 1) + kr + 8 * i];
-#pragma unroll
-            for (int j = 0; j < kBalMaxD / 32; ++j) {
-                if (c + 32 * j >= p.D) break;
-                const float uv = t.su[r * t.ld + c + 32 * j];
-#pragma unroll
-                for (int i = 0; i < KP; ++i) acc[i][j] = fmaf(g[i], uv, acc[i][j]);
-            }
-        }
+        t.landed();
+        t.logits(p);
+        t.softmax<true>(p, nh, f, by);
+        tile_mm(acc, kBalRows, Across<4>{t.sp, kLdP, ty}, Across<DT / 16>{t.su, t.ld, tx});
     }
+    t.landed();                         // also where there was no tile
 #pragma unroll
-    for (int i = 0; i < KP; ++i)
+    for (int i = 0; i < 4; ++i) {
+        const int e = pairs(ty, i);
+        if (e >= ne) continue;
+        float *out = p.part + ((int64_t)slice * p.H * p.K + h0 * p.K + e) * p.D;
 #pragma unroll
-        for (int j = 0; j < kBalMaxD / 32; ++j)
-            if (kr + 8 * i < p.K && c + 32 * j < p.D)
-                p.part[(((int64_t)slice * p.H + h) * p.K + kr + 8 * i) * p.D + c + 32 * j] =
-                    acc[i][j];
+        for (int j = 0; j < DT / 16; ++j)
+            if (pairs(tx, j) < p.D) out[pairs(tx, j)] = acc[i][j];
+    }
 }
 
 // g_W: the slices' sums in order
@@ -296,48 +288,45 @@ __global__ void k_bal_gw_sum(BalParams p, float *g_W) {
     g_W[e] = s;
 }
 
-// slices of the steps per head: fill the GPU, at least one tile each
-int bal_slices(int64_t rows, int64_t H) {
+// slices of the steps per group: two CTAs per SM, at least one tile each
+int bal_slices(int64_t rows, int groups) {
     const int64_t tiles = (rows + kBalRows - 1) / kBalRows;
-    int64_t n = (148 * 4 + H - 1) / H;
+    int64_t n = (148 * 2 + groups - 1) / groups;
     if (n > tiles) n = tiles;
     return (int)(n < 1 ? 1 : n);
 }
 
-// slices of the heads for fp32 g_u: as many as the GPU takes beside the tiles
-int bal_hslices(int64_t rows, int64_t H) {
+// slices of the groups for g_u: as many as the GPU takes beside the tiles
+int bal_gslices(int64_t rows, int groups) {
     const int64_t tiles = (rows + kBalRows - 1) / kBalRows;
     const int64_t n = tiles > 0 ? 148 / tiles : 1;
-    return (int)(n < 1 ? 1 : n > H ? H : n);
+    return (int)(n < 1 ? 1 : n > groups ? groups : n);
 }
 
 template <void (*KERN)(BalParams)>
-cudaError_t launch(int64_t grid, size_t smem, cudaStream_t st, const BalParams &p) {
+cudaError_t launch(int64_t grid, cudaStream_t st, const BalParams &p) {
     static std::atomic<int> set[kLimitDevices];
-    const cudaError_t e = allow_smem((const void *)KERN, (int)smem, set);
+    const cudaError_t e = allow_smem((const void *)KERN, (int)bal_smem(kBalMaxD), set);
     if (e != cudaSuccess) return e;
-    KERN<<<dim3((unsigned)grid), kBalThreads, smem, st>>>(p);
+    KERN<<<dim3((unsigned)grid), kBalThreads, bal_smem(p.D), st>>>(p);
     return cudaGetLastError();
 }
 
-template <int KT>
-cudaError_t run(const BalParams &p, int what, cudaStream_t st) {
-    const size_t smem = bal_smem<KT>(p.D);
-    if (what == 0) return launch<k_bal_sums<KT>>((int64_t)p.H * p.slices, smem, st, p);
-    if (what == 1) {
-        const int64_t tiles = (p.rows + kBalRows - 1) / kBalRows;
-        const cudaError_t e = launch<k_bal_gu<KT>>(tiles * p.hslices, smem, st, p);
-        if (e != cudaSuccess || p.hslices == 1) return e;
-        k_bal_gu_sum<<<(unsigned)((p.rows * p.D + 255) / 256), 256, 0, st>>>(p);
-        return cudaGetLastError();
-    }
-    return launch<k_bal_gw<KT>>((int64_t)p.H * p.slices, smem, st, p);
+template <int DT>
+cudaError_t run_grads(const BalParams &p, int what, cudaStream_t st) {
+    if (what == 2) return launch<k_bal_gw<DT>>((int64_t)p.groups * p.slices, st, p);
+    const int64_t tiles = (p.rows + kBalRows - 1) / kBalRows;
+    const cudaError_t e = launch<k_bal_gu<DT>>(tiles * p.gslices, st, p);
+    if (e != cudaSuccess || p.gslices == 1) return e;
+    k_bal_gu_sum<<<(unsigned)((p.rows * p.D + 255) / 256), 256, 0, st>>>(p);
+    return cudaGetLastError();
 }
 
-cudaError_t run_k(const BalParams &p, int what, cudaStream_t st) {
-    if (p.K <= 8) return run<8>(p, what, st);
-    if (p.K <= 16) return run<16>(p, what, st);
-    return run<32>(p, what, st);
+cudaError_t run_f32(const BalParams &p, int what, cudaStream_t st) {
+    if (what == 0) return launch<k_bal_sums>((int64_t)p.groups * p.slices, st, p);
+    if (p.D <= 64) return run_grads<64>(p, what, st);
+    if (p.D <= 128) return run_grads<128>(p, what, st);
+    return run_grads<256>(p, what, st);
 }
 
 bool aligned(const void *p, size_t a) { return ((uintptr_t)p % a) == 0; }
@@ -362,9 +351,9 @@ size_t bal_partials(const pdssm_dims &d, int slices) {
 
 size_t bal_scratch(const pdssm_dims &d) {
     const BalTcPlan pl = bal_tc_plan(d);
-    const size_t a = bal_partials(d, bal_slices(d.B * d.L, d.H));
+    const size_t a = bal_partials(d, bal_slices(d.B * d.L, bal_groups((int)d.H, (int)d.K)));
     const size_t b = bal_partials(d, pl.slices) + bal_tc_extra(pl);
-    const int hs = bal_hslices(d.B * d.L, d.H);
+    const int hs = bal_gslices(d.B * d.L, bal_groups((int)d.H, (int)d.K));
     const size_t c = hs > 1 ? (size_t)hs * (size_t)(d.B * d.L * d.D_in) * 4 : 0;
     return a > b ? (a > c ? a : c) : (b > c ? b : c);
 }
@@ -386,8 +375,11 @@ pdssm_status bal_common(const pdssm_dims *d, const void *u, pdssm_dtype dt, cons
     q.B = (int)d->B; q.H = (int)d->H; q.K = (int)d->K; q.D = (int)d->D_in;
     q.L = d->L; q.rows = d->B * d->L;
     q.u = u; q.W = W; q.lengths = lengths; q.inv_tau = inv_tau;
-    q.slices = dt == PDSSM_BF16 ? bal_tc_plan(*d).slices : bal_slices(q.rows, d->H);
-    q.hslices = bal_hslices(q.rows, d->H);
+    q.slices = dt == PDSSM_BF16 ? bal_tc_plan(*d).slices : bal_slices(q.rows, bal_groups(q.H, q.K));
+    q.heads = bal_heads(q.K);
+    q.groups = bal_groups(q.H, q.K);
+    q.gslices = bal_gslices(q.rows, q.groups);
+    q.vec = q.D % 4 == 0 && aligned(u, 16) && aligned(W, 16);
     q.part = (float *)scratch;
     q.part_n = (int32_t *)(q.part + (int64_t)q.slices * q.H * q.K);
     *p = q;
@@ -398,7 +390,7 @@ pdssm_status bal_common(const pdssm_dims *d, const void *u, pdssm_dtype dt, cons
 // behind the partial sums in scratch)
 cudaError_t run_any(const pdssm_dims &d, const BalParams &p, pdssm_dtype dt, int what,
                     cudaStream_t st) {
-    if (dt != PDSSM_BF16) return run_k(p, what, st);
+    if (dt != PDSSM_BF16) return run_f32(p, what, st);
     const BalTcPlan pl = bal_tc_plan(d);
     unsigned char *parts = reinterpret_cast<unsigned char *>(p.part) + bal_partials(d, pl.slices);
     if (what == 0 || what == 1 || !p.g_u) {
@@ -451,6 +443,7 @@ pdssm_status pdssm_select_balance_bwd(const pdssm_dims *dims, const void *u, pds
     p.counts = counts;
     p.g_loss = g_loss;
     p.g_u = g_u;
+    p.vec = p.vec && aligned(g_u, 16);
     cudaStream_t s = (cudaStream_t)stream;
     cudaError_t e;
     if (g_u && p.rows > 0) {

@@ -18,7 +18,9 @@ struct BalParams {
     const int32_t *counts;
     const float *g_loss;
     void *g_u;
-    int slices, hslices;                // of the steps; of the heads (fp32 g_u)
+    int slices;                         // of the steps
+    int heads, groups, gslices, vec;    // fp32: heads per group, groups, their slices for g_u,
+                                        // 16-byte accesses
     float *part;                        // per slice: sums of p [H][K], of g_W [H][K][D], or of
                                         // g_u [rows][D]
     int32_t *part_n;                    // per slice: counts [H][K]
