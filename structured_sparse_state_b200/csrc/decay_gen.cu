@@ -14,6 +14,7 @@ namespace pdssm {
 namespace {
 
 constexpr int kThreads = 256;
+constexpr int kC = 32;                  // steps of a chunk
 
 // Rows t0..t0+C-1 of a [step][width] tensor on their way to shared rows of
 // WT + 4 floats; zero behind `len` and behind the width.  A chunk's rows are
@@ -76,23 +77,23 @@ struct Steps {
 // The state alone over one segment from zero.  Forward (REV = false): rows u
 // = b, v = x, weights e^{G_C - G_t}, chunks in order.  Reverse: u = c, v =
 // g_y, weights e^{G_t}, chunks in reverse.
-template <int C, int WT, bool REV>
+template <int C, int NT, int PT, bool REV>
 __global__ void __launch_bounds__(kThreads) k_decay_seg_gen(DecayParams p) {
     extern __shared__ float sm[];
-    constexpr int LD = WT + 4;
-    float *su = sm, *sv = su + C * LD;
-    float2 *sG = reinterpret_cast<float2 *>(sv + C * LD);
+    constexpr int LN = NT + 4, LP = PT + 4, TN = NT / 16, TP = PT / 16;
+    float *su = sm, *sv = su + C * LN;
+    float2 *sG = reinterpret_cast<float2 *>(sv + C * LP);
     const int seg = blockIdx.x % p.nseg;
     const Head hd = head_of(p, blockIdx.x / p.nseg);
     const int ty = threadIdx.x / 16, tx = threadIdx.x % 16;
     const float *u = (const float *)(REV ? p.c : p.b) + hd.b * p.key_b + (hd.h / p.rep) * p.key_h;
     const float *v = (const float *)(REV ? p.g_y : p.x) + hd.b * p.val_b + hd.h * p.val_h;
-    constexpr int TN = WT / 16;
-    float S[TN][TN];
+    float S[TN][TP];
     zero(S);
     double total = 0.0;
     const int c0 = seg * p.seg_chunks, c1 = min(c0 + p.seg_chunks, p.nchunks);
-    Rows<C, WT> ru, rv;
+    Rows<C, NT> ru;
+    Rows<C, PT> rv;
     Steps<C> rl;
     auto fetch = [&](int i) {
         const int64_t t0 = i < c1 ? (int64_t)(REV ? c1 - 1 - (i - c0) : i) * C : hd.len;
@@ -114,38 +115,38 @@ __global__ void __launch_bounds__(kThreads) k_decay_seg_gen(DecayParams p) {
         __syncthreads();
         const float2 end = sG[C - 1];
         total += (double)end.x + (double)end.y;
-        for (int e = threadIdx.x; e < C * WT; e += kThreads) {
-            const int t = e / WT;
+        for (int e = threadIdx.x; e < C * NT; e += kThreads) {
+            const int t = e / NT;
             const float w = REV ? decay_from_start(sG[t]) : decay_between(end, sG[t]);
-            su[t * LD + e % WT] *= w;
+            su[t * LN + e % NT] *= w;
         }
         __syncthreads();
         const float a = decay_from_start(end);
 #pragma unroll
         for (int m = 0; m < TN; ++m)
 #pragma unroll
-            for (int n = 0; n < TN; ++n) S[m][n] *= a;
-        tile_mm(S, C, Across<TN>{su, LD, ty}, Across<TN>{sv, LD, tx});
+            for (int n = 0; n < TP; ++n) S[m][n] *= a;
+        tile_mm(S, C, Across<TN>{su, LN, ty}, Across<TP>{sv, LP, tx});
         __syncthreads();
     }
     float *out = p.seg_state + ((int64_t)hd.bh * p.nseg + seg) * p.N * p.P;
 #pragma unroll
     for (int m = 0; m < TN; ++m)
 #pragma unroll
-        for (int n = 0; n < TN; ++n) {
+        for (int n = 0; n < TP; ++n) {
             const int r = pairs(ty, m), q = pairs(tx, n);
             if (r < p.N && q < p.P) out[r * p.P + q] = S[m][n];
         }
     if (threadIdx.x == 0) p.seg_decay[(int64_t)hd.bh * p.nseg + seg] = exp2f((float)total);
 }
 
-template <int C, int WT>
+template <int C, int NT, int PT>
 __global__ void __launch_bounds__(kThreads) k_decay_fwd_gen(DecayParams p) {
-    constexpr int PS = WT < 64 ? WT : 64;
-    constexpr int LD = WT + 4, LP = PS + 4, LC = C + 4;
-    constexpr int TM = C / 16, TN = WT / 16, TP = PS / 16;
+    constexpr int PS = PT < 64 ? PT : 64;
+    constexpr int LD = NT + 4, LP = PS + 4, LC = C + 4;
+    constexpr int TM = C / 16, TN = NT / 16, TP = PS / 16;
     extern __shared__ float sm[];
-    float *sc = sm, *sb = sc + C * LD, *sx = sb + C * LD, *sS = sx + C * LP, *sP = sS + WT * LP;
+    float *sc = sm, *sb = sc + C * LD, *sx = sb + C * LD, *sS = sx + C * LP, *sP = sS + NT * LP;
     float2 *sG = reinterpret_cast<float2 *>(sP + C * LC);
     const int seg = blockIdx.x % p.nseg;
     const int ps = (blockIdx.x / p.nseg) % p.pslices;
@@ -163,12 +164,12 @@ __global__ void __launch_bounds__(kThreads) k_decay_fwd_gen(DecayParams p) {
     // the segment's incoming state
     const float *in = p.nseg > 1 ? p.seg_state + ((int64_t)hd.bh * p.nseg + seg) * np
                                  : (p.h0 ? p.h0 + (int64_t)hd.bh * np : nullptr);
-    for (int e = threadIdx.x; e < WT * PS; e += kThreads) {
+    for (int e = threadIdx.x; e < NT * PS; e += kThreads) {
         const int n = e / PS, q = e % PS;
         sS[n * LP + q] = (in && n < p.N && q < pw) ? in[(int64_t)n * p.P + p0 + q] : 0.f;
     }
     const int c0 = seg * p.seg_chunks, c1 = min(c0 + p.seg_chunks, p.nchunks);
-    Rows<C, WT> rc, rb;
+    Rows<C, NT> rc, rb;
     Rows<C, PS> rx;
     Steps<C> rl;
     auto fetch = [&](int i) {
@@ -191,7 +192,7 @@ __global__ void __launch_bounds__(kThreads) k_decay_fwd_gen(DecayParams p) {
         }
         if (p.carry && i > 0) {
             float *out = p.carry + ((int64_t)hd.bh * p.nchunks + i) * np + p0;
-            for (int e = threadIdx.x; e < WT * PS; e += kThreads) {
+            for (int e = threadIdx.x; e < NT * PS; e += kThreads) {
                 const int n = e / PS, q = e % PS;
                 if (n < p.N && q < pw) out[(int64_t)n * p.P + q] = sS[n * LP + q];
             }
@@ -208,7 +209,7 @@ __global__ void __launch_bounds__(kThreads) k_decay_fwd_gen(DecayParams p) {
         {
             float acc[TM][TM];
             zero(acc);
-            tile_mm(acc, WT, Along<TM, true>{sc, LD, ty}, Along<TM, false>{sb, LD, tx});
+            tile_mm(acc, NT, Along<TM, true>{sc, LD, ty}, Along<TM, false>{sb, LD, tx});
 #pragma unroll
             for (int m = 0; m < TM; ++m)
 #pragma unroll
@@ -221,7 +222,7 @@ __global__ void __launch_bounds__(kThreads) k_decay_fwd_gen(DecayParams p) {
         {
             float acc[TM][TP];
             zero(acc);
-            tile_mm(acc, WT, Along<TM, true>{sc, LD, ty}, Across<TP>{sS, LP, tx});
+            tile_mm(acc, NT, Along<TM, true>{sc, LD, ty}, Across<TP>{sS, LP, tx});
 #pragma unroll
             for (int m = 0; m < TM; ++m) {
                 const float e = decay_from_start(sG[pairs(ty, m)]);
@@ -238,8 +239,8 @@ __global__ void __launch_bounds__(kThreads) k_decay_fwd_gen(DecayParams p) {
                         y[t * p.val_t + pairs(tx, n)] = t < hd.len ? acc[m][n] : 0.f;
             }
         }
-        for (int e = threadIdx.x; e < C * WT; e += kThreads)
-            sb[(e / WT) * LD + e % WT] *= decay_between(end, sG[e / WT]);
+        for (int e = threadIdx.x; e < C * NT; e += kThreads)
+            sb[(e / NT) * LD + e % NT] *= decay_between(end, sG[e / NT]);
         __syncthreads();
         {
             float acc[TN][TP];
@@ -258,7 +259,7 @@ __global__ void __launch_bounds__(kThreads) k_decay_fwd_gen(DecayParams p) {
     __syncthreads();
     if (p.h_last && seg == p.nseg - 1) {
         float *out = p.h_last + (int64_t)hd.bh * np + p0;
-        for (int e = threadIdx.x; e < WT * PS; e += kThreads) {
+        for (int e = threadIdx.x; e < NT * PS; e += kThreads) {
             const int n = e / PS, q = e % PS;
             if (n < p.N && q < pw) out[(int64_t)n * p.P + q] = sS[n * LP + q];
         }
@@ -266,12 +267,12 @@ __global__ void __launch_bounds__(kThreads) k_decay_fwd_gen(DecayParams p) {
 }
 
 // Adjoint of one segment's chunks in reverse; sR is dl/dS at the chunk's end.
-template <int C, int WT>
+template <int C, int NT, int PT>
 __global__ void __launch_bounds__(kThreads) k_decay_bwd_gen(DecayParams p) {
-    constexpr int LD = WT + 4, LC = C + 4, TM = C / 16, TN = WT / 16;
+    constexpr int LN = NT + 4, LP = PT + 4, LC = C + 4, TM = C / 16, TN = NT / 16, TP = PT / 16;
     extern __shared__ float sm[];
-    float *sc = sm, *sb = sc + C * LD, *sx = sb + C * LD, *sg = sx + C * LD, *sR = sg + C * LD;
-    float *sS = sR + WT * LD, *sP = sS + WT * LD, *sQ = sP + C * LC;
+    float *sc = sm, *sb = sc + C * LN, *sx = sb + C * LN, *sg = sx + C * LP, *sR = sg + C * LP;
+    float *sS = sR + NT * LP, *sP = sS + NT * LP, *sQ = sP + C * LC;
     float *sfrom = sQ + C * LC, *sto = sfrom + C;       // per step: pairs' and states' sums
     float *sred = sto + C;                              // 16 x C + 32
     float2 *sG = reinterpret_cast<float2 *>(sred + 16 * C + 32);
@@ -291,12 +292,13 @@ __global__ void __launch_bounds__(kThreads) k_decay_bwd_gen(DecayParams p) {
 
     const float *in = p.nseg > 1 ? p.seg_state + ((int64_t)hd.bh * p.nseg + seg) * np
                                  : (p.g_hlast ? p.g_hlast + (int64_t)hd.bh * np : nullptr);
-    for (int e = threadIdx.x; e < WT * WT; e += kThreads) {
-        const int n = e / WT, q = e % WT;
-        sR[n * LD + q] = (in && n < p.N && q < p.P) ? in[(int64_t)n * p.P + q] : 0.f;
+    for (int e = threadIdx.x; e < NT * PT; e += kThreads) {
+        const int n = e / PT, q = e % PT;
+        sR[n * LP + q] = (in && n < p.N && q < p.P) ? in[(int64_t)n * p.P + q] : 0.f;
     }
     const int c0 = seg * p.seg_chunks, c1 = min(c0 + p.seg_chunks, p.nchunks);
-    Rows<C, WT> rc, rb, rx, rg;
+    Rows<C, NT> rc, rb;
+    Rows<C, PT> rx, rg;
     Steps<C> rl;
     auto fetch = [&](int i) {
         const int64_t t0 = i >= c0 ? (int64_t)i * C : hd.len;
@@ -306,7 +308,7 @@ __global__ void __launch_bounds__(kThreads) k_decay_bwd_gen(DecayParams p) {
         rg.fetch(gy, p.val_t, p.P, t0, hd.len);
         rl.fetch(p, hd, t0);
     };
-    constexpr bool kAhead = WT <= 64;       // wider rows would not fit the registers
+    constexpr bool kAhead = NT + PT <= 192; // wider rows would not fit the registers
     if (kAhead) fetch(c1 - 1);
     for (int i = c1 - 1; i >= c0; --i) {
         const int64_t t0 = (int64_t)i * C;
@@ -321,17 +323,18 @@ __global__ void __launch_bounds__(kThreads) k_decay_bwd_gen(DecayParams p) {
             const float *S0 = i > 0 ? p.carry + ((int64_t)hd.bh * p.nchunks + i) * np
                                     : (p.h0 ? p.h0 + (int64_t)hd.bh * np : nullptr);
 #pragma unroll 4
-            for (int e = threadIdx.x; e < WT * WT; e += kThreads) {
-                const int n = e / WT, q = e % WT;
-                sS[n * LD + q] = S0 && n < p.N && q < p.P ? S0[(int64_t)n * p.P + q] : 0.f;
+            for (int e = threadIdx.x; e < NT * PT; e += kThreads) {
+                const int n = e / PT, q = e % PT;
+                sS[n * LP + q] = S0 && n < p.N && q < p.P ? S0[(int64_t)n * p.P + q] : 0.f;
             }
             rl.sums(sG);
         }
         if (kAhead) fetch(i - 1);
         if (!live) {                    // behind the end: zero gradients, the state's stays
-            for (int e = threadIdx.x; e < C * WT; e += kThreads) {
-                const int64_t t = t0 + e / WT;
-                const int q = e % WT;
+            constexpr int W = NT > PT ? NT : PT;
+            for (int e = threadIdx.x; e < C * W; e += kThreads) {
+                const int64_t t = t0 + e / W;
+                const int q = e % W;
                 if (t >= p.L) continue;
                 if (q < p.P) gx[t * p.val_t + q] = 0.f;
                 if (q < p.N) {
@@ -355,8 +358,8 @@ __global__ void __launch_bounds__(kThreads) k_decay_bwd_gen(DecayParams p) {
             float s[TM][TM], v[TM][TM];
             zero(s);
             zero(v);
-            tile_mm(s, WT, Along<TM, true>{sc, LD, ty}, Along<TM, false>{sb, LD, tx});
-            tile_mm(v, WT, Along<TM, true>{sg, LD, ty}, Along<TM, false>{sx, LD, tx});
+            tile_mm(s, NT, Along<TM, true>{sc, LN, ty}, Along<TM, false>{sb, LN, tx});
+            tile_mm(v, PT, Along<TM, true>{sg, LP, ty}, Along<TM, false>{sx, LP, tx});
             float col[TM];
 #pragma unroll
             for (int n = 0; n < TM; ++n) col[n] = 0.f;
@@ -394,7 +397,7 @@ __global__ void __launch_bounds__(kThreads) k_decay_bwd_gen(DecayParams p) {
         {
             float acc[TM][TN];
             zero(acc);
-            tile_mm(acc, WT, Along<TM, true>{sg, LD, ty}, Along<TN, true>{sS, LD, tx});
+            tile_mm(acc, PT, Along<TM, true>{sg, LP, ty}, Along<TN, true>{sS, LP, tx});
 #pragma unroll
             for (int m = 0; m < TM; ++m) {
                 const float e = decay_from_start(sG[pairs(ty, m)]);
@@ -402,10 +405,10 @@ __global__ void __launch_bounds__(kThreads) k_decay_bwd_gen(DecayParams p) {
 #pragma unroll
                 for (int n = 0; n < TN; ++n) {
                     acc[m][n] *= e;
-                    uc[m] = fmaf(acc[m][n], sc[pairs(ty, m) * LD + pairs(tx, n)], uc[m]);
+                    uc[m] = fmaf(acc[m][n], sc[pairs(ty, m) * LN + pairs(tx, n)], uc[m]);
                 }
             }
-            tile_mm(acc, C, Along<TM, true>{sQ, LC, ty}, Across<TN>{sb, LD, tx});
+            tile_mm(acc, C, Along<TM, true>{sQ, LC, ty}, Across<TN>{sb, LN, tx});
 #pragma unroll
             for (int m = 0; m < TM; ++m) {
                 const int64_t t = t0 + pairs(ty, m);
@@ -425,7 +428,7 @@ __global__ void __launch_bounds__(kThreads) k_decay_bwd_gen(DecayParams p) {
         {
             float acc[TM][TN];
             zero(acc);
-            tile_mm(acc, WT, Along<TM, true>{sx, LD, ty}, Along<TN, true>{sR, LD, tx});
+            tile_mm(acc, PT, Along<TM, true>{sx, LP, ty}, Along<TN, true>{sR, LP, tx});
 #pragma unroll
             for (int m = 0; m < TM; ++m) {
                 const float w = decay_between(end, sG[pairs(ty, m)]);
@@ -433,10 +436,10 @@ __global__ void __launch_bounds__(kThreads) k_decay_bwd_gen(DecayParams p) {
 #pragma unroll
                 for (int n = 0; n < TN; ++n) {
                     acc[m][n] *= w;
-                    vb[m] = fmaf(acc[m][n], sb[pairs(ty, m) * LD + pairs(tx, n)], vb[m]);
+                    vb[m] = fmaf(acc[m][n], sb[pairs(ty, m) * LN + pairs(tx, n)], vb[m]);
                 }
             }
-            tile_mm(acc, C, Across<TM>{sQ, LC, ty}, Across<TN>{sc, LD, tx});
+            tile_mm(acc, C, Across<TM>{sQ, LC, ty}, Across<TN>{sc, LN, tx});
 #pragma unroll
             for (int m = 0; m < TM; ++m) {
                 const int64_t t = t0 + pairs(ty, m);
@@ -454,29 +457,29 @@ __global__ void __launch_bounds__(kThreads) k_decay_bwd_gen(DecayParams p) {
         }
         // g_x
         {
-            float acc[TM][TN];
+            float acc[TM][TP];
             zero(acc);
-            tile_mm(acc, WT, Along<TM, true>{sb, LD, ty}, Across<TN>{sR, LD, tx});
+            tile_mm(acc, NT, Along<TM, true>{sb, LN, ty}, Across<TP>{sR, LP, tx});
 #pragma unroll
             for (int m = 0; m < TM; ++m) {
                 const float w = decay_between(end, sG[pairs(ty, m)]);
 #pragma unroll
-                for (int n = 0; n < TN; ++n) acc[m][n] *= w;
+                for (int n = 0; n < TP; ++n) acc[m][n] *= w;
             }
-            tile_mm(acc, C, Across<TM>{sP, LC, ty}, Across<TN>{sg, LD, tx});
+            tile_mm(acc, C, Across<TM>{sP, LC, ty}, Across<TP>{sg, LP, tx});
 #pragma unroll
             for (int m = 0; m < TM; ++m) {
                 const int64_t t = t0 + pairs(ty, m);
 #pragma unroll
-                for (int n = 0; n < TN; ++n)
+                for (int n = 0; n < TP; ++n)
                     if (t < p.L && pairs(tx, n) < p.P)
                         gx[t * p.val_t + pairs(tx, n)] = t < hd.len ? acc[m][n] : 0.f;
             }
         }
         // e^{G_C} <S0, R>, the row sums u_i + R_i and v_j
         float dot = 0.f;
-        for (int e = threadIdx.x; e < WT * WT; e += kThreads)
-            dot = fmaf(sS[(e / WT) * LD + e % WT], sR[(e / WT) * LD + e % WT], dot);
+        for (int e = threadIdx.x; e < NT * PT; e += kThreads)
+            dot = fmaf(sS[(e / PT) * LP + e % PT], sR[(e / PT) * LP + e % PT], dot);
 #pragma unroll
         for (int d = 16; d; d >>= 1) dot += __shfl_xor_sync(kFull, dot, d);
 #pragma unroll
@@ -494,8 +497,8 @@ __global__ void __launch_bounds__(kThreads) k_decay_bwd_gen(DecayParams p) {
                 sred[pairs(ty, m)] = uc[m];
                 sred[C + pairs(ty, m)] = vb[m];
             }
-        for (int e = threadIdx.x; e < C * WT; e += kThreads)
-            sc[(e / WT) * LD + e % WT] *= decay_from_start(sG[e / WT]);
+        for (int e = threadIdx.x; e < C * NT; e += kThreads)
+            sc[(e / NT) * LN + e % NT] *= decay_from_start(sG[e / NT]);
         __syncthreads();
         if (threadIdx.x < 32) {
             // g_log_a[t] = sum_{i>=t} (row_i + u_i - col_i) + sum_{j<t} v_j + e^{G_C} <S0, R>
@@ -536,14 +539,14 @@ __global__ void __launch_bounds__(kThreads) k_decay_bwd_gen(DecayParams p) {
             }
         }
         {
-            float acc[TN][TN];
+            float acc[TN][TP];
             zero(acc);
-            tile_mm(acc, C, Across<TN>{sc, LD, ty}, Across<TN>{sg, LD, tx});
+            tile_mm(acc, C, Across<TN>{sc, LN, ty}, Across<TP>{sg, LP, tx});
 #pragma unroll
             for (int m = 0; m < TN; ++m)
 #pragma unroll
-                for (int n = 0; n < TN; ++n) {
-                    float *s = &sR[pairs(ty, m) * LD + pairs(tx, n)];
+                for (int n = 0; n < TP; ++n) {
+                    float *s = &sR[pairs(ty, m) * LP + pairs(tx, n)];
                     *s = fmaf(aend, *s, acc[m][n]);
                 }
         }
@@ -551,9 +554,9 @@ __global__ void __launch_bounds__(kThreads) k_decay_bwd_gen(DecayParams p) {
     __syncthreads();
     if (p.g_h0 && seg == 0) {
         float *out = p.g_h0 + (int64_t)hd.bh * np;
-        for (int e = threadIdx.x; e < WT * WT; e += kThreads) {
-            const int n = e / WT, q = e % WT;
-            if (n < p.N && q < p.P) out[(int64_t)n * p.P + q] = sR[n * LD + q];
+        for (int e = threadIdx.x; e < NT * PT; e += kThreads) {
+            const int n = e / PT, q = e % PT;
+            if (n < p.N && q < p.P) out[(int64_t)n * p.P + q] = sR[n * LP + q];
         }
     }
 }
@@ -689,36 +692,55 @@ cudaError_t launch(int64_t grid, size_t smem, cudaStream_t st, const DecayParams
     return cudaGetLastError();
 }
 
-template <int C, int WT, bool REV>
+template <int NT, int PT, bool REV>
 cudaError_t seg_gen(const DecayParams &p, cudaStream_t st) {
-    const size_t smem = (size_t)(2 * C * (WT + 4) + 2 * C) * 4;
-    return launch<k_decay_seg_gen<C, WT, REV>>((int64_t)p.B * p.H * p.nseg, smem, st, p);
+    const size_t smem = (size_t)(kC * (NT + PT + 8) + 2 * kC) * 4;
+    return launch<k_decay_seg_gen<kC, NT, PT, REV>>((int64_t)p.B * p.H * p.nseg, smem, st, p);
 }
 
-template <int C, int WT>
-cudaError_t fwd_gen(const DecayParams &p, cudaStream_t st) {
-    constexpr int PS = WT < 64 ? WT : 64;
-    if (p.nseg > 1) {
-        cudaError_t e = seg_gen<C, WT, false>(p, st);
-        if (e != cudaSuccess) return e;
-        e = launch_decay_join(p, p.h0, false, nullptr, st);
-        if (e != cudaSuccess) return e;
+template <int NT, int PT>
+struct Fwd {
+    static cudaError_t run(const DecayParams &p, cudaStream_t st) {
+        constexpr int PS = PT < 64 ? PT : 64;
+        if (p.nseg > 1) {
+            cudaError_t e = seg_gen<NT, PT, false>(p, st);
+            if (e != cudaSuccess) return e;
+            e = launch_decay_join(p, p.h0, false, nullptr, st);
+            if (e != cudaSuccess) return e;
+        }
+        const size_t smem =
+            (size_t)(2 * kC * (NT + 4) + (kC + NT) * (PS + 4) + kC * (kC + 4) + 2 * kC) * 4;
+        return launch<k_decay_fwd_gen<kC, NT, PT>>((int64_t)p.B * p.H * p.nseg * p.pslices, smem, st, p);
     }
-    const size_t smem = (size_t)(2 * C * (WT + 4) + (C + WT) * (PS + 4) + C * (C + 4) + 2 * C) * 4;
-    return launch<k_decay_fwd_gen<C, WT>>((int64_t)p.B * p.H * p.nseg * p.pslices, smem, st, p);
-}
+};
 
-template <int C, int WT>
-cudaError_t bwd_gen(const DecayParams &p, cudaStream_t st) {
-    if (p.nseg > 1) {
-        cudaError_t e = seg_gen<C, WT, true>(p, st);
-        if (e != cudaSuccess) return e;
-        e = launch_decay_join(p, p.g_hlast, true, nullptr, st);
-        if (e != cudaSuccess) return e;
+template <int NT, int PT>
+struct Bwd {
+    static cudaError_t run(const DecayParams &p, cudaStream_t st) {
+        if (p.nseg > 1) {
+            cudaError_t e = seg_gen<NT, PT, true>(p, st);
+            if (e != cudaSuccess) return e;
+            e = launch_decay_join(p, p.g_hlast, true, nullptr, st);
+            if (e != cudaSuccess) return e;
+        }
+        const size_t smem = (size_t)(2 * kC * (NT + PT + 8) + 2 * NT * (PT + 4) + 2 * kC * (kC + 4) +
+                                     2 * kC + 16 * kC + 32 + 2 * kC) * 4;
+        return launch<k_decay_bwd_gen<kC, NT, PT>>((int64_t)p.B * p.H * p.nseg, smem, st, p);
     }
-    const size_t smem = (size_t)((4 * C + 2 * WT) * (WT + 4) + 2 * C * (C + 4) + 2 * C + 16 * C + 32 +
-                                 2 * C) * 4;
-    return launch<k_decay_bwd_gen<C, WT>>((int64_t)p.B * p.H * p.nseg, smem, st, p);
+};
+
+// the widths in shared memory: N and P rounded up to 32, 64 or 128 each
+template <template <int, int> class WHAT, int NT>
+cudaError_t by_p(const DecayParams &p, cudaStream_t st) {
+    if (p.P <= 32) return WHAT<NT, 32>::run(p, st);
+    if (p.P <= 64) return WHAT<NT, 64>::run(p, st);
+    return WHAT<NT, 128>::run(p, st);
+}
+template <template <int, int> class WHAT>
+cudaError_t by_widths(const DecayParams &p, cudaStream_t st) {
+    if (p.N <= 32) return by_p<WHAT, 32>(p, st);
+    if (p.N <= 64) return by_p<WHAT, 64>(p, st);
+    return by_p<WHAT, 128>(p, st);
 }
 
 }  // namespace
@@ -769,17 +791,11 @@ cudaError_t launch_decay_sum_steps(const DecayParams &p, const float *part, floa
 }
 
 cudaError_t launch_decay_fwd_gen(const DecayParams &p, cudaStream_t st) {
-    const int w = p.N > p.P ? p.N : p.P;
-    if (w <= 32) return fwd_gen<32, 32>(p, st);
-    if (w <= 64) return fwd_gen<32, 64>(p, st);
-    return fwd_gen<32, 128>(p, st);
+    return by_widths<Fwd>(p, st);
 }
 
 cudaError_t launch_decay_bwd_gen(const DecayParams &p, cudaStream_t st) {
-    const int w = p.N > p.P ? p.N : p.P;
-    if (w <= 32) return bwd_gen<32, 32>(p, st);
-    if (w <= 64) return bwd_gen<32, 64>(p, st);
-    return bwd_gen<32, 128>(p, st);
+    return by_widths<Bwd>(p, st);
 }
 
 }  // namespace pdssm
