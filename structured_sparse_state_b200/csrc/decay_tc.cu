@@ -27,9 +27,10 @@
 // where the product does not.
 //
 // Warps: 0-3 and 4-7 take chunks in turn (steps 2 and 5), 8-15 hold the state
-// (32 columns each), 16-23 build the split operand, 24-26 issue the
-// products (scores, Y, state: one thread would hold each of them back by the
-// others' waits), 27 the copies, 28 and 29 compute the decays in turn.  Accumulators, decays and (N <= 64) split parts are double-buffered,
+// (32 columns each), 16-23 build the split operand, 24-27 issue the
+// products (scores; Y; Yi and the state by the chunk's first half; by its second:
+// one thread would hold each of them back by the others' waits, and takes about
+// 100 cycles per product), 28 the copies, 29 and 30 compute the decays in turn.  Accumulators, decays and (N <= 64) split parts are double-buffered,
 // c and b tiles three deep (N <= 64; the scores of chunk i + 1 run ahead of
 // the rest of chunk i, so two stages would expose each copy's latency), all
 // handed over by mbarriers.
@@ -44,9 +45,9 @@ namespace {
 
 constexpr int kC = 128;                 // steps per chunk
 // warps by role
-constexpr int kState = 8, kBuild = 16, kScores = 24, kOutputs = 25, kStates = 26, kProducer = 27,
-              kDecay = 28;
-constexpr int kTcTh = 30 * 32;
+constexpr int kState = 8, kBuild = 16, kScores = 24, kOutputs = 25, kStates = 26, kProducer = 28,
+              kDecay = 29;
+constexpr int kTcTh = 31 * 32;
 constexpr int kLoaders = 32;            // threads of plain loads (the producer's warp)
 constexpr uint32_t kTile = kC * 128;    // 128 rows of 64 bf16
 
@@ -175,9 +176,9 @@ __global__ void __launch_bounds__(kTcTh, 1)
             mbar_init(bar(kScFull, s), 1);
             mbar_init(bar(kPReady, s), 128);
             mbar_init(bar(kPlReady, s), 256);
-            mbar_init(bar(kPlRead, s), 1);
+            mbar_init(bar(kPlRead, s), 2);
             mbar_init(bar(kPlLate, s), 256);
-            mbar_init(bar(kDFull, s), 1);
+            mbar_init(bar(kDFull, s), 2);
             mbar_init(bar(kS0Ready, s), 256);
             mbar_init(bar(kYFull, s), 1);
             mbar_init(bar(kYFree, s), 128);
@@ -499,35 +500,41 @@ __global__ void __launch_bounds__(kTcTh, 1)
             if (n > 0 && ok) wait(kYFull, n - 1);
         }
         __syncwarp();
-    } else if (warp == kStates) {
-        // ---- products: Yi, then what the chunk adds to the state
+    } else if (warp == kStates || warp == kStates + 1) {
+        // ---- products: Yi (the first warp), then what the warp's half of the chunk
+        // adds to the state
+        const int half = warp - kStates;
         if (lane == 0) {
             constexpr uint32_t kIdY = umma_idesc_bf16(64, false, true);
             constexpr uint32_t kIdD = umma_idesc_bf16(64, true, true);
             constexpr uint32_t kRow16 = umma_step(2048);    // 16 rows of a tile
             const uint32_t key0 = umma_lo(sm + SM::kC0, kTile), x0 = umma_lo(sm + SM::kX, 0),
                            pl0 = umma_lo(sm + SM::kPl, kTile), s0 = umma_lo(sm + SM::kS0, 0);
+            const uint32_t dD = tcol(half, 192);
             for (int i = 0; i < n; ++i) {
                 const uint32_t ct = key0 + (uint32_t)(i % SM::kNCB) * umma_step(SM::kStage);
                 const uint32_t bt = ct + umma_step(SM::kB);
                 const uint32_t xr = x0 + (uint32_t)(i % SM::kNX) * umma_step(kTile);
                 if (!wait_cb(i)) break;
+                // the accumulators of the chunk's halves are free: the state took the
+                // last chunk's before it gave this one's S0
                 if (FWD) {
-                    if (!wait(kS0Ready, i) || (i >= 2 && !wait(kYFree, i - 2))) break;
-                    tc_fence_after();
-                    const uint32_t dYi = tcol(i, 128);
+                    if (!wait(kS0Ready, i)) break;
+                    if (half == 0) {
+                        if (i >= 2 && !wait(kYFree, i - 2)) break;
+                        tc_fence_after();
+                        const uint32_t dYi = tcol(i, 128);
 #pragma unroll
-                    for (int k = 0; k < (STK ? 4 : 8); ++k)
-                        umma_ss(dYi, ct + (k >> 2) * umma_step(kTile) + (k & 3) * umma_step(32),
-                                s0 + k * kRow16, kIdY, k > 0);
+                        for (int k = 0; k < (STK ? 4 : 8); ++k)
+                            umma_ss(dYi, ct + (k >> 2) * umma_step(kTile) + (k & 3) * umma_step(32),
+                                    s0 + k * kRow16, kIdY, k > 0);
+                    }
                 } else if (i >= 1 && !wait(kS0Ready, i - 1)) {
                     break;
                 }
                 if (!wait(kPlReady, i) || !wait_x(i)) break;
                 tc_fence_after();
                 const uint32_t pl = pl0 + (uint32_t)(i % SM::kNPL) * umma_step(SM::kParts * kTile);
-                // the accumulators of the chunk's halves are free: the state took the
-                // last chunk's before it gave this one's S0
                 // STK: the parts' 64 columns twice as the 128 rows (leading offset 0;
                 // part 2 lies in b's place)
 #pragma unroll 1
@@ -537,12 +544,15 @@ __global__ void __launch_bounds__(kTcTh, 1)
                         if (!wait(kPlLate, i)) break;
                         tc_fence_after();
                     }
-                    const uint32_t ar = STK ? (part < 2 ? pl + part * umma_step(kTile) : bt) - umma_lo(0, kTile) : bt;
-                    const uint32_t br = STK ? xr : pl + (SM::kLate && part == 2 ? 0 : part) * umma_step(kTile);
+                    const uint32_t ar =
+                        (STK ? (part < 2 ? pl + part * umma_step(kTile) : bt) - umma_lo(0, kTile) : bt) +
+                        half * 4 * kRow16;
+                    const uint32_t br =
+                        (STK ? xr : pl + (SM::kLate && part == 2 ? 0 : part) * umma_step(kTile)) +
+                        half * 4 * kRow16;
 #pragma unroll
-                    for (int k = 0; k < 8; ++k)
-                        umma_ss(tcol(k >> 2, 192), ar + k * kRow16, br + k * kRow16, kIdD,
-                                (k & 3) > 0 || part < 2);
+                    for (int k = 0; k < 4; ++k)
+                        umma_ss(dD, ar + k * kRow16, br + k * kRow16, kIdD, k > 0 || part < 2);
                 }
                 if (!ok) break;
                 umma_commit(bar(kDFull, i));
