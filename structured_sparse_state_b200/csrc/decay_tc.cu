@@ -9,8 +9,8 @@
 //     3. Y  = P x                              128 x 64, K = 128, P from TMEM
 //     4. Yi = c S0                             128 x 64, K = N
 //     5. y  = Y + e^{G_i} Yi
-//     6. S  = e^{G_C} S0 + sum_j (e^{G_C - G_j} b_j) x_j^T, in halves of 64 steps
-//        (so that the adjoint, which has chunks of 64, finds each one's state)
+//     6. S  = e^{G_C} S0 + sum_j (e^{G_C - G_j} b_j) x_j^T; for the adjoint, whose
+//        chunks are 64 steps, in two halves, each one's state written out
 // The state is an fp32 register of one of 128 threads per row and is decayed
 // there; only product 6 adds to it.  Its decayed operand is split into three
 // bf16 parts (8 + 8 + 8 bits), so that the state keeps fp32 accuracy (two
@@ -28,9 +28,8 @@
 //
 // Warps: 0-3 and 4-7 take chunks in turn (steps 2 and 5), 8-15 hold the state
 // (32 columns each), 16-23 build the split operand, 24-27 issue the
-// products (scores; Y; Yi and the state by the chunk's first half; by its second:
-// one thread would hold each of them back by the others' waits, and takes about
-// 100 cycles per product), 28 the copies, 29 and 30 compute the decays in turn.  Accumulators, decays and (N <= 64) split parts are double-buffered,
+// products (scores; Yi and Y; two for the state: one thread would hold each of
+// them back by the others' waits, and takes about 100 cycles per product), 28 the copies, 29 and 30 compute the decays in turn.  Accumulators, decays and (N <= 64) split parts are double-buffered,
 // c and b tiles three deep (N <= 64; the scores of chunk i + 1 run ahead of
 // the rest of chunk i, so two stages would expose each copy's latency), all
 // handed over by mbarriers.
@@ -59,18 +58,23 @@ enum { kFwd = 0, kSegFwd = 1, kSegRev = 2, kFwdCarry = 3 };
 struct __align__(16) Decays {
     float2 G[kC];           // cumulated, base 2, hi + lo
     float start[kC];        // e^{G_t}
-    float weight[kC];       // of the state's update: to the end of t's half of the chunk (in
-                            // reverse: from its start)
+    float weight[kC];       // of the state's update: to the end of the chunk (kFwdCarry: of t's
+                            // half of it; in reverse: from its start)
     float col[kC];          // e^{G_e - G_t}, e = last step of t's block of 32
     float row[3][kC];       // e^{G_t - G_e}, e = last step of block 0..2 (t behind it)
-    float half[2], pad[2];  // decay over the first and the second half
+    float half[2], all[2];  // decay over each half; over the chunk (and padding)
 };
+
+// Sets of decays.  The state gives one back a whole chunk after the operand's
+// builders; with two sets the decays, the operand and its products of a chunk
+// stood in one line behind that (the state alone: 1.45 us a chunk, with four XX).
+constexpr int kNDec = 4;
 
 // Barriers: four slots of each kind (chunk i: slot i & 3, phase i >> 2, so
 // that no role can be a whole round of a slot behind), and the rings' own.
 enum {
     kFullCB, kFullX, kScFull, kPReady, kPlReady, kDFull, kS0Ready, kYFull, kYFree,
-    kDecReady, kDecFree, kPlRead, kPlLate, kNumBars
+    kDecReady, kDecFree, kPlRead, kPlLate, kYiFull, kNumBars
 };
 
 // Shared memory.  The state alone needs no c (in reverse no b) and no S0, so it
@@ -92,7 +96,7 @@ struct Smem {
     static constexpr uint32_t kPl = kX + kNX * kTile;   // [kNPL][kParts]
     static constexpr uint32_t kS0 = kPl + kNPL * kParts * kTile;
     static constexpr uint32_t kDec = kS0 + (SEG ? 0 : kTile);
-    static constexpr uint32_t kBar = kDec + 2 * sizeof(Decays);
+    static constexpr uint32_t kBar = kDec + kNDec * sizeof(Decays);
     static constexpr uint32_t kTotal = kBar + 32 * kNumBars + 1024;     // + alignment
 };
 
@@ -138,6 +142,7 @@ __global__ void __launch_bounds__(kTcTh, 1)
     k_decay_tc(const __grid_constant__ CUtensorMap cmap, const __grid_constant__ CUtensorMap bmap,
                const __grid_constant__ CUtensorMap xmap, const TcParams tp) {
     constexpr bool FWD = MODE == kFwd || MODE == kFwdCarry;
+    constexpr bool HALVES = MODE == kFwdCarry;
     using SM = Smem<STK, !FWD>;
     const DecayParams &p = tp.d;
     extern __shared__ unsigned char sm_raw[];
@@ -176,9 +181,10 @@ __global__ void __launch_bounds__(kTcTh, 1)
             mbar_init(bar(kScFull, s), 1);
             mbar_init(bar(kPReady, s), 128);
             mbar_init(bar(kPlReady, s), 256);
-            mbar_init(bar(kPlRead, s), 2);
+            mbar_init(bar(kPlRead, s), HALVES ? 2 : 1);
+            mbar_init(bar(kYiFull, s), 1);
             mbar_init(bar(kPlLate, s), 256);
-            mbar_init(bar(kDFull, s), 2);
+            mbar_init(bar(kDFull, s), HALVES ? 2 : 1);
             mbar_init(bar(kS0Ready, s), 256);
             mbar_init(bar(kYFull, s), 1);
             mbar_init(bar(kYFree, s), 128);
@@ -193,7 +199,8 @@ __global__ void __launch_bounds__(kTcTh, 1)
     tc_fence_after();
     const uint32_t tmem = tmem_slot;
     // TMEM columns of buffer i & 1: Sc 128 (P in its first 64, Y in its last 64,
-    // Yi 64), and what the chunk's first and second half add to the state, 64 each
+    // Yi 64), and what the chunk adds to the state, 64 (with HALVES buffer 0 is the
+    // first half's and 1 the second's of every chunk)
     auto tcol = [&](int i, int col) { return tmem + (uint32_t)((i & 1) * 256 + col); };
 
     // Bounded waits of one thread, or of a whole warp (which then agrees on the
@@ -221,7 +228,7 @@ __global__ void __launch_bounds__(kTcTh, 1)
             const uint32_t tlane = (uint32_t)(quad * 32) << 16;
             __nv_bfloat16 *y = (__nv_bfloat16 *)p.y + b * p.oval_b + h * p.oval_h + p0;
             for (int i = warp >> 2; i < n; i += 2) {
-                const Decays &dc = dec[i & 1];
+                const Decays &dc = dec[i & (kNDec - 1)];
                 if (!wait_warp(kDecReady, i) || !wait_warp(kScFull, i)) break;
                 tc_fence_after();
                 const float es = dc.start[r];
@@ -270,8 +277,7 @@ __global__ void __launch_bounds__(kTcTh, 1)
                 mbar_arrive(bar(kPReady, i));
                 mbar_arrive(bar(kDecFree, i));
 
-                // Yi was done before what its chunk adds to the state
-                if (!wait_warp(kYFull, i) || !wait_warp(kDFull, i)) break;
+                if (!wait_warp(kYFull, i)) break;       // Y, and Yi before it
                 tc_fence_after();
                 const int64_t t = chunk_t0(i) + r;
 #pragma unroll 1
@@ -365,26 +371,27 @@ __global__ void __launch_bounds__(kTcTh, 1)
         if (FWD && n > 0) put_S0(0);
         for (int i = 0; i < n; ++i) {
             if (!wait_warp(kDecReady, i)) break;
-            const float a[2] = {dec[i & 1].half[0], dec[i & 1].half[1]};
+            const float a[2] = {HALVES ? dec[i & (kNDec - 1)].half[0] : dec[i & (kNDec - 1)].all[0], dec[i & (kNDec - 1)].half[1]};
             mbar_arrive(bar(kDecFree, i));
-            if (MODE == kFwdCarry) carry(2 * (c0 + i));
+            if (HALVES) carry(2 * (c0 + i));
             if (!wait_warp(kDFull, i)) break;
             tc_fence_after();
 #pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                const int half = MODE == kSegRev ? 1 - k : k;
-                if (MODE == kFwdCarry && k == 1) carry(2 * (c0 + i) + 1);
+            for (int k = 0; k < (HALVES ? 2 : 1); ++k) {
+                if (k == 1) carry(2 * (c0 + i) + 1);
 #pragma unroll
                 for (int q = 0; q < kCols; q += 16) {
                     uint32_t v[16];
-                    tmem_ld16_raw(tcol(half, 192 + q0 + q) + tlane, v);
+                    tmem_ld16_raw(tcol(HALVES ? k : i, 192 + q0 + q) + tlane, v);
                     tmem_wait_ld();
 #pragma unroll
-                    for (int e = 0; e < 16; ++e) S[q + e] = fmaf(a[half], S[q + e], __uint_as_float(v[e]));
+                    for (int e = 0; e < 16; ++e) S[q + e] = fmaf(a[k], S[q + e], __uint_as_float(v[e]));
                 }
             }
             if (FWD) {
-                if (i + 1 < n) put_S0(i + 1);
+                if (i + 1 == n) break;
+                if (!wait_warp(kYiFull, i)) break;          // S0 has been read
+                put_S0(i + 1);
             } else {
                 tc_fence_before();
                 mbar_arrive(bar(kS0Ready, i));              // the accumulators are free
@@ -400,7 +407,7 @@ __global__ void __launch_bounds__(kTcTh, 1)
         const int r = tid & 127, h0 = ((warp - kBuild) >> 2) * 4;
         for (int i = 0; i < n; ++i) {
             if (!wait_warp(kDecReady, i)) break;
-            const float w = dec[i & 1].weight[r];
+            const float w = dec[i & (kNDec - 1)].weight[r];
             mbar_arrive(bar(kDecFree, i));
             const bool on = chunk_t0(i) + r < len;
             if (!wait_cb_warp(i)) break;
@@ -484,11 +491,21 @@ __global__ void __launch_bounds__(kTcTh, 1)
         }
         __syncwarp();
     } else if (warp == kOutputs) {
-        // ---- products: Y
+        // ---- products: Yi and Y
         if (lane == 0 && FWD) {
             constexpr uint32_t kIdY = umma_idesc_bf16(64, false, true);
-            const uint32_t x0 = umma_lo(sm + SM::kX, 0);
+            const uint32_t key0 = umma_lo(sm + SM::kC0, kTile), x0 = umma_lo(sm + SM::kX, 0),
+                           s0 = umma_lo(sm + SM::kS0, 0);
             for (int i = 0; i < n; ++i) {
+                if (!wait_cb(i) || !wait(kS0Ready, i) || (i >= 2 && !wait(kYFree, i - 2))) break;
+                tc_fence_after();
+                const uint32_t ct = key0 + (uint32_t)(i % SM::kNCB) * umma_step(SM::kStage);
+                const uint32_t dYi = tcol(i, 128);
+#pragma unroll
+                for (int k = 0; k < (STK ? 4 : 8); ++k)
+                    umma_ss(dYi, ct + (k >> 2) * umma_step(kTile) + (k & 3) * umma_step(32),
+                            s0 + k * umma_step(2048), kIdY, k > 0);
+                umma_commit(bar(kYiFull, i));
                 if (!wait(kPReady, i) || !wait_x(i) || !wait(kPlReady, i)) break;
                 tc_fence_after();
                 const uint32_t dY = tcol(i, 64), pa = tcol(i, 0);
@@ -497,43 +514,32 @@ __global__ void __launch_bounds__(kTcTh, 1)
                 for (int k = 0; k < 8; ++k) umma_ts(dY, pa + 8 * k, xr + k * umma_step(2048), kIdY, k > 0);
                 umma_commit(bar(kYFull, i));
             }
-            if (n > 0 && ok) wait(kYFull, n - 1);
+            if (n > 0) wait(kYiFull, n - 1) && wait(kYFull, n - 1);
         }
         __syncwarp();
     } else if (warp == kStates || warp == kStates + 1) {
-        // ---- products: Yi (the first warp), then what the warp's half of the chunk
-        // adds to the state
-        const int half = warp - kStates;
+        // ---- products: what the chunk adds to the state; the two warps take chunks in
+        // turn, or (HALVES) a half of each chunk
+        const int w = warp - kStates;
         if (lane == 0) {
-            constexpr uint32_t kIdY = umma_idesc_bf16(64, false, true);
             constexpr uint32_t kIdD = umma_idesc_bf16(64, true, true);
             constexpr uint32_t kRow16 = umma_step(2048);    // 16 rows of a tile
-            const uint32_t key0 = umma_lo(sm + SM::kC0, kTile), x0 = umma_lo(sm + SM::kX, 0),
-                           pl0 = umma_lo(sm + SM::kPl, kTile), s0 = umma_lo(sm + SM::kS0, 0);
-            const uint32_t dD = tcol(half, 192);
-            for (int i = 0; i < n; ++i) {
-                const uint32_t ct = key0 + (uint32_t)(i % SM::kNCB) * umma_step(SM::kStage);
-                const uint32_t bt = ct + umma_step(SM::kB);
+            constexpr int kSteps = HALVES ? 4 : 8;
+            const uint32_t key0 = umma_lo(sm + SM::kC0, kTile) + (HALVES ? w * 4 * kRow16 : 0),
+                           x0 = umma_lo(sm + SM::kX, 0) + (HALVES ? w * 4 * kRow16 : 0),
+                           pl0 = umma_lo(sm + SM::kPl, kTile) + (HALVES ? w * 4 * kRow16 : 0);
+            int last = -1;
+            for (int i = HALVES ? 0 : w; i < n; i += HALVES ? 1 : 2) {
+                const uint32_t bt = key0 + (uint32_t)(i % SM::kNCB) * umma_step(SM::kStage) +
+                                    umma_step(SM::kB);
                 const uint32_t xr = x0 + (uint32_t)(i % SM::kNX) * umma_step(kTile);
-                if (!wait_cb(i)) break;
-                // the accumulators of the chunk's halves are free: the state took the
-                // last chunk's before it gave this one's S0
-                if (FWD) {
-                    if (!wait(kS0Ready, i)) break;
-                    if (half == 0) {
-                        if (i >= 2 && !wait(kYFree, i - 2)) break;
-                        tc_fence_after();
-                        const uint32_t dYi = tcol(i, 128);
-#pragma unroll
-                        for (int k = 0; k < (STK ? 4 : 8); ++k)
-                            umma_ss(dYi, ct + (k >> 2) * umma_step(kTile) + (k & 3) * umma_step(32),
-                                    s0 + k * kRow16, kIdY, k > 0);
-                    }
-                } else if (i >= 1 && !wait(kS0Ready, i - 1)) {
-                    break;
-                }
+                // the accumulators are free: the state took chunk i - 2's (HALVES: i - 1's)
+                // before it left S0 of the chunk behind (the state alone: before it said so)
+                const int taken = HALVES ? i : FWD ? i - 1 : i - 2;
+                if (!wait_cb(i) || (taken > 0 - !FWD && !wait(kS0Ready, taken))) break;
                 if (!wait(kPlReady, i) || !wait_x(i)) break;
                 tc_fence_after();
+                const uint32_t dD = tcol(HALVES ? w : i, 192);
                 const uint32_t pl = pl0 + (uint32_t)(i % SM::kNPL) * umma_step(SM::kParts * kTile);
                 // STK: the parts' 64 columns twice as the 128 rows (leading offset 0;
                 // part 2 lies in b's place)
@@ -544,20 +550,17 @@ __global__ void __launch_bounds__(kTcTh, 1)
                         if (!wait(kPlLate, i)) break;
                         tc_fence_after();
                     }
-                    const uint32_t ar =
-                        (STK ? (part < 2 ? pl + part * umma_step(kTile) : bt) - umma_lo(0, kTile) : bt) +
-                        half * 4 * kRow16;
-                    const uint32_t br =
-                        (STK ? xr : pl + (SM::kLate && part == 2 ? 0 : part) * umma_step(kTile)) +
-                        half * 4 * kRow16;
+                    const uint32_t ar = STK ? (part < 2 ? pl + part * umma_step(kTile) : bt) - umma_lo(0, kTile) : bt;
+                    const uint32_t br = STK ? xr : pl + (SM::kLate && part == 2 ? 0 : part) * umma_step(kTile);
 #pragma unroll
-                    for (int k = 0; k < 4; ++k)
+                    for (int k = 0; k < kSteps; ++k)
                         umma_ss(dD, ar + k * kRow16, br + k * kRow16, kIdD, k > 0 || part < 2);
                 }
                 if (!ok) break;
                 umma_commit(bar(kDFull, i));
+                last = i;
             }
-            if (n > 0 && ok) wait(kDFull, n - 1);
+            if (last >= 0 && ok) wait(kDFull, last);    // nothing is in flight when the CTA ends
         }
         __syncwarp();
     } else if (warp >= kDecay) {
@@ -592,8 +595,8 @@ __global__ void __launch_bounds__(kTcTh, 1)
                 const float hi = (float)c;
                 G[q] = make_float2(hi, (float)(c - (double)hi));
             }
-            if (i >= 2 && !wait_warp(kDecFree, i - 2)) break;
-            Decays &dc = dec[i & 1];
+            if (i >= kNDec && !wait_warp(kDecFree, i - kNDec)) break;
+            Decays &dc = dec[i & (kNDec - 1)];
             float4 *gs = reinterpret_cast<float4 *>(dc.G + 4 * lane);
             gs[0] = make_float4(G[0].x, G[0].y, G[1].x, G[1].y);
             gs[1] = make_float4(G[2].x, G[2].y, G[3].x, G[3].y);
@@ -605,10 +608,8 @@ __global__ void __launch_bounds__(kTcTh, 1)
                 const float2 g = dc.G[t];
                 const float es = ex2(g.x + g.y);
                 dc.start[t] = es;
-                const float2 to = q < 2 ? mid : end;
-                dc.weight[t] = MODE != kSegRev ? ex2((to.x - g.x) + (to.y - g.y))
-                               : q < 2         ? es
-                                               : ex2((g.x - mid.x) + (g.y - mid.y));
+                const float2 to = HALVES && q < 2 ? mid : end;
+                dc.weight[t] = MODE == kSegRev ? es : ex2((to.x - g.x) + (to.y - g.y));
                 if (FWD) {
                     const float2 own = dc.G[32 * q + 31];
                     dc.col[t] = ex2((own.x - g.x) + (own.y - g.y));
@@ -620,6 +621,7 @@ __global__ void __launch_bounds__(kTcTh, 1)
                 }
             }
             if (lane == 0) {
+                dc.all[0] = ex2(end.x + end.y);
                 dc.half[0] = ex2(mid.x + mid.y);
                 dc.half[1] = ex2((end.x - mid.x) + (end.y - mid.y));
             }
@@ -632,7 +634,8 @@ __global__ void __launch_bounds__(kTcTh, 1)
             int i = 0;
             for (; i < n && ok; ++i) {
                 const int t0 = (int)chunk_t0(i);
-                if (i >= SM::kNCB && !wait(kDFull, i - SM::kNCB)) break;
+                if (i >= SM::kNCB && (!wait(kDFull, i - SM::kNCB) || (FWD && !wait(kYiFull, i - SM::kNCB))))
+                    break;
                 const uint32_t keys = sm + SM::kC0 + (uint32_t)(i % SM::kNCB) * SM::kStage;
                 const uint32_t cb = bar_cb(i);
                 const int subs = STK ? 1 : 2;
@@ -675,7 +678,8 @@ __global__ void __launch_bounds__(kTcTh, 1)
         };
         for (int i = 0; i < n && ok; ++i) {
             const int64_t t0 = chunk_t0(i);
-            if (i >= SM::kNCB && !wait_warp(kDFull, i - SM::kNCB)) break;
+            if (i >= SM::kNCB && (!wait_warp(kDFull, i - SM::kNCB) || (FWD && !wait_warp(kYiFull, i - SM::kNCB))))
+                break;
             const uint32_t keys = sm + SM::kC0 + (uint32_t)(i % SM::kNCB) * SM::kStage;
             for (int q = 0; q < (STK ? 1 : 2); ++q) {
                 if (FWD)
