@@ -23,32 +23,37 @@
 namespace pdssm {
 namespace {
 
-constexpr int kC = 64, kTh = 256;           // steps of a chunk; threads of the products
-constexpr int kAll = kTh + 32;              // and a warp for decays and g_log_a
+constexpr int kC = 64;                      // steps of a chunk
 constexpr uint32_t kTile = 64 * 128;        // 64 rows of 64 bf16, 128-byte swizzle
 
 // Per chunk, double-buffered: its decays (made a chunk ahead) and what
-// g_log_a adds up (taken a chunk later).
+// g_log_a adds up (taken a chunk later).  WC: column groups of the warps.
+template <int WC>
 struct Sums {
     float2 G[kC];           // cumulated, base 2, hi + lo
     float e[kC], w[kC];     // e_i, w_j
-    float row[2][kC];       // pair sums by row, per column half
+    float row[WC][kC];      // pair sums by row, per column group
     float col[4][kC];       // by column, per row block
-    float u[2][kC], v[2][kC];
-    float dot[8];
+    float u[WC][kC], v[WC][kC];
+    float dot[4 * WC];
 };
 
 // NT and PT: N and P in units of 64.  Above 64 x 64 R's parts take the place of
-// S0's once those have been read.
+// S0's once those have been read, and as one CTA fits an SM it has twice the
+// warps (64 heads x 2048 steps forward and backward, 128 x 128: 510 us, with
+// eight 554).
 template <int NT, int PT>
 struct Smem {
     static constexpr bool kShare = NT * PT > 1;
+    // warps of the products: 4 by rows times WC by columns; then one for decays and
+    // g_log_a
+    static constexpr int kWC = kShare ? 4 : 2, kWarps = 4 * kWC, kTh = 32 * kWarps, kAll = kTh + 32;
     static constexpr uint32_t kState = NT * PT * kTile;             // one part
     static constexpr uint32_t kc = 0, kb = NT * kTile, kx = 2 * NT * kTile, kg = kx + PT * kTile;
     static constexpr uint32_t kS = kg + PT * kTile, kR = kShare ? kS : kS + 3 * kState;
     static constexpr uint32_t kP = kR + 3 * kState, kQ = kP + kTile;
     static constexpr uint32_t kF = kQ + kTile;                      // floats below
-    static constexpr uint32_t kTotal = kF + 2 * sizeof(Sums);
+    static constexpr uint32_t kTotal = kF + 2 * sizeof(Sums<kWC>);
 };
 
 __device__ __forceinline__ uint32_t piece(int r, int q) {
@@ -118,18 +123,23 @@ __device__ __forceinline__ float quad_sum(float v) {
 }
 
 // Barrier of the product warps.
-__device__ __forceinline__ void sync_products() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
+template <int TH>
+__device__ __forceinline__ void sync_products() {
+    asm volatile("bar.sync 1, %0;" ::"n"(TH) : "memory");
+}
 
 template <int NT, int PT>
-__global__ void __launch_bounds__(kAll, NT * PT > 1 ? 1 : 2) k_decay_bwd_mma(DecayParams p) {
+__global__ void __launch_bounds__(Smem<NT, PT>::kAll, NT * PT > 1 ? 1 : 2) k_decay_bwd_mma(DecayParams p) {
     using SM = Smem<NT, PT>;
+    constexpr int kTh = SM::kTh, WC = SM::kWC, F = 8 / WC;     // F: 8-column pieces of a warp
+    using Sums = Sums<WC>;
     extern __shared__ __align__(128) unsigned char sm_raw[];
     const uint32_t sm = smem_u32(sm_raw);
     Sums *sums = reinterpret_cast<Sums *>(sm_raw + SM::kF);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int wr = warp & 3, wc = warp >> 2;    // 16 rows and 32 columns of each product
+    const int wr = warp & 3, wc = warp >> 2;    // 16 rows and 8 F columns of each product
     const int g = lane >> 2, q2 = (lane & 3) * 2;
-    const int m0 = 16 * wr, n0 = 32 * wc;
+    const int m0 = 16 * wr, n0 = 8 * F * wc;
 
     const int seg = blockIdx.x % p.nseg;
     const int64_t bh = blockIdx.x / p.nseg;
@@ -148,7 +158,7 @@ __global__ void __launch_bounds__(kAll, NT * PT > 1 ? 1 : 2) k_decay_bwd_mma(Dec
 
     const int c0 = seg * p.seg_chunks, c1 = min(c0 + p.seg_chunks, p.nchunks);
 
-    if (warp == 8) {
+    if (warp == SM::kWarps) {
         // ---- decays of the next chunk and g_log_a of the last one, while the
         // product warps work on this one
         auto decays = [&](int ch) {
@@ -170,15 +180,19 @@ __global__ void __launch_bounds__(kAll, NT * PT > 1 ? 1 : 2) k_decay_bwd_mma(Dec
             if (ch >= c1 || t0 >= len) return;
             const Sums &s = sums[ch & 1];
             double through = 0.0;
-            for (int w = 0; w < 8; ++w) through += (double)s.dot[w];
+            for (int w = 0; w < SM::kWarps; ++w) through += (double)s.dot[w];
             through *= (double)s.e[kC - 1];
             double before = 0.0, total = 0.0, inc[2], pre[2];
 #pragma unroll
             for (int q = 0; q < 2; ++q) {
                 const int t = q * 32 + lane;
-                double a = (double)s.row[0][t] + (double)s.row[1][t] + (double)s.u[0][t] + (double)s.u[1][t] -
-                           ((double)s.col[0][t] + (double)s.col[1][t] + (double)s.col[2][t] + (double)s.col[3][t]);
-                double v = (double)s.v[0][t] + (double)s.v[1][t];
+                double a = 0.0, v = 0.0;
+#pragma unroll
+                for (int w = 0; w < WC; ++w) {
+                    a += (double)s.row[w][t] + (double)s.u[w][t];
+                    v += (double)s.v[w][t];
+                }
+                a -= (double)s.col[0][t] + (double)s.col[1][t] + (double)s.col[2][t] + (double)s.col[3][t];
                 const double a0 = a, v0 = v;
 #pragma unroll
                 for (int d = 1; d < 32; d *= 2) {
@@ -215,7 +229,7 @@ __global__ void __launch_bounds__(kAll, NT * PT > 1 ? 1 : 2) k_decay_bwd_mma(Dec
     }
 
     // R: per 64 x 64 rows m0 + g (+ 8), columns n0 + 8 f + q2 (+ 1)
-    float R[NT][PT][4][4];
+    float R[NT][PT][F][4];
     auto each = [&](auto &&f) {         // f(nt, pt)
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
@@ -227,7 +241,7 @@ __global__ void __launch_bounds__(kAll, NT * PT > 1 ? 1 : 2) k_decay_bwd_mma(Dec
                                      : (p.g_hlast ? p.g_hlast + bh * np : nullptr);
         each([&](int nt, int pt) {
 #pragma unroll
-            for (int f = 0; f < 4; ++f)
+            for (int f = 0; f < F; ++f)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     const int n = 64 * nt + m0 + g + 8 * (e >> 1), q = 64 * pt + n0 + 8 * f + q2 + (e & 1);
@@ -284,7 +298,7 @@ __global__ void __launch_bounds__(kAll, NT * PT > 1 ? 1 : 2) k_decay_bwd_mma(Dec
         // ---- tiles: zero behind the end and behind the widths
         if (p.vec) {
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
+            for (int i = 0; i < 512 / kTh; ++i) {
                 const int e = tid + i * kTh, r = e >> 3, q = e & 7;
                 const bool on = t0 + r < len;
                 const int64_t t = on ? t0 + r : t0;
@@ -338,9 +352,11 @@ __global__ void __launch_bounds__(kAll, NT * PT > 1 ? 1 : 2) k_decay_bwd_mma(Dec
         // the next chunk's rows and state on their way to L2
         if (ch > c0) {
             const int64_t tn = t0 - kC + (tid & 63);
+            if (tid < 256) {
             const void *at = tid < 64 ? (const void *)(c + tn * p.key_t) : tid < 128 ? (const void *)(bb + tn * p.key_t)
                              : tid < 192 ? (const void *)(x + tn * p.val_t) : (const void *)(gy + tn * p.val_t);
             asm volatile("prefetch.global.L2 [%0];" ::"l"(at));
+            }
 #pragma unroll
             for (int j = tid; j < NT * PT * 128; j += kTh)
                 if (ch > 1 && j * 32 < np)
@@ -353,9 +369,9 @@ __global__ void __launch_bounds__(kAll, NT * PT > 1 ? 1 : 2) k_decay_bwd_mma(Dec
             float dot = 0.f;
             const bool even = p.P % 2 == 0 && ((uintptr_t)S0 & 7) == 0;
             each([&](int nt, int pt) {
-                float S[4][4];
+                float S[F][4];
 #pragma unroll
-                for (int f = 0; f < 4; ++f)
+                for (int f = 0; f < F; ++f)
 #pragma unroll
                     for (int e = 0; e < 4; e += 2) {
                         const int n = 64 * nt + m0 + g + 4 * e, q = 64 * pt + n0 + 8 * f + q2;
@@ -371,7 +387,7 @@ __global__ void __launch_bounds__(kAll, NT * PT > 1 ? 1 : 2) k_decay_bwd_mma(Dec
                         }
                     }
 #pragma unroll
-                for (int f = 0; f < 4; ++f)
+                for (int f = 0; f < F; ++f)
 #pragma unroll
                     for (int e = 0; e < 4; e += 2) {
                         const float(&r)[4] = R[nt][pt][f];
@@ -394,10 +410,10 @@ __global__ void __launch_bounds__(kAll, NT * PT > 1 ? 1 : 2) k_decay_bwd_mma(Dec
             if (lane == 0) sw.dot[warp] = dot;
         }
         asm volatile("cp.async.wait_group 0;" ::: "memory");
-        sync_products();
+        sync_products<kTh>();
         const float aend = sw.e[kC - 1];
 
-        // ---- P and Q of rows m0.., the 16-column blocks k = wc, wc + 2, .. <= wr
+        // ---- P and Q of rows m0.., the 16-column blocks k = wc, wc + WC, .. <= wr
         {
             // rows' operands: kept over the blocks, or fetched for each (registers)
             uint32_t ca[4][4], ga[4][4];
@@ -411,7 +427,7 @@ __global__ void __launch_bounds__(kAll, NT * PT > 1 ? 1 : 2) k_decay_bwd_mma(Dec
             const float2 gr0 = sw.G[m0 + g], gr1 = sw.G[m0 + g + 8];
             float row0 = 0.f, row1 = 0.f;
 #pragma unroll 1
-            for (int k = wc; k < 4; k += 2) {
+            for (int k = wc; k < 4; k += WC) {
                 float *col = sw.col[wr] + 16 * k;
                 if (k > wr) {
                     if (lane < 16) col[lane] = 0.f;
@@ -480,12 +496,12 @@ __global__ void __launch_bounds__(kAll, NT * PT > 1 ? 1 : 2) k_decay_bwd_mma(Dec
                 sw.row[wc][m0 + g + 8] = row1;
             }
         }
-        sync_products();
+        sync_products<kTh>();
 
-        float acc[4][4];
+        float acc[F][4];
         auto zero = [&]() {
 #pragma unroll
-            for (int f = 0; f < 4; ++f)
+            for (int f = 0; f < F; ++f)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) acc[f][e] = 0.f;
         };
@@ -498,19 +514,19 @@ __global__ void __launch_bounds__(kAll, NT * PT > 1 ? 1 : 2) k_decay_bwd_mma(Dec
             for (int k = 2; k >= 0; --k)        // the small parts first: additions truncate
 #pragma unroll
                 for (int ks = 0; ks < 4; ++ks) {
-                    uint32_t f0[4], f1[4];
-                    ldm4(f0, at_b(parts + k * SM::kState, n0, ks, lane));
-                    ldm4(f1, at_b(parts + k * SM::kState, n0 + 16, ks, lane));
-                    mma(acc[0], a[ks], f0[0], f0[1]);
-                    mma(acc[1], a[ks], f0[2], f0[3]);
-                    mma(acc[2], a[ks], f1[0], f1[1]);
-                    mma(acc[3], a[ks], f1[2], f1[3]);
+#pragma unroll
+                    for (int f = 0; f < F; f += 2) {
+                        uint32_t b[4];
+                        ldm4(b, at_b(parts + k * SM::kState, n0 + 8 * f, ks, lane));
+                        mma(acc[f], a[ks], b[0], b[1]);
+                        mma(acc[f + 1], a[ks], b[2], b[3]);
+                    }
                 }
         };
         // acc *= by row factors; the rows' products with a tile's rows
         auto scale_rows = [&](float f0, float f1) {
 #pragma unroll
-            for (int f = 0; f < 4; ++f) {
+            for (int f = 0; f < F; ++f) {
                 acc[f][0] *= f0;
                 acc[f][1] *= f0;
                 acc[f][2] *= f1;
@@ -520,14 +536,14 @@ __global__ void __launch_bounds__(kAll, NT * PT > 1 ? 1 : 2) k_decay_bwd_mma(Dec
         float d0, d1;
         auto row_dots = [&](uint32_t tile) {
 #pragma unroll
-            for (int f = 0; f < 4; ++f) {
+            for (int f = 0; f < F; ++f) {
                 const uint32_t w0 = lds_u32(sm + tile + piece(m0 + g, n0 / 8 + f) + q2 * 2),
                                w1 = lds_u32(sm + tile + piece(m0 + g + 8, n0 / 8 + f) + q2 * 2);
                 d0 = fmaf(acc[f][0], lo_of(w0), fmaf(acc[f][1], hi_of(w0), d0));
                 d1 = fmaf(acc[f][2], lo_of(w1), fmaf(acc[f][3], hi_of(w1), d1));
             }
         };
-        auto leave_dots = [&](float (&out)[2][kC]) {
+        auto leave_dots = [&](float (&out)[WC][kC]) {
             d0 = quad_sum(d0);
             d1 = quad_sum(d1);
             if ((lane & 3) == 0) {
@@ -536,13 +552,13 @@ __global__ void __launch_bounds__(kAll, NT * PT > 1 ? 1 : 2) k_decay_bwd_mma(Dec
             }
         };
         auto add_pairs = [&](const uint32_t (&a)[4], uint32_t tile, int ks) {
-            uint32_t f0[4], f1[4];
-            ldm4t(f0, at_bt(tile, n0, ks, lane));
-            ldm4t(f1, at_bt(tile, n0 + 16, ks, lane));
-            mma(acc[0], a, f0[0], f0[1]);
-            mma(acc[1], a, f0[2], f0[3]);
-            mma(acc[2], a, f1[0], f1[1]);
-            mma(acc[3], a, f1[2], f1[3]);
+#pragma unroll
+            for (int f = 0; f < F; f += 2) {
+                uint32_t b[4];
+                ldm4t(b, at_bt(tile, n0 + 8 * f, ks, lane));
+                mma(acc[f], a, b[0], b[1]);
+                mma(acc[f + 1], a, b[2], b[3]);
+            }
         };
         const int64_t tr0 = t0 + m0 + g, tr1 = tr0 + 8;
 
@@ -563,17 +579,17 @@ __global__ void __launch_bounds__(kAll, NT * PT > 1 ? 1 : 2) k_decay_bwd_mma(Dec
                 add_pairs(a, sm + SM::kb + nt * kTile, ks);
             }
 #pragma unroll
-            for (int f = 0; f < 4; ++f) {
+            for (int f = 0; f < F; ++f) {
                 store_key(p.g_c, tr0, 64 * nt + n0 + 8 * f + q2, acc[f][0], acc[f][1]);
                 store_key(p.g_c, tr1, 64 * nt + n0 + 8 * f + q2, acc[f][2], acc[f][3]);
             }
         }
         leave_dots(sw.u);
         if (SM::kShare) {
-            sync_products();            // S0's parts have been read
+            sync_products<kTh>();            // S0's parts have been read
             each([&](int nt, int pt) {
 #pragma unroll
-                for (int f = 0; f < 4; ++f)
+                for (int f = 0; f < F; ++f)
 #pragma unroll
                     for (int e = 0; e < 4; e += 2) {
                         const float(&r)[4] = R[nt][pt][f];
@@ -585,7 +601,7 @@ __global__ void __launch_bounds__(kAll, NT * PT > 1 ? 1 : 2) k_decay_bwd_mma(Dec
                         for (int k = 0; k < 3; ++k) sts32(at + k * SM::kState, o[k]);
                     }
             });
-            sync_products();
+            sync_products<kTh>();
         }
         // ---- g_b
         const float w0 = sw.w[m0 + g], w1 = sw.w[m0 + g + 8];
@@ -605,7 +621,7 @@ __global__ void __launch_bounds__(kAll, NT * PT > 1 ? 1 : 2) k_decay_bwd_mma(Dec
                 add_pairs(a, sm + SM::kc + nt * kTile, ks);
             }
 #pragma unroll
-            for (int f = 0; f < 4; ++f) {
+            for (int f = 0; f < F; ++f) {
                 store_key(p.g_b, tr0, 64 * nt + n0 + 8 * f + q2, acc[f][0], acc[f][1]);
                 store_key(p.g_b, tr1, 64 * nt + n0 + 8 * f + q2, acc[f][2], acc[f][3]);
             }
@@ -631,7 +647,7 @@ __global__ void __launch_bounds__(kAll, NT * PT > 1 ? 1 : 2) k_decay_bwd_mma(Dec
                 add_pairs(a, sm + SM::kg + pt * kTile, ks);
             }
 #pragma unroll
-            for (int f = 0; f < 4; ++f) {
+            for (int f = 0; f < F; ++f) {
                 const int q = 64 * pt + n0 + 8 * f + q2;
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
@@ -654,10 +670,11 @@ __global__ void __launch_bounds__(kAll, NT * PT > 1 ? 1 : 2) k_decay_bwd_mma(Dec
             zero();
 #pragma unroll
             for (int ks = 0; ks < 4; ++ks) {
-                uint32_t a[4], parts[3][4], f0[4], f1[4];
+                uint32_t a[4], parts[3][4], fb[F / 2][4];
                 ldm4t(a, at_at(sm + SM::kc + nt * kTile, m0, ks, lane));
-                ldm4t(f0, at_bt(sm + SM::kg + pt * kTile, n0, ks, lane));
-                ldm4t(f1, at_bt(sm + SM::kg + pt * kTile, n0 + 16, ks, lane));
+#pragma unroll
+                for (int f = 0; f < F / 2; ++f)
+                    ldm4t(fb[f], at_bt(sm + SM::kg + pt * kTile, n0 + 16 * f, ks, lane));
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     const float2 w = *reinterpret_cast<const float2 *>(sw.e + 16 * ks + 8 * (e >> 1) + q2);
@@ -667,15 +684,15 @@ __global__ void __launch_bounds__(kAll, NT * PT > 1 ? 1 : 2) k_decay_bwd_mma(Dec
                     for (int k = 0; k < 3; ++k) parts[k][e] = o[k];
                 }
 #pragma unroll
-                for (int k = 0; k < 3; ++k) {
-                    mma(acc[0], parts[k], f0[0], f0[1]);
-                    mma(acc[1], parts[k], f0[2], f0[3]);
-                    mma(acc[2], parts[k], f1[0], f1[1]);
-                    mma(acc[3], parts[k], f1[2], f1[3]);
-                }
+                for (int k = 0; k < 3; ++k)
+#pragma unroll
+                    for (int f = 0; f < F / 2; ++f) {
+                        mma(acc[2 * f], parts[k], fb[f][0], fb[f][1]);
+                        mma(acc[2 * f + 1], parts[k], fb[f][2], fb[f][3]);
+                    }
             }
 #pragma unroll
-            for (int f = 0; f < 4; ++f)
+            for (int f = 0; f < F; ++f)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) R[nt][pt][f][e] = fmaf(aend, R[nt][pt][f][e], acc[f][e]);
         });
@@ -685,7 +702,7 @@ __global__ void __launch_bounds__(kAll, NT * PT > 1 ? 1 : 2) k_decay_bwd_mma(Dec
         float *out = p.g_h0 + bh * np;
         each([&](int nt, int pt) {
 #pragma unroll
-            for (int f = 0; f < 4; ++f)
+            for (int f = 0; f < F; ++f)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     const int n = 64 * nt + m0 + g + 8 * (e >> 1), q = 64 * pt + n0 + 8 * f + q2 + (e & 1);
@@ -701,7 +718,7 @@ cudaError_t go(const DecayParams &p, cudaStream_t st) {
     constexpr int smem = (int)Smem<NT, PT>::kTotal;
     const cudaError_t e = allow_smem((const void *)k_decay_bwd_mma<NT, PT>, smem, set);
     if (e != cudaSuccess) return e;
-    k_decay_bwd_mma<NT, PT><<<dim3((unsigned)((int64_t)p.B * p.H * p.nseg)), kAll, smem, st>>>(p);
+    k_decay_bwd_mma<NT, PT><<<dim3((unsigned)((int64_t)p.B * p.H * p.nseg)), Smem<NT, PT>::kAll, smem, st>>>(p);
     return cudaGetLastError();
 }
 

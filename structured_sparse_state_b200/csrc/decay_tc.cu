@@ -67,7 +67,8 @@ struct __align__(16) Decays {
 
 // Sets of decays.  The state gives one back a whole chunk after the operand's
 // builders; with two sets the decays, the operand and its products of a chunk
-// stood in one line behind that (the state alone: 1.45 us a chunk, with four XX).
+// stood in one line behind that (training step of 32 heads x 16384, 64 x 64:
+// 603 us with two, 597 with four).
 constexpr int kNDec = 4;
 
 // Barriers: four slots of each kind (chunk i: slot i & 3, phase i >> 2, so
