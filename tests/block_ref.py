@@ -86,7 +86,8 @@ def decay_bounds(dtype, N, P, L, mag, roundings):
     """{output: largest error}, elementwise, from the sums of magnitudes.
 
     fp32 roundings of a term: the chain of additions over a chunk's steps (at
-    most 64) and over the widths N and P, the decay (exponent rounded to fp32:
+    most 64: 32 one by one, or on the tensor cores 128 in eight additions of
+    each of three parts, truncated and so of two units) and over the widths N and P, the decay (exponent rounded to fp32:
     at most 126 ln 2 units before the decay underflows, plus 4), once per
     chunk on the way 4 more, and 16 for the products around them.
     `roundings` bf16 roundings where the tensor cores take a decayed score or

@@ -39,6 +39,16 @@ CASES = [
     (BF, 2, 2, 2, 200, 64, 128, "bhl", "head", True, True),
     (BF, 1, 2, 1, 513, 128, 128, "bhl", "step", False, False),
     (BF, 1, 1, 1, 3000, 48, 40, "bhl", "step", True, False),
+    # widths in different units of 32 and 64, several segments, odd widths
+    (F32, 1, 2, 2, 300, 128, 32, "bhl", "step", True, False),
+    (F32, 2, 2, 1, 250, 40, 128, "blh", "step", True, True),
+    (F32, 1, 3, 3, 140, 24, 50, "bhl", "head", False, False),
+    (BF, 2, 4, 2, 1500, 100, 72, "blh", "step", True, True),
+    (BF, 1, 2, 2, 1300, 128, 128, "bhl", "head", True, False),
+    (BF, 1, 2, 1, 1200, 65, 31, "blh", "step", True, False),
+    (BF, 2, 2, 2, 700, 17, 127, "bhl", "step", False, True),
+    (BF, 3, 3, 1, 1, 1, 1, "blh", "head", True, False),
+    (BF, 1, 2, 2, 640, 64, 9, "blh", "step", True, False),
 ]
 
 
@@ -270,6 +280,25 @@ def test_pointers_off_the_16_byte_grid(offset):
         assert torch.equal(got[n], want[n]), n
 
 
+def test_odd_widths_at_other_addresses_in_the_adjoint():
+    """The adjoint of rows of odd width, with inputs that the forward saw at
+    addresses off the 16-byte grid."""
+    t = make(BF, 2, 2, 1, 130, 31, 24, "blh", "step", True, False, seed=12)
+    want = fwd_bwd(t, "blh")
+    moved = dict(t)
+    for n in ("c", "b", "x"):
+        room = torch.empty(t[n].numel() + 8, dtype=BF, device="cuda")
+        moved[n] = room[1:1 + t[n].numel()].view(t[n].shape)
+        moved[n].copy_(t[n])
+    y, _, ws = pd.pdssm_decay_scan_fwd(moved["c"], moved["b"], moved["x"], t["log_a"], t["h0"],
+                                       layout="blh", for_bwd=True)
+    assert torch.equal(y, want["y"])
+    g = pd.pdssm_decay_scan_bwd(t["c"], t["b"], t["x"], t["log_a"], t["h0"], t["g_y"], ws,
+                                g_hlast=t["g_hlast"], layout="blh")
+    for got, n in zip(g, ("g_c", "g_b", "g_x", "g_log_a", "g_h0")):
+        assert torch.equal(got, want[n]), n
+
+
 # ----------------------------------------------------------------------------
 # single tokens
 # ----------------------------------------------------------------------------
@@ -281,6 +310,13 @@ STEPS = [
     (BF, 130, 140, 2, 2, 32, 63, "step"),
     (BF, 2, 2, 2, 2, 128, 128, "head"),
     (F32, 4, 4, 2, 2, 100, 7, "step"),
+    # several heads per CTA, the last one with fewer
+    (F32, 5, 6, 7, 7, 8, 16, "step"),
+    (BF, 9, 9, 18, 6, 16, 64, "step"),
+    (F32, 2, 3, 40, 8, 1, 4, "head"),
+    (BF, 3, 5, 33, 11, 16, 8, "head"),
+    (F32, 2, 2, 9, 3, 5, 3, "step"),
+    (BF, 600, 601, 3, 3, 16, 64, "step"),
 ]
 
 

@@ -22,6 +22,12 @@ CASES = [
     (F32, 2, 63, 3, 7, 33, 1.5, True),
     (F32, 3, 100, 2, 32, 256, 0.5, False),
     (F32, 1, 1000, 5, 8, 64, 2.0, False),
+    # several groups of heads, split over CTAs or not; many tiles per CTA
+    (F32, 1, 1, 16, 32, 64, 1.0, False),
+    (F32, 2, 30, 19, 7, 24, 1.0, True),
+    (F32, 4, 1200, 16, 8, 200, 1.0, False),
+    (F32, 1, 30000, 3, 2, 128, 1.0, False),
+    (F32, 3, 50, 5, 31, 250, 0.5, False),
     (BF, 2, 64, 4, 16, 128, 1.0, False),
     (BF, 1, 65, 1, 2, 16, 1.0, False),
     (BF, 4, 301, 3, 16, 96, 1.0, True),
