@@ -130,20 +130,26 @@ __device__ __forceinline__ float row_reduce(float v, float *red, OP op) {
     return v;
 }
 
-// The sum alone, with one barrier: the caller alternates between two buffers,
-// so that a buffer is written again only after the next call's barrier.
-template <int TPR>
-__device__ __forceinline__ float row_sum_once(float v, float *red) {
+// The sums alone, of NR rows, with one barrier: the caller alternates between
+// two buffers, so that a buffer is written again only after the next call's
+// barrier.
+template <int TPR, int NR>
+__device__ __forceinline__ void row_sums_once(float (&v)[NR], float *red) {
 #pragma unroll
-    for (int d = 16; d; d >>= 1) v += __shfl_xor_sync(kFull, v, d);
-    if constexpr (TPR > 32) {
-        if (threadIdx.x % 32 == 0) red[threadIdx.x / 32] = v;
-        __syncthreads();
-        v = red[0];
+    for (int k = 0; k < NR; ++k) {
 #pragma unroll
-        for (int w = 1; w < TPR / 32; ++w) v += red[w];
+        for (int d = 16; d; d >>= 1) v[k] += __shfl_xor_sync(kFull, v[k], d);
+        if (TPR > 32 && threadIdx.x % 32 == 0) red[k * (TPR / 32) + threadIdx.x / 32] = v[k];
     }
-    return v;
+    if constexpr (TPR > 32) {
+        __syncthreads();
+#pragma unroll
+        for (int k = 0; k < NR; ++k) {
+            v[k] = red[k * (TPR / 32)];
+#pragma unroll
+            for (int w = 1; w < TPR / 32; ++w) v[k] += red[k * (TPR / 32) + w];
+        }
+    }
 }
 
 struct NormParams {
@@ -158,8 +164,12 @@ struct NormParams {
 
 constexpr int kRowValues = 32;      // most values of a row per thread
 
-// TPR = 32: a warp per row, 4 rows per CTA; else a CTA per row.
-template <int TPR, int V>
+// TPR = 32: a warp per row, 4 rows per CTA; else a CTA per row.  A thread takes
+// pieces of V values.  SHIFT: rows of a width that is no multiple of 8, whose
+// first pieces start before the row, so that every piece lies on its 8 values;
+// the row's first and last pieces go value by value (2020 rows of 4143 bf16
+// values: 30 us, all values by themselves 95).
+template <int TPR, int V, bool SHIFT>
 __global__ void __launch_bounds__(TPR == 32 ? 128 : TPR) k_add_rmsnorm(NormParams p) {
     constexpr int NV = kRowValues / V;
     __shared__ float red[32];
@@ -167,28 +177,50 @@ __global__ void __launch_bounds__(TPR == 32 ? 128 : TPR) k_add_rmsnorm(NormParam
     const int64_t row = TPR == 32 ? (int64_t)blockIdx.x * 4 + threadIdx.x / 32 : blockIdx.x;
     if (row >= p.rows) return;          // TPR = 32 only, where no barrier follows
     const int64_t base = row * p.D;
+    const int shift = SHIFT ? (int)(base & 7) : 0;
+    auto col_of = [&](int i) { return (i * TPR + lane) * V - shift; };
+    auto whole = [&](int col) { return !SHIFT || (col >= 0 && col + V <= p.D); };
+    auto load = [&](float (&v)[V], const void *src, int64_t from, int col, int dt) {
+        if (whole(col)) {
+            load_vec<V>(v, src, from + col, dt);
+        } else {
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                float one[1] = {0.f};
+                if (col + j >= 0 && col + j < p.D) load_vec<1>(one, src, from + col + j, dt);
+                v[j] = one[0];
+            }
+        }
+    };
+    auto store = [&](const float (&v)[V], void *dst, int col, int dt) {
+        if (whole(col)) {
+            store_vec<V>(v, dst, base + col, dt);
+        } else {
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                const float one[1] = {v[j]};
+                if (col + j >= 0 && col + j < p.D) store_vec<1>(one, dst, base + col + j, dt);
+            }
+        }
+    };
     float s[NV][V];
     float sum = 0.f;
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        const int col = (i * TPR + lane) * V;
-        if (col < p.D) load_vec<V>(s[i], p.x, base + col, p.x_dt);
-    }
+    for (int i = 0; i < NV; ++i)
+        if (col_of(i) < p.D) load(s[i], p.x, base, col_of(i), p.x_dt);
     if (p.residual) {
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            const int col = (i * TPR + lane) * V;
-            if (col >= p.D) continue;
+            if (col_of(i) >= p.D) continue;
             float r[V];
-            load_vec<V>(r, p.residual, base + col, p.res_dt);
+            load(r, p.residual, base, col_of(i), p.res_dt);
 #pragma unroll
             for (int j = 0; j < V; ++j) s[i][j] += r[j];
         }
     }
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-        const int col = (i * TPR + lane) * V;
-        if (col >= p.D) continue;
+        if (col_of(i) >= p.D) continue;
         if (p.res_dt == PDSSM_BF16) {   // the norm is of the rounded sum
 #pragma unroll
             for (int j = 0; j < V; ++j) s[i][j] = __bfloat162float(__float2bfloat16_rn(s[i][j]));
@@ -202,17 +234,28 @@ __global__ void __launch_bounds__(TPR == 32 ? 128 : TPR) k_add_rmsnorm(NormParam
     float top = 0.f;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-        const int col = (i * TPR + lane) * V;
+        const int col = col_of(i);
         if (col >= p.D) continue;
-        if (p.res_out) store_vec<V>(s[i], p.res_out, base + col, p.res_dt);
+        if (p.res_out) store(s[i], p.res_out, col, p.res_dt);
         float w[V];
-        load_vec<V>(w, p.weight, col, p.w_dt);
+        if constexpr (SHIFT) {
+            const bool f32 = p.w_dt == PDSSM_F32;
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                const int c = min(max(col + j, 0), p.D - 1);
+                w[j] = f32 ? __ldg((const float *)p.weight + c)
+                           : __bfloat162float(((const __nv_bfloat16 *)p.weight)[c]);
+            }
+        } else {
+            load_vec<V>(w, p.weight, col, p.w_dt);
+        }
 #pragma unroll
         for (int j = 0; j < V; ++j) {
             s[i][j] = s[i][j] * rstd * w[j];
+            if (SHIFT && (col + j < 0 || col + j >= p.D)) s[i][j] = 0.f;    // no part of the row
             top = max_nan(top, fabsf(s[i][j]));
         }
-        if (p.out_dt != PDSSM_E4M3) store_vec<V>(s[i], p.out, base + col, p.out_dt);
+        if (p.out_dt != PDSSM_E4M3) store(s[i], p.out, col, p.out_dt);
     }
     if (p.out_dt != PDSSM_E4M3) return;
     top = row_reduce<TPR>(top, red, MaxOp());
@@ -221,11 +264,10 @@ __global__ void __launch_bounds__(TPR == 32 ? 128 : TPR) k_add_rmsnorm(NormParam
     if (lane == 0) p.scale[row] = scale;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-        const int col = (i * TPR + lane) * V;
-        if (col >= p.D) continue;
+        if (col_of(i) >= p.D) continue;
 #pragma unroll
         for (int j = 0; j < V; ++j) s[i][j] = s[i][j] / scale;
-        store_vec<V>(s[i], p.out, base + col, p.out_dt);
+        store(s[i], p.out, col_of(i), p.out_dt);
     }
 }
 
@@ -239,16 +281,18 @@ struct NormBwdParams {
     int g_dt, res_dt, w_dt;
 };
 
-constexpr int kBwdValues = 16;      // values of a row per thread
+constexpr int kBwdValues = 16;      // values per thread: of one row, or of two
 
-// TPR = 32: 4 warps per CTA, a row per warp at a time; else a row per CTA.
-// The weights are read again for every row (from L1): held in registers they
-// would cost a CTA per SM.
-template <int TPR, int V, int GD, int RD>
+// TPR = 32: 4 warps per CTA, a row per warp at a time; else a row per CTA, or
+// NR rows of at most kBwdValues / NR values per thread (65536 rows of 1024 in
+// bf16: one row, 24 bytes of three tensors per thread in flight, 161 us; two
+// 144, and with the next rows prefetched 111).  The weights are read again for every row (from L1): held in registers
+// they would cost a CTA per SM.
+template <int TPR, int V, int GD, int RD, int NR>
 __global__ void __launch_bounds__(TPR == 32 ? 128 : TPR, TPR <= 128 ? 5 : TPR == 256 ? 2 : 1)
     k_add_rmsnorm_bwd(NormBwdParams p) {
-    constexpr int NV = kBwdValues / V;
-    constexpr int RPC = TPR == 32 ? 4 : 1;
+    constexpr int NV = kBwdValues / NR / V;
+    constexpr int RPC = TPR == 32 ? 4 : NR;
     __shared__ float red[64];
     __shared__ float comb[TPR == 32 ? 4 * 32 * kBwdValues : 1];
     const int lane = TPR == 32 ? threadIdx.x % 32 : threadIdx.x;
@@ -259,53 +303,66 @@ __global__ void __launch_bounds__(TPR == 32 ? 128 : TPR, TPR <= 128 ? 5 : TPR ==
 #pragma unroll
         for (int j = 0; j < V; ++j) gw[i][j] = 0.f;
     int turn = 0;
-    for (int64_t row = (int64_t)blockIdx.x * RPC + sub; row < p.rows;
-         row += (int64_t)gridDim.x * RPC) {
-        const int64_t base = row * p.D;
-        const float rstd = p.rstd[row];
-        float g[NV][V], h[NV][V], r[NV][V];
-        float dot = 0.f;
+    for (int64_t row0 = (int64_t)blockIdx.x * RPC + sub; row0 < p.rows;
+         row0 += (int64_t)gridDim.x * RPC) {
+        float g[NR][NV][V], h[NR][NV][V], r[NR][NV][V], rstd[NR], dot[NR];
+        auto each = [&](auto &&f) {         // f(k, i, col) of the values there are
 #pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const int col = (i * TPR + lane) * V;
-            if (col >= p.D) continue;
-            load_vec<V>(g[i], p.g_out, base + col, GD);
-            load_vec<V>(h[i], p.s, base + col, RD);
+            for (int k = 0; k < NR; ++k)
+#pragma unroll
+                for (int i = 0; i < NV; ++i) {
+                    const int col = (i * TPR + lane) * V;
+                    if (col < p.D && (NR == 1 || row0 + k < p.rows)) f(k, i, col);
+                }
+        };
+#pragma unroll
+        for (int k = 0; k < NR; ++k) {
+            rstd[k] = NR == 1 || row0 + k < p.rows ? p.rstd[row0 + k] : 0.f;
+            dot[k] = 0.f;
         }
-        if (p.g_res) {
-#pragma unroll
-            for (int i = 0; i < NV; ++i) {
-                const int col = (i * TPR + lane) * V;
-                if (col < p.D) load_vec<V>(r[i], p.g_res, base + col, RD);
-            }
+        each([&](int k, int i, int col) {
+            load_vec<V>(g[k][i], p.g_out, (row0 + k) * p.D + col, GD);
+            load_vec<V>(h[k][i], p.s, (row0 + k) * p.D + col, RD);
+        });
+        if (p.g_res)
+            each([&](int k, int i, int col) {
+                load_vec<V>(r[k][i], p.g_res, (row0 + k) * p.D + col, RD);
+            });
+        // the next turn's rows on their way to L2
+        const int64_t next = row0 + (int64_t)gridDim.x * RPC;
+        if (next < p.rows) {
+            const int64_t n = NR == 1 ? p.D : imin64(NR, p.rows - next) * p.D;
+            auto ahead = [&](const void *t, int size) {
+                const char *at = (const char *)t + next * p.D * size;
+                for (int64_t o = lane * 128; o < n * size; o += TPR * 128)
+                    asm volatile("prefetch.global.L2 [%0];" ::"l"(at + o));
+            };
+            ahead(p.g_out, GD == PDSSM_F32 ? 4 : 2);
+            ahead(p.s, RD == PDSSM_F32 ? 4 : 2);
+            if (p.g_res) ahead(p.g_res, RD == PDSSM_F32 ? 4 : 2);
         }
-#pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const int col = (i * TPR + lane) * V;
-            if (col >= p.D) continue;
+        each([&](int k, int i, int col) {
             float w[V];
             load_vec<V>(w, p.weight, col, p.w_dt);
 #pragma unroll
             for (int j = 0; j < V; ++j) {
-                h[i][j] *= rstd;
-                gw[i][j] = fmaf(g[i][j], h[i][j], gw[i][j]);
-                g[i][j] *= w[j];
-                dot = fmaf(g[i][j], h[i][j], dot);
+                h[k][i][j] *= rstd[k];
+                gw[i][j] = fmaf(g[k][i][j], h[k][i][j], gw[i][j]);
+                g[k][i][j] *= w[j];
+                dot[k] = fmaf(g[k][i][j], h[k][i][j], dot[k]);
             }
-        }
-        // rows take the two halves of `red` in turn: one barrier per row
-        dot = row_sum_once<TPR>(dot, red + 32 * (turn ^= 1)) / (float)p.D;
-#pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const int col = (i * TPR + lane) * V;
-            if (col >= p.D) continue;
+        });
+        // rows take the two halves of `red` in turn: one barrier per turn
+        row_sums_once<TPR, NR>(dot, red + 32 * (turn ^= 1));
+        each([&](int k, int i, int col) {
+            const float mean = dot[k] / (float)p.D;
 #pragma unroll
             for (int j = 0; j < V; ++j) {
-                g[i][j] = (g[i][j] - h[i][j] * dot) * rstd;
-                if (p.g_res) g[i][j] += r[i][j];
+                g[k][i][j] = (g[k][i][j] - h[k][i][j] * mean) * rstd[k];
+                if (p.g_res) g[k][i][j] += r[k][i][j];
             }
-            store_vec<V>(g[i], p.g_x, base + col, RD);
-        }
+            store_vec<V>(g[k][i], p.g_x, (row0 + k) * p.D + col, RD);
+        });
     }
     if constexpr (TPR == 32) {          // the CTA's four warps hold the same columns
 #pragma unroll
@@ -355,9 +412,11 @@ int bwd_tpr(int64_t D) {
     return D <= 32 * kBwdValues ? 32 : D <= 128 * kBwdValues ? 128 : D <= 256 * kBwdValues ? 256
            : D <= 512 * kBwdValues ? 512 : 1024;
 }
+// rows of a CTA at once
+int bwd_rows(int64_t D) { return bwd_tpr(D) == 128 && D <= 64 * kBwdValues ? 2 : 1; }
 int64_t bwd_ctas(int64_t rows, int64_t D) {
     const int tpr = bwd_tpr(D);
-    const int rpc = tpr == 32 ? 4 : 1;
+    const int rpc = tpr == 32 ? 4 : bwd_rows(D);
     const int per_sm = tpr <= 128 ? 5 : tpr == 256 ? 2 : 1;     // as many as are resident
     const int64_t n = (rows + rpc - 1) / rpc, most = 148 * per_sm;
     return n < most ? (n > 0 ? n : 1) : most;
@@ -375,17 +434,18 @@ int width_of(int64_t D, std::initializer_list<const void *> ptrs) {
 }
 bool wide(int dt) { return dt == PDSSM_F32 || dt == PDSSM_BF16; }
 
-template <int V>
+template <int V, bool SHIFT>
 cudaError_t run_fwd(const NormParams &p, cudaStream_t st) {
     const unsigned rows = (unsigned)p.rows;
-    if (p.D <= 32 * kRowValues)
-        k_add_rmsnorm<32, V><<<(rows + 3) / 4, 128, 0, st>>>(p);
-    else if (p.D <= 128 * kRowValues)
-        k_add_rmsnorm<128, V><<<rows, 128, 0, st>>>(p);
-    else if (p.D <= 256 * kRowValues)
-        k_add_rmsnorm<256, V><<<rows, 256, 0, st>>>(p);
+    const int width = p.D + (SHIFT ? 7 : 0);
+    if (width <= 32 * kRowValues)
+        k_add_rmsnorm<32, V, SHIFT><<<(rows + 3) / 4, 128, 0, st>>>(p);
+    else if (width <= 128 * kRowValues)
+        k_add_rmsnorm<128, V, SHIFT><<<rows, 128, 0, st>>>(p);
+    else if (width <= 256 * kRowValues)
+        k_add_rmsnorm<256, V, SHIFT><<<rows, 256, 0, st>>>(p);
     else
-        k_add_rmsnorm<512, V><<<rows, 512, 0, st>>>(p);
+        k_add_rmsnorm<512, V, SHIFT><<<rows, 512, 0, st>>>(p);
     return cudaGetLastError();
 }
 
@@ -395,11 +455,16 @@ cudaError_t run_fwd(const NormParams &p, cudaStream_t st) {
 template <int V, int GD, int RD>
 cudaError_t run_bwd_t(const NormBwdParams &p, cudaStream_t st) {
     switch (bwd_tpr(p.D)) {
-        case 32: k_add_rmsnorm_bwd<32, V, GD, RD><<<p.ctas, 128, 0, st>>>(p); break;
-        case 128: k_add_rmsnorm_bwd<128, V, GD, RD><<<p.ctas, 128, 0, st>>>(p); break;
-        case 256: k_add_rmsnorm_bwd<256, V, GD, RD><<<p.ctas, 256, 0, st>>>(p); break;
-        case 512: k_add_rmsnorm_bwd<512, V, GD, RD><<<p.ctas, 512, 0, st>>>(p); break;
-        default: k_add_rmsnorm_bwd<1024, V, GD, RD><<<p.ctas, 1024, 0, st>>>(p); break;
+        case 32: k_add_rmsnorm_bwd<32, V, GD, RD, 1><<<p.ctas, 128, 0, st>>>(p); break;
+        case 128:
+            if (bwd_rows(p.D) == 2)
+                k_add_rmsnorm_bwd<128, V, GD, RD, 2><<<p.ctas, 128, 0, st>>>(p);
+            else
+                k_add_rmsnorm_bwd<128, V, GD, RD, 1><<<p.ctas, 128, 0, st>>>(p);
+            break;
+        case 256: k_add_rmsnorm_bwd<256, V, GD, RD, 1><<<p.ctas, 256, 0, st>>>(p); break;
+        case 512: k_add_rmsnorm_bwd<512, V, GD, RD, 1><<<p.ctas, 512, 0, st>>>(p); break;
+        default: k_add_rmsnorm_bwd<1024, V, GD, RD, 1><<<p.ctas, 1024, 0, st>>>(p); break;
     }
     return cudaGetLastError();
 }
@@ -445,9 +510,12 @@ pdssm_status pdssm_add_rmsnorm_fwd(int64_t rows, int64_t D, const void *x, pdssm
     if (!x || !weight || !out) return arg_fail(PDSSM_ERR_INVALID_ARG, "NULL tensor pointer");
     NormParams p{rows, (int)D, x, residual, weight, out, res_out, rstd, scale,
                  x_dtype, res_dtype, w_dtype, out_dtype, eps};
-    const int v = width_of(D, {x, residual, weight, res_out, out});
+    bool grid = true;
+    for (const void *q : {x, residual, (const void *)res_out, (const void *)out}) grid = grid && aligned(q, 16);
     cudaStream_t s = (cudaStream_t)stream;
-    cudaError_t e = v == 8 ? run_fwd<8>(p, s) : v == 2 ? run_fwd<2>(p, s) : run_fwd<1>(p, s);
+    cudaError_t e = grid && D % 8 == 0 && aligned(weight, 16) ? run_fwd<8, false>(p, s)
+                    : grid && D + 7 <= kMaxD                  ? run_fwd<8, true>(p, s)
+                                                              : run_fwd<1, false>(p, s);
     return e == cudaSuccess ? PDSSM_OK : cuda_fail(e, "add + norm");
 }
 

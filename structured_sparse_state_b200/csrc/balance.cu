@@ -20,19 +20,26 @@ namespace {
 
 constexpr int kBalThreads = 256;        // 16 x 16
 constexpr int kBalRows = 64;            // steps per tile
-constexpr int kBalCols = 64;            // entries per group: whole heads
-constexpr int kLdP = kBalCols + 2;
 
-int bal_heads(int K) { return kBalCols / K; }
-int bal_groups(int H, int K) { return (H + bal_heads(K) - 1) / bal_heads(K); }
+// Entries per group (whole heads): 64, or 32 where all the heads have no more
+// (4 x 9607 steps, 8 heads of 4, D = 256: 212 us, with 64 314; 16 heads of 16:
+// 1029 us, with 64 937).
+int bal_cols(int H, int K) { return H * K <= 32 ? 32 : 64; }
+int bal_heads(int H, int K) { return bal_cols(H, K) / K; }
+int bal_groups(int H, int K) {
+    const int n = bal_heads(H, K);
+    return (H + n - 1) / n;
+}
 
 // A CTA's work on one tile of steps and one group of heads in fp32: u and W
 // rows in shared memory, the logits (then softmax weights, then gradients) of
-// 64 steps x 64 entries beside them.  Per 4 of D a thread reads eight 16-byte
-// pieces for 64 multiply-adds, so the logits run at the FFMA units' rate, not
-// at shared memory's.
+// 64 steps x EC entries beside them.  Per 4 of D a thread reads eight 16-byte
+// pieces for 64 multiply-adds (EC = 32: six for 32), so the logits run at the
+// FFMA units' rate, not at shared memory's.
+template <int EC>
 struct Tile {
-    float *su, *sW, *sp;                // [64][ld], [64][ld], [64][kLdP]
+    static constexpr int kLdP = EC + 2;
+    float *su, *sW, *sp;                // [64][ld], [EC][ld], [64][kLdP]
     int *live;                          // [64]
     int ld, Dp;
     __device__ __forceinline__ Tile(float *sm, int D) {
@@ -40,16 +47,16 @@ struct Tile {
         ld = Dp + 4;                    // an odd number of 16-byte pieces
         su = sm;
         sW = su + kBalRows * ld;
-        sp = sW + kBalCols * ld;
+        sp = sW + EC * ld;
         live = reinterpret_cast<int *>(sp + kBalRows * kLdP);
     }
     // rows of D values, on their way to shared memory; zero where on(r) is false
-    template <class ON>
+    template <int ROWS, class ON>
     __device__ __forceinline__ void load(float *dst, const float *src, int D, bool vec, ON on) const {
         const uint32_t to = smem_u32(dst);
         if (vec) {
             const int pieces = Dp / 4;
-            for (int i = threadIdx.x; i < 64 * pieces; i += kBalThreads) {
+            for (int i = threadIdx.x; i < ROWS * pieces; i += kBalThreads) {
                 const int r = i / pieces, q = 4 * (i - r * pieces);
                 const bool in = q < D && on(r);
                 asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to + 4u * (r * ld + q)),
@@ -57,7 +64,7 @@ struct Tile {
                              : "memory");
             }
         } else {
-            for (int i = threadIdx.x; i < 64 * Dp; i += kBalThreads) {
+            for (int i = threadIdx.x; i < ROWS * Dp; i += kBalThreads) {
                 const int r = i / Dp, q = i - r * Dp;
                 const bool in = q < D && on(r);
                 asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(to + 4u * (r * ld + q)),
@@ -68,10 +75,10 @@ struct Tile {
     }
     __device__ __forceinline__ void load_u(const BalParams &p, int64_t r0) const {
         if (threadIdx.x < kBalRows) live[threadIdx.x] = bal_live(p, r0 + threadIdx.x);
-        load(su, (const float *)p.u + r0 * p.D, p.D, p.vec, [&](int r) { return bal_live(p, r0 + r); });
+        load<kBalRows>(su, (const float *)p.u + r0 * p.D, p.D, p.vec, [&](int r) { return bal_live(p, r0 + r); });
     }
     __device__ __forceinline__ void load_W(const BalParams &p, int e0, int ne) const {
-        load(sW, p.W + (int64_t)e0 * p.D, p.D, p.vec, [&](int r) { return r < ne; });
+        load<EC>(sW, p.W + (int64_t)e0 * p.D, p.D, p.vec, [&](int r) { return r < ne; });
     }
     __device__ __forceinline__ void landed() const {
         asm volatile("cp.async.wait_all;" ::: "memory");
@@ -80,13 +87,13 @@ struct Tile {
     // sp = inv_tau u W^T; a barrier follows
     __device__ __forceinline__ void logits(const BalParams &p) const {
         const int ty = threadIdx.x / 16, tx = threadIdx.x % 16;
-        float acc[4][4];
+        float acc[4][EC / 16];
         zero(acc);
-        tile_mm(acc, Dp, Along<4, false>{su, ld, ty}, Along<4, false>{sW, ld, tx});
+        tile_mm(acc, Dp, Along<4, false>{su, ld, ty}, Along<EC / 16, false>{sW, ld, tx});
 #pragma unroll
         for (int i = 0; i < 4; ++i)
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
+            for (int j = 0; j < EC / 16; ++j)
                 sp[strided(ty, i) * kLdP + strided(tx, j)] = acc[i][j] * p.inv_tau;
         __syncthreads();
     }
@@ -116,27 +123,29 @@ struct Tile {
     }
 };
 
-size_t bal_smem(int D) {
-    return (size_t)((kBalRows + kBalCols) * ((D + 7) / 8 * 8 + 4) + kBalRows * kLdP + kBalRows) * 4;
+size_t bal_smem(int D, int cols) {
+    return (size_t)((kBalRows + cols) * ((D + 7) / 8 * 8 + 4) + kBalRows * (cols + 2) + kBalRows) * 4;
 }
 
 // Sums of p and counts over one slice of the steps of one group of heads.
+template <int EC>
 __global__ void __launch_bounds__(kBalThreads) k_bal_sums(BalParams p) {
     extern __shared__ float sm[];
-    __shared__ int scount[kBalCols];
-    const Tile t(sm, p.D);
+    __shared__ int scount[EC];
+    const Tile<EC> t(sm, p.D);
     const int group = blockIdx.x % p.groups, slice = blockIdx.x / p.groups;
     const int h0 = group * p.heads, nh = min(p.heads, p.H - h0), e0 = h0 * p.K, ne = nh * p.K;
-    const int col = threadIdx.x % kBalCols, rg = threadIdx.x / kBalCols;
+    constexpr int RG = kBalThreads / EC;
+    const int col = threadIdx.x % EC, rg = threadIdx.x / EC;
     t.load_W(p, e0, ne);
-    if (threadIdx.x < kBalCols) scount[threadIdx.x] = 0;
-    float sum = 0.f;                    // column col, a quarter of the rows
+    if (threadIdx.x < EC) scount[threadIdx.x] = 0;
+    float sum = 0.f;                    // column col, rows rg, rg + RG, ..
     for (int64_t r0 = (int64_t)slice * kBalRows; r0 < p.rows; r0 += (int64_t)p.slices * kBalRows) {
         __syncthreads();
         t.load_u(p, r0);
         t.landed();
         t.logits(p);
-        t.softmax<false>(p, nh, nullptr, nullptr);
+        t.template softmax<false>(p, nh, nullptr, nullptr);
         for (int i = threadIdx.x; i < kBalRows * nh; i += kBalThreads) {
             const int hh = i / kBalRows;
             const uint32_t r = (uint32_t)r0 + i % kBalRows;
@@ -146,14 +155,16 @@ __global__ void __launch_bounds__(kBalThreads) k_bal_sums(BalParams p) {
             if (kk >= 0 && kk < p.K) atomicAdd(&scount[hh * p.K + kk], 1);      // integers: any order
         }
 #pragma unroll
-        for (int r = 0; r < kBalRows / 4; ++r) sum += t.sp[(4 * r + rg) * kLdP + col];
+        for (int r = 0; r < kBalRows / RG; ++r) sum += t.sp[(RG * r + rg) * t.kLdP + col];
     }
     t.landed();                         // also where there was no tile
     t.sp[threadIdx.x] = sum;
     __syncthreads();
     if (threadIdx.x < ne) {
         const int64_t at = (int64_t)slice * p.H * p.K + e0 + threadIdx.x;
-        p.part[at] = (t.sp[col] + t.sp[64 + col]) + (t.sp[128 + col] + t.sp[192 + col]);
+        float total = 0.f;
+        for (int q = 0; q < RG; ++q) total += t.sp[q * EC + col];
+        p.part[at] = total;
         p.part_n[at] = scount[threadIdx.x];
     }
 }
@@ -194,11 +205,11 @@ __device__ __forceinline__ void bal_factors(const BalParams &p, int h0, int nh, 
 // ty + 16 i and pairs of columns, D <= DT.  A group takes about 10 us, so
 // where the tiles do not fill the GPU the groups are split over CTAs too, and
 // k_bal_gu_sum adds their sums in order.
-template <int DT>
+template <int EC, int DT>
 __global__ void __launch_bounds__(kBalThreads) k_bal_gu(BalParams p) {
     extern __shared__ float sm[];
-    __shared__ float f[kBalCols], by[kBalCols];
-    const Tile t(sm, p.D);
+    __shared__ float f[EC], by[EC];
+    const Tile<EC> t(sm, p.D);
     const int gs = blockIdx.x % p.gslices;
     const int64_t r0 = (int64_t)(blockIdx.x / p.gslices) * kBalRows;
     const int ty = threadIdx.x / 16, tx = threadIdx.x % 16;
@@ -212,9 +223,9 @@ __global__ void __launch_bounds__(kBalThreads) k_bal_gu(BalParams p) {
         bal_factors(p, h0, nh, f, by);
         t.landed();
         t.logits(p);
-        t.softmax<true>(p, nh, f, by);
+        t.template softmax<true>(p, nh, f, by);
         // entries behind the group's have zero weights, and logits that are zero
-        tile_mm(acc, kBalCols, Along2<4>{t.sp, kLdP, ty}, Across<DT / 16>{t.sW, t.ld, tx});
+        tile_mm(acc, EC, Along2<4>{t.sp, t.kLdP, ty}, Across<DT / 16>{t.sW, t.ld, tx});
     }
     float *gu = p.gslices > 1 ? p.part + gs * p.rows * p.D : (float *)p.g_u;
 #pragma unroll
@@ -246,15 +257,15 @@ __global__ void k_bal_gu_sum(BalParams p) {
 }
 
 // g_W of one group over one slice of the steps
-template <int DT>
+template <int EC, int DT>
 __global__ void __launch_bounds__(kBalThreads) k_bal_gw(BalParams p) {
     extern __shared__ float sm[];
-    __shared__ float f[kBalCols], by[kBalCols];
-    const Tile t(sm, p.D);
+    __shared__ float f[EC], by[EC];
+    const Tile<EC> t(sm, p.D);
     const int group = blockIdx.x % p.groups, slice = blockIdx.x / p.groups;
     const int h0 = group * p.heads, nh = min(p.heads, p.H - h0), ne = nh * p.K;
     const int ty = threadIdx.x / 16, tx = threadIdx.x % 16;
-    float acc[4][DT / 16];
+    float acc[EC / 16][DT / 16];
     zero(acc);
     t.load_W(p, h0 * p.K, ne);
     bal_factors(p, h0, nh, f, by);
@@ -263,12 +274,12 @@ __global__ void __launch_bounds__(kBalThreads) k_bal_gw(BalParams p) {
         t.load_u(p, r0);
         t.landed();
         t.logits(p);
-        t.softmax<true>(p, nh, f, by);
-        tile_mm(acc, kBalRows, Across<4>{t.sp, kLdP, ty}, Across<DT / 16>{t.su, t.ld, tx});
+        t.template softmax<true>(p, nh, f, by);
+        tile_mm(acc, kBalRows, Across<EC / 16>{t.sp, t.kLdP, ty}, Across<DT / 16>{t.su, t.ld, tx});
     }
     t.landed();                         // also where there was no tile
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < EC / 16; ++i) {
         const int e = pairs(ty, i);
         if (e >= ne) continue;
         float *out = p.part + ((int64_t)slice * p.H * p.K + h0 * p.K + e) * p.D;
@@ -303,30 +314,35 @@ int bal_gslices(int64_t rows, int groups) {
     return (int)(n < 1 ? 1 : n > groups ? groups : n);
 }
 
-template <void (*KERN)(BalParams)>
+template <int EC, void (*KERN)(BalParams)>
 cudaError_t launch(int64_t grid, cudaStream_t st, const BalParams &p) {
     static std::atomic<int> set[kLimitDevices];
-    const cudaError_t e = allow_smem((const void *)KERN, (int)bal_smem(kBalMaxD), set);
+    const cudaError_t e = allow_smem((const void *)KERN, (int)bal_smem(kBalMaxD, EC), set);
     if (e != cudaSuccess) return e;
-    KERN<<<dim3((unsigned)grid), kBalThreads, bal_smem(p.D), st>>>(p);
+    KERN<<<dim3((unsigned)grid), kBalThreads, bal_smem(p.D, EC), st>>>(p);
     return cudaGetLastError();
 }
 
-template <int DT>
+template <int EC, int DT>
 cudaError_t run_grads(const BalParams &p, int what, cudaStream_t st) {
-    if (what == 2) return launch<k_bal_gw<DT>>((int64_t)p.groups * p.slices, st, p);
+    if (what == 2) return launch<EC, k_bal_gw<EC, DT>>((int64_t)p.groups * p.slices, st, p);
     const int64_t tiles = (p.rows + kBalRows - 1) / kBalRows;
-    const cudaError_t e = launch<k_bal_gu<DT>>(tiles * p.gslices, st, p);
+    const cudaError_t e = launch<EC, k_bal_gu<EC, DT>>(tiles * p.gslices, st, p);
     if (e != cudaSuccess || p.gslices == 1) return e;
     k_bal_gu_sum<<<(unsigned)((p.rows * p.D + 255) / 256), 256, 0, st>>>(p);
     return cudaGetLastError();
 }
 
+template <int EC>
+cudaError_t run_cols(const BalParams &p, int what, cudaStream_t st) {
+    if (what == 0) return launch<EC, k_bal_sums<EC>>((int64_t)p.groups * p.slices, st, p);
+    if (p.D <= 64) return run_grads<EC, 64>(p, what, st);
+    if (p.D <= 128) return run_grads<EC, 128>(p, what, st);
+    return run_grads<EC, 256>(p, what, st);
+}
+
 cudaError_t run_f32(const BalParams &p, int what, cudaStream_t st) {
-    if (what == 0) return launch<k_bal_sums>((int64_t)p.groups * p.slices, st, p);
-    if (p.D <= 64) return run_grads<64>(p, what, st);
-    if (p.D <= 128) return run_grads<128>(p, what, st);
-    return run_grads<256>(p, what, st);
+    return bal_cols(p.H, p.K) == 32 ? run_cols<32>(p, what, st) : run_cols<64>(p, what, st);
 }
 
 bool aligned(const void *p, size_t a) { return ((uintptr_t)p % a) == 0; }
@@ -376,7 +392,7 @@ pdssm_status bal_common(const pdssm_dims *d, const void *u, pdssm_dtype dt, cons
     q.L = d->L; q.rows = d->B * d->L;
     q.u = u; q.W = W; q.lengths = lengths; q.inv_tau = inv_tau;
     q.slices = dt == PDSSM_BF16 ? bal_tc_plan(*d).slices : bal_slices(q.rows, bal_groups(q.H, q.K));
-    q.heads = bal_heads(q.K);
+    q.heads = bal_heads(q.H, q.K);
     q.groups = bal_groups(q.H, q.K);
     q.gslices = bal_gslices(q.rows, q.groups);
     q.vec = q.D % 4 == 0 && aligned(u, 16) && aligned(W, 16);

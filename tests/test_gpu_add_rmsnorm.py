@@ -18,7 +18,9 @@ def _need_gpu():
 
 
 BF, F32, E4 = torch.bfloat16, torch.float32, torch.float8_e4m3fn
-WIDTHS = [1, 7, 96, 512, 513, 1000, 1024, 1032, 2048, 4096, 4100, 5120, 8192, 9000, 16384]
+WIDTHS = [1, 7, 96, 512, 513, 1000, 1024, 1032, 2048, 4096, 4100, 5120, 8192, 9000, 16384,
+          # odd widths, around the sizes where a row takes more threads
+          9, 1018, 1023, 2047, 4091, 16373, 16379]
 
 
 def normal(g, *shape, dtype=F32, by=1.0):
@@ -89,9 +91,18 @@ def test_row_counts(rows):
 @pytest.mark.parametrize("types", [(F32, F32), (BF, BF), (BF, F32)], ids=str)
 @pytest.mark.parametrize("with_res", [False, True])
 def test_backward(D, types, with_res):
-    g_t, r_t = types
+    check_backward(37, D, *types, with_res)
+
+
+@pytest.mark.parametrize("D", [96, 640, 1001, 1024, 2048])
+@pytest.mark.parametrize("types", [(F32, F32), (BF, BF)], ids=str)
+def test_backward_of_many_rows(D, types):
+    """Several turns of every CTA, the last one with fewer rows."""
+    check_backward(3001, D, *types, True)
+
+
+def check_backward(rows, D, g_t, r_t, with_res):
     g = torch.Generator(device="cuda").manual_seed(D + 1)
-    rows = 37
     s, g_out = normal(g, rows, D, dtype=r_t, by=2.0), normal(g, rows, D, dtype=g_t)
     w = (1 + normal(g, D, by=0.2)).to(BF if D % 2 else F32)
     rstd = (s.double().square().mean(-1) + 1e-5).rsqrt().float()
@@ -130,7 +141,7 @@ def test_gradients_against_differences():
 
 def test_in_place_and_same_bits():
     g = torch.Generator(device="cuda").manual_seed(4)
-    for D in (96, 1000, 2048):
+    for D in (96, 1000, 1001, 2048, 4099):
         x, res, w = normal(g, 50, D, dtype=BF), normal(g, 50, D, dtype=BF), normal(g, D)
         out, s, rstd, _ = pd.pdssm_add_rmsnorm_fwd(x, res, w)
         x2, r2 = x.clone(), res.clone()
