@@ -170,7 +170,7 @@ constexpr int kRowValues = 32;      // most values of a row per thread
 // the row's first and last pieces go value by value (2020 rows of 4143 bf16
 // values: 30 us, all values by themselves 95).
 template <int TPR, int V, bool SHIFT>
-__global__ void __launch_bounds__(TPR == 32 ? 128 : TPR) k_add_rmsnorm(NormParams p) {
+__global__ void __launch_bounds__(TPR == 32 ? 128 : TPR, TPR == 128 && V == 8 ? 8 : 0) k_add_rmsnorm(NormParams p) {
     constexpr int NV = kRowValues / V;
     __shared__ float red[32];
     const int lane = TPR == 32 ? threadIdx.x % 32 : threadIdx.x;
