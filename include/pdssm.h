@@ -504,8 +504,10 @@ typedef enum pdssm_layout { PDSSM_BHL = 0, PDSSM_BLH = 1 } pdssm_layout;
  *    run on the tensor cores: the decayed products (c . b) and the state read
  *    by c are rounded to bf16 there; the state itself is not.
  *  * Limits: 1 <= N, P <= 128; B, H, G >= 1, H a multiple of G, L >= 0.
- *  * for_bwd = 1 also leaves in ws the state at every chunk's start, which
- *    pdssm_decay_scan_bwd needs.  ws: pdssm_decay_workspace_bytes(dims,
+ *  * bf16 rows whose width is not a multiple of 8 are copied to padded ones
+ *    in ws first.
+ *  * for_bwd = 1 also leaves in ws the state at every chunk's start (and the
+ *    padded rows), which pdssm_decay_scan_bwd needs.  ws: pdssm_decay_workspace_bytes(dims,
  *    dtype, for_bwd) bytes, 256-byte aligned, overwritten; pdssm_ws_status
  *    reads its status word.
  * Deterministic: every sum in a fixed order.

@@ -11,7 +11,9 @@
 // The backward's CTAs are persistent: each thread owns the same columns of
 // every row it sees and sums its share of g_w in registers; a CTA's sums go to
 // scratch and a second kernel adds the CTAs in order, so the result does not
-// depend on timing.
+// depend on timing.  Of the measured copy rate the forward reaches 0.92 (65536 x
+// 1024 bf16, 87 us) to 0.94 (16384 x 2048, fp32 stream, 66 us), the backward
+// 0.88 (16384 x 2048, fp32 stream, 82 us) and 0.74 (65536 x 1024 bf16, 111 us).
 #include <cuda_fp8.h>
 
 #include <initializer_list>
@@ -85,12 +87,8 @@ __device__ __forceinline__ void store_vec(const float (&v)[V], void *p, int64_t 
     } else if constexpr (V == 2) {
         if (dt == PDSSM_F32)
             *reinterpret_cast<float2 *>((float *)p + at) = make_float2(v[0], v[1]);
-        else if (dt == PDSSM_BF16)
-            *reinterpret_cast<unsigned *>((__nv_bfloat16 *)p + at) = pack_bf16(v[0], v[1]);
         else
-            *reinterpret_cast<unsigned short *>((unsigned char *)p + at) =
-                (unsigned short)__nv_cvt_float2_to_fp8x2(make_float2(v[0], v[1]), __NV_SATFINITE,
-                                                         __NV_E4M3);
+            *reinterpret_cast<unsigned *>((__nv_bfloat16 *)p + at) = pack_bf16(v[0], v[1]);
     } else {
         if (dt == PDSSM_F32)
             ((float *)p)[at] = v[0];
@@ -285,9 +283,9 @@ constexpr int kBwdValues = 16;      // values per thread: of one row, or of two
 
 // TPR = 32: 4 warps per CTA, a row per warp at a time; else a row per CTA, or
 // NR rows of at most kBwdValues / NR values per thread (65536 rows of 1024 in
-// bf16: one row, 24 bytes of three tensors per thread in flight, 161 us; two
-// 144, and with the next rows prefetched 111).  The weights are read again for every row (from L1): held in registers
-// they would cost a CTA per SM.
+// bf16: one row, too little in flight, 161 us; two 144, and with the next rows
+// prefetched 111).  The weights are read again for every row (from L1): held in
+// registers they would cost a CTA per SM.
 template <int TPR, int V, int GD, int RD, int NR>
 __global__ void __launch_bounds__(TPR == 32 ? 128 : TPR, TPR <= 128 ? 5 : TPR == 256 ? 2 : 1)
     k_add_rmsnorm_bwd(NormBwdParams p) {

@@ -18,8 +18,10 @@
 //           a CTA's 14 tiles that cost 5.6e-6 of g_W's norm)
 // L is double-buffered: the next tile's products run under this one's softmax.
 //
-// Bound: tensor pipe and the softmax's issue slots, about equal; u is read
-// once per group (from L2 after the first).
+// Bound: tensor pipe and the softmax's issue slots, about equal (leaving out a
+// third of g_u's logit products changed its time by less than 1 %); u is read
+// once per group (from L2 after the first).  8 x 16384 steps, 16 heads of 16
+// entries, D = 128: sums 40 us, g_u 71, g_W 93.
 #include <string.h>
 
 #include "balance.cuh"

@@ -5,7 +5,8 @@
 //
 // Bound: shared-memory bandwidth.  Both orientations of a product are read by
 // 16- or 8-byte loads (see Along and Across): about half of the wavefronts and
-// a third of the instructions of 4-byte loads.
+// a third of the instructions of 4-byte loads.  64 heads x 1024 steps of 64 x
+// 64: forward 144 us, forward and adjoint 506 us.
 #include "decay.cuh"
 #include "launch.cuh"
 #include "tile_mm.cuh"

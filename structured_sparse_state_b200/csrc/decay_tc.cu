@@ -27,12 +27,19 @@
 // where the product does not.
 //
 // Warps: 0-3 and 4-7 take chunks in turn (steps 2 and 5), 8-15 hold the state
-// (32 columns each), 16-23 build the split operand, 24-27 issue the
-// products (scores; Yi and Y; two for the state: one thread would hold each of
-// them back by the others' waits, and takes about 100 cycles per product), 28 the copies, 29 and 30 compute the decays in turn.  Accumulators, decays and (N <= 64) split parts are double-buffered,
-// c and b tiles three deep (N <= 64; the scores of chunk i + 1 run ahead of
-// the rest of chunk i, so two stages would expose each copy's latency), all
-// handed over by mbarriers.
+// (32 columns each), 16-23 build the split operand, 24-27 issue the products
+// (scores; Yi and Y; two for the state: one thread would hold each of them back
+// by the others' waits, and takes about 100 cycles per product), 28 makes the
+// copies, 29 and 30 compute the decays in turn.  Accumulators and (N <= 64)
+// split parts are double-buffered, c and b tiles three deep (N <= 64; the
+// scores of chunk i + 1 run ahead of the rest of chunk i, so two stages would
+// expose each copy's latency), all handed over by mbarriers.
+//
+// Bound: shared memory.  A chunk of 64 x 64 moves 330 KB through it (products'
+// operands 210, split parts 64, copies 48), 2600 of the 4200 cycles that a chunk
+// takes, and the tensor pipe is busy for 1900; the rest is the hand-overs
+// between the roles.  128 heads x 16384 steps: 297 us, 3.6 TB/s; the state alone
+// 2500 cycles a chunk for 1900 of shared memory.
 #include <string.h>
 
 #include "decay.cuh"
