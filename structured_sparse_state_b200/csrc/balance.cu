@@ -171,19 +171,32 @@ __global__ void __launch_bounds__(kBalThreads) k_bal_sums(BalParams p) {
     }
 }
 
-// counts, probs and loss of one head from the slices' sums
-__global__ void k_bal_loss(BalParams p, float *loss, int32_t *counts, float *probs) {
-    const int h = blockIdx.x, k = threadIdx.x;
-    const int64_t T = bal_steps(p);
-    const double inv = T > 0 ? 1.0 / (double)T : 0.0;
+// counts, probs and loss of one head from the slices' sums: a warp takes every
+// kSumWays-th slice, and the warps' sums are added in order
+constexpr int kSumWays = 8;
+__global__ void __launch_bounds__(32 * kSumWays) k_bal_loss(BalParams p, float *loss, int32_t *counts,
+                                                            float *probs) {
+    __shared__ double sums[kSumWays][32];
+    __shared__ int ns[kSumWays][32];
+    const int h = blockIdx.x, k = threadIdx.x % 32, way = threadIdx.x / 32;
     double s = 0.0;
     int n = 0;
     if (k < p.K)
-        for (int q = 0; q < p.slices; ++q) {
+        for (int q = way; q < p.slices; q += kSumWays) {
             const int64_t at = ((int64_t)q * p.H + h) * p.K + k;
             s += (double)p.part[at];
             n += p.part_n[at];
         }
+    sums[way][k] = s;
+    ns[way][k] = n;
+    __syncthreads();
+    if (way) return;
+    for (int w = 1; w < kSumWays; ++w) {
+        s += sums[w][k];
+        n += ns[w][k];
+    }
+    const int64_t T = bal_steps(p);
+    const double inv = T > 0 ? 1.0 / (double)T : 0.0;
     if (k < p.K) {
         counts[h * p.K + k] = n;
         probs[h * p.K + k] = (float)(s * inv);
@@ -291,13 +304,19 @@ __global__ void __launch_bounds__(kBalThreads) k_bal_gw(BalParams p) {
     }
 }
 
-// g_W: the slices' sums in order
-__global__ void k_bal_gw_sum(BalParams p, float *g_W) {
+// g_W: the slices' sums, likewise
+__global__ void __launch_bounds__(32 * kSumWays) k_bal_gw_sum(BalParams p, float *g_W) {
+    __shared__ float sums[kSumWays][32];
     const int64_t n = (int64_t)p.H * p.K * p.D;
-    const int64_t e = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
-    if (e >= n) return;
+    const int lane = threadIdx.x % 32, way = threadIdx.x / 32;
+    const int64_t e = (int64_t)blockIdx.x * 32 + lane;
     float s = 0.f;
-    for (int q = 0; q < p.slices; ++q) s += p.part[q * n + e];
+    if (e < n)
+        for (int q = way; q < p.slices; q += kSumWays) s += p.part[q * n + e];
+    sums[way][lane] = s;
+    __syncthreads();
+    if (way || e >= n) return;
+    for (int w = 1; w < kSumWays; ++w) s += sums[w][lane];
     g_W[e] = s;
 }
 
@@ -444,7 +463,7 @@ pdssm_status pdssm_select_balance_fwd(const pdssm_dims *dims, const void *u, pds
     cudaStream_t s = (cudaStream_t)stream;
     cudaError_t e = run_any(*dims, p, u_dtype, 0, s);
     if (e != cudaSuccess) return cuda_fail(e, "balance sums");
-    k_bal_loss<<<p.H, 32, 0, s>>>(p, loss, counts, probs);
+    k_bal_loss<<<p.H, 32 * kSumWays, 0, s>>>(p, loss, counts, probs);
     e = cudaGetLastError();
     return e == cudaSuccess ? PDSSM_OK : cuda_fail(e, "balance loss");
 }
@@ -472,7 +491,7 @@ pdssm_status pdssm_select_balance_bwd(const pdssm_dims *dims, const void *u, pds
         e = run_any(*dims, p, u_dtype, 2, s);
         if (e != cudaSuccess) return cuda_fail(e, "balance g_W");
         const int64_t n = (int64_t)p.H * p.K * p.D;
-        k_bal_gw_sum<<<(unsigned)((n + 255) / 256), 256, 0, s>>>(p, g_W);
+        k_bal_gw_sum<<<(unsigned)((n + 31) / 32), 32 * kSumWays, 0, s>>>(p, g_W);
         e = cudaGetLastError();
         if (e != cudaSuccess) return cuda_fail(e, "balance g_W sum");
     }
