@@ -5,8 +5,9 @@
 // memory as three bf16 parts (8 + 8 + 8 bits of fp32), so that the logits
 //     L = u W^T            128 rows x N, K = D, three products
 // have fp32 accuracy (u is bf16 by itself); the small parts are multiplied
-// first, since a product's additions truncate the sum so far.  Eight warps take a finished L
-// from TMEM, a row and half of its columns per thread: softmax per head, then
+// first, since a product's additions truncate the sum so far.  Sixteen warps (N = 64: eight)
+// take a finished L from TMEM, a row and 32 of its columns per thread: softmax per
+// head, then
 //   sums    column sums of p over the rows, in registers over the CTA's tiles;
 //           counts by shared-memory atomics (integers)
 //   g_u     G, the logits' gradients, back to TMEM as bf16, and
@@ -32,8 +33,8 @@ namespace pdssm {
 namespace {
 
 enum { kSums = 0, kGu = 1, kGw = 2 };
-constexpr int kEpi = 8;                         // softmax warps
-constexpr int kTh = (kEpi + 2) * 32;            // + products, + copies
+// softmax warps of a group of N entries: 4 by rows times N / 32 by entries
+__host__ __device__ constexpr int epi_of(int N) { return N / 8; }
 constexpr int kRows = 128;
 
 enum { kUFull, kWFull, kLFull, kGReady, kGHalf, kGThird, kDone, kGuFull, kGuFree, kBars };
@@ -93,9 +94,11 @@ __device__ __forceinline__ void softmax32(float (&v)[32], int K, float scale, bo
     }
 }
 
-template <int KT, int MODE>
-__global__ void __launch_bounds__(kTh, 1)
+template <int KT, int MODE, int N>
+__global__ void __launch_bounds__((epi_of(N) + 2) * 32, 1)
     k_bal_tc(const __grid_constant__ CUtensorMap umap, const TcP t) {
+    constexpr int kEpi = epi_of(N), kTh = (kEpi + 2) * 32;      // + products, + copies
+    constexpr int kBlocks = N / 32;                             // of 32 entries
     const BalParams &p = t.p;
     const BalTcPlan &pl = t.pl;
     extern __shared__ unsigned char sm_raw[];
@@ -103,7 +106,7 @@ __global__ void __launch_bounds__(kTh, 1)
     unsigned char *smg = sm_raw + (sm - smem_u32(sm_raw));
     __shared__ uint32_t tmem_slot;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int N = pl.N, Dp = pl.Dp, atoms = Dp / 64;
+    const int Dp = pl.Dp, atoms = Dp / 64;
     const uint32_t ubytes = (uint32_t)kRows * Dp * 2, wpart = (uint32_t)N * Dp * 2;
     auto bar = [&](int which, int i) { return sm + t.o_bar + 8u * (uint32_t)(4 * which + (i & 3)); };
     bool ok = true;
@@ -154,30 +157,31 @@ __global__ void __launch_bounds__(kTh, 1)
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = tmem_slot;
-    // TMEM: L 2 x 128 columns (g_u: G as bf16 in the first half of each half),
+    // TMEM: L 2 x 128 columns (g_u: G as bf16 in the first half of each 32),
     // then g_u or g_W, Dp columns
     auto tL = [&](int i) { return tmem + (uint32_t)(i & 1) * 128; };
     const uint32_t tAcc = tmem + 256;
 
     const float scale = p.inv_tau * 1.4426950408889634f;
-    const int quad = warp & 3, half = (warp >> 2) & 1, r = quad * 32 + lane;
-    const int cols = N / 2;                                     // of this thread
+    const int quad = warp & 3, block = warp >> 2, r = quad * 32 + lane;
+    const int col0 = 32 * block;                                // this thread's entries
     const uint32_t tlane = (uint32_t)(quad * 32) << 16;
 
     if (warp < kEpi) {
-        // sums: this thread's columns; g_W: entry and 64 columns of d (a group of
+        // sums: this thread's entries; g_W: one entry and a quarter of d (a group of
         // 64 entries lies in the lanes twice, so their second half takes others)
-        float acc[MODE == kGu ? 1 : 64];
+        constexpr int kAcc = MODE == kGu ? 1 : MODE == kGw && N == 64 ? 64 : 32;
+        float acc[kAcc];
 #pragma unroll
-        for (int q = 0; q < (MODE == kGu ? 1 : 64); ++q) acc[q] = 0.f;
+        for (int q = 0; q < kAcc; ++q) acc[q] = 0.f;
         const int we = N > 64 ? r : r & 63;
-        const int wd = N > 64 ? half * (Dp / 2) : (half * 2 + (r >> 6)) * (Dp / 4);
-        const int wn = N > 64 ? Dp / 2 : Dp / 4;
+        const int wn = Dp / 4;
+        const int wd = (N > 64 ? block : block * 2 + (r >> 6)) * wn;
         auto take = [&]() {         // the finished tile's g_W
             if constexpr (MODE == kGw) {
                 tc_fence_after();
 #pragma unroll
-                for (int q = 0; q < 4; ++q) {
+                for (int q = 0; q < kAcc / 16; ++q) {
                     if (16 * q >= wn) break;
                     uint32_t raw[16];
                     tmem_ld16_raw(tAcc + wd + 16 * q + tlane, raw);
@@ -189,19 +193,19 @@ __global__ void __launch_bounds__(kTh, 1)
         };
         for (int i = 0; i < items; ++i) {
             const int tile = i / ng, gi = i % ng;
-            const int c0 = (group0 + gi) * N + half * cols;     // first entry of this thread
+            const int c0 = (group0 + gi) * N + col0;            // first entry of this thread
             const int64_t row = row0(tile) + r;
             const bool live = bal_live(p, row);
             // the selections of this thread's heads: on their way while the
             // products run
-            constexpr int kHeads = MODE == kSums ? 64 / KT : 1;
+            constexpr int kHeads = MODE == kSums ? 32 / KT : 1;
             int sel[kHeads];
             if (MODE == kSums) {
                 const uint32_t b = (uint32_t)row / (uint32_t)p.L, s = (uint32_t)row - b * (uint32_t)p.L;
                 const int32_t *kr = p.k + ((int64_t)b * p.H + c0 / KT) * p.L + s;
 #pragma unroll
                 for (int h = 0; h < kHeads; ++h)
-                    sel[h] = live && h < cols / KT && c0 / KT + h < p.H ? kr[(int64_t)h * p.L] : -1;
+                    sel[h] = live && c0 / KT + h < p.H ? kr[(int64_t)h * p.L] : -1;
             }
             if (!wait_warp(kLFull, i)) break;
             tc_fence_after();
@@ -213,26 +217,24 @@ __global__ void __launch_bounds__(kTh, 1)
                 }
                 if (!live) {        // behind an end: u must not meet a zero gradient as a NaN
                     const uint32_t ut = sm + t.o_u + (uint32_t)(tile % t.ustages) * ubytes;
-                    for (int a = half; a < atoms; a += 2)
+                    for (int a = block; a < atoms; a += kBlocks)
                         for (int q = 0; q < 8; ++q) sts128(ut + a * (kRows * 128) + piece(r, q), 0, 0, 0, 0);
                 }
             }
-            uint32_t third[MODE == kGw ? 32 : 1];
-#pragma unroll
-            for (int q = 0; q < 2; ++q) {
-                if (32 * q >= cols) break;
+            uint32_t third[MODE == kGw ? 16 : 1];
+            {
                 uint32_t raw[32];
                 float v[32];
-                tmem_ld32(tL(i) + half * cols + 32 * q + tlane, raw);
+                tmem_ld32(tL(i) + col0 + tlane, raw);
                 tmem_wait_ld();
 #pragma unroll
                 for (int e = 0; e < 32; ++e) v[e] = __uint_as_float(raw[e]);
                 softmax32<KT>(v, p.K, scale, live);
                 if constexpr (MODE == kSums) {
 #pragma unroll
-                    for (int e = 0; e < 32; ++e) acc[32 * q + e] += v[e];
+                    for (int e = 0; e < 32; ++e) acc[e] += v[e];
                 } else {
-                    const float4 *tf = reinterpret_cast<const float4 *>(t.freq + c0 + 32 * q);
+                    const float4 *tf = reinterpret_cast<const float4 *>(t.freq + c0);
                     const int heads = pl.groups * N / KT;
                     float fq[32];
 #pragma unroll
@@ -245,7 +247,7 @@ __global__ void __launch_bounds__(kTh, 1)
                     }
 #pragma unroll
                     for (int h = 0; h < 32 / KT; ++h) {
-                        const float by = __ldg(t.freq + heads * KT + (c0 + 32 * q) / KT + h);
+                        const float by = __ldg(t.freq + heads * KT + c0 / KT + h);
                         float dot = 0.f;
 #pragma unroll
                         for (int k = 0; k < KT; ++k) dot = fmaf(v[h * KT + k], fq[h * KT + k], dot);
@@ -257,9 +259,9 @@ __global__ void __launch_bounds__(kTh, 1)
                         uint32_t o[16];
 #pragma unroll
                         for (int e = 0; e < 16; ++e) o[e] = pack2(v[2 * e], v[2 * e + 1]);
-                        tmem_st16(tL(i) + half * cols + 16 * q + tlane, o);
+                        tmem_st16(tL(i) + col0 + tlane, o);
                     } else {
-                        // piece e of this row: entries half * cols + 32 q + 8 e
+                        // piece e of this row: entries col0 + 8 e
                         const uint32_t gt = sm + t.o_g;
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
@@ -268,13 +270,13 @@ __global__ void __launch_bounds__(kTh, 1)
                             for (int k = 0; k < 4; ++k) {
                                 float a = v[8 * e + 2 * k], b = v[8 * e + 2 * k + 1];
                                 const uint32_t w = pack2(a, b);
-                                third[16 * q + 4 * e + k] = w;
+                                third[4 * e + k] = w;
                                 a -= lo_of(w);
                                 b -= hi_of(w);
                                 p1[k] = pack2(a, b);
                                 p2[k] = pack2(a - lo_of(p1[k]), b - hi_of(p1[k]));
                             }
-                            const int col = half * cols + 32 * q + 8 * e;
+                            const int col = col0 + 8 * e;
                             const uint32_t at = gt + (uint32_t)(col / 64) * (kRows * 128) + piece(r, (col & 63) / 8);
                             sts128(at, p1[0], p1[1], p1[2], p1[3]);
                             sts128(at + (uint32_t)kRows * N * 2, p2[0], p2[1], p2[2], p2[3]);
@@ -286,7 +288,7 @@ __global__ void __launch_bounds__(kTh, 1)
 #pragma unroll
                 for (int h = 0; h < kHeads; ++h)
                     if (sel[h] >= 0 && sel[h] < p.K)
-                        atomicAdd(&cnt[half * cols + h * KT + sel[h]], 1);
+                        atomicAdd(&cnt[col0 + h * KT + sel[h]], 1);
             }
             if (MODE == kGu) tmem_wait_st();
             if (MODE == kGw) fence_proxy_async_smem();
@@ -295,9 +297,8 @@ __global__ void __launch_bounds__(kTh, 1)
             if constexpr (MODE == kGw) {
                 if (!wait_warp(kGHalf, i)) break;       // part 1's buffer has been read
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    if (8 * e >= cols) break;
-                    const int col = half * cols + 8 * e;
+                for (int e = 0; e < 4; ++e) {
+                    const int col = col0 + 8 * e;
                     sts128(sm + t.o_g + (uint32_t)(col / 64) * (kRows * 128) + piece(r, (col & 63) / 8),
                            third[4 * e], third[4 * e + 1], third[4 * e + 2], third[4 * e + 3]);
                 }
@@ -308,16 +309,16 @@ __global__ void __launch_bounds__(kTh, 1)
                 if (!wait_warp(kGuFull, tile)) break;
                 tc_fence_after();
                 __nv_bfloat16 *out = (__nv_bfloat16 *)p.g_u + row * p.D;
-                const int dcols = Dp / 2;
+                const int dcols = Dp / kBlocks;
 #pragma unroll 1
                 for (int q = 0; q < dcols; q += 16) {
                     uint32_t raw[16];
                     float v[16];
-                    tmem_ld16_raw(tAcc + half * dcols + q + tlane, raw);
+                    tmem_ld16_raw(tAcc + block * dcols + q + tlane, raw);
                     tmem_wait_ld();
 #pragma unroll
                     for (int e = 0; e < 16; ++e) v[e] = live ? __uint_as_float(raw[e]) : 0.f;
-                    const int col = half * dcols + q;
+                    const int col = block * dcols + q;
                     if (row >= p.rows) continue;
                     if (t.vec) {
 #pragma unroll
@@ -344,18 +345,18 @@ __global__ void __launch_bounds__(kTh, 1)
             const bool mine = h < p.H && k < p.K;
             float *out = p.part + (((int64_t)slice * p.H + h) * p.K + k) * p.D + wd;
 #pragma unroll
-            for (int e = 0; e < 64; ++e)
+            for (int e = 0; e < kAcc; ++e)
                 if (mine && e < wn && wd + e < p.D) out[e] = acc[e];
         }
         if constexpr (MODE == kSums) {
-            // column sums over the warp's rows, one warp's 64 columns at a time
-            float *red = reinterpret_cast<float *>(smg + t.o_g);        // [8][64]
+            // column sums over the warp's rows
+            float *red = reinterpret_cast<float *>(smg + t.o_g);        // [kEpi][32]
 #pragma unroll
-            for (int q = 0; q < 64; ++q) {
+            for (int q = 0; q < 32; ++q) {
                 float s = acc[q];
 #pragma unroll
                 for (int d = 16; d; d >>= 1) s += __shfl_xor_sync(kFull, s, d);
-                if (lane == 0) red[warp * 64 + q] = s;
+                if (lane == 0) red[warp * 32 + q] = s;
             }
         }
     } else if (warp == kEpi) {
@@ -376,18 +377,13 @@ __global__ void __launch_bounds__(kTh, 1)
                     const uint32_t wb = wmn0 + (uint32_t)wslot(j) * umma_step((uint32_t)pl.w_bytes);
 #pragma unroll 1
                     for (int part = 0; part < 2; ++part) {
-                        // entries 16 k.. lie in half kh of the columns, packed two to one
-#pragma unroll 1
-                        for (int kh = 0; kh < 2; ++kh) {
-                            const uint32_t ar = tL(j) + kh * (N / 2);
-                            const uint32_t br = wb + part * umma_step(wpart) + kh * (N / 32) * umma_step(2048);
-                            const bool more = gi > 0 || part > 0 || kh > 0;
-                            umma_ts(tAcc, ar, br, idU, more);
+                        // a block's 32 entries lie packed in its first 16 columns
+#pragma unroll
+                        for (int kb = 0; kb < kBlocks; ++kb) {
+                            const uint32_t ar = tL(j) + kb * 32;
+                            const uint32_t br = wb + part * umma_step(wpart) + kb * 2 * umma_step(2048);
+                            umma_ts(tAcc, ar, br, idU, gi > 0 || part > 0 || kb > 0);
                             umma_ts(tAcc, ar + 8, br + umma_step(2048), idU, true);
-                            if (N > 64) {
-                                umma_ts(tAcc, ar + 16, br + 2 * umma_step(2048), idU, true);
-                                umma_ts(tAcc, ar + 24, br + 3 * umma_step(2048), idU, true);
-                            }
                         }
                     }
                     if (gi == ng - 1) umma_commit(bar(kGuFull, tile));
@@ -517,9 +513,9 @@ __global__ void __launch_bounds__(kTh, 1)
         for (int e = tid; e < N; e += kTh) {
             const int c = group0 * N + e, h = c / KT, k = c % KT;
             if (h >= p.H || k >= p.K) continue;
-            const int w = e / (N / 2) * 4, col = e % (N / 2);
-            const float s = (red[w * 64 + col] + red[(w + 1) * 64 + col]) +
-                            (red[(w + 2) * 64 + col] + red[(w + 3) * 64 + col]);
+            const int w = e / 32 * 4, col = e % 32;
+            const float s = (red[w * 32 + col] + red[(w + 1) * 32 + col]) +
+                            (red[(w + 2) * 32 + col] + red[(w + 3) * 32 + col]);
             const int64_t at = ((int64_t)slice * p.H + h) * p.K + k;
             p.part[at] = failed ? nan : s;
             p.part_n[at] = cnt[e];
@@ -576,7 +572,7 @@ __global__ void k_bal_parts(BalParams p, BalTcPlan pl, unsigned char *parts, flo
     }
 }
 
-template <int KT, int MODE>
+template <int KT, int MODE, int N>
 cudaError_t go(const BalParams &p, const BalTcPlan &pl, const void *parts, cudaStream_t st) {
     TcP t;
     memset(&t, 0, sizeof(t));
@@ -589,7 +585,7 @@ cudaError_t go(const BalParams &p, const BalTcPlan &pl, const void *parts, cudaS
     const uint32_t u = (uint32_t)kRows * pl.Dp * 2;
     uint32_t o = t.nslot * (uint32_t)pl.w_bytes;
     t.o_u = o; o += t.ustages * u;
-    t.o_g = o; o += MODE == kGw ? 2u * kRows * pl.N * 2 : MODE == kSums ? 8 * 64 * 4 : 0;
+    t.o_g = o; o += MODE == kGw ? 2u * kRows * pl.N * 2 : MODE == kSums ? epi_of(N) * 32 * 4 : 0;
     t.o_tab = o; o += MODE == kSums ? pl.N * 4 : 0;
     t.o_bar = o; o += 32 * kBars;
     const int smem = (int)o + 1024;
@@ -608,20 +604,25 @@ cudaError_t go(const BalParams &p, const BalTcPlan &pl, const void *parts, cudaS
                                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
             return cudaErrorInvalidValue;
     }
-    auto kern = k_bal_tc<KT, MODE>;
+    auto kern = k_bal_tc<KT, MODE, N>;
     static std::atomic<int> set[kLimitDevices];
     const cudaError_t e = allow_smem((const void *)kern, smem, set);
     if (e != cudaSuccess) return e;
     const int grid = MODE == kGu ? (pl.tiles < 148 ? pl.tiles : 148) : pl.groups * pl.slices;
-    kern<<<grid, kTh, smem, st>>>(map, t);
+    kern<<<grid, (epi_of(N) + 2) * 32, smem, st>>>(map, t);
     return cudaGetLastError();
+}
+
+template <int KT, int N>
+cudaError_t go_n(const BalParams &p, const BalTcPlan &pl, int what, const void *parts, cudaStream_t st) {
+    if (what == kSums) return go<KT, kSums, N>(p, pl, parts, st);
+    if (what == kGu) return go<KT, kGu, N>(p, pl, parts, st);
+    return go<KT, kGw, N>(p, pl, parts, st);
 }
 
 template <int KT>
 cudaError_t go_k(const BalParams &p, const BalTcPlan &pl, int what, const void *parts, cudaStream_t st) {
-    if (what == kSums) return go<KT, kSums>(p, pl, parts, st);
-    if (what == kGu) return go<KT, kGu>(p, pl, parts, st);
-    return go<KT, kGw>(p, pl, parts, st);
+    return pl.N == 128 ? go_n<KT, 128>(p, pl, what, parts, st) : go_n<KT, 64>(p, pl, what, parts, st);
 }
 
 }  // namespace
