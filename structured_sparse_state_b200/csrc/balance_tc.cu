@@ -22,7 +22,8 @@
 // Bound: tensor pipe and the softmax's issue slots, about equal (leaving out a
 // third of g_u's logit products changed its time by less than 1 %); u is read
 // once per group (from L2 after the first).  8 x 16384 steps, 16 heads of 16
-// entries, D = 128: sums 40 us, g_u 71, g_W 93.
+// entries, D = 128: sums 36 us, g_u 62, g_W 86 (one issuing thread and eight
+// softmax warps: 40, 70, 93).
 #include <string.h>
 
 #include "balance.cuh"
@@ -94,10 +95,14 @@ __device__ __forceinline__ void softmax32(float (&v)[32], int K, float scale, bo
     }
 }
 
+// and two that issue products (a thread takes 100 to 200 cycles for each), one
+// for copies
+__host__ __device__ constexpr int threads_of(int N) { return (epi_of(N) + 3) * 32; }
+
 template <int KT, int MODE, int N>
-__global__ void __launch_bounds__((epi_of(N) + 2) * 32, 1)
+__global__ void __launch_bounds__(threads_of(N), 1)
     k_bal_tc(const __grid_constant__ CUtensorMap umap, const TcP t) {
-    constexpr int kEpi = epi_of(N), kTh = (kEpi + 2) * 32;      // + products, + copies
+    constexpr int kEpi = epi_of(N), kTh = threads_of(N);
     constexpr int kBlocks = N / 32;                             // of 32 entries
     const BalParams &p = t.p;
     const BalTcPlan &pl = t.pl;
@@ -359,20 +364,53 @@ __global__ void __launch_bounds__((epi_of(N) + 2) * 32, 1)
                 if (lane == 0) red[warp * 32 + q] = s;
             }
         }
-    } else if (warp == kEpi) {
-        // ---- products
+    } else if (warp == kEpi || (MODE == kSums && warp == kEpi + 1)) {
+        // ---- products: logits.  Sums: the two warps take items in turn, each with its
+        // stage of u; with one stage (whose phases a warp must see one by one) the
+        // first takes all
+        const bool two = MODE == kSums && t.ustages > 1;
+        if (lane == 0 && (two || warp == kEpi)) {
+            const uint32_t idL = umma_idesc_bf16(N);
+            const uint32_t w0 = umma_lo(sm, 16), u0 = umma_lo(sm + t.o_u, 16);
+            int last = -1;
+            for (int i = warp - kEpi; i < items; i += two ? 2 : 1) {
+                const int tile = i / ng;
+                if (!wait_u(tile) || !wait_w(i)) break;
+                // L's buffer: its columns have been read (g_u: its G has gone into the
+                // second product)
+                if (i >= 2 && !wait(MODE == kGu ? kDone : kGReady, i - 2)) break;
+                tc_fence_after();
+                const uint32_t ub = u0 + (uint32_t)(tile % t.ustages) * umma_step(ubytes);
+                const uint32_t wb = w0 + (uint32_t)wslot(i) * umma_step((uint32_t)pl.w_bytes);
+#pragma unroll 1
+                for (int part = 2; part >= 0; --part)       // the small ones first
+#pragma unroll 1
+                    for (int a = 0; a < atoms; ++a) {
+                        const uint32_t ar = ub + a * umma_step(kRows * 128);
+                        const uint32_t br = wb + part * umma_step(wpart) + a * umma_step((uint32_t)N * 128);
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            umma_ss(tL(i), ar + k * umma_step(32), br + k * umma_step(32), idL,
+                                    part < 2 || a > 0 || k > 0);
+                    }
+                umma_commit(bar(kLFull, i));
+                last = i;
+            }
+            if (last >= 0 && ok) wait(kLFull, last);    // nothing is in flight when the CTA ends
+        }
+        __syncwarp();
+    } else if (warp == kEpi + 1) {
+        // ---- products: what an item's G goes into
         if (lane == 0) {
-            const uint32_t idL = umma_idesc_bf16(N), idU = umma_idesc_bf16(Dp, false, true),
-                           idW = umma_idesc_bf16(Dp, true, true);
-            const uint32_t w0 = umma_lo(sm, 16), wmn0 = umma_lo(sm, (uint32_t)N * 128);
-            const uint32_t u0 = umma_lo(sm + t.o_u, 16), umn0 = umma_lo(sm + t.o_u, kRows * 128);
+            const uint32_t idU = umma_idesc_bf16(Dp, false, true), idW = umma_idesc_bf16(Dp, true, true);
+            const uint32_t wmn0 = umma_lo(sm, (uint32_t)N * 128), umn0 = umma_lo(sm + t.o_u, kRows * 128);
             // the two 64-entry blocks of G (one: the same rows twice)
             const uint32_t g0 = umma_lo(sm + t.o_g, N > 64 ? kRows * 128 : 0);
-            auto second = [&](int j) {          // what an item's G goes into
+            for (int j = 0; j < items; ++j) {
                 const int tile = j / ng, gi = j % ng;
-                if (!wait(kGReady, j)) return;
+                if (!wait(kGReady, j)) break;
                 if (MODE == kGu) {
-                    if (gi == 0 && tile > 0 && !wait(kGuFree, tile - 1)) return;
+                    if (gi == 0 && tile > 0 && !wait(kGuFree, tile - 1)) break;
                     tc_fence_after();
                     const uint32_t wb = wmn0 + (uint32_t)wslot(j) * umma_step((uint32_t)pl.w_bytes);
 #pragma unroll 1
@@ -393,7 +431,7 @@ __global__ void __launch_bounds__((epi_of(N) + 2) * 32, 1)
                     for (int part = 0; part < 3; ++part) {      // parts 2, 1, 0 of G
                         if (part == 2) {
                             umma_commit(bar(kGHalf, j));
-                            if (!wait(kGThird, j)) return;
+                            if (!wait(kGThird, j)) break;
                         }
                         tc_fence_after();
                         const uint32_t ar = g0 + (part == 0 ? umma_step((uint32_t)kRows * N * 2) : 0u);
@@ -403,39 +441,10 @@ __global__ void __launch_bounds__((epi_of(N) + 2) * 32, 1)
                                     part > 0 || k > 0);
                     }
                 }
+                if (!ok) break;
                 umma_commit(bar(kDone, j));
-            };
-            // an item's logits run ahead of the last item's second product, unless
-            // what they need comes only when that is done: the weights (one slot
-            // for several groups), or u (one stage, which g_W's product reads)
-            const bool ahead = (resident || t.nslot > 1) && (MODE != kGw || t.ustages > 1);
-            for (int i = 0; i < items && ok; ++i) {
-                const int tile = i / ng;
-                if (MODE != kSums && i > 0 && !ahead) second(i - 1);
-                if (!wait_u(tile) || !wait_w(i)) break;
-                // L's buffer: its G was taken by the second product (g_u, g_W), or
-                // its columns have been read
-                if (i >= 2 && !wait(kGReady, i - 2)) break;
-                tc_fence_after();
-                const uint32_t ub = u0 + (uint32_t)(tile % t.ustages) * umma_step(ubytes);
-                const uint32_t wb = w0 + (uint32_t)wslot(i) * umma_step((uint32_t)pl.w_bytes);
-#pragma unroll 1
-                for (int part = 2; part >= 0; --part)       // the small ones first
-#pragma unroll 1
-                    for (int a = 0; a < atoms; ++a) {
-                        const uint32_t ar = ub + a * umma_step(kRows * 128);
-                        const uint32_t br = wb + part * umma_step(wpart) + a * umma_step((uint32_t)N * 128);
-#pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            umma_ss(tL(i), ar + k * umma_step(32), br + k * umma_step(32), idL,
-                                    part < 2 || a > 0 || k > 0);
-                    }
-                umma_commit(bar(kLFull, i));
-                if (MODE != kSums && i > 0 && ahead) second(i - 1);
             }
-            if (MODE != kSums && items > 0 && ok) second(items - 1);
-            // nothing is in flight when the CTA ends
-            if (items > 0 && ok) wait(MODE == kSums ? kLFull : kDone, items - 1);
+            if (items > 0 && ok) wait(kDone, items - 1);
         }
         __syncwarp();
     } else {
@@ -609,7 +618,7 @@ cudaError_t go(const BalParams &p, const BalTcPlan &pl, const void *parts, cudaS
     const cudaError_t e = allow_smem((const void *)kern, smem, set);
     if (e != cudaSuccess) return e;
     const int grid = MODE == kGu ? (pl.tiles < 148 ? pl.tiles : 148) : pl.groups * pl.slices;
-    kern<<<grid, (epi_of(N) + 2) * 32, smem, st>>>(map, t);
+    kern<<<grid, threads_of(N), smem, st>>>(map, t);
     return cudaGetLastError();
 }
 
