@@ -19,10 +19,11 @@
 //           a CTA's 14 tiles that cost 5.6e-6 of g_W's norm)
 // L is double-buffered: the next tile's products run under this one's softmax.
 //
-// Bound: tensor pipe and the softmax's issue slots, about equal (leaving out a
-// third of g_u's logit products changed its time by less than 1 %); u is read
+// Bound: the chain of a tile through the roles (copy, logits, softmax, second
+// product); the products alone take a third of the time, and leaving two of the
+// three parts out of the logits saves 20 % of the sums, 4 % of g_W.  u is read
 // once per group (from L2 after the first).  8 x 16384 steps, 16 heads of 16
-// entries, D = 128: sums 36 us, g_u 62, g_W 86 (one issuing thread and eight
+// entries, D = 128: sums 36 us, g_u 56, g_W 86 (one issuing thread and eight
 // softmax warps: 40, 70, 93).
 #include <string.h>
 
@@ -34,6 +35,9 @@ namespace pdssm {
 namespace {
 
 enum { kSums = 0, kGu = 1, kGw = 2 };
+// W's parts that a kernel takes: the loss, the probabilities and g_W are fp32;
+// g_u is bf16, and 16 bits of W move its logits by 1e-5 of them at most
+__host__ __device__ constexpr int parts_of(int mode) { return mode == kGu ? 2 : 3; }
 // softmax warps of a group of N entries: 4 by rows times N / 32 by entries
 __host__ __device__ constexpr int epi_of(int N) { return N / 8; }
 constexpr int kRows = 128;
@@ -47,7 +51,7 @@ struct TcP {
     const float *freq;                          // counts / T [groups * N], then per head the
                                                 // factor g_loss K inv_tau / T
     int vec;
-    int nslot, ustages;
+    int nslot, ustages;                         // of W, of u
     uint32_t o_u, o_g, o_tab, o_bar;            // shared-memory offsets (weights at 0)
 };
 
@@ -113,6 +117,8 @@ __global__ void __launch_bounds__(threads_of(N), 1)
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int Dp = pl.Dp, atoms = Dp / 64;
     const uint32_t ubytes = (uint32_t)kRows * Dp * 2, wpart = (uint32_t)N * Dp * 2;
+    constexpr int kParts = parts_of(MODE);
+    const uint32_t wslotb = kParts * wpart;
     auto bar = [&](int which, int i) { return sm + t.o_bar + 8u * (uint32_t)(4 * which + (i & 3)); };
     bool ok = true;
     auto wait = [&](int which, int i) {
@@ -375,15 +381,16 @@ __global__ void __launch_bounds__(threads_of(N), 1)
             int last = -1;
             for (int i = warp - kEpi; i < items; i += two ? 2 : 1) {
                 const int tile = i / ng;
-                if (!wait_u(tile) || !wait_w(i)) break;
                 // L's buffer: its columns have been read (g_u: its G has gone into the
-                // second product)
+                // second product).  Ahead of the wait for u: then every earlier copy has
+                // landed, also those that the other warp waited for.
                 if (i >= 2 && !wait(MODE == kGu ? kDone : kGReady, i - 2)) break;
+                if (!wait_u(tile) || !wait_w(i)) break;
                 tc_fence_after();
                 const uint32_t ub = u0 + (uint32_t)(tile % t.ustages) * umma_step(ubytes);
-                const uint32_t wb = w0 + (uint32_t)wslot(i) * umma_step((uint32_t)pl.w_bytes);
+                const uint32_t wb = w0 + (uint32_t)wslot(i) * umma_step(wslotb);
 #pragma unroll 1
-                for (int part = 2; part >= 0; --part)       // the small ones first
+                for (int part = kParts - 1; part >= 0; --part)      // the small ones first
 #pragma unroll 1
                     for (int a = 0; a < atoms; ++a) {
                         const uint32_t ar = ub + a * umma_step(kRows * 128);
@@ -391,7 +398,7 @@ __global__ void __launch_bounds__(threads_of(N), 1)
 #pragma unroll
                         for (int k = 0; k < 4; ++k)
                             umma_ss(tL(i), ar + k * umma_step(32), br + k * umma_step(32), idL,
-                                    part < 2 || a > 0 || k > 0);
+                                    part < kParts - 1 || a > 0 || k > 0);
                     }
                 umma_commit(bar(kLFull, i));
                 last = i;
@@ -412,7 +419,7 @@ __global__ void __launch_bounds__(threads_of(N), 1)
                 if (MODE == kGu) {
                     if (gi == 0 && tile > 0 && !wait(kGuFree, tile - 1)) break;
                     tc_fence_after();
-                    const uint32_t wb = wmn0 + (uint32_t)wslot(j) * umma_step((uint32_t)pl.w_bytes);
+                    const uint32_t wb = wmn0 + (uint32_t)wslot(j) * umma_step(wslotb);
 #pragma unroll 1
                     for (int part = 0; part < 2; ++part) {
                         // a block's 32 entries lie packed in its first 16 columns
@@ -457,7 +464,7 @@ __global__ void __launch_bounds__(threads_of(N), 1)
                     if (!resident && i >= t.nslot) wait(kDone, i - t.nslot);
                     if (ok) {
                         const uint32_t wb = bar(kWFull, wslot(i));
-                        const uint32_t bytes = (uint32_t)pl.w_bytes;
+                        const uint32_t bytes = wslotb;
                         mbar_expect_tx(wb, bytes);
                         const unsigned char *src = t.parts + (size_t)(group0 + gi) * pl.w_bytes;
                         for (uint32_t o = 0; o < bytes; o += 16384)
@@ -589,10 +596,19 @@ cudaError_t go(const BalParams &p, const BalTcPlan &pl, const void *parts, cudaS
     t.pl = pl;
     t.parts = (const unsigned char *)parts;
     t.freq = reinterpret_cast<const float *>(t.parts + (size_t)pl.groups * pl.w_bytes);
-    t.nslot = MODE == kGu && pl.groups > 1 && pl.Dp <= 128 ? 2 : 1;
-    t.ustages = MODE == kGu || pl.Dp > 128 ? 1 : 2;
-    const uint32_t u = (uint32_t)kRows * pl.Dp * 2;
-    uint32_t o = t.nslot * (uint32_t)pl.w_bytes;
+    const uint32_t u = (uint32_t)kRows * pl.Dp * 2, slot = parts_of(MODE) * (uint32_t)pl.N * pl.Dp * 2;
+    t.nslot = 1;
+    t.ustages = pl.Dp > 128 ? 1 : 2;
+    if (MODE == kGu) {
+        // as many groups' weights as fit (at most four slots); two stages of u where
+        // they fit too and a tile has at most three groups (a barrier's slots
+        // come round after four)
+        const uint32_t room = 227 * 1024 - 2048;
+        t.nslot = pl.groups < 4 ? pl.groups : 4;
+        while (t.nslot > 1 && t.nslot * slot + u > room) --t.nslot;
+        t.ustages = pl.groups <= 3 && t.nslot * slot + 2 * u <= room ? 2 : 1;
+    }
+    uint32_t o = t.nslot * slot;
     t.o_u = o; o += t.ustages * u;
     t.o_g = o; o += MODE == kGw ? 2u * kRows * pl.N * 2 : MODE == kSums ? epi_of(N) * 32 * 4 : 0;
     t.o_tab = o; o += MODE == kSums ? pl.N * 4 : 0;
