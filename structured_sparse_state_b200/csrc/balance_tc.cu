@@ -4,10 +4,10 @@
 // takes K entries rounded up to a power of two).  Its weights lie in shared
 // memory as three bf16 parts (8 + 8 + 8 bits of fp32), so that the logits
 //     L = u W^T            128 rows x N, K = D, three products
-// have fp32 accuracy (u is bf16 by itself); the small parts are multiplied
-// first, since a product's additions truncate the sum so far.  Sixteen warps (N = 64: eight)
-// take a finished L from TMEM, a row and 32 of its columns per thread: softmax per
-// head, then
+// have fp32 accuracy (u is bf16 by itself; g_u takes two parts); the small parts
+// are multiplied first, since a product's additions truncate the sum so far.
+// Sixteen warps (N = 64: eight) take a finished L from TMEM, a row and 32 of its
+// columns per thread: softmax per head, then
 //   sums    column sums of p over the rows, in registers over the CTA's tiles;
 //           counts by shared-memory atomics (integers)
 //   g_u     G, the logits' gradients, back to TMEM as bf16, and
