@@ -347,11 +347,13 @@ __global__ void __launch_bounds__(kTcTh, 1)
 #pragma unroll
             for (int q = 0; q < kCols; ++q) S[q] = in && q < left ? in[at + q] : 0.f;
         }
-        auto leave = [&](float *out) {                      // this thread's part of the state
+        // this thread's part of the state; a caller's buffer may start anywhere
+        auto leave = [&](float *out) {
+            const bool wide = p.P % 4 == 0 && ((uintptr_t)out & 15) == 0;
             out += at;
 #pragma unroll
             for (int q = 0; q < kCols; q += 4) {
-                if (p.P % 4 == 0) {
+                if (wide) {
                     if (q < left)
                         *reinterpret_cast<float4 *>(out + q) = make_float4(S[q], S[q + 1], S[q + 2], S[q + 3]);
                 } else {

@@ -280,6 +280,38 @@ def test_pointers_off_the_16_byte_grid(offset):
         assert torch.equal(got[n], want[n]), n
 
 
+@pytest.mark.parametrize("offset", [1, 2, 3])
+@pytest.mark.parametrize("case", [
+    (BF, 1, 2, 2, 130, 64, 64, "bhl", "step", True, False), (BF, 2, 2, 1, 130, 128, 100, "blh", "head", True, True),
+    (BF, 1, 1, 1, 1100, 32, 64, "bhl", "step", True, False), (BF, 1, 2, 2, 1, 16, 4, "blh", "step", True, False),
+    (F32, 1, 2, 2, 130, 64, 64, "bhl", "step", True, False), (F32, 1, 2, 1, 300, 40, 96, "blh", "head", True, True)],
+    ids=lambda c: "-".join(str(v).replace("torch.", "") for v in c))
+def test_every_buffer_off_the_16_byte_grid(case, offset):
+    """Inputs, states and the caller's own outputs that start inside a storage,
+    each 1 to 3 values off: the same bits, and nothing around them is written."""
+    t, layout = make(*case, seed=13), case[7]
+    want = fwd_bwd(t, layout)
+
+    def off(v, fill=None):
+        room = torch.full((v.numel() + 8,), 7.0, dtype=v.dtype, device="cuda")
+        at = room[offset:offset + v.numel()].view(v.shape)
+        at.copy_(v) if fill is None else at.fill_(fill)
+        return room, at
+
+    moved = {n: v if v is None or n == "lengths" else off(v)[1] for n, v in t.items()}
+    rooms = {n: off(v, math.nan) for n, v in want.items()}
+    out = {n: v[1] for n, v in rooms.items()}
+    _, _, ws = pd.pdssm_decay_scan_fwd(*(moved[n] for n in ("c", "b", "x", "log_a", "h0")), lengths=t["lengths"],
+                                       layout=layout, for_bwd=True, y=out["y"], h_last=out["h_last"])
+    pd.pdssm_decay_scan_bwd(*(moved[n] for n in ("c", "b", "x", "log_a", "h0", "g_y")), ws, g_hlast=moved["g_hlast"],
+                            lengths=t["lengths"], layout=layout,
+                            out=[out[n] for n in ("g_c", "g_b", "g_x", "g_log_a", "g_h0")])
+    for n in want:
+        assert torch.equal(out[n], want[n]), n
+        room = rooms[n][0]
+        assert (room[:offset] == 7).all() and (room[offset + want[n].numel():] == 7).all(), n
+
+
 def test_odd_widths_at_other_addresses_in_the_adjoint():
     """The adjoint of rows of odd width, with inputs that the forward saw at
     addresses off the 16-byte grid."""
