@@ -231,6 +231,7 @@ __global__ void __launch_bounds__(threads_of(N), 1)
                     for (int a = block; a < atoms; a += kBlocks)
                         for (int q = 0; q < 8; ++q) sts128(ut + a * (kRows * 128) + piece(r, q), 0, 0, 0, 0);
                 }
+                __syncwarp();       // the loads below are the whole warp's
             }
             uint32_t third[MODE == kGw ? 16 : 1];
             {
@@ -330,19 +331,21 @@ __global__ void __launch_bounds__(threads_of(N), 1)
 #pragma unroll
                     for (int e = 0; e < 16; ++e) v[e] = live ? __uint_as_float(raw[e]) : 0.f;
                     const int col = block * dcols + q;
-                    if (row >= p.rows) continue;
-                    if (t.vec) {
+                    if (row < p.rows) {
+                        if (t.vec) {
 #pragma unroll
-                        for (int e = 0; e < 16; e += 8)
-                            if (col + e < p.D)
-                                *reinterpret_cast<uint4 *>(out + col + e) =
-                                    make_uint4(pack2(v[e], v[e + 1]), pack2(v[e + 2], v[e + 3]),
-                                               pack2(v[e + 4], v[e + 5]), pack2(v[e + 6], v[e + 7]));
-                    } else {
+                            for (int e = 0; e < 16; e += 8)
+                                if (col + e < p.D)
+                                    *reinterpret_cast<uint4 *>(out + col + e) =
+                                        make_uint4(pack2(v[e], v[e + 1]), pack2(v[e + 2], v[e + 3]),
+                                                   pack2(v[e + 4], v[e + 5]), pack2(v[e + 6], v[e + 7]));
+                        } else {
 #pragma unroll
-                        for (int e = 0; e < 16; ++e)
-                            if (col + e < p.D) out[col + e] = __float2bfloat16_rn(v[e]);
+                            for (int e = 0; e < 16; ++e)
+                                if (col + e < p.D) out[col + e] = __float2bfloat16_rn(v[e]);
+                        }
                     }
+                    __syncwarp();   // rows behind the last part ways: together again for the next load
                 }
                 tc_fence_before();
                 mbar_arrive(bar(kGuFree, tile));

@@ -490,6 +490,7 @@ __global__ void __launch_bounds__(Smem<NT, PT>::kAll, NT * PT > 1 ? 1 : 2) k_dec
                     sts32(a0 + SM::kQ, pack2(qv[0], qv[1]));
                     sts32(a1 + SM::kQ, pack2(qv[2], qv[3]));
                 }
+                __syncwarp();
             }
             row0 = quad_sum(row0);
             row1 = quad_sum(row1);
@@ -552,6 +553,7 @@ __global__ void __launch_bounds__(Smem<NT, PT>::kAll, NT * PT > 1 ? 1 : 2) k_dec
                 out[wc][m0 + g] = d0;
                 out[wc][m0 + g + 8] = d1;
             }
+            __syncwarp();
         };
         auto add_pairs = [&](const uint32_t (&a)[4], uint32_t tile, int ks) {
 #pragma unroll
@@ -585,6 +587,7 @@ __global__ void __launch_bounds__(Smem<NT, PT>::kAll, NT * PT > 1 ? 1 : 2) k_dec
                 store_key(p.g_c, tr0, 64 * nt + n0 + 8 * f + q2, acc[f][0], acc[f][1]);
                 store_key(p.g_c, tr1, 64 * nt + n0 + 8 * f + q2, acc[f][2], acc[f][3]);
             }
+            __syncwarp();               // rows behind the end part ways; products are the whole warp's
         }
         leave_dots(sw.u);
         if (SM::kShare) {
@@ -627,6 +630,7 @@ __global__ void __launch_bounds__(Smem<NT, PT>::kAll, NT * PT > 1 ? 1 : 2) k_dec
                 store_key(p.g_b, tr0, 64 * nt + n0 + 8 * f + q2, acc[f][0], acc[f][1]);
                 store_key(p.g_b, tr1, 64 * nt + n0 + 8 * f + q2, acc[f][2], acc[f][3]);
             }
+            __syncwarp();
         }
         leave_dots(sw.v);
         // ---- g_x
@@ -665,6 +669,7 @@ __global__ void __launch_bounds__(Smem<NT, PT>::kAll, NT * PT > 1 ? 1 : 2) k_dec
                     }
                 }
             }
+            __syncwarp();
         }
         // ---- R: the chunk's part from zero, then one fp32 multiply-add (a product's
         // own additions truncate, which would pile up over a long memory)

@@ -306,24 +306,26 @@ __global__ void __launch_bounds__(kTcTh, 1)
                         mbar_arrive(bar(kYFree, i));
                     }
                     const int left = pw - 16 * q;               // columns left
-                    if (t >= p.L || left <= 0) continue;
-                    __nv_bfloat16 *row = y + t * p.oval_t + 16 * q;
-                    if (p.ovec == 2 && left > 8) {
-                        asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(row),
-                                     "r"(o[0]), "r"(o[1]), "r"(o[2]), "r"(o[3]), "r"(o[4]), "r"(o[5]),
-                                     "r"(o[6]), "r"(o[7])
-                                     : "memory");
-                    } else if (p.ovec) {                        // rows in eights
-                        *reinterpret_cast<uint4 *>(row) = make_uint4(o[0], o[1], o[2], o[3]);
-                        if (left > 8)
-                            *reinterpret_cast<uint4 *>(row + 8) = make_uint4(o[4], o[5], o[6], o[7]);
-                    } else {
+                    if (t < p.L && left > 0) {
+                        __nv_bfloat16 *row = y + t * p.oval_t + 16 * q;
+                        if (p.ovec == 2 && left > 8) {
+                            asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(row),
+                                         "r"(o[0]), "r"(o[1]), "r"(o[2]), "r"(o[3]), "r"(o[4]), "r"(o[5]),
+                                         "r"(o[6]), "r"(o[7])
+                                         : "memory");
+                        } else if (p.ovec) {                    // rows in eights
+                            *reinterpret_cast<uint4 *>(row) = make_uint4(o[0], o[1], o[2], o[3]);
+                            if (left > 8)
+                                *reinterpret_cast<uint4 *>(row + 8) = make_uint4(o[4], o[5], o[6], o[7]);
+                        } else {
 #pragma unroll
-                        for (int e = 0; e < 16; ++e)
-                            if (e < left)
-                                reinterpret_cast<unsigned short *>(row)[e] =
-                                    (unsigned short)(o[e / 2] >> (16 * (e % 2)));
+                            for (int e = 0; e < 16; ++e)
+                                if (e < left)
+                                    reinterpret_cast<unsigned short *>(row)[e] =
+                                        (unsigned short)(o[e / 2] >> (16 * (e % 2)));
+                        }
                     }
+                    __syncwarp();       // rows behind the end part ways: together again for the next load
                 }
             }
         }
@@ -389,6 +391,7 @@ __global__ void __launch_bounds__(kTcTh, 1)
 #pragma unroll
             for (int k = 0; k < (HALVES ? 2 : 1); ++k) {
                 if (k == 1) carry(2 * (c0 + i) + 1);
+                __syncwarp();                               // the loads below are the whole warp's
 #pragma unroll
                 for (int q = 0; q < kCols; q += 16) {
                     uint32_t v[16];

@@ -127,6 +127,15 @@ def test_forward_and_adjoint(case):
               ("y", "h_last", "g_c", "g_b", "g_x", "g_log_a", "g_h0"))
 
 
+@pytest.mark.parametrize("widths", [(64, 64), (31, 63), (128, 64), (96, 128)], ids=str)
+@pytest.mark.parametrize("L", [1, 15, 33, 62, 95, 97, 126, 161, 287])
+def test_the_last_rows_of_a_tile(L, widths):
+    """Sequences that end inside a warp's 32 rows, at every width of the
+    tensor-core kernels."""
+    t = make(BF, 1, 2, 1, L, *widths, "blh", "step", True, False, seed=L)
+    check_all(t, fwd_bwd(t, "blh"), "blh", ("y", "h_last", "g_c", "g_b", "g_x", "g_log_a", "g_h0"))
+
+
 @pytest.mark.parametrize("dtype", [F32, BF])
 def test_adjoint_against_differences(dtype):
     """<g, dx> against (f(x + dx) - f(x - dx)) / 2 in 64 bits on a direction of

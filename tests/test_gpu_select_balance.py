@@ -95,6 +95,26 @@ def test_loss_counts_and_gradients(case):
     close("g_W", g_W, want["g_W"], (tol + rows * ref.U32) * want["mag_W"] + 1e-37)
 
 
+@pytest.mark.parametrize("D", [64, 33, 200])
+@pytest.mark.parametrize("L", [1, 31, 33, 127, 159, 170])
+def test_the_last_rows_of_a_tile(L, D):
+    """B L rows that end inside a warp's 32, and lengths that do."""
+    u, W, k, g_loss, _ = make(BF, 2, L, 3, 8, D, 1.0, False, seed=L)
+    for n in (None, torch.tensor([L, L // 2], dtype=torch.int32, device="cuda")):
+        want = ref.balance(u, W, k, 1.0, n, g_loss)
+        loss, counts, probs = pd.pdssm_select_balance_fwd(u, W, k, lengths=n)
+        g_u, g_W = pd.pdssm_select_balance_bwd(u, W, counts, g_loss, lengths=n)
+        assert torch.equal(counts, want["counts"])
+        e = logit_error(u, W, 1.0) + 20 * ref.U32
+        tol = e + 2 * L * ref.U32
+        close("probs", probs, want["probs"], tol * want["probs"])
+        close("loss", loss, want["loss"], (tol + 2 * ref.U32) * want["loss"])
+        # as in test_loss_counts_and_gradients
+        tol = 3 * e + 24 * ref.U32
+        close("g_u", g_u, want["g_u"], (tol + 24 * ref.U32 + 2 * ref.UBF + 2.0 ** -16) * want["mag_u"] + 1e-37)
+        close("g_W", g_W, want["g_W"], (tol + 2 * L * ref.U32) * want["mag_W"] + 1e-37)
+
+
 def test_gradients_against_differences():
     u, W, k, g_loss, n = make(F32, 2, 40, 2, 6, 24, 1.3, False, seed=1)
     _, counts, _ = pd.pdssm_select_balance_fwd(u, W, k, inv_tau=1.3)
