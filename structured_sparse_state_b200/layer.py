@@ -78,6 +78,9 @@ class AddRMSNormFunction(torch.autograd.Function):
 
     @staticmethod
     def forward(ctx, x, residual, weight, eps, out_dtype):
+        if out_dtype not in (None, torch.float32, torch.bfloat16):
+            raise ValueError(f"add_rmsnorm gives float32 or bfloat16, not {out_dtype}: 8-bit rows "
+                             "come with their scales from pdssm_add_rmsnorm_fwd")
         out, res_out, rstd, _ = pdssm_add_rmsnorm_fwd(x, residual, weight, eps, out_dtype)
         ctx.save_for_backward(res_out, weight, rstd)
         ctx.types = x.dtype, None if residual is None else residual.dtype
@@ -101,7 +104,8 @@ class AddRMSNormFunction(torch.autograd.Function):
 
 def add_rmsnorm(x, residual, weight, eps=1e-6, out_dtype=None):
     """s = x + residual (residual None: s = x) and its root-mean-square norm:
-    returns (norm(s) * weight in out_dtype, s in residual's type)."""
+    returns (norm(s) * weight in out_dtype, s in residual's type).  out_dtype is
+    float32, bfloat16 or None (x's); ValueError otherwise."""
     return AddRMSNormFunction.apply(x, residual, weight, eps, out_dtype)
 
 

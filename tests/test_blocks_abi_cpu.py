@@ -152,3 +152,11 @@ def test_binding_refuses_cpu_tensors():
         pd.pdssm_select_balance_fwd(z(1, 4, 8), z(1, 2, 8), z(1, 1, 4, dtype=torch.int32))
     with pytest.raises(ValueError, match="layout"):
         pd.pdssm_decay_scan_fwd(z(1, 1, 4, 8), z(1, 1, 4, 8), z(1, 1, 4, 8), z(1, 1, 4), layout="lbh")
+
+
+@pytest.mark.parametrize("out_dtype", [torch.float8_e4m3fn, torch.float16, torch.float64], ids=str)
+def test_differentiable_norm_refuses_types_whose_values_it_would_lose(out_dtype):
+    """8-bit rows mean nothing without the scales that the raw call returns."""
+    from structured_sparse_state_b200.layer import add_rmsnorm
+    with pytest.raises(ValueError, match="float32 or bfloat16"):
+        add_rmsnorm(torch.zeros(2, 8), torch.zeros(2, 8), torch.ones(8), out_dtype=out_dtype)
