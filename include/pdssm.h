@@ -510,6 +510,9 @@ typedef enum pdssm_layout { PDSSM_BHL = 0, PDSSM_BLH = 1 } pdssm_layout;
  *    padded rows), which pdssm_decay_scan_bwd needs.  ws: pdssm_decay_workspace_bytes(dims,
  *    dtype, for_bwd) bytes, 256-byte aligned, overwritten; pdssm_ws_status
  *    reads its status word.
+ *  * Waits inside the kernels are bounded (2 s).  One that gives up, which no
+ *    sound run sees, leaves PDSSM_ERR_TIMEOUT in the status word and NaN in
+ *    the y, states and h_last that it was to make.
  * Deterministic: every sum in a fixed order.
  */
 size_t pdssm_decay_workspace_bytes(const pdssm_decay_dims *dims,
@@ -521,6 +524,18 @@ pdssm_status pdssm_decay_scan_fwd(const pdssm_decay_dims *dims, const void *c,
                                   const float *h0, const int32_t *lengths,
                                   void *y, float *h_last, int for_bwd,
                                   void *ws, size_t ws_bytes, void *stream);
+
+/*
+ * Self-test of those waits, with a failure made on purpose but no fault: the
+ * bf16 forward (layout PDSSM_BHL, log_a per step, G = H, N = P in eights) with
+ * its copies held back, so that every wait for them gives up after 2 s.  y
+ * (16-byte aligned) and h_last are then NaN, with for_bwd = 1 the states in ws
+ * too, and pdssm_ws_status returns PDSSM_ERR_TIMEOUT.
+ */
+pdssm_status pdssm_decay_wait_selftest(const pdssm_decay_dims *dims,
+                                       const float *log_a, void *y,
+                                       float *h_last, int for_bwd, void *ws,
+                                       size_t ws_bytes, void *stream);
 
 /*
  * Exact adjoint of pdssm_decay_scan_fwd for the loss

@@ -41,7 +41,7 @@ EXPORTS = ("pdssm_status_str", "pdssm_last_error", "pdssm_version",
            "pdssm_soft_maps", "pdssm_scan_fwd_maps", "pdssm_surrogate_scratch_bytes",
            "pdssm_surrogate_bwd", "pdssm_select_scan_fwd", "pdssm_scan_fwd_single_pass",
            "pdssm_decay_workspace_bytes", "pdssm_decay_scan_fwd", "pdssm_decay_scan_bwd",
-           "pdssm_decay_step", "pdssm_add_rmsnorm_fwd", "pdssm_add_rmsnorm_scratch_bytes",
+           "pdssm_decay_wait_selftest", "pdssm_decay_step", "pdssm_add_rmsnorm_fwd", "pdssm_add_rmsnorm_scratch_bytes",
            "pdssm_add_rmsnorm_bwd", "pdssm_select_balance_scratch_bytes",
            "pdssm_select_balance_fwd", "pdssm_select_balance_bwd")
 
@@ -117,6 +117,7 @@ def _load() -> ctypes.CDLL:
         "pdssm_decay_scan_fwd": (I32, [DD, P, P, P, I32, I32, P, I32, P, P, P, P, I32, P, SZ, P]),
         "pdssm_decay_scan_bwd": (I32, [DD, P, P, P, I32, I32, P, I32, P, P, P, P, P, P, P, P, P,
                                        P, SZ, P]),
+        "pdssm_decay_wait_selftest": (I32, [DD, P, P, P, I32, P, SZ, P]),
         "pdssm_decay_step": (I32, [DD, P, P, P, I32, P, I32, P, I64, P, P, P]),
         "pdssm_add_rmsnorm_fwd": (I32, [I64, I64, P, I32, P, I32, P, I32, ctypes.c_float, P, I32,
                                         P, P, P, P]),
@@ -654,5 +655,5 @@ def pdssm_surrogate_bwd(u, W_sel, A, pi_dict, k, d, b, h0, lam, ws, chunk, inv_t
 # the operators around the scan in a pre-norm block (same names as the C ABI)
 from .blocks import (pdssm_add_rmsnorm_bwd, pdssm_add_rmsnorm_fwd,  # noqa: E402,F401
                      pdssm_decay_scan_bwd, pdssm_decay_scan_fwd, pdssm_decay_step,
-                     pdssm_decay_workspace_bytes, pdssm_select_balance_bwd,
-                     pdssm_select_balance_fwd)
+                     pdssm_decay_wait_selftest, pdssm_decay_workspace_bytes,
+                     pdssm_select_balance_bwd, pdssm_select_balance_fwd)

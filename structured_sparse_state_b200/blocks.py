@@ -21,7 +21,8 @@ from contextlib import contextmanager
 
 import torch
 
-from . import PDSSM_BF16, PDSSM_F32, DecayDims, PdssmError, _lib, lib
+from . import (PDSSM_BF16, PDSSM_F32, DecayDims, PdssmError, _check, _lib, _ptr, _stream, lib,
+               pdssm_ws_status)
 
 BINDING_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "_blocks.so")
 LAYOUTS = {"bhl": False, "blh": True}
@@ -105,6 +106,22 @@ def pdssm_decay_scan_bwd(c, b, x, log_a, h0, g_y, ws, g_hlast=None, lengths=None
     for_bwd=True).  Returns (g_c, g_b, g_x, g_log_a, g_h0)."""
     return _call(_native.decay_scan_bwd, x, stream, c, b, x, log_a, h0, g_y, ws, g_hlast, lengths,
                  _layout(layout), *(out if out is not None else (None,) * 5))
+
+
+def pdssm_decay_wait_selftest(B, H, L, N, for_bwd=False):
+    """The bf16 forward with its copies held back: its bounded waits give up
+    after 2 s.  Returns (status of ws, y, h_last, ws): PDSSM_ERR_TIMEOUT (5)
+    and NaN everywhere expected.  Synchronises."""
+    dev = torch.device("cuda", torch.cuda.current_device())
+    ws = torch.zeros(pdssm_decay_workspace_bytes(B, H, H, L, N, N, torch.bfloat16, for_bwd),
+                     dtype=torch.uint8, device=dev)
+    log_a = torch.zeros(B, H, L, device=dev)
+    y = torch.zeros(B, H, L, N, dtype=torch.bfloat16, device=dev)
+    h_last = torch.zeros(B, H, N, N, device=dev)
+    _check(_lib.pdssm_decay_wait_selftest(ctypes.byref(DecayDims(B, H, H, L, N, N)), _ptr(log_a), _ptr(y),
+                                          _ptr(h_last), int(bool(for_bwd)), _ptr(ws), ws.numel(), _stream(None)),
+           "pdssm_decay_wait_selftest")
+    return pdssm_ws_status(ws), y, h_last, ws
 
 
 def pdssm_decay_step(c, b, x, log_a, state, slots=None, y=None, stream=None):

@@ -52,6 +52,7 @@ struct DecayParams {
     int nseg, seg_chunks, nchunks, pslices;
     int vec, ovec;                      // inputs' rows and pointers allow 16-byte accesses; results'
                                         // (2: y by 32 bytes)
+    int hold;                           // self-test: the tensor-core forward makes no copies
 };
 
 // One step's log decay in base 2, floored (a NaN passes).

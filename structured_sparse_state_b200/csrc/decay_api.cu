@@ -232,6 +232,29 @@ pdssm_status pdssm_decay_scan_fwd(const pdssm_decay_dims *dims, const void *c, c
     return e == cudaSuccess ? PDSSM_OK : cuda_fail(e, "decay scan");
 }
 
+pdssm_status pdssm_decay_wait_selftest(const pdssm_decay_dims *dims, const float *log_a, void *y,
+                                       float *h_last, int for_bwd, void *ws, size_t ws_bytes,
+                                       void *stream) {
+    DecayWs w;
+    pdssm_status st = check_scan(dims, PDSSM_BF16, PDSSM_BHL, log_a, ws, ws_bytes, for_bwd != 0, &w);
+    if (st != PDSSM_OK) return st;
+    if (!y || !h_last || !log_a) return arg_fail(PDSSM_ERR_INVALID_ARG, "NULL tensor pointer");
+    if (!aligned(y, 16) || dims->L < 1 || dims->G != dims->H || dims->N != dims->P || dims->N % 8)
+        return arg_fail(PDSSM_ERR_INVALID_ARG, "need L >= 1, G = H, N = P in eights and y on 16 bytes");
+    if (!decay_tc_copies()) return arg_fail(PDSSM_ERR_UNSUPPORTED, "no tensor maps");
+    DecayParams p;
+    memset(&p, 0, sizeof(p));
+    unsigned char *base = reinterpret_cast<unsigned char *>(ws);
+    set_strides(p, *dims, PDSSM_BHL, true);
+    set_plan(p, decay_plan(*dims, true, false), w, base);
+    p.c = p.b = p.x = y;                // named by the tensor maps, never copied
+    p.log_a = log_a; p.y = y; p.h_last = h_last;
+    if (for_bwd) p.carry = reinterpret_cast<float *>(base + w.carry);
+    p.vec = p.ovec = p.hold = 1;
+    const cudaError_t e = launch_decay_fwd_tc(p, (cudaStream_t)stream);
+    return e == cudaSuccess ? PDSSM_OK : cuda_fail(e, "decay wait self-test");
+}
+
 pdssm_status pdssm_decay_scan_bwd(const pdssm_decay_dims *dims, const void *c, const void *b,
                                   const void *x, pdssm_dtype dtype, pdssm_layout layout,
                                   const float *log_a, int log_a_per_step, const float *h0,

@@ -145,6 +145,20 @@ __device__ __forceinline__ void sts128(uint32_t a, uint32_t x, uint32_t y, uint3
                  : "memory");
 }
 
+// What a wait that gave up left must not pass for a result: NaN in `n` rows of
+// y, and in `count` states one behind another (a CTA's columns of each).  Out of
+// line, since the place of the roles' code moves the time by several percent.
+__device__ __noinline__ void spoil_rows(__nv_bfloat16 *y, int64_t stride, int64_t n, int width) {
+    for (int64_t t = threadIdx.x / 32; t < n; t += kTcTh / 32)
+        for (int q = threadIdx.x % 32; q < width; q += 32)
+            y[t * stride + q] = __ushort_as_bfloat16(0x7fff);
+}
+__device__ __noinline__ void spoil_states(float *s, int count, int N, int P, int width) {
+    for (int i = 0; i < count; ++i, s += (int64_t)N * P)
+        for (int e = threadIdx.x; e < N * width; e += kTcTh)
+            s[(int64_t)(e / width) * P + e % width] = __int_as_float(0x7fffffff);
+}
+
 template <bool STK, int MODE>
 __global__ void __launch_bounds__(kTcTh, 1)
     k_decay_tc(const __grid_constant__ CUtensorMap cmap, const __grid_constant__ CUtensorMap bmap,
@@ -643,7 +657,7 @@ __global__ void __launch_bounds__(kTcTh, 1)
         if (!FWD && lane == 0) totals[warp - kDecay] = total;
     } else if (p.vec) {
         // ---- copies
-        if (warp == kProducer && lane == 0) {
+        if (warp == kProducer && lane == 0 && !p.hold) {
             int i = 0;
             for (; i < n && ok; ++i) {
                 const int t0 = (int)chunk_t0(i);
@@ -710,7 +724,8 @@ __global__ void __launch_bounds__(kTcTh, 1)
         }
     }
     tc_fence_before();
-    if (__syncthreads_or(!ok)) {
+    const bool failed = __syncthreads_or(!ok);
+    if (failed) {
         // a wait gave up (the status word says so): let copies and products in
         // flight land, for a millisecond at most, before the CTA ends
         const uint64_t t = global_ns();
@@ -727,6 +742,17 @@ __global__ void __launch_bounds__(kTcTh, 1)
         const int64_t t_end = imin64((int64_t)c1 * kC, p.L);
         for (int64_t t = (int64_t)(c0 + n) * kC + warp; t < t_end; t += kTcTh / 32)
             for (int q = lane; q < pw; q += 32) y[t * p.oval_t + q] = __float2bfloat16_rn(0.f);
+        if (failed)
+            spoil_rows(y + (int64_t)c0 * kC * p.oval_t, p.oval_t, min((int64_t)n * kC, t_end - (int64_t)c0 * kC), pw);
+    }
+    if (failed) {
+        const int64_t np = (int64_t)p.N * p.P;
+        if (!FWD) spoil_states(p.seg_state + (bh * p.nseg + seg) * np + p0, 1, p.N, p.P, pw);
+        if (FWD && p.h_last && seg == p.nseg - 1) spoil_states(p.h_last + bh * np + p0, 1, p.N, p.P, pw);
+        if (HALVES) {
+            const int chunks64 = (int)((p.L + 63) / 64), ch = max(2 * c0, 1);
+            spoil_states(p.carry + (bh * chunks64 + ch) * np + p0, min(2 * c1, chunks64) - ch, p.N, p.P, pw);
+        }
     }
 }
 

@@ -160,3 +160,16 @@ def test_differentiable_norm_refuses_types_whose_values_it_would_lose(out_dtype)
     from structured_sparse_state_b200.layer import add_rmsnorm
     with pytest.raises(ValueError, match="float32 or bfloat16"):
         add_rmsnorm(torch.zeros(2, 8), torch.zeros(2, 8), torch.ones(8), out_dtype=out_dtype)
+
+
+def test_decay_wait_selftest_refuses_arguments():
+    def run(dm, log_a=P, y=P, h=P, ws=P, n=BIG):
+        return pd.lib().pdssm_decay_wait_selftest(ctypes.byref(dm), log_a, y, h, 0, ws, n, None)
+
+    ok = dict(G=4, N=16, P=16)
+    assert run(dd(**ok, B=0)) == 1
+    assert run(dd(**{**ok, "G": 2})) == 1 and run(dd(**{**ok, "N": 24})) == 1 and run(dd(G=4, N=12, P=12)) == 1
+    assert run(dd(**{**ok, "L": 0})) == 1
+    for bad in (dict(log_a=None), dict(y=None), dict(h=None), dict(ws=None), dict(y=ctypes.c_void_p(4096 + 8))):
+        assert run(dd(**ok), **bad) == 1
+    assert run(dd(**ok), n=256) == 6

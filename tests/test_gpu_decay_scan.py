@@ -340,6 +340,20 @@ def test_odd_widths_at_other_addresses_in_the_adjoint():
         assert torch.equal(got, want[n]), n
 
 
+@pytest.mark.parametrize("N,L,for_bwd", [(64, 200, False), (128, 200, True), (64, 1100, True)])
+def test_a_wait_that_gives_up_leaves_no_result(N, L, for_bwd):
+    """Copies held back: the status word says so, and y, the last state and the
+    states for the adjoint are NaN (one segment, and two); the context stays
+    usable."""
+    st, y, h_last, ws = pd.pdssm_decay_wait_selftest(1, 2, L, N, for_bwd)
+    assert st == 5 and torch.isnan(y).all() and torch.isnan(h_last).all()
+    t = make(BF, 1, 2, 2, L, N, N, "bhl", "step", False, False, seed=14)
+    if for_bwd:         # a gradient that rests on a state is NaN too (the first 64 steps' rest on none)
+        g = pd.pdssm_decay_scan_bwd(t["c"], t["b"], t["x"], t["log_a"], None, t["g_y"], ws)
+        assert torch.isnan(g[0][:, :, 64:]).all()
+    check_all(t, fwd_bwd(t, "bhl"), "bhl", ("y", "h_last", "g_c", "g_b", "g_x", "g_log_a", "g_h0"))
+
+
 # ----------------------------------------------------------------------------
 # single tokens
 # ----------------------------------------------------------------------------
