@@ -5,6 +5,9 @@ marshals PyTorch tensors (device memory, the current stream) into the C ABI
 declared in ``include/pdssm.h``; all arithmetic runs in the CUDA kernels.
 There is no CPU path: importing this package without the built library, or
 calling it with CPU tensors, raises.
+A `stream` other than the current one is ordered with it by the caller, who
+also keeps the tensors of a call alive until that stream has passed it (the
+operators of blocks.py see to the latter themselves).
 
     k = pdssm_select(u, W_sel)                          # hard selection
     y, h_last, ws = pdssm_scan_fwd(pi, k, d, b, c, h0, chunk=128, for_bwd=True)

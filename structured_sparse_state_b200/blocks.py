@@ -8,7 +8,9 @@ checks and allocations run natively (``csrc/blocks_py.cpp``): these calls are
 short.
 
 Every tensor of a call lies on one CUDA device, which need not be the current
-one; work goes to that device's current stream, or to ``stream``.  A wrong
+one; work goes to that device's current stream, or to ``stream``, whose order
+with the streams that made the inputs and read the results is the caller's to
+keep (``stream.wait_stream``).  Inputs may be dropped after the call.  A wrong
 argument raises ValueError, a status of the library PdssmError.
 """
 from __future__ import annotations
@@ -64,14 +66,19 @@ def _layout(layout):
 
 
 def _call(fn, x, stream, *args):
-    """fn on the current stream of the tensors' device, or on `stream` (then
-    allocations belong to it too)."""
+    """fn on the current stream of the tensors' device, or on `stream`: then
+    what it allocates belongs to that stream, and what it was given is not
+    handed out again before that stream is done with it."""
     if stream is None:
         return fn(*args)
     if isinstance(x, torch.Tensor) and x.is_cuda and stream.device != x.device:
         raise ValueError(f"stream is on {stream.device}, expected {x.device}")
     with _enter(stream):
-        return fn(*args)
+        result = fn(*args)
+    for t in args:
+        if isinstance(t, torch.Tensor):
+            t.record_stream(stream)
+    return result
 
 
 # ----------------------------------------------------------------------------

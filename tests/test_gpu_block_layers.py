@@ -8,6 +8,7 @@ import pytest
 import torch
 
 import block_ref as ref
+import structured_sparse_state_b200 as pd
 from structured_sparse_state_b200.layer import (DecayLayer, PDSSMLayer, ResidualStack, add_rmsnorm,
                                                 decay_scan, select_balance)
 
@@ -209,3 +210,37 @@ def test_missing_gradients_and_inference():
     assert not counts.requires_grad and not probs.requires_grad
     loss.sum().backward()
     assert torch.isfinite(u.grad).all() and torch.isfinite(W.grad).all()
+
+
+def calls_on_a_stream():
+    """{name: (input, call of it on a stream)}, for two calls each."""
+    x, w = rand(4096, 256, seed=20), rand(256, seed=21)
+    rstd = x[:, 0].abs()
+    k = torch.zeros(1, 2, 4096, dtype=torch.int32, device="cuda")
+    W, c, log_a = rand(2, 4, 256, seed=22), rand(1, 1, 4096, 16, seed=23), -rand(4, seed=25).abs()
+    token = c.view(4096, 1, 16)
+    state = rand(4096, 4, 16, 64, seed=24)
+    states = [state, state.clone()]
+    return dict(
+        norm=(x, lambda t, s: pd.pdssm_add_rmsnorm_fwd(t, None, w, stream=s)[0]),
+        norm_backward=(x, lambda t, s: pd.pdssm_add_rmsnorm_bwd(t, x, w, rstd, stream=s)[0]),
+        balance=(x.view(1, 4096, 256), lambda t, s: pd.pdssm_select_balance_fwd(t, W, k, stream=s)[2]),
+        scan=(x.view(1, 4, 4096, 64), lambda t, s: pd.pdssm_decay_scan_fwd(c, c, t, log_a, stream=s)[0]),
+        step=(x.view(4096, 4, 64), lambda t, s: pd.pdssm_decay_step(token, token, t, log_a, states.pop(), stream=s)))
+
+
+@pytest.mark.parametrize("call", ["norm", "norm_backward", "balance", "scan", "step"])
+def test_an_input_dropped_after_a_call_on_another_stream(call):
+    """Its memory is not handed out again while that stream has yet to read it."""
+    src, run = calls_on_a_stream()[call]
+    want = run(src, None)
+    side = torch.cuda.Stream()
+    t = src.clone()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(100_000_000)          # about 50 ms
+    got = run(t, side)
+    del t
+    others = [torch.full_like(src, float("nan")) for _ in range(3)]
+    torch.cuda.synchronize()
+    assert torch.equal(got, want) and len(others) == 3
