@@ -14,6 +14,7 @@ struct BalParams {
     const float *W;
     const int32_t *k;
     const int32_t *lengths;
+    const int64_t *steps;               // in front of the lengths, of more than kBalWarpB sequences
     float inv_tau;
     const int32_t *counts;
     const float *g_loss;
@@ -32,11 +33,16 @@ __device__ __forceinline__ int64_t bal_len(const BalParams &p, int b) {
     return n < 0 ? 0 : (n > p.L ? p.L : n);
 }
 
-// steps in front of the lengths, by one warp or more; every thread gets it
+// steps in front of the lengths, for a whole warp: of more sequences than a
+// warp has lanes, they have been counted before (k_bal_steps)
+constexpr int kBalWarpB = 32;
 __device__ __forceinline__ int64_t bal_steps(const BalParams &p) {
     if (!p.lengths) return p.rows;
-    int64_t n = 0;
-    for (int b = 0; b < p.B; ++b) n += bal_len(p, b);
+    if (p.steps) return *p.steps;
+    const int lane = threadIdx.x % 32;
+    int64_t n = lane < p.B ? bal_len(p, lane) : 0;
+#pragma unroll
+    for (int d = 16; d; d >>= 1) n += __shfl_xor_sync(kFull, n, d);
     return n;
 }
 

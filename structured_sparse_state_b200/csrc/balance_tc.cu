@@ -561,16 +561,17 @@ __global__ void __launch_bounds__(threads_of(N), 1)
 __global__ void k_bal_parts(BalParams p, BalTcPlan pl, unsigned char *parts, float *freq) {
     const int64_t n = (int64_t)pl.groups * pl.N * (pl.Dp / 2);
     const int64_t e = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
-    if (e >= n) return;
+    if (e >= n) return;                 // n is a multiple of 2048: whole CTAs
     const int d = (int)(e % (pl.Dp / 2)) * 2;
     const int64_t c = e / (pl.Dp / 2);
     const int h = (int)(c / pl.KT), k = (int)(c % pl.KT);
     const int g = (int)(c / pl.N), row = (int)(c % pl.N);
-    if (p.counts && d == 0) {
+    // d = 0 falls on a warp's first thread, since Dp / 2 is a multiple of 32
+    if (p.counts && __shfl_sync(kFull, d, 0) == 0) {
         const int64_t steps = bal_steps(p);
         const float inv = steps > 0 ? 1.f / (float)steps : 0.f;
-        freq[c] = h < p.H && k < p.K ? (float)p.counts[h * p.K + k] * inv : 0.f;
-        if (k == 0)
+        if (d == 0) freq[c] = h < p.H && k < p.K ? (float)p.counts[h * p.K + k] * inv : 0.f;
+        if (d == 0 && k == 0)
             freq[(int64_t)pl.groups * pl.N + h] =
                 h < p.H ? p.g_loss[h] * ((float)p.K * p.inv_tau) * inv : 0.f;
     }

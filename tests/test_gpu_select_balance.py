@@ -197,6 +197,28 @@ def test_same_bits_again_and_in_a_graph(dtype):
         assert torch.equal(a, b) and torch.equal(a, c)
 
 
+@pytest.mark.parametrize("dtype", [F32, BF])
+@pytest.mark.parametrize("B,L", [(31, 9), (32, 9), (33, 9), (1025, 3), (5000, 5)])
+def test_many_ragged_sequences(dtype, B, L):
+    """Up to as many lengths as a warp has lanes, and thousands; some negative or
+    beyond L."""
+    u, W, k, g_loss, n = make(dtype, B, L, 5, 16, 48, 1.0, True, seed=B)
+    n[1], n[2] = L + 7, -3
+    want = ref.balance(u, W, k, 1.0, n.clamp(0, L), g_loss)
+    loss, counts, probs = pd.pdssm_select_balance_fwd(u, W, k, lengths=n)
+    g_u, g_W = pd.pdssm_select_balance_bwd(u, W, counts, g_loss, lengths=n)
+    assert torch.equal(counts, want["counts"])
+    # as in test_loss_counts_and_gradients
+    e = logit_error(u, W, 1.0) + 28 * ref.U32
+    tol = e + B * L * ref.U32
+    close("probs", probs, want["probs"], tol * want["probs"])
+    close("loss", loss, want["loss"], (tol + 2 * ref.U32) * want["loss"])
+    tol = 3 * e + 32 * ref.U32
+    low = 2 * ref.UBF + 2.0 ** -16 if dtype == BF else ref.U32
+    close("g_u", g_u, want["g_u"], (tol + 80 * ref.U32 + low) * want["mag_u"] + 1e-37)
+    close("g_W", g_W, want["g_W"], (tol + B * L * ref.U32) * want["mag_W"] + 1e-37)
+
+
 def test_selection_then_balance():
     """The selection's own indices: what the layer does."""
     u, W, _, g_loss, _ = make(BF, 2, 300, 4, 16, 64, 1.0, False, seed=6)
