@@ -81,7 +81,9 @@ class AddRMSNormFunction(torch.autograd.Function):
         if out_dtype not in (None, torch.float32, torch.bfloat16):
             raise ValueError(f"add_rmsnorm gives float32 or bfloat16, not {out_dtype}: 8-bit rows "
                              "come with their scales from pdssm_add_rmsnorm_fwd")
-        out, res_out, rstd, _ = pdssm_add_rmsnorm_fwd(x, residual, weight, eps, out_dtype)
+        out, res_out, rstd, _ = pdssm_add_rmsnorm_fwd(
+            x.contiguous(), None if residual is None else residual.contiguous(), weight, eps,
+            out_dtype)
         ctx.save_for_backward(res_out, weight, rstd)
         ctx.types = x.dtype, None if residual is None else residual.dtype
         ctx.set_materialize_grads(False)
@@ -105,7 +107,8 @@ class AddRMSNormFunction(torch.autograd.Function):
 def add_rmsnorm(x, residual, weight, eps=1e-6, out_dtype=None):
     """s = x + residual (residual None: s = x) and its root-mean-square norm:
     returns (norm(s) * weight in out_dtype, s in residual's type).  out_dtype is
-    float32, bfloat16 or None (x's); ValueError otherwise."""
+    float32, bfloat16 or None (x's); ValueError otherwise.  x and residual may
+    have any strides."""
     return AddRMSNormFunction.apply(x, residual, weight, eps, out_dtype)
 
 
@@ -303,6 +306,7 @@ class DecayLayer(torch.nn.Module):
 class ResidualStack(torch.nn.Module):
     """Blocks (PDSSMLayer or DecayLayer) over one residual stream with a final
     norm; a block's output is added to the stream inside the next norm.
+    (It calls their `block`, so forward hooks of blocks and norms do not run.)
     balance=True also returns the mean balance loss of the selecting blocks."""
 
     def __init__(self, blocks, d_model, device=None):

@@ -212,6 +212,32 @@ def test_missing_gradients_and_inference():
     assert torch.isfinite(u.grad).all() and torch.isfinite(W.grad).all()
 
 
+def test_blocks_and_steps_take_any_strides():
+    """What forward accepts, block, step and a stack accept too: a token cut out
+    of a batch, a transposed batch, and their gradients."""
+    torch.manual_seed(4)
+    layer = DecayLayer(64, 2, 16, 16, device="cuda")
+    x = rand(3, 20, 64, seed=30)
+    state = torch.zeros(3, 2, 16, 16, device="cuda")
+    for t in range(3):
+        a, s = state.clone(), state.clone()
+        res = rand(3, 20, 64, seed=31)
+        got = layer.step(x[:, t], res[:, t], a)
+        want = layer.step(x[:, t].contiguous(), res[:, t].contiguous(), s)
+        assert all(torch.equal(u, v) for u, v in zip(got, want)) and torch.equal(a, s)
+        state = a
+    xt = rand(20, 3, 64, seed=32).requires_grad_()
+    xc = xt.detach().transpose(0, 1).contiguous().requires_grad_()
+    for model in (layer, ResidualStack([layer], 64, device="cuda")):
+        call = model.block if model is layer else (lambda v: (model(v),))
+        got, want = call(xt.transpose(0, 1))[0], call(xc)[0]
+        g = rand(*got.shape, seed=33)
+        assert torch.equal(got, want)
+        gt, = torch.autograd.grad(got, xt, g)
+        gc, = torch.autograd.grad(want, xc, g)
+        assert torch.equal(gt.transpose(0, 1), gc)
+
+
 def calls_on_a_stream():
     """{name: (input, call of it on a stream)}, for two calls each."""
     x, w = rand(4096, 256, seed=20), rand(256, seed=21)
