@@ -60,7 +60,7 @@ def _enter(stream):
 
 
 def _layout(layout):
-    if layout not in LAYOUTS:
+    if layout not in tuple(LAYOUTS):
         raise ValueError(f"layout must be one of {tuple(LAYOUTS)}")
     return LAYOUTS[layout]
 
@@ -85,7 +85,9 @@ def _call(fn, x, stream, *args):
 # decay scan
 # ----------------------------------------------------------------------------
 def pdssm_decay_workspace_bytes(B, H, G, L, N, P, dtype=torch.float32, for_bwd=False) -> int:
-    code = {torch.float32: PDSSM_F32, torch.bfloat16: PDSSM_BF16}[dtype]
+    if dtype not in (torch.float32, torch.bfloat16):
+        raise ValueError(f"dtype {dtype}, expected float32 or bfloat16")
+    code = PDSSM_BF16 if dtype == torch.bfloat16 else PDSSM_F32
     n = _lib.pdssm_decay_workspace_bytes(ctypes.byref(DecayDims(B, H, G, L, N, P)), code,
                                          int(bool(for_bwd)))
     if n == 0:

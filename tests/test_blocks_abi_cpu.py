@@ -173,3 +173,13 @@ def test_decay_wait_selftest_refuses_arguments():
     for bad in (dict(log_a=None), dict(y=None), dict(h=None), dict(ws=None), dict(y=ctypes.c_void_p(4096 + 8))):
         assert run(dd(**ok), **bad) == 1
     assert run(dd(**ok), n=256) == 6
+
+
+def test_wrong_arguments_are_value_errors():
+    for dtype in (torch.float16, torch.float64, None, "bf16"):
+        with pytest.raises(ValueError, match="dtype"):
+            pd.pdssm_decay_workspace_bytes(1, 1, 1, 10, 16, 16, dtype)
+    z = torch.zeros
+    for layout in (None, 1, ["bhl"]):
+        with pytest.raises(ValueError, match="layout"):
+            pd.pdssm_decay_scan_fwd(z(1, 1, 4, 8), z(1, 1, 4, 8), z(1, 1, 4, 8), z(1, 1, 4), layout=layout)
