@@ -119,7 +119,7 @@ struct DecayPad {
 };
 
 // launchers (each returns the launch's error)
-cudaError_t launch_decay_join(const DecayParams &p, const float *first, bool reverse, float *last,
+cudaError_t launch_decay_join(const DecayParams &p, const float *first, bool reverse,
                               cudaStream_t st);
 cudaError_t launch_decay_sum_heads(const DecayParams &p, pdssm_dtype dt, const float *part_c,
                                    const float *part_b, void *g_c, void *g_b, cudaStream_t st);

@@ -740,7 +740,7 @@ cudaError_t launch_decay_bwd_mma(const DecayParams &p, cudaStream_t st) {
         s.pslices = (p.P + 63) / 64;
         cudaError_t e = launch_decay_seg_rev_tc(s, st);
         if (e != cudaSuccess) return e;
-        e = launch_decay_join(p, p.g_hlast, true, nullptr, st);
+        e = launch_decay_join(p, p.g_hlast, true, st);
         if (e != cudaSuccess) return e;
     }
     if (p.N <= 64) return p.P <= 64 ? go<1, 1>(p, st) : go<1, 2>(p, st);

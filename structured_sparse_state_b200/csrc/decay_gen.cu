@@ -564,7 +564,7 @@ __global__ void __launch_bounds__(kThreads) k_decay_bwd_gen(DecayParams p) {
 
 // Joins the segments: seg_state[s] becomes the state that enters segment s
 // (from its left, or, reversed, its right), starting from `first`.
-__global__ void k_decay_join(DecayParams p, const float *first, int reverse, float *last) {
+__global__ void k_decay_join(DecayParams p, const float *first, int reverse) {
     const int64_t np = (int64_t)p.N * p.P;
     const int64_t e = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
     if (e >= (int64_t)p.B * p.H * np) return;
@@ -588,7 +588,6 @@ __global__ void k_decay_join(DecayParams p, const float *first, int reverse, flo
             s = fmaf(a[k], s, loc[k]);
         }
     }
-    if (last) last[e] = s;
 }
 
 // g_c, g_b of shared keys: the sum over their heads, in head order.
@@ -706,7 +705,7 @@ struct Fwd {
         if (p.nseg > 1) {
             cudaError_t e = seg_gen<NT, PT, false>(p, st);
             if (e != cudaSuccess) return e;
-            e = launch_decay_join(p, p.h0, false, nullptr, st);
+            e = launch_decay_join(p, p.h0, false, st);
             if (e != cudaSuccess) return e;
         }
         const size_t smem =
@@ -721,7 +720,7 @@ struct Bwd {
         if (p.nseg > 1) {
             cudaError_t e = seg_gen<NT, PT, true>(p, st);
             if (e != cudaSuccess) return e;
-            e = launch_decay_join(p, p.g_hlast, true, nullptr, st);
+            e = launch_decay_join(p, p.g_hlast, true, st);
             if (e != cudaSuccess) return e;
         }
         const size_t smem = (size_t)(2 * kC * (NT + PT + 8) + 2 * NT * (PT + 4) + 2 * kC * (kC + 4) +
@@ -746,10 +745,10 @@ cudaError_t by_widths(const DecayParams &p, cudaStream_t st) {
 
 }  // namespace
 
-cudaError_t launch_decay_join(const DecayParams &p, const float *first, bool reverse, float *last,
+cudaError_t launch_decay_join(const DecayParams &p, const float *first, bool reverse,
                               cudaStream_t st) {
     const int64_t n = (int64_t)p.B * p.H * p.N * p.P;
-    k_decay_join<<<dim3((unsigned)((n + 127) / 128)), 128, 0, st>>>(p, first, reverse ? 1 : 0, last);
+    k_decay_join<<<dim3((unsigned)((n + 127) / 128)), 128, 0, st>>>(p, first, reverse ? 1 : 0);
     return cudaGetLastError();
 }
 

@@ -796,7 +796,7 @@ cudaError_t fwd_tc(const DecayParams &p, cudaStream_t st) {
     if (p.nseg > 1) {
         cudaError_t e = go<STK, kSegFwd>(p, true, st);
         if (e != cudaSuccess) return e;
-        e = launch_decay_join(p, p.h0, false, nullptr, st);
+        e = launch_decay_join(p, p.h0, false, st);
         if (e != cudaSuccess) return e;
     }
     return p.carry ? go<STK, kFwdCarry>(p, p.nseg <= 1, st) : go<STK, kFwd>(p, p.nseg <= 1, st);
