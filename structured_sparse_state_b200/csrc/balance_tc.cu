@@ -29,6 +29,7 @@
 
 #include "balance.cuh"
 #include "launch.cuh"
+#include "tile_bf16.cuh"
 #include "umma.cuh"
 
 namespace pdssm {
@@ -54,27 +55,6 @@ struct TcP {
     int nslot, ustages;                         // of W, of u
     uint32_t o_u, o_g, o_tab, o_bar;            // shared-memory offsets (weights at 0)
 };
-
-__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
-    uint32_t r;
-    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-    return r;
-}
-__device__ __forceinline__ float lo_of(uint32_t w) { return __uint_as_float(w << 16); }
-__device__ __forceinline__ float hi_of(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
-__device__ __forceinline__ uint32_t piece(int r, int q) {
-    return (uint32_t)(r * 128 + ((q ^ (r & 7)) << 4));
-}
-__device__ __forceinline__ void sts128(uint32_t a, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
-    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(x), "r"(y), "r"(z), "r"(w)
-                 : "memory");
-}
-
-__device__ __forceinline__ float ex2(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
 
 // Softmax of the heads in 32 columns, logits in units of log2 e / tau applied
 // here; columns of absent entries (k >= K) get 0.

@@ -21,6 +21,7 @@
 // 32 heads x 16384 steps of 64 x 64: 373 us (107 kflop per step, 150 TFLOP/s).
 #include "decay.cuh"
 #include "launch.cuh"
+#include "tile_bf16.cuh"
 
 namespace pdssm {
 namespace {
@@ -57,17 +58,6 @@ struct Smem {
     static constexpr uint32_t kF = kQ + kTile;                      // floats below
     static constexpr uint32_t kTotal = kF + 2 * sizeof(Sums<kWC>);
 };
-
-__device__ __forceinline__ uint32_t piece(int r, int q) {
-    return (uint32_t)(r * 128 + ((q ^ (r & 7)) << 4));
-}
-__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
-    uint32_t r;
-    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-    return r;
-}
-__device__ __forceinline__ float lo_of(uint32_t w) { return __uint_as_float(w << 16); }
-__device__ __forceinline__ float hi_of(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
 
 __device__ __forceinline__ void ldm4(uint32_t (&r)[4], uint32_t a) {
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"

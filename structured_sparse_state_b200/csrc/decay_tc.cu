@@ -44,6 +44,7 @@
 
 #include "decay.cuh"
 #include "launch.cuh"
+#include "tile_bf16.cuh"
 #include "umma.cuh"
 
 namespace pdssm {
@@ -113,36 +114,12 @@ struct TcParams {
     int first;              // this launch clears the status word
 };
 
-__device__ __forceinline__ float ex2(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-
-__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
-    uint32_t r;
-    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-    return r;
-}
-__device__ __forceinline__ float lo_of(uint32_t w) { return __uint_as_float(w << 16); }
-__device__ __forceinline__ float hi_of(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
-
-// Byte offset of 16-byte piece q of row r in a 128-byte-swizzled tile of
-// 128-byte rows.
-__device__ __forceinline__ uint32_t piece(int r, int q) {
-    return (uint32_t)(r * 128 + ((q ^ (r & 7)) << 4));
-}
-
 __device__ __forceinline__ uint4 lds128(uint32_t a) {
     uint4 v;
     asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
                  : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
                  : "r"(a));
     return v;
-}
-__device__ __forceinline__ void sts128(uint32_t a, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
-    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(x), "r"(y), "r"(z), "r"(w)
-                 : "memory");
 }
 
 // What a wait that gave up left must not pass for a result: NaN in `n` rows of
