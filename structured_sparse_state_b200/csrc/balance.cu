@@ -226,12 +226,13 @@ __global__ void __launch_bounds__(32 * kSumWays) k_bal_loss(BalParams p, float *
     if (k == 0) loss[h] = (float)(v * p.K);
 }
 
-// what the gradients of a group need: counts / T, and per head the factor
+// what the gradients of a group need: its entries' excess counts / T, and per
+// head the factor
 __device__ __forceinline__ void bal_factors(const BalParams &p, int h0, int nh, float *f, float *by) {
     const int64_t steps = bal_steps(p);
     const float inv = steps > 0 ? 1.f / (float)steps : 0.f;
     const int i = threadIdx.x;
-    if (i < nh * p.K) f[i] = (float)p.counts[h0 * p.K + i] * inv;
+    if (i < nh * p.K) f[i] = bal_excess(p.counts[h0 * p.K + i], p.K, steps);
     if (i < nh) by[i] = p.g_loss[h0 + i] * ((float)p.K * p.inv_tau) * inv;
 }
 

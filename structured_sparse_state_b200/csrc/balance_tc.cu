@@ -49,7 +49,7 @@ struct TcP {
     BalParams p;
     BalTcPlan pl;
     const unsigned char *parts;                 // [groups][3][Dp/64][N][128 bytes], swizzled
-    const float *freq;                          // counts / T [groups * N], then per head the
+    const float *freq;                          // excess counts / T [groups * N], then per head the
                                                 // factor g_loss K inv_tau / T
     int vec;
     int nslot, ustages;                         // of W, of u
@@ -537,7 +537,7 @@ __global__ void __launch_bounds__(threads_of(N), 1)
 
 // W's three bf16 parts, per group in the shared-memory image of a K-major
 // operand: [3][Dp / 64][N rows][128 bytes], 128-byte swizzle.
-// With counts (backward) also the table of counts / T and the heads' factors.
+// With counts (backward) also the table of their excess and the heads' factors.
 __global__ void k_bal_parts(BalParams p, BalTcPlan pl, unsigned char *parts, float *freq) {
     const int64_t n = (int64_t)pl.groups * pl.N * (pl.Dp / 2);
     const int64_t e = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
@@ -550,7 +550,7 @@ __global__ void k_bal_parts(BalParams p, BalTcPlan pl, unsigned char *parts, flo
     if (p.counts && __shfl_sync(kFull, d, 0) == 0) {
         const int64_t steps = bal_steps(p);
         const float inv = steps > 0 ? 1.f / (float)steps : 0.f;
-        if (d == 0) freq[c] = h < p.H && k < p.K ? (float)p.counts[h * p.K + k] * inv : 0.f;
+        if (d == 0) freq[c] = h < p.H && k < p.K ? bal_excess(p.counts[h * p.K + k], p.K, steps) : 0.f;
         if (d == 0 && k == 0)
             freq[(int64_t)pl.groups * pl.N + h] =
                 h < p.H ? p.g_loss[h] * ((float)p.K * p.inv_tau) * inv : 0.f;

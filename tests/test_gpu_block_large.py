@@ -117,3 +117,25 @@ def test_balance(dtype):
     tol = 4 * logit + 64 * ref.U32 + (ref.UBF if dtype == BF else 0.0)
     assert ((g_u[0, -999:].double() - want).abs() <= tol * mag + ref.unit(dtype) * want.abs()).all()
     assert torch.isfinite(g_W).all() and abs(probs.sum().item() - 1) <= 1e-5
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_balance_weights_gradient(dtype):
+    """g_W over 2^23 rows against the formula in 64 bits, by its norm: units as in
+    the balance's own test of it, and 12 for the sums over a CTA's hundreds of
+    tiles (each addition of them off by half a unit at most, in squares)."""
+    L, D, K = 2 ** 23 + 333, 256, 4
+    g = torch.Generator(device="cuda").manual_seed(5)
+    u, W = normal(g, 1, L, D, dtype=dtype), normal(g, 1, K, D) * D ** -0.5
+    k = (torch.rand(1, 1, L, generator=g, device="cuda").square() * K).to(torch.int32).clamp_(max=K - 1)
+    _, counts, probs = pd.pdssm_select_balance_fwd(u, W, k)
+    _, g_W = pd.pdssm_select_balance_bwd(u, W, counts, torch.ones(1, device="cuda"))
+    f = counts[0].double() / L
+    want, mean = torch.zeros(K, D, dtype=torch.float64, device="cuda"), torch.zeros(K, dtype=torch.float64, device="cuda")
+    for part in u[0].split(1 << 20):
+        p = torch.softmax(part.double() @ W[0].double().T, -1)
+        want += (K / L * p * (f - (p * f).sum(-1, keepdim=True))).T @ part.double()
+        mean += p.sum(0) / L
+    units = 1.5 * (D / 16 + 8 + 8) + 12
+    assert (g_W[0].double() - want).norm() <= units * ref.U32 * want.norm()
+    assert (probs[0].double() - mean).norm() <= units * ref.U32 * mean.norm()

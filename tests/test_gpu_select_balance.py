@@ -115,6 +115,29 @@ def test_the_last_rows_of_a_tile(L, D):
         close("g_W", g_W, want["g_W"], (tol + 2 * L * ref.U32) * want["mag_W"] + 1e-37)
 
 
+@pytest.mark.parametrize("case", [
+    (BF, 2, 3000, 16, 16, 128, 1.0, False), (BF, 2, 20000, 4, 16, 64, 1.0, False), (BF, 3, 14000, 2, 8, 256, 1.0, False),
+    (BF, 2, 257, 16, 32, 256, 1.0, False), (F32, 4, 1200, 16, 8, 200, 1.0, False), (F32, 1, 30000, 3, 2, 128, 1.0, False)],
+    ids=lambda c: "-".join(str(v).replace("torch.", "") for v in c))
+def test_weights_gradient_in_norm(case):
+    """Tighter than the counted sums of worst cases: a lost bf16 part of the
+    weights or of the logits' gradients (2.7e-6 in the mean square) would show.
+
+    In units of 2^-24: a product's additions are truncated, by one unit on
+    average: D / 16 of a logit (of size one), 8 of a tile's g_W; the roundings
+    of exp (4), its argument (4), the division (2), the norm (4) and the factors
+    (3) add up in squares, to 8.  With half as much again for the sums over
+    tiles (fp32: for the chains over D and the rows)."""
+    u, W, k, g_loss, _ = make(*case)
+    want = ref.balance(u, W, k, case[6], None, g_loss)
+    loss, counts, probs = pd.pdssm_select_balance_fwd(u, W, k, inv_tau=case[6])
+    _, g_W = pd.pdssm_select_balance_bwd(u, W, counts, g_loss, inv_tau=case[6])
+    units = 1.5 * (max(case[5], 64) / 16 + 8 + 8)
+    for n, got in (("probs", probs), ("loss", loss), ("g_W", g_W)):
+        err = ((got.double() - want[n]).norm() / want[n].norm()).item()
+        assert err <= units * ref.U32, (n, err / ref.U32)
+
+
 def test_gradients_against_differences():
     u, W, k, g_loss, n = make(F32, 2, 40, 2, 6, 24, 1.3, False, seed=1)
     _, counts, _ = pd.pdssm_select_balance_fwd(u, W, k, inv_tau=1.3)
