@@ -127,6 +127,81 @@ def test_forward_and_adjoint(case):
               ("y", "h_last", "g_c", "g_b", "g_x", "g_log_a", "g_h0"))
 
 
+# The counted bounds above are sums of worst cases.  These are of a result's norm,
+# in units of 2^-24, and tight enough that a lost bf16 part of a split operand
+# shows (two parts of three: each rounding leaves (1 / sqrt 12) 2^-7 / 1.36 =
+# 1.66e-3 in the mean square, so 2.7e-6 of the operand).
+#   last state, bf16: the largest part's eight additions of a chunk, truncated (2
+#   units each at most), decay of a step (ex2: 4, its argument: 4), split, sum: 26
+#   first state's gradient, bf16: twelve such additions (three parts of four), 34
+#   fp32: 32 additions of a chunk, decay and sum, 40
+STATE_UNITS = {("h_last", BF): 26, ("g_h0", BF): 34, ("h_last", F32): 40, ("g_h0", F32): 40}
+#   g_log_a: 128 additions over a width, 32 over a chunk, 8 around them; and a
+#   chunk's pairs that do not straddle the step cancel (twice as many at most)
+DECAY_UNITS = 2 * 168
+
+NORMS = [
+    (BF, 1, 2, 2, 1100, 64, 64, "bhl", "step", True, False),
+    (BF, 2, 4, 2, 1500, 100, 72, "blh", "step", True, True),
+    (BF, 1, 2, 2, 1300, 128, 128, "bhl", "step", True, False),
+    (BF, 1, 1, 1, 3000, 48, 40, "bhl", "step", True, False),
+    (BF, 1, 2, 1, 513, 128, 128, "bhl", "step", True, False),
+    (F32, 1, 1, 1, 1500, 16, 128, "blh", "step", True, False),
+    (F32, 1, 2, 2, 700, 64, 48, "bhl", "step", True, False),
+    (F32, 2, 2, 2, 330, 128, 100, "bhl", "step", True, False),
+]
+
+
+def heads_of(v, layout):
+    """[B, H, L] of a per-step log decay's gradient."""
+    return v.double() if layout == "bhl" else v.double().transpose(1, 2)
+
+
+@pytest.mark.parametrize("case", NORMS, ids=lambda c: "-".join(str(v).replace("torch.", "") for v in c))
+def test_states_and_decay_gradients_in_norm(case):
+    dtype, layout = case[0], case[7]
+    t = make(*case, seed=15)
+    got = fwd_bwd(t, layout)
+    want = ref.decay_scan(t["c"], t["b"], t["x"], t["log_a"], t["h0"], t["lengths"], layout, t["g_y"], t["g_hlast"])
+    for n in ("h_last", "g_h0"):
+        err = (got[n].double() - want[n]).norm() / want[n].norm()
+        assert err <= STATE_UNITS[n, dtype] * ref.U32, (n, err.item() / ref.U32)
+    a, w = heads_of(got["g_log_a"], layout), heads_of(want["g_log_a"], layout)
+    err, size = (a - w).norm(dim=-1), w.norm(dim=-1)
+    assert (err <= DECAY_UNITS * ref.U32 * size).all(), (err / size).max().item() / ref.U32
+    live = torch.full((case[1],), case[4], device="cuda") if t["lengths"] is None else t["lengths"]
+    assert (size[live > 0] > 0).all()       # nothing but an empty sequence's could be zero
+
+
+@pytest.mark.parametrize("dtype,L,N,P", [(BF, 1300, 128, 128), (BF, 1100, 64, 64), (F32, 1100, 32, 48)], ids=str)
+def test_decays_gradient_of_a_head_against_its_steps_and_differences(dtype, L, N, P):
+    """A decay for each head over several segments: the sum of the steps'
+    gradients, and the difference of the loss in 64 bits."""
+    t = make(dtype, 2, 3, 3, L, N, P, "bhl", "head", True, True, seed=16)
+    got = fwd_bwd(t, "bhl")["g_log_a"].double()
+
+    def at(h):
+        la = t["log_a"].double() + h
+        return ref.decay_scan(t["c"], t["b"], t["x"], la[None, :, None].expand(2, 3, L), t["h0"], t["lengths"], "bhl",
+                              t["g_y"], t["g_hlast"])
+
+    steps = at(0.0)["g_log_a"]
+    bound = DECAY_UNITS * ref.U32 * steps.abs().sum((0, 2))
+    want = steps.sum((0, 2))
+    assert ((got - want).abs() <= bound).all()
+    assert (want.abs() > bound).all()       # a zero would not pass
+
+    def loss(h):
+        o = at(h)
+        return ((o["y"] * t["g_y"].double()).sum((0, 2, 3)) + (o["h_last"] * t["g_hlast"].double()).sum((0, 2, 3)))
+
+    h = 1e-5        # a head's loss depends on its own decay alone
+    numeric = (loss(h) - loss(-h)) / (2 * h)
+    # the difference's own error: h^2 / 6 of a third derivative, of at most (1 / (1 - a))^2 the first's
+    memory = (1 / (1 - t["log_a"].double().exp())).clamp(max=L)
+    assert ((got - numeric).abs() <= bound + h * h * memory ** 2 * steps.abs().sum((0, 2)) + 1e-9 * numeric.abs()).all()
+
+
 @pytest.mark.parametrize("widths", [(64, 64), (31, 63), (128, 64), (96, 128)], ids=str)
 @pytest.mark.parametrize("L", [1, 15, 33, 62, 95, 97, 126, 161, 287])
 def test_the_last_rows_of_a_tile(L, widths):
