@@ -497,7 +497,8 @@ typedef enum pdssm_layout { PDSSM_BHL = 0, PDSSM_BLH = 1 } pdssm_layout;
  *  * log_a below -200 counts as -200 (whose exp is 0 in fp32), so -inf resets
  *    the state: sequences packed one behind another are separated by it (the
  *    gradient of a log_a at or below -200 is zero).
- *    log_a > 0 grows the state, as the formula says.
+ *    log_a > 0 grows the state, as the formula says; its sum over any of up to
+ *    128 steps in a row has to stay below 88, where exp leaves fp32.
  *  * The sums run over chunks of steps: a non-finite value in x reaches the
  *    y of earlier steps of its chunk too, not only later ones.
  *  * States, sums and decays are fp32 (cumulated decays fp64).  bf16 inputs

@@ -268,6 +268,18 @@ def test_strong_and_absent_decay(dtype):
 
 
 @pytest.mark.parametrize("dtype", [F32, BF])
+def test_growing_states(dtype):
+    """log_a of either sign, and a head that grows by e^77 over a chunk."""
+    t = make(dtype, 1, 3, 3, 300, 32, 64, "bhl", "step", True, False, seed=17)
+    g = torch.Generator(device="cuda").manual_seed(18)
+    t["log_a"] = 0.3 * torch.randn(1, 3, 300, generator=g, device="cuda")
+    t["log_a"][:, 1] = -0.6
+    t["log_a"][:, 1, 128:256] = 0.6
+    t["log_a"][:, 2] = 0.05
+    check_all(t, fwd_bwd(t, "bhl"), "bhl", ("y", "h_last", "g_c", "g_b", "g_x", "g_log_a", "g_h0"))
+
+
+@pytest.mark.parametrize("dtype", [F32, BF])
 @pytest.mark.parametrize("layout", ["bhl", "blh"])
 def test_nothing_behind_a_length_is_read(dtype, layout):
     t = make(dtype, 3, 2, 2, 150, 64, 64, layout, "step", True, False, seed=5)
