@@ -200,6 +200,8 @@ pdssm_status pdssm_decay_scan_fwd(const pdssm_decay_dims *dims, const void *c, c
     cudaStream_t s = (cudaStream_t)stream;
     cudaError_t e;
     if (dims->L == 0) {
+        e = cudaMemsetAsync(ws, 0, sizeof(int), s);     // the status word
+        if (e != cudaSuccess) return cuda_fail(e, "status for L = 0");
         if (h_last && h_last != h0) {
             const size_t bytes = (size_t)(dims->B * dims->H * dims->N * dims->P) * 4;
             e = h0 ? cudaMemcpyAsync(h_last, h0, bytes, cudaMemcpyDeviceToDevice, s)

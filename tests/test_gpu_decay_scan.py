@@ -279,6 +279,13 @@ def test_growing_states(dtype):
     check_all(t, fwd_bwd(t, "bhl"), "bhl", ("y", "h_last", "g_c", "g_b", "g_x", "g_log_a", "g_h0"))
 
 
+def test_the_status_of_a_scan_of_no_steps():
+    t = make(BF, 2, 2, 1, 0, 8, 8, "blh", "head", True, False)
+    ws = torch.full((1 << 16,), 255, dtype=torch.uint8, device="cuda")
+    pd.pdssm_decay_scan_fwd(t["c"], t["b"], t["x"], t["log_a"], t["h0"], layout="blh", ws=ws)
+    assert pd.pdssm_ws_status(ws) == 0
+
+
 @pytest.mark.parametrize("dtype", [F32, BF])
 @pytest.mark.parametrize("layout", ["bhl", "blh"])
 def test_nothing_behind_a_length_is_read(dtype, layout):
