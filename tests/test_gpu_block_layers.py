@@ -270,3 +270,46 @@ def test_an_input_dropped_after_a_call_on_another_stream(call):
     others = [torch.full_like(src, float("nan")) for _ in range(3)]
     torch.cuda.synchronize()
     assert torch.equal(got, want) and len(others) == 3
+
+
+@pytest.mark.parametrize("call", ["norm", "norm_backward", "balance", "scan"])
+def test_a_given_stream_inside_a_capture(call):
+    """stream= named in a captured call, its inputs dropped before the replay of
+    what it made from them."""
+    src, run = calls_on_a_stream()[call]
+    want = run(src, None)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        t = src * 1.0
+        got = run(t, torch.cuda.current_stream())
+        del t
+        later = torch.full_like(src, float("nan"))
+    got.fill_(0)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(got, want) and torch.isnan(later).all()
+
+
+@pytest.mark.parametrize("call", ["norm", "norm_backward", "balance", "scan"])
+def test_calls_from_several_threads(call):
+    """Each thread on a stream of its own, at the same time."""
+    import threading
+
+    src, run = calls_on_a_stream()[call]
+    want, got, start = run(src, None), [None] * 4, threading.Barrier(4)
+    torch.cuda.synchronize()
+
+    def work(i):
+        side = torch.cuda.Stream()
+        start.wait()
+        for _ in range(20):
+            got[i] = run(src, side)
+        side.synchronize()
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    for g in got:
+        assert torch.equal(g, want)
